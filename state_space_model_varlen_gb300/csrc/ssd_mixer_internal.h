@@ -1,0 +1,32 @@
+// Internal declarations of the mixer operators' translation units.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/ssd_mixer.h"
+
+namespace ssd {
+
+// Each launches exactly one kernel; the arguments have been checked.
+cudaError_t launch_conv(const ssd_conv_params &p, cudaStream_t stream);
+cudaError_t launch_gated_norm(const ssd_gated_norm_params &p, cudaStream_t stream);
+cudaError_t launch_state_store(const ssd_state_params &p, cudaStream_t stream);
+cudaError_t launch_state_load(const ssd_state_params &p, cudaStream_t stream);
+// The step, one translation unit per state storage size.
+cudaError_t launch_step_32(const ssd_step_params &p, cudaStream_t stream);
+cudaError_t launch_step_16(const ssd_step_params &p, cudaStream_t stream);
+cudaError_t launch_step_8(const ssd_step_params &p, cudaStream_t stream);
+
+inline bool aligned_to(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) % bytes) == 0; }
+
+// The widest vector of a state row, in elements of `size` bytes: 16 bytes
+// where the row's bytes and the base allow it, then 4 elements, then 1.
+// Eight lanes share a row, so rows of fewer than eight vectors take narrower ones.
+inline int state_vector(int n, int size, const void *base) {
+    for (int v : {16 / size, 8 / size, 4})
+        if (v >= 4 && n % v == 0 && n / v >= 8 && aligned_to(base, (size_t)v * size)) return v;
+    return 1;
+}
+
+}  // namespace ssd
