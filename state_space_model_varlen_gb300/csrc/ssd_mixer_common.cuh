@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <stdint.h>
+#include <string.h>
 
 #include "../../include/ssd_mixer.h"
 #include "ssd_common.cuh"
@@ -34,6 +35,27 @@ __device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.f + __ex
 // softplus(z) = log(1 + e^z) in the overflow-safe form max(z,0) + log1p(e^-|z|)
 __device__ __forceinline__ float softplus(float z) { return fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))); }
 
+// Two fp32 operations in one instruction, each rounded as by itself.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t r, x, y, z;
+    memcpy(&x, &a, 8);
+    memcpy(&y, &b, 8);
+    memcpy(&z, &c, 8);
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    float2 o;
+    memcpy(&o, &r, 8);
+    return o;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t r, x, y;
+    memcpy(&x, &a, 8);
+    memcpy(&y, &b, 8);
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    float2 o;
+    memcpy(&o, &r, 8);
+    return o;
+}
+
 // ---------------------------------------------------------------------------
 // state storage
 // ---------------------------------------------------------------------------
@@ -49,32 +71,61 @@ template <int kType> constexpr float code_limit() { return kType == SSD_I8 ? 127
 
 // Stored values as floats; 8-bit codes without their scale.
 template <int kType, int V>
-__device__ __forceinline__ void decode(const Pack<typename Stored<kType>::T, V> &p, float (&out)[V]) {
+__device__ __forceinline__ void decode(const Pack<typename Stored<kType>::T, V> &p, float *out) {
+    if constexpr (kType == SSD_E4M3 && V >= 2) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        if constexpr (kType == SSD_F32) out[j] = p.v[j];
-        else if constexpr (kType == SSD_BF16) out[j] = __bfloat162float(p.v[j]);
-        else if constexpr (kType == SSD_F16) out[j] = __half2float(p.v[j]);
-        else if constexpr (kType == SSD_E4M3)
-            out[j] = __half2float(__half(__nv_cvt_fp8_to_halfraw(p.v[j], __NV_E4M3)));
-        else
-            out[j] = (float)(int8_t)p.v[j];
+        for (int j = 0; j < V; j += 2) {
+            const __half2_raw two =
+                __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(p.v[j] | p.v[j + 1] << 8), __NV_E4M3);
+            const float2 f = __half22float2(__half2(two));
+            out[j] = f.x;
+            out[j + 1] = f.y;
+        }
+    } else if constexpr (kType == SSD_I8 && V >= 4) {
+        // the code + 128 as the low byte of 2^23's mantissa
+#pragma unroll
+        for (int j = 0; j < V; j += 4) {
+            uint32_t w;
+            memcpy(&w, p.v + j, 4);
+            w ^= 0x80808080u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                out[j + i] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 | i)) - 8388736.f;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            if constexpr (kType == SSD_F32) out[j] = p.v[j];
+            else if constexpr (kType == SSD_BF16) out[j] = __bfloat162float(p.v[j]);
+            else if constexpr (kType == SSD_F16) out[j] = __half2float(p.v[j]);
+            else if constexpr (kType == SSD_E4M3)
+                out[j] = __half2float(__half(__nv_cvt_fp8_to_halfraw(p.v[j], __NV_E4M3)));
+            else
+                out[j] = (float)(int8_t)p.v[j];
+        }
     }
 }
 
-// What a row's largest magnitude (as float bits, sign cleared) makes of its
-// scale: inv multiplies the values, scale multiplies the codes.
-__device__ __forceinline__ void row_scale(uint32_t max_bits, float limit, float *inv, float *scale) {
-    const float m = __uint_as_float(max_bits);
-    if (max_bits >= 0x7f800000u) {              // an infinity or a NaN in the row
+// What a row's largest magnitude makes of its scale: inv multiplies the
+// values, scale multiplies the codes.
+__device__ __forceinline__ void row_scale(float m, float limit, float *inv, float *scale) {
+    *inv = __fmul_rn(__frcp_rn(m), limit);
+    *scale = __fmul_rn(m, 1.f / limit);
+    if (!(m < __int_as_float(0x7f800000))) {    // an infinity or a NaN in the row
         *inv = 0.f;
-        *scale = __uint_as_float(0x7fffffffu);
+        *scale = __int_as_float(0x7fffffff);
     } else if (m < 7.888609052210118e-31f) {    // 2^-100
         *inv = *scale = 0.f;
-    } else {
-        *inv = __fmul_rn(__frcp_rn(m), limit);
-        *scale = __fmul_rn(m, 1.f / limit);
     }
+}
+
+// sr_f16 with the dropped bits as an integer where fp16 is normal: there
+// (|v| - |lo|) / spacing is the 13 dropped bits over 2^13.
+__device__ __forceinline__ __half sr_f16_fast(float v, uint32_t r) {
+    const uint32_t bits = __float_as_uint(v), a = bits & 0x7fffffffu;
+    if (a < 0x38800000u || a >= 0x47800000u) return sr_f16(v, r);       // below 2^-14, from 2^16 on, inf, NaN
+    const uint32_t h = ((a - 0x38000000u) >> 13) + ((a << 19) > r ? 1u : 0u);
+    return __ushort_as_half((unsigned short)(h | (bits >> 16 & 0x8000u)));
 }
 
 // Eight-bit stochastic rounding, the random bytes of elements 16 q .. 16 q + 15.
@@ -82,16 +133,23 @@ __device__ __forceinline__ uint4 sr_bytes(uint64_t seed, uint64_t q) { return sr
 
 // V values times inv as codes, to nearest even.
 template <int kType, int V>
-__device__ __forceinline__ Pack<uint8_t, V> encode8(const float (&h)[V], float inv) {
+__device__ __forceinline__ Pack<uint8_t, V> encode8(const float *h, float inv) {
     Pack<uint8_t, V> out;
+    if constexpr (kType == SSD_E4M3 && V >= 2) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const float v = __fmul_rn(h[j], inv);
-        if constexpr (kType == SSD_E4M3) {
-            out.v[j] = __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
-        } else {
-            // 1.5 2^23 + v: the sum's rounding is the rounding to an integer
-            out.v[j] = (uint8_t)__float_as_uint(__fadd_rn(v, 12582912.f));
+        for (int j = 0; j < V; j += 2) {
+            const __nv_fp8x2_storage_t two = __nv_cvt_float2_to_fp8x2(
+                make_float2(__fmul_rn(h[j], inv), __fmul_rn(h[j + 1], inv)), __NV_SATFINITE, __NV_E4M3);
+            out.v[j] = (uint8_t)two;
+            out.v[j + 1] = (uint8_t)(two >> 8);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float v = __fmul_rn(h[j], inv);
+            // int8: 1.5 2^23 + v, whose rounding is the rounding to an integer
+            out.v[j] = kType == SSD_E4M3 ? (uint8_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3)
+                                         : (uint8_t)__float_as_uint(__fadd_rn(v, 12582912.f));
         }
     }
     return out;
@@ -111,24 +169,76 @@ __device__ __forceinline__ uint8_t encode8_sr(float h, float inv, uint32_t byte)
     }
 }
 
-template <int kType, int V>
-__device__ __forceinline__ Pack<uint8_t, V> encode8_sr(const float (&h)[V], float inv, uint64_t seed, uint64_t e0) {
-    Pack<uint8_t, V> out;
-    uint4 w = make_uint4(0, 0, 0, 0);
+// Four values with the four random bytes of `word`, packed low to high.
+template <int kType>
+__device__ __forceinline__ uint32_t encode8_sr4(const float *h, float inv, uint32_t word) {
+    if constexpr (kType == SSD_E4M3) {
+        // two fp16 at a time; after the sum and a shift left by one, the high
+        // byte of each half holds the seven bits that stay (fp16's top exponent
+        // bit is 0 below 2), its sign comes from the unshifted word
+        const float s = inv * 0.00390625f;
+        const uint32_t r = word & 0x7f7f7f7fu;
+        uint32_t x[2];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const uint64_t e = e0 + (uint64_t)j;
-        if (j == 0 || (e & 15) == 0) w = sr_bytes(seed, e >> 4);
-        const uint32_t word = sr_word(w, (uint32_t)(e >> 2) & 3u);
-        out.v[j] = encode8_sr<kType>(h[j], inv, (word >> (8 * ((uint32_t)e & 3u))) & 0xffu);
+        for (int i = 0; i < 2; ++i) {
+            const __half2 two = __floats2half2_rn(__fmul_rn(h[2 * i], s), __fmul_rn(h[2 * i + 1], s));
+            uint32_t f;
+            memcpy(&f, &two, 4);
+            f += __byte_perm(r, 0u, i ? 0x4342 : 0x4140);
+            x[i] = (f & 0x80008000u) | ((f << 1) & 0x7fff7fffu);
+        }
+        return __byte_perm(x[0], x[1], 0x7531);
+    } else {
+        uint32_t t[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // 128 + byte / 256 + 1/512
+            const float u = __uint_as_float(__byte_perm(word, 0x43000080u, 0x7604 | (i << 4))) - 128.f;
+            t[i] = __float_as_uint(__fadd_rd(__fmaf_rn(h[i], inv, u), 12582912.f));
+        }
+        return __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
+    }
+}
+
+template <int kType, int V>
+__device__ __forceinline__ Pack<uint8_t, V> encode8_sr(const float *h, float inv, uint64_t seed, uint64_t e0) {
+    Pack<uint8_t, V> out;
+    if constexpr (V >= 4) {         // e0 is a multiple of V: whole words
+        const uint4 w = sr_bytes(seed, e0 >> 4);
+        uint32_t word[4] = {w.x, w.y, w.z, w.w};
+        if constexpr (V == 8) {
+            word[0] = (e0 & 8) ? w.z : w.x;
+            word[1] = (e0 & 8) ? w.w : w.y;
+        } else if constexpr (V == 4) {
+            word[0] = sr_word(w, (uint32_t)(e0 >> 2) & 3u);
+        }
+#pragma unroll
+        for (int j = 0; j < V; j += 4) {
+            const uint32_t c = encode8_sr4<kType>(h + j, inv, word[j / 4]);
+            memcpy(out.v + j, &c, 4);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const uint64_t e = e0 + (uint64_t)j;
+            const uint32_t word = sr_word(sr_bytes(seed, e >> 4), (uint32_t)(e >> 2) & 3u);
+            out.v[j] = encode8_sr<kType>(h[j], inv, (word >> (8 * ((uint32_t)e & 3u))) & 0xffu);
+        }
     }
     return out;
 }
 
-// Largest magnitude over the eight lanes that share a row, as float bits.
-__device__ __forceinline__ uint32_t max8(uint32_t m) {
+// The larger magnitude; NaN if either is NaN.
+__device__ __forceinline__ float max_abs(float m, float v) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+    return r;
+}
+
+// Largest magnitude over the eight lanes that share a row (NaN if any is).
+__device__ __forceinline__ float max8(float m) {
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 4; o > 0; o >>= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
     return m;
 }
 __device__ __forceinline__ float sum8(float v) {

@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(kThreads) store_kernel(const ssd_state_params 
     const bool live = r < per;
     const DnT *src = static_cast<const DnT *>(a.states) + ((int64_t)s * per + r) * N;
     float v[E / V][V];
-    uint32_t big = 0;
+    float big = 0.f;
 #pragma unroll
     for (int k = 0; k < E / V; ++k) {
         const int n = (k * 8 + lane8) * V;
@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(kThreads) store_kernel(const ssd_state_params 
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             v[k][j] = to_float(p.v[j]);
-            big = max(big, __float_as_uint(v[k][j]) & 0x7fffffffu);
+            big = max_abs(big, v[k][j]);
         }
     }
     float inv, scale;

@@ -5,16 +5,18 @@
 //   h <- exp(dt' A) h + dt' x B^T,   y = (C h + D x) SiLU(z)
 //
 // The state is read once and written once and dwarfs the rest (N values for
-// each x): the kernel is bound by HBM, for small batches by latency.  One CTA
-// takes a request's head, or a block of its rows.  Eight lanes share a state
-// row, so that a row's sums and maxima take three shuffles, and a warp's four
-// rows are neighbours in memory.  Every thread issues the loads of all its
-// rows before the convolution, which needs the same indices: one memory round
-// trip covers both.
+// each x): the kernel is bound by HBM, for small batches by latency.
+//
+// A request's states are H P rows of N values; the rows of a group share B and
+// C.  A CTA takes a run of one group's rows, whatever heads they belong to,
+// and walks it in tiles; the loads of the next tile are issued before the
+// current one is worked on, and those of the first before the convolution,
+// which needs the same indices.  Eight lanes share a row, so that its sums and
+// maxima take three shuffles, and a warp's four rows are neighbours in memory.
 //
 // The convolution cache is a ring, so the row the call writes (pos mod rows)
 // is none of those its other CTAs read, and they need no order among them.
-// Every CTA of a group convolves the group's B and C for itself (from L2).
+// Every CTA convolves its group's B and C for itself (from L2).
 #pragma once
 
 #include "ssd_mixer_common.cuh"
@@ -24,9 +26,16 @@ namespace ssd {
 namespace {
 
 constexpr int kStepThreads = 128;
-constexpr int kStepGroups = kStepThreads / 8;      // state rows in flight at a time
+constexpr int kStepGroups = kStepThreads / 8;      // rows worked on at a time
+constexpr int kStepMaxRows = 256;                  // of one CTA
 
-// One channel's convolution at position pos; the newest input is `now`.
+struct StepPlan {
+    int rows;          // rows of a CTA, a multiple of the kernel's tile
+    int runs;          // CTAs of a group
+    int vec4;          // four channels of xbc, weight, bias and ring make aligned vectors, width 4
+};
+
+// One channel's convolution at position pos.
 template <typename IoT>
 __device__ __forceinline__ float conv_channel(const ssd_step_params &a, const IoT *xbc, const IoT *ring, int channels,
                                               int c, int pos, int row) {
@@ -44,185 +53,279 @@ __device__ __forceinline__ float conv_channel(const ssd_step_params &a, const Io
     return a.activation ? silu(acc) : acc;
 }
 
+// Four neighbouring channels, width 4, all loads issued together.
+template <typename IoT>
+__device__ __forceinline__ void conv_channels4(const ssd_step_params &a, const IoT *xbc, IoT *ring, int channels,
+                                               int c, int pos, int row, bool keep, float *dst) {
+    const Pack<IoT, 16> w = load_pack<IoT, 16>(static_cast<const IoT *>(a.weight) + (int64_t)c * 4);
+    Pack<IoT, 4> in[4], bias{};
+    in[0] = load_pack<IoT, 4>(xbc + c);
+#pragma unroll
+    for (int k = 1; k < 4; ++k) {
+        int r = row - k;
+        if (r < 0) r += a.conv_rows;
+        in[k] = Pack<IoT, 4>{};
+        if (k <= pos) in[k] = load_pack<IoT, 4>(ring + (int64_t)r * channels + c);
+    }
+    if (a.bias) bias = load_pack<IoT, 4>(static_cast<const IoT *>(a.bias) + c);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float acc = to_float(bias.v[j]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc = fmaf(to_float(w.v[4 * j + 3 - k]), to_float(in[k].v[j]), acc);
+        dst[j] = a.activation ? silu(acc) : acc;
+    }
+    if (keep) store_pack<IoT, 4>(ring + (int64_t)row * channels + c, in[0]);
+}
+
 // kType: storage of the state; E: state values a lane holds of a row (8 E >=
-// N); V: values of one load.  kRows: rows a lane works on.
+// N); V: values of one load; kRows: rows a lane works on at a time.
 template <int kType, int E, int V, int kRows>
-__global__ void __launch_bounds__(kStepThreads) step_kernel(const ssd_step_params a, int row_blocks) {
+__global__ void __launch_bounds__(kStepThreads, E == 32 ? 3 : 4) step_kernel(const ssd_step_params a, const StepPlan plan) {
     using StT = typename Stored<kType>::T;
     constexpr int kTile = kStepGroups * kRows;
     constexpr int kChunks = E / V;
     constexpr bool k8bit = kType == SSD_E4M3 || kType == SSD_I8;
-    __shared__ float s_b[8 * E], s_c[8 * E], s_x[kTile], s_y[kTile], s_dt[2];
+    // s_x: x, later y; s_dx: dt' x; s_keep: the decay
+    __shared__ __align__(16) float s_b[8 * E], s_c[8 * E], s_x[kStepMaxRows], s_y[kStepMaxRows];
+    __shared__ float s_dx[kStepMaxRows], s_keep[kStepMaxRows];
 
     const int N = a.dstate, P = a.headdim, H = a.nheads;
-    const int pb = blockIdx.x % row_blocks;
-    const int h = (blockIdx.x / row_blocks) % H;
-    const int b = blockIdx.x / row_blocks / H;
+    const int rows_g = H / a.ngroups * P;               // rows of a group
+    const int run = blockIdx.x % plan.runs;
+    const int g = (blockIdx.x / plan.runs) % a.ngroups;
+    const int b = blockIdx.x / plan.runs / a.ngroups;
     const int tid = threadIdx.x, lane8 = tid & 7, grp = tid >> 3;
-    const int p0 = pb * kTile, rows = min(kTile, P - p0);
-    const int64_t yrow = ((int64_t)b * H + h) * P + p0;
+    const int r0 = g * rows_g + run * plan.rows;        // the CTA's rows of the request: r0 .. r0 + rows - 1
+    const int rows = min(plan.rows, rows_g - run * plan.rows);
     const bool bf16 = a.io_dtype == SSD_BF16;
 
     const int slot = a.slot_idx[(int64_t)b * (a.slot_idx_stride ? a.slot_idx_stride : 1)];
     const int pos = a.pos[b];
+    const int64_t y0 = (int64_t)b * H * P + r0;
     if (slot < 0 || slot >= a.num_slots || pos < 0) {
         if (slot == -1) {
             for (int i = tid; i < rows; i += kStepThreads) {
-                if (bf16) static_cast<__nv_bfloat16 *>(a.out_y)[yrow + i] = __float2bfloat16_rn(0.f);
-                else static_cast<float *>(a.out_y)[yrow + i] = 0.f;
+                if (bf16) static_cast<__nv_bfloat16 *>(a.out_y)[y0 + i] = __float2bfloat16_rn(0.f);
+                else static_cast<float *>(a.out_y)[y0 + i] = 0.f;
             }
-        } else if (tid == 0 && pb == 0 && h == 0 && a.device_status) {
+        } else if (tid == 0 && run == 0 && g == 0 && a.device_status) {
             atomicOr(a.device_status, pos < 0 ? SSD_DEV_BAD_POS : SSD_DEV_BAD_SLOT);
         }
         return;
     }
 
     // ---- the state's loads -------------------------------------------------
-    const int64_t row0 = ((int64_t)slot * H + h) * P + p0;         // row of the cache
+    const int64_t row0 = (int64_t)slot * H * P + r0;    // row of the cache
     StT *cache = static_cast<StT *>(a.state_cache) + row0 * N;
     Pack<StT, V> raw[kRows][kChunks];
     float scale[kRows];
+    auto load_tile = [&](int t) {
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int r = grp + i * kStepGroups;
-        scale[i] = 0.f;
+        for (int i = 0; i < kRows; ++i) {
+            const int r = t + grp + i * kStepGroups;
+            scale[i] = 0.f;
 #pragma unroll
-        for (int k = 0; k < kChunks; ++k) {
-            const int n = (k * 8 + lane8) * V;
-            raw[i][k] = Pack<StT, V>{};
-            if (r < rows && n < N && pos > 0) raw[i][k] = load_pack<StT, V>(cache + (int64_t)r * N + n);
+            for (int k = 0; k < kChunks; ++k) {
+                const int n = (k * 8 + lane8) * V;
+                raw[i][k] = Pack<StT, V>{};
+                if (r < rows && n < N && pos > 0) raw[i][k] = load_pack<StT, V>(cache + (int64_t)r * N + n);
+            }
+            if (k8bit && r < rows && pos > 0) scale[i] = a.state_scale[row0 + r];
         }
-        if (k8bit && r < rows && pos > 0) scale[i] = a.state_scale[row0 + r];
-    }
+    };
+    load_tile(0);
 
     // ---- convolution -------------------------------------------------------
     const int channels = H * P + 2 * a.ngroups * N;
-    const int g = h / (H / a.ngroups);
     const int ring_row = pos % a.conv_rows;
-    const bool writes_bc = pb == 0 && h % (H / a.ngroups) == 0;
+    const int cb = H * P + g * N, cc = H * P + (a.ngroups + g) * N;     // first channels of B and C
     auto convolve = [&](auto io) {
         using IoT = decltype(io);
         const IoT *xbc = static_cast<const IoT *>(a.xbc) + (int64_t)b * a.xbc_stride;
         IoT *ring = static_cast<IoT *>(a.conv_cache) + (int64_t)slot * a.conv_rows * channels;
-        for (int i = tid; i < 2 * N + rows; i += kStepThreads) {
-            int c;
-            float *dst;
-            if (i < N) {
-                c = H * P + g * N + i;
-                dst = s_b + i;
-            } else if (i < 2 * N) {
-                c = H * P + (a.ngroups + g) * N + (i - N);
-                dst = s_c + (i - N);
-            } else {
-                c = h * P + p0 + (i - 2 * N);
-                dst = s_x + (i - 2 * N);
+        if (plan.vec4) {
+            for (int i = 4 * tid; i < 2 * N + rows; i += 4 * kStepThreads) {
+                const int c = i < N ? cb + i : i < 2 * N ? cc + i - N : r0 + i - 2 * N;
+                float *dst = i < N ? s_b + i : i < 2 * N ? s_c + i - N : s_x + i - 2 * N;
+                conv_channels4<IoT>(a, xbc, ring, channels, c, pos, ring_row, i >= 2 * N || run == 0, dst);
             }
-            *dst = conv_channel<IoT>(a, xbc, ring, channels, c, pos, ring_row);
-            if (i >= 2 * N || writes_bc) ring[(int64_t)ring_row * channels + c] = xbc[c];
+        } else {
+            for (int i = tid; i < 2 * N + rows; i += kStepThreads) {
+                const int c = i < N ? cb + i : i < 2 * N ? cc + i - N : r0 + i - 2 * N;
+                float *dst = i < N ? s_b + i : i < 2 * N ? s_c + i - N : s_x + i - 2 * N;
+                *dst = conv_channel<IoT>(a, xbc, ring, channels, c, pos, ring_row);
+                if (i >= 2 * N || run == 0) ring[(int64_t)ring_row * channels + c] = xbc[c];
+            }
         }
-        if (tid == 0) {
+        // dt' and decay, kept per row
+        const int h0 = r0 / P, h1 = (r0 + rows - 1) / P;
+        for (int h = h0 + tid; h <= h1; h += kStepThreads) {
             float dt = to_float(static_cast<const IoT *>(a.dt)[(int64_t)b * a.dt_stride + h]);
             if (a.dt_bias) dt += a.dt_bias[h];
             if (a.dt_softplus) dt = softplus(dt);
-            s_dt[0] = dt;
-            s_dt[1] = expf(dt * a.A[h]);
+            s_dx[h - h0] = dt;
+            s_keep[h - h0] = expf(dt * a.A[h]);
         }
+        return h0;
     };
-    for (int i = tid; i < 8 * E; i += kStepThreads)
-        if (i >= N) s_b[i] = s_c[i] = 0.f;
-    if (bf16) convolve(__nv_bfloat16{});
-    else convolve(float{});
+    for (int i = N + tid; i < 8 * E; i += kStepThreads) s_b[i] = s_c[i] = 0.f;
+    const int h0 = bf16 ? convolve(__nv_bfloat16{}) : convolve(float{});
+    __syncthreads();
+    {
+        float dx[kStepMaxRows / kStepThreads], keep[kStepMaxRows / kStepThreads];
+#pragma unroll
+        for (int k = 0; k < kStepMaxRows / kStepThreads; ++k) {
+            const int i = tid + k * kStepThreads;
+            if (i < rows) {
+                const int h = (r0 + i) / P - h0;
+                dx[k] = s_dx[h] * s_x[i];
+                keep[k] = s_keep[h];
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kStepMaxRows / kStepThreads; ++k) {
+            const int i = tid + k * kStepThreads;
+            if (i < rows) {
+                s_dx[i] = dx[k];
+                s_keep[i] = keep[k];
+            }
+        }
+    }
     __syncthreads();
 
     // ---- update and read-out -----------------------------------------------
-    const float dt = s_dt[0], decay = s_dt[1];
-    float bv[E], cv[E];
+    float2 bv[E / 2], cv[E / 2];
 #pragma unroll
     for (int k = 0; k < kChunks; ++k)
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            bv[k * V + j] = s_b[(k * 8 + lane8) * V + j];
-            cv[k * V + j] = s_c[(k * 8 + lane8) * V + j];
+            const int e = k * V + j, n = (k * 8 + lane8) * V + j;
+            (e & 1 ? bv[e / 2].y : bv[e / 2].x) = s_b[n];
+            (e & 1 ? cv[e / 2].y : cv[e / 2].x) = s_c[n];
         }
     const uint64_t seed = a.sr_seed ? *a.sr_seed : 0;
+    for (int t = 0; t < rows; t += kTile) {
+        Pack<StT, V> now[kRows][kChunks];
+        float now_scale[kRows];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int r = grp + i * kStepGroups;
-        const float dx = r < rows ? dt * s_x[r] : 0.f;
-        const float keep = k8bit ? decay * scale[i] : decay;
-        float st[kChunks][V];
-        float acc = 0.f;
-        uint32_t big = 0;
+        for (int i = 0; i < kRows; ++i) {
+            now_scale[i] = scale[i];
 #pragma unroll
-        for (int k = 0; k < kChunks; ++k) {
-            decode<kType, V>(raw[i][k], st[k]);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                st[k][j] = fmaf(keep, st[k][j], dx * bv[k * V + j]);
-                acc = fmaf(cv[k * V + j], st[k][j], acc);
-                if (k8bit) big = max(big, __float_as_uint(st[k][j]) & 0x7fffffffu);
-            }
+            for (int k = 0; k < kChunks; ++k) now[i][k] = raw[i][k];
         }
-        acc = sum8(acc);
-        if (lane8 == 0 && r < rows) s_y[r] = acc;
-        float inv = 0.f, sc = 0.f;
-        if constexpr (k8bit) {
-            row_scale(max8(big), code_limit<kType>(), &inv, &sc);
-            if (lane8 == 0 && r < rows) a.state_scale[row0 + r] = sc;
-        }
+        if (t + kTile < rows) load_tile(t + kTile);
 #pragma unroll
-        for (int k = 0; k < kChunks; ++k) {
-            const int n = (k * 8 + lane8) * V;
-            if (r >= rows || n >= N) continue;
-            StT *dst = cache + (int64_t)r * N + n;
-            const uint64_t e = (uint64_t)(row0 + r) * N + n;
-            Pack<StT, V> p;
-            if constexpr (kType == SSD_F32) {
+        for (int i = 0; i < kRows; ++i) {
+            const int r = t + grp + i * kStepGroups;
+            const bool live = r < rows;
+            const float dx = live ? s_dx[r] : 0.f;
+            float keep = live ? s_keep[r] : 0.f;
+            if (k8bit) keep *= now_scale[i];
+            float st[E];
+            const float2 dx2 = make_float2(dx, dx), keep2 = make_float2(keep, keep);
+            float2 acc = make_float2(0.f, 0.f);
+            float big = 0.f;
 #pragma unroll
-                for (int j = 0; j < V; ++j) p.v[j] = st[k][j];
-            } else if constexpr (kType == SSD_BF16) {
+            for (int k = 0; k < kChunks; ++k) {
+                if ((k * 8 + lane8) * V >= N) continue;     // past the row: an infinite x must not meet a zero there
+                decode<kType, V>(now[i][k], st + k * V);
+                if constexpr (V == 1) {
+                    st[k] = fmaf(keep, st[k], dx * (k & 1 ? bv[k / 2].y : bv[k / 2].x));
+                    acc.x = fmaf(k & 1 ? cv[k / 2].y : cv[k / 2].x, st[k], acc.x);
+                    if (k8bit) big = max_abs(big, st[k]);
+                } else {
 #pragma unroll
-                for (int j = 0; j < V; ++j) p.v[j] = __float2bfloat16_rn(st[k][j]);
-            } else if constexpr (kType == SSD_F16) {
-                uint4 w = make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    if (a.sr_seed) {
-                        if (j == 0 || ((e + j) & 3) == 0) w = sr_block(seed, (e + j) >> 2, 0u);
-                        p.v[j] = sr_f16(st[k][j], sr_word(w, (uint32_t)(e + j) & 3u));
-                    } else {
-                        p.v[j] = __float2half_rn(st[k][j]);
+                    for (int e = k * V; e < (k + 1) * V; e += 2) {
+                        const float2 s = fma2(keep2, make_float2(st[e], st[e + 1]), mul2(dx2, bv[e / 2]));
+                        acc = fma2(cv[e / 2], s, acc);
+                        st[e] = s.x;
+                        st[e + 1] = s.y;
+                        if (k8bit) big = max_abs(max_abs(big, s.x), s.y);
                     }
                 }
-            } else {
-                p = a.sr_seed ? encode8_sr<kType, V>(st[k], inv, seed, e) : encode8<kType, V>(st[k], inv);
             }
-            store_pack<StT, V>(dst, p);
+            const float sum = sum8(acc.x + acc.y);
+            if (lane8 == 0 && live) s_y[r] = sum;
+            float inv = 0.f, sc = 0.f;
+            if constexpr (k8bit) {
+                row_scale(max8(big), code_limit<kType>(), &inv, &sc);
+                if (lane8 == 0 && live) a.state_scale[row0 + r] = sc;
+            }
+#pragma unroll
+            for (int k = 0; k < kChunks; ++k) {
+                const int n = (k * 8 + lane8) * V;
+                if (!live || n >= N) continue;
+                const float *v = st + k * V;
+                const uint64_t e = (uint64_t)(row0 + r) * N + n;
+                Pack<StT, V> p;
+                if constexpr (kType == SSD_F32) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) p.v[j] = v[j];
+                } else if constexpr (kType == SSD_BF16) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) p.v[j] = __float2bfloat16_rn(v[j]);
+                } else if constexpr (kType == SSD_F16) {
+                    if (a.sr_seed) {
+                        uint4 w = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                        for (int j = 0; j < V; ++j) {
+                            if constexpr (V >= 4) {         // e is a multiple of 4
+                                if (j % 4 == 0) w = sr_block(seed, (e + j) >> 2, 0u);
+                                p.v[j] = sr_f16_fast(v[j], sr_word(w, j % 4));
+                            } else {
+                                w = sr_block(seed, (e + j) >> 2, 0u);
+                                p.v[j] = sr_f16_fast(v[j], sr_word(w, (uint32_t)(e + j) & 3u));
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < V; ++j) p.v[j] = __float2half_rn(v[j]);
+                    }
+                } else {
+                    p = a.sr_seed ? encode8_sr<kType, V>(v, inv, seed, e) : encode8<kType, V>(v, inv);
+                }
+                store_pack<StT, V>(cache + (int64_t)r * N + n, p);
+            }
         }
     }
     __syncthreads();
 
     // ---- y ------------------------------------------------------------------
     for (int i = tid; i < rows; i += kStepThreads) {
-        float y = s_y[i] + (a.D ? a.D[h] * s_x[i] : 0.f);
+        float y = s_y[i] + (a.D ? a.D[(r0 + i) / P] * s_x[i] : 0.f);
         if (bf16) {
-            if (a.z) y *= silu(__bfloat162float(static_cast<const __nv_bfloat16 *>(a.z)[(int64_t)b * a.z_stride + h * P + p0 + i]));
-            static_cast<__nv_bfloat16 *>(a.out_y)[yrow + i] = __float2bfloat16_rn(y);
+            if (a.z) y *= silu(__bfloat162float(static_cast<const __nv_bfloat16 *>(a.z)[(int64_t)b * a.z_stride + r0 + i]));
+            static_cast<__nv_bfloat16 *>(a.out_y)[y0 + i] = __float2bfloat16_rn(y);
         } else {
-            if (a.z) y *= silu(static_cast<const float *>(a.z)[(int64_t)b * a.z_stride + h * P + p0 + i]);
-            static_cast<float *>(a.out_y)[yrow + i] = y;
+            if (a.z) y *= silu(static_cast<const float *>(a.z)[(int64_t)b * a.z_stride + r0 + i]);
+            static_cast<float *>(a.out_y)[y0 + i] = y;
         }
     }
 }
 
 template <int kType, int E, int V>
 cudaError_t launch_step(const ssd_step_params &p, cudaStream_t stream) {
-    // a lane's raw state values: 4 rows, or 2 where they would take 512 bytes
-    constexpr int kRows = E * (int)sizeof(typename Stored<kType>::T) > 64 ? 2 : 4;
-    const int row_blocks = (p.headdim + kStepGroups * kRows - 1) / (kStepGroups * kRows);
-    const int64_t grid = (int64_t)p.batch * p.nheads * row_blocks;
+    constexpr int size = (int)sizeof(typename Stored<kType>::T);
+    // rows in flight: 64 values a lane (32 of fp32), at most four rows
+    constexpr int kRows = (size == 4 ? 32 : 64) / E < 4 ? (size == 4 ? 32 : 64) / E : 4;
+    constexpr int kTile = kStepGroups * kRows;
+    StepPlan plan;
+    const int rows_g = p.nheads / p.ngroups * p.headdim;
+    const int64_t tiles = ((int64_t)rows_g + kTile - 1) / kTile * p.ngroups * p.batch;
+    // long runs share the convolution of B and C; short ones fill the GPU
+    int run_tiles = (int)(tiles / (152 * 8));
+    run_tiles = run_tiles < 1 ? 1 : run_tiles > kStepMaxRows / kTile ? kStepMaxRows / kTile : run_tiles;
+    plan.rows = run_tiles * kTile;
+    plan.runs = (rows_g + plan.rows - 1) / plan.rows;
+    const int io = p.io_dtype == SSD_F32 ? 4 : 2, vec = 4 * io;
+    plan.vec4 = p.width == 4 && p.dstate % 4 == 0 && rows_g % 4 == 0 && p.xbc_stride % 4 == 0 &&
+                aligned_to(p.xbc, vec) && aligned_to(p.conv_cache, vec) && aligned_to(p.bias, vec) &&
+                aligned_to(p.weight, 16);
+    const int64_t grid = (int64_t)p.batch * p.ngroups * plan.runs;
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    step_kernel<kType, E, V, kRows><<<(unsigned)grid, kStepThreads, 0, stream>>>(p, row_blocks);
+    step_kernel<kType, E, V, kRows><<<(unsigned)grid, kStepThreads, 0, stream>>>(p, plan);
     return cudaGetLastError();
 }
 
