@@ -9,10 +9,12 @@
 //
 // A request's states are H P rows of N values; the rows of a group share B and
 // C.  A CTA takes a run of one group's rows, whatever heads they belong to,
-// and walks it in tiles; the loads of the next tile are issued before the
-// current one is worked on, and those of the first before the convolution,
-// which needs the same indices.  Eight lanes share a row, so that its sums and
-// maxima take three shuffles, and a warp's four rows are neighbours in memory.
+// sixteen at a time.  Eight lanes share a row, so that its sums and maxima take
+// three shuffles, and a warp's four rows are neighbours in memory.  A thread
+// copies its own share of the next rows into shared memory asynchronously, a
+// few steps ahead, and alone reads it back: no barriers, no registers for data
+// in flight, and the first copies run while the convolution, which needs the
+// same indices, loads its inputs.
 //
 // The convolution cache is a ring, so the row the call writes (pos mod rows)
 // is none of those its other CTAs read, and they need no order among them.
@@ -30,7 +32,7 @@ constexpr int kStepGroups = kStepThreads / 8;      // rows worked on at a time
 constexpr int kStepMaxRows = 256;                  // of one CTA
 
 struct StepPlan {
-    int rows;          // rows of a CTA, a multiple of the kernel's tile
+    int rows;          // rows of a CTA, a multiple of 16
     int runs;          // CTAs of a group
     int vec4;          // four channels of xbc, weight, bias and ring make aligned vectors, width 4
 };
@@ -78,17 +80,30 @@ __device__ __forceinline__ void conv_channels4(const ssd_step_params &a, const I
     if (keep) store_pack<IoT, 4>(ring + (int64_t)row * channels + c, in[0]);
 }
 
+// A thread's share of a row, kBytes of it, into its own place in shared memory;
+// zeros where `live` is false.
+template <int kBytes>
+__device__ __forceinline__ void copy_async(void *dst, const void *src, bool live) {
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst);
+    const int n = live ? kBytes : 0;
+    if constexpr (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(src), "n"(kBytes), "r"(n) : "memory");
+}
+
 // kType: storage of the state; E: state values a lane holds of a row (8 E >=
-// N); V: values of one load; kRows: rows a lane works on at a time.
-template <int kType, int E, int V, int kRows>
-__global__ void __launch_bounds__(kStepThreads, E == 32 ? 3 : 4) step_kernel(const ssd_step_params a, const StepPlan plan) {
+// N); V: values of one copy; kDepth: row steps copied ahead.
+template <int kType, int E, int V, int kDepth>
+__global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(const ssd_step_params a, const StepPlan plan) {
     using StT = typename Stored<kType>::T;
-    constexpr int kTile = kStepGroups * kRows;
     constexpr int kChunks = E / V;
     constexpr bool k8bit = kType == SSD_E4M3 || kType == SSD_I8;
-    // s_x: x, later y; s_dx: dt' x; s_keep: the decay
+    constexpr bool kAsync = V * sizeof(StT) >= 4;       // narrower shares are loaded when they are needed
     __shared__ __align__(16) float s_b[8 * E], s_c[8 * E], s_x[kStepMaxRows], s_y[kStepMaxRows];
-    __shared__ float s_dx[kStepMaxRows], s_keep[kStepMaxRows];
+    __shared__ float s_dx[kStepMaxRows], s_keep[kStepMaxRows];     // dt' x; decay (times the row's scale)
+    __shared__ float s_scale[k8bit ? kStepMaxRows : 1];
+    __shared__ Pack<StT, V> s_raw[kAsync ? kDepth * kChunks * kStepThreads : 1];
 
     const int N = a.dstate, P = a.headdim, H = a.nheads;
     const int rows_g = H / a.ngroups * P;               // rows of a group
@@ -115,26 +130,25 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 3 : 4) step_kernel(con
         return;
     }
 
-    // ---- the state's loads -------------------------------------------------
+    // ---- the state's first copies ------------------------------------------
     const int64_t row0 = (int64_t)slot * H * P + r0;    // row of the cache
     StT *cache = static_cast<StT *>(a.state_cache) + row0 * N;
-    Pack<StT, V> raw[kRows][kChunks];
-    float scale[kRows];
-    auto load_tile = [&](int t) {
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int r = t + grp + i * kStepGroups;
-            scale[i] = 0.f;
+    // the rows t .. t + 15, to the stage's places
+    auto copy_rows = [&](int t, int stage) {
+        if constexpr (kAsync) {
+            const int r = t + grp;
 #pragma unroll
             for (int k = 0; k < kChunks; ++k) {
                 const int n = (k * 8 + lane8) * V;
-                raw[i][k] = Pack<StT, V>{};
-                if (r < rows && n < N && pos > 0) raw[i][k] = load_pack<StT, V>(cache + (int64_t)r * N + n);
+                const bool live = r < rows && n < N && pos > 0;
+                copy_async<V * (int)sizeof(StT)>(&s_raw[(stage * kChunks + k) * kStepThreads + tid],
+                                                 live ? cache + (int64_t)r * N + n : cache, live);
             }
-            if (k8bit && r < rows && pos > 0) scale[i] = a.state_scale[row0 + r];
+            asm volatile("cp.async.commit_group;" ::: "memory");
         }
     };
-    load_tile(0);
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) copy_rows(d * kStepGroups, d);
 
     // ---- convolution -------------------------------------------------------
     const int channels = H * P + 2 * a.ngroups * N;
@@ -181,6 +195,7 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 3 : 4) step_kernel(con
                 const int h = (r0 + i) / P - h0;
                 dx[k] = s_dx[h] * s_x[i];
                 keep[k] = s_keep[h];
+                if (k8bit) keep[k] *= pos > 0 ? a.state_scale[row0 + i] : 0.f;
             }
         }
         __syncthreads();
@@ -206,94 +221,93 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 3 : 4) step_kernel(con
             (e & 1 ? cv[e / 2].y : cv[e / 2].x) = s_c[n];
         }
     const uint64_t seed = a.sr_seed ? *a.sr_seed : 0;
-    for (int t = 0; t < rows; t += kTile) {
-        Pack<StT, V> now[kRows][kChunks];
-        float now_scale[kRows];
+    int stage = 0;
+#pragma unroll 1
+    for (int t = 0; t < rows; t += kStepGroups) {
+        const int r = t + grp;
+        const bool live = r < rows;
+        const float dx = live ? s_dx[r] : 0.f;
+        const float keep = live ? s_keep[r] : 0.f;
+        const float2 dx2 = make_float2(dx, dx), keep2 = make_float2(keep, keep);
+        float2 acc = make_float2(0.f, 0.f);
+        float st[E];
+        float big = 0.f;
+        if constexpr (kAsync) asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            now_scale[i] = scale[i];
+        for (int k = 0; k < kChunks; ++k) {
+            const int n = (k * 8 + lane8) * V;
+            if (n >= N) continue;       // past the row: an infinite x must not meet a zero there
+            Pack<StT, V> now{};
+            if constexpr (kAsync) now = s_raw[(stage * kChunks + k) * kStepThreads + tid];
+            else if (live && pos > 0) now = load_pack<StT, V>(cache + (int64_t)r * N + n);
+            decode<kType, V>(now, st + k * V);
+            if constexpr (V == 1) {
+                st[k] = fmaf(keep, st[k], dx * (k & 1 ? bv[k / 2].y : bv[k / 2].x));
+                acc.x = fmaf(k & 1 ? cv[k / 2].y : cv[k / 2].x, st[k], acc.x);
+                if (k8bit) big = max_abs(big, st[k]);
+            } else {
 #pragma unroll
-            for (int k = 0; k < kChunks; ++k) now[i][k] = raw[i][k];
+                for (int e = k * V; e < (k + 1) * V; e += 2) {
+                    const float2 s = fma2(keep2, make_float2(st[e], st[e + 1]), mul2(dx2, bv[e / 2]));
+                    acc = fma2(cv[e / 2], s, acc);
+                    st[e] = s.x;
+                    st[e + 1] = s.y;
+                    if (k8bit) big = max_abs(max_abs(big, s.x), s.y);
+                }
+            }
         }
-        if (t + kTile < rows) load_tile(t + kTile);
+        // the values are in registers: their places take the rows kDepth steps on
+        copy_rows(t + kDepth * kStepGroups, stage);
+        stage = stage + 1 == kDepth ? 0 : stage + 1;
+        const float sum = sum8(acc.x + acc.y);
+        if (lane8 == 0 && live) s_y[r] = sum;
+        float inv = 0.f, sc = 0.f;
+        if constexpr (k8bit) {
+            row_scale(max8(big), code_limit<kType>(), &inv, &sc);
+            if (lane8 == 0 && live) s_scale[r] = sc;
+        }
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int r = t + grp + i * kStepGroups;
-            const bool live = r < rows;
-            const float dx = live ? s_dx[r] : 0.f;
-            float keep = live ? s_keep[r] : 0.f;
-            if (k8bit) keep *= now_scale[i];
-            float st[E];
-            const float2 dx2 = make_float2(dx, dx), keep2 = make_float2(keep, keep);
-            float2 acc = make_float2(0.f, 0.f);
-            float big = 0.f;
+        for (int k = 0; k < kChunks; ++k) {
+            const int n = (k * 8 + lane8) * V;
+            if (!live || n >= N) continue;
+            const float *v = st + k * V;
+            const uint64_t e = (uint64_t)(row0 + r) * N + n;
+            Pack<StT, V> p;
+            if constexpr (kType == SSD_F32) {
 #pragma unroll
-            for (int k = 0; k < kChunks; ++k) {
-                if ((k * 8 + lane8) * V >= N) continue;     // past the row: an infinite x must not meet a zero there
-                decode<kType, V>(now[i][k], st + k * V);
-                if constexpr (V == 1) {
-                    st[k] = fmaf(keep, st[k], dx * (k & 1 ? bv[k / 2].y : bv[k / 2].x));
-                    acc.x = fmaf(k & 1 ? cv[k / 2].y : cv[k / 2].x, st[k], acc.x);
-                    if (k8bit) big = max_abs(big, st[k]);
-                } else {
+                for (int j = 0; j < V; ++j) p.v[j] = v[j];
+            } else if constexpr (kType == SSD_BF16) {
 #pragma unroll
-                    for (int e = k * V; e < (k + 1) * V; e += 2) {
-                        const float2 s = fma2(keep2, make_float2(st[e], st[e + 1]), mul2(dx2, bv[e / 2]));
-                        acc = fma2(cv[e / 2], s, acc);
-                        st[e] = s.x;
-                        st[e + 1] = s.y;
-                        if (k8bit) big = max_abs(max_abs(big, s.x), s.y);
-                    }
-                }
-            }
-            const float sum = sum8(acc.x + acc.y);
-            if (lane8 == 0 && live) s_y[r] = sum;
-            float inv = 0.f, sc = 0.f;
-            if constexpr (k8bit) {
-                row_scale(max8(big), code_limit<kType>(), &inv, &sc);
-                if (lane8 == 0 && live) a.state_scale[row0 + r] = sc;
-            }
+                for (int j = 0; j < V; ++j) p.v[j] = __float2bfloat16_rn(v[j]);
+            } else if constexpr (kType == SSD_F16) {
+                if (a.sr_seed) {
+                    uint4 w = make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int k = 0; k < kChunks; ++k) {
-                const int n = (k * 8 + lane8) * V;
-                if (!live || n >= N) continue;
-                const float *v = st + k * V;
-                const uint64_t e = (uint64_t)(row0 + r) * N + n;
-                Pack<StT, V> p;
-                if constexpr (kType == SSD_F32) {
-#pragma unroll
-                    for (int j = 0; j < V; ++j) p.v[j] = v[j];
-                } else if constexpr (kType == SSD_BF16) {
-#pragma unroll
-                    for (int j = 0; j < V; ++j) p.v[j] = __float2bfloat16_rn(v[j]);
-                } else if constexpr (kType == SSD_F16) {
-                    if (a.sr_seed) {
-                        uint4 w = make_uint4(0, 0, 0, 0);
-#pragma unroll
-                        for (int j = 0; j < V; ++j) {
-                            if constexpr (V >= 4) {         // e is a multiple of 4
-                                if (j % 4 == 0) w = sr_block(seed, (e + j) >> 2, 0u);
-                                p.v[j] = sr_f16_fast(v[j], sr_word(w, j % 4));
-                            } else {
-                                w = sr_block(seed, (e + j) >> 2, 0u);
-                                p.v[j] = sr_f16_fast(v[j], sr_word(w, (uint32_t)(e + j) & 3u));
-                            }
+                    for (int j = 0; j < V; ++j) {
+                        if constexpr (V >= 4) {         // e is a multiple of 4
+                            if (j % 4 == 0) w = sr_block(seed, (e + j) >> 2, 0u);
+                            p.v[j] = sr_f16_fast(v[j], sr_word(w, j % 4));
+                        } else {
+                            w = sr_block(seed, (e + j) >> 2, 0u);
+                            p.v[j] = sr_f16_fast(v[j], sr_word(w, (uint32_t)(e + j) & 3u));
                         }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < V; ++j) p.v[j] = __float2half_rn(v[j]);
                     }
                 } else {
-                    p = a.sr_seed ? encode8_sr<kType, V>(v, inv, seed, e) : encode8<kType, V>(v, inv);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) p.v[j] = __float2half_rn(v[j]);
                 }
-                store_pack<StT, V>(cache + (int64_t)r * N + n, p);
+            } else {
+                p = a.sr_seed ? encode8_sr<kType, V>(v, inv, seed, e) : encode8<kType, V>(v, inv);
             }
+            store_pack<StT, V>(cache + (int64_t)r * N + n, p);
         }
     }
+    if constexpr (kAsync) asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
 
     // ---- y ------------------------------------------------------------------
     for (int i = tid; i < rows; i += kStepThreads) {
+        if (k8bit) a.state_scale[row0 + i] = s_scale[i];
         float y = s_y[i] + (a.D ? a.D[(r0 + i) / P] * s_x[i] : 0.f);
         if (bf16) {
             if (a.z) y *= silu(__bfloat162float(static_cast<const __nv_bfloat16 *>(a.z)[(int64_t)b * a.z_stride + r0 + i]));
@@ -308,16 +322,14 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 3 : 4) step_kernel(con
 template <int kType, int E, int V>
 cudaError_t launch_step(const ssd_step_params &p, cudaStream_t stream) {
     constexpr int size = (int)sizeof(typename Stored<kType>::T);
-    // rows in flight: 64 values a lane (32 of fp32), at most four rows
-    constexpr int kRows = (size == 4 ? 32 : 64) / E < 4 ? (size == 4 ? 32 : 64) / E : 4;
-    constexpr int kTile = kStepGroups * kRows;
+    // steps in flight: 24 KB of a CTA's states, at least two, at most six
+    constexpr int kFit = 24576 / (kStepThreads * E * size);
+    constexpr int kDepth = kFit < 2 ? 2 : kFit > 6 ? 6 : kFit;
     StepPlan plan;
     const int rows_g = p.nheads / p.ngroups * p.headdim;
-    const int64_t tiles = ((int64_t)rows_g + kTile - 1) / kTile * p.ngroups * p.batch;
     // long runs share the convolution of B and C; short ones fill the GPU
-    int run_tiles = (int)(tiles / (152 * 8));
-    run_tiles = run_tiles < 1 ? 1 : run_tiles > kStepMaxRows / kTile ? kStepMaxRows / kTile : run_tiles;
-    plan.rows = run_tiles * kTile;
+    const int64_t share = (int64_t)rows_g * p.ngroups * p.batch / (152 * 12);
+    plan.rows = share >= kStepMaxRows ? kStepMaxRows : share >= 128 ? 128 : share >= 64 ? 64 : 32;
     plan.runs = (rows_g + plan.rows - 1) / plan.rows;
     const int io = p.io_dtype == SSD_F32 ? 4 : 2, vec = 4 * io;
     plan.vec4 = p.width == 4 && p.dstate % 4 == 0 && rows_g % 4 == 0 && p.xbc_stride % 4 == 0 &&
@@ -325,7 +337,7 @@ cudaError_t launch_step(const ssd_step_params &p, cudaStream_t stream) {
                 aligned_to(p.weight, 16);
     const int64_t grid = (int64_t)p.batch * p.ngroups * plan.runs;
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    step_kernel<kType, E, V, kRows><<<(unsigned)grid, kStepThreads, 0, stream>>>(p, plan);
+    step_kernel<kType, E, V, kDepth><<<(unsigned)grid, kStepThreads, 0, stream>>>(p, plan);
     return cudaGetLastError();
 }
 
