@@ -69,29 +69,32 @@ template <> struct Stored<SSD_I8> { using T = uint8_t; };
 // Largest code of the 8-bit types.
 template <int kType> constexpr float code_limit() { return kType == SSD_I8 ? 127.f : 448.f; }
 
+// Four codes, packed low to high, as floats without their scale.
+template <int kType> __device__ __forceinline__ void decode4(uint32_t w, float *out) {
+    if constexpr (kType == SSD_E4M3) {
+        const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
+        const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
+        const float2 f0 = __half22float2(__half2(lo)), f1 = __half22float2(__half2(hi));
+        out[0] = f0.x;
+        out[1] = f0.y;
+        out[2] = f1.x;
+        out[3] = f1.y;
+    } else {
+        // the code + 128 as the low byte of 2^23's mantissa
+        w ^= 0x80808080u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out[i] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 | i)) - 8388736.f;
+    }
+}
+
 // Stored values as floats; 8-bit codes without their scale.
 template <int kType, int V>
 __device__ __forceinline__ void decode(const Pack<typename Stored<kType>::T, V> &p, float *out) {
-    if constexpr (kType == SSD_E4M3 && V >= 2) {
+    if constexpr ((kType == SSD_E4M3 || kType == SSD_I8) && V >= 4) {
+        uint32_t w[V / 4];
+        memcpy(w, p.v, V);
 #pragma unroll
-        for (int j = 0; j < V; j += 2) {
-            const __half2_raw two =
-                __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(p.v[j] | p.v[j + 1] << 8), __NV_E4M3);
-            const float2 f = __half22float2(__half2(two));
-            out[j] = f.x;
-            out[j + 1] = f.y;
-        }
-    } else if constexpr (kType == SSD_I8 && V >= 4) {
-        // the code + 128 as the low byte of 2^23's mantissa
-#pragma unroll
-        for (int j = 0; j < V; j += 4) {
-            uint32_t w;
-            memcpy(&w, p.v + j, 4);
-            w ^= 0x80808080u;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                out[j + i] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 | i)) - 8388736.f;
-        }
+        for (int j = 0; j < V; j += 4) decode4<kType>(w[j / 4], out + j);
     } else {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -128,38 +131,69 @@ __device__ __forceinline__ __half sr_f16_fast(float v, uint32_t r) {
     return __ushort_as_half((unsigned short)(h | (bits >> 16 & 0x8000u)));
 }
 
-// Eight-bit stochastic rounding, the random bytes of elements 16 q .. 16 q + 15.
-__device__ __forceinline__ uint4 sr_bytes(uint64_t seed, uint64_t q) { return sr_block(seed, q, 2u); }
+// ---- nearest ---------------------------------------------------------------
+template <int kType> __device__ __forceinline__ uint32_t encode4(const float *h, float inv) {
+    if constexpr (kType == SSD_E4M3) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(h[0], inv), __fmul_rn(h[1], inv)),
+                                                     __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(h[2], inv), __fmul_rn(h[3], inv)),
+                                                     __NV_SATFINITE, __NV_E4M3);
+        return __byte_perm(lo, hi, 0x5410);
+    } else {
+        // 1.5 2^23 + v, whose rounding is the rounding to an integer
+        uint32_t t[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] = __float_as_uint(__fadd_rn(__fmul_rn(h[i], inv), 12582912.f));
+        return __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
+    }
+}
+template <int kType> __device__ __forceinline__ uint8_t encode1(float h, float inv) {
+    const float v = __fmul_rn(h, inv);
+    return kType == SSD_E4M3 ? (uint8_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3)
+                             : (uint8_t)__float_as_uint(__fadd_rn(v, 12582912.f));
+}
 
 // V values times inv as codes, to nearest even.
 template <int kType, int V>
 __device__ __forceinline__ Pack<uint8_t, V> encode8(const float *h, float inv) {
     Pack<uint8_t, V> out;
-    if constexpr (kType == SSD_E4M3 && V >= 2) {
+    if constexpr (V >= 4) {
+        uint32_t w[V / 4];
 #pragma unroll
-        for (int j = 0; j < V; j += 2) {
-            const __nv_fp8x2_storage_t two = __nv_cvt_float2_to_fp8x2(
-                make_float2(__fmul_rn(h[j], inv), __fmul_rn(h[j + 1], inv)), __NV_SATFINITE, __NV_E4M3);
-            out.v[j] = (uint8_t)two;
-            out.v[j + 1] = (uint8_t)(two >> 8);
-        }
+        for (int j = 0; j < V; j += 4) w[j / 4] = encode4<kType>(h + j, inv);
+        memcpy(out.v, w, V);
     } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float v = __fmul_rn(h[j], inv);
-            // int8: 1.5 2^23 + v, whose rounding is the rounding to an integer
-            out.v[j] = kType == SSD_E4M3 ? (uint8_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3)
-                                         : (uint8_t)__float_as_uint(__fadd_rn(v, 12582912.f));
-        }
+        for (int j = 0; j < V; ++j) out.v[j] = encode1<kType>(h[j], inv);
     }
     return out;
 }
 
-// The same with random bytes: stochastic rounding, see SSD_E4M3 in ssd_mixer.h.
-template <int kType>
-__device__ __forceinline__ uint8_t encode8_sr(float h, float inv, uint32_t byte) {
+// ---- stochastic, see SSD_E4M3 in ssd_mixer.h ---------------------------------
+// Random bytes of the 16 elements of block q: Philox as sr_block, with the ten
+// rounds' keys prepared (keys[2 r], keys[2 r + 1]).
+__device__ __forceinline__ void round_keys(uint64_t seed, int i, uint32_t *keys) {
+    const uint32_t r = (uint32_t)i >> 1;
+    keys[i] = (i & 1) ? (uint32_t)(seed >> 32) + r * 0xBB67AE85u : (uint32_t)seed + r * 0x9E3779B9u;
+}
+__device__ __forceinline__ uint4 sr_keyed(const uint32_t *keys, uint64_t q, uint32_t stream) {
+    uint4 c = make_uint4((uint32_t)q, (uint32_t)(q >> 32), stream, 0u);
+#pragma unroll
+    for (int r = 0; r < 10; r += 2) {
+        const uint4 k = *reinterpret_cast<const uint4 *>(keys + 2 * r);
+        uint64_t p0 = (uint64_t)0xD2511F53u * c.x, p1 = (uint64_t)0xCD9E8D57u * c.z;
+        c = make_uint4((uint32_t)(p1 >> 32) ^ c.y ^ k.x, (uint32_t)p1, (uint32_t)(p0 >> 32) ^ c.w ^ k.y, (uint32_t)p0);
+        p0 = (uint64_t)0xD2511F53u * c.x;
+        p1 = (uint64_t)0xCD9E8D57u * c.z;
+        c = make_uint4((uint32_t)(p1 >> 32) ^ c.y ^ k.z, (uint32_t)p1, (uint32_t)(p0 >> 32) ^ c.w ^ k.w, (uint32_t)p0);
+    }
+    return c;
+}
+
+// One value with its random byte.
+template <int kType> __device__ __forceinline__ uint8_t encode1_sr(float h, float inv, uint32_t byte) {
     if constexpr (kType == SSD_E4M3) {
-        const uint32_t f = __half_as_ushort(__float2half_rn(__fmul_rn(h, inv) * 0.00390625f));
+        const uint32_t f = __half_as_ushort(__float2half_rn(__fmul_rn(h, inv * 0.00390625f)));
         return (uint8_t)((((f & 0x7fffu) + (byte & 0x7fu)) >> 7) | ((f >> 8) & 0x80u));
     } else {
         // floor(h inv + u), u = (byte + 1/2) / 256 (the mantissa of 128 + u, exactly), as
@@ -170,29 +204,23 @@ __device__ __forceinline__ uint8_t encode8_sr(float h, float inv, uint32_t byte)
 }
 
 // Four values with the four random bytes of `word`, packed low to high.
-template <int kType>
-__device__ __forceinline__ uint32_t encode8_sr4(const float *h, float inv, uint32_t word) {
+template <int kType> __device__ __forceinline__ uint32_t encode4_sr(const float *h, float inv, uint32_t word) {
     if constexpr (kType == SSD_E4M3) {
-        // two fp16 at a time; after the sum and a shift left by one, the high
-        // byte of each half holds the seven bits that stay (fp16's top exponent
-        // bit is 0 below 2), its sign comes from the unshifted word
+        // values 0, 2 and 1, 3 as pairs of fp16, doubled with the random bits
+        // doubled: the high byte of each half then holds the seven bits that stay
+        // (fp16's top exponent bit is 0 below 2); the sign comes from the fp16
         const float s = inv * 0.00390625f;
-        const uint32_t r = word & 0x7f7f7f7fu;
-        uint32_t x[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const __half2 two = __floats2half2_rn(__fmul_rn(h[2 * i], s), __fmul_rn(h[2 * i + 1], s));
-            uint32_t f;
-            memcpy(&f, &two, 4);
-            f += __byte_perm(r, 0u, i ? 0x4342 : 0x4140);
-            x[i] = (f & 0x80008000u) | ((f << 1) & 0x7fff7fffu);
-        }
-        return __byte_perm(x[0], x[1], 0x7531);
+        const __half2 even = __floats2half2_rn(__fmul_rn(h[0], s), __fmul_rn(h[2], s));
+        const __half2 odd = __floats2half2_rn(__fmul_rn(h[1], s), __fmul_rn(h[3], s));
+        uint32_t fe, fo;
+        memcpy(&fe, &even, 4);
+        memcpy(&fo, &odd, 4);
+        const uint32_t xe = 2u * fe + ((word << 1) & 0x00fe00feu), xo = 2u * fo + ((word >> 7) & 0x00fe00feu);
+        return __byte_perm((fe & 0x80008000u) | (xe & 0x7f007f00u), (fo & 0x80008000u) | (xo & 0x7f007f00u), 0x7351);
     } else {
         uint32_t t[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            // 128 + byte / 256 + 1/512
             const float u = __uint_as_float(__byte_perm(word, 0x43000080u, 0x7604 | (i << 4))) - 128.f;
             t[i] = __float_as_uint(__fadd_rd(__fmaf_rn(h[i], inv, u), 12582912.f));
         }
@@ -200,50 +228,52 @@ __device__ __forceinline__ uint32_t encode8_sr4(const float *h, float inv, uint3
     }
 }
 
+// V values of flat elements e0 .. (a multiple of V where V >= 4).
 template <int kType, int V>
-__device__ __forceinline__ Pack<uint8_t, V> encode8_sr(const float *h, float inv, uint64_t seed, uint64_t e0) {
+__device__ __forceinline__ Pack<uint8_t, V> encode8_sr(const float *h, float inv, const uint32_t *keys, uint64_t e0) {
     Pack<uint8_t, V> out;
-    if constexpr (V >= 4) {         // e0 is a multiple of V: whole words
-        const uint4 w = sr_bytes(seed, e0 >> 4);
-        uint32_t word[4] = {w.x, w.y, w.z, w.w};
+    if constexpr (V >= 4) {
+        const uint4 r = sr_keyed(keys, e0 >> 4, 2u);
+        uint32_t word[4] = {r.x, r.y, r.z, r.w}, w[V / 4];
         if constexpr (V == 8) {
-            word[0] = (e0 & 8) ? w.z : w.x;
-            word[1] = (e0 & 8) ? w.w : w.y;
+            word[0] = (e0 & 8) ? r.z : r.x;
+            word[1] = (e0 & 8) ? r.w : r.y;
         } else if constexpr (V == 4) {
-            word[0] = sr_word(w, (uint32_t)(e0 >> 2) & 3u);
+            word[0] = sr_word(r, (uint32_t)(e0 >> 2) & 3u);
         }
 #pragma unroll
-        for (int j = 0; j < V; j += 4) {
-            const uint32_t c = encode8_sr4<kType>(h + j, inv, word[j / 4]);
-            memcpy(out.v + j, &c, 4);
-        }
+        for (int j = 0; j < V; j += 4) w[j / 4] = encode4_sr<kType>(h + j, inv, word[j / 4]);
+        memcpy(out.v, w, V);
     } else {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const uint64_t e = e0 + (uint64_t)j;
-            const uint32_t word = sr_word(sr_bytes(seed, e >> 4), (uint32_t)(e >> 2) & 3u);
-            out.v[j] = encode8_sr<kType>(h[j], inv, (word >> (8 * ((uint32_t)e & 3u))) & 0xffu);
+            const uint32_t word = sr_word(sr_keyed(keys, e >> 4, 2u), (uint32_t)(e >> 2) & 3u);
+            out.v[j] = encode1_sr<kType>(h[j], inv, (word >> (8 * ((uint32_t)e & 3u))) & 0xffu);
         }
     }
     return out;
 }
 
-// The larger magnitude; NaN if either is NaN.
-__device__ __forceinline__ float max_abs(float m, float v) {
+// The larger magnitude; NaN if any is NaN.
+__device__ __forceinline__ float max_abs(float m, float u, float v) {
     float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(u), "f"(v));
     return r;
 }
 
-// Largest magnitude over the eight lanes that share a row (NaN if any is).
-__device__ __forceinline__ float max8(float m) {
+// Largest magnitude and sum over the L lanes that share a row.
+template <int L> __device__ __forceinline__ float lanes_max(float m) {
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = L / 2; o > 0; o >>= 1) {
+        const float v = __shfl_xor_sync(0xffffffffu, m, o);
+        m = max_abs(m, v, v);
+    }
     return m;
 }
-__device__ __forceinline__ float sum8(float v) {
+template <int L> __device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 

@@ -26,6 +26,9 @@ __global__ void __launch_bounds__(kThreads) store_kernel(const ssd_state_params 
     const int64_t per = (int64_t)a.nheads * a.headdim;
     const int64_t r = (int64_t)(blockIdx.x % blocks) * kGroups + (threadIdx.x >> 3);
     const int lane8 = threadIdx.x & 7;
+    __shared__ __align__(16) uint32_t keys[20];
+    if (a.sr_seed && threadIdx.x < 20) round_keys(*a.sr_seed, threadIdx.x, keys);
+    __syncthreads();
     const int slot = checked_slot(a, s, threadIdx.x == 0 && blockIdx.x % blocks == 0);
     if (slot < 0) return;
     const bool live = r < per;
@@ -40,21 +43,20 @@ __global__ void __launch_bounds__(kThreads) store_kernel(const ssd_state_params 
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             v[k][j] = to_float(p.v[j]);
-            big = max_abs(big, v[k][j]);
+            big = max_abs(big, v[k][j], v[k][j]);
         }
     }
     float inv, scale;
-    row_scale(max8(big), code_limit<kType>(), &inv, &scale);
+    row_scale(lanes_max<8>(big), code_limit<kType>(), &inv, &scale);
     if (!live) return;
     const int64_t row = (int64_t)slot * per + r;
     if (lane8 == 0) a.state_scale[row] = scale;
     uint8_t *dst = static_cast<uint8_t *>(a.state_cache) + row * N;
-    const uint64_t seed = a.sr_seed ? *a.sr_seed : 0;
 #pragma unroll
     for (int k = 0; k < E / V; ++k) {
         const int n = (k * 8 + lane8) * V;
         if (n >= N) continue;
-        store_pack<uint8_t, V>(dst + n, a.sr_seed ? encode8_sr<kType, V>(v[k], inv, seed, (uint64_t)(row * N + n))
+        store_pack<uint8_t, V>(dst + n, a.sr_seed ? encode8_sr<kType, V>(v[k], inv, keys, (uint64_t)(row * N + n))
                                                   : encode8<kType, V>(v[k], inv));
     }
 }

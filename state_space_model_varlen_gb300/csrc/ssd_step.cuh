@@ -9,8 +9,8 @@
 //
 // A request's states are H P rows of N values; the rows of a group share B and
 // C.  A CTA takes a run of one group's rows, whatever heads they belong to,
-// sixteen at a time.  Eight lanes share a row, so that its sums and maxima take
-// three shuffles, and a warp's four rows are neighbours in memory.  A thread
+// sixteen or 32 at a time.  Eight or four lanes share a row, so that its sums and
+// maxima take two or three shuffles, and a warp's rows are neighbours in memory.  A thread
 // copies its own share of the next rows into shared memory asynchronously, a
 // few steps ahead, and alone reads it back: no barriers, no registers for data
 // in flight, and the first copies run while the convolution, which needs the
@@ -28,7 +28,6 @@ namespace ssd {
 namespace {
 
 constexpr int kStepThreads = 128;
-constexpr int kStepGroups = kStepThreads / 8;      // rows worked on at a time
 constexpr int kStepMaxRows = 256;                  // of one CTA
 
 struct StepPlan {
@@ -92,17 +91,18 @@ __device__ __forceinline__ void copy_async(void *dst, const void *src, bool live
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(src), "n"(kBytes), "r"(n) : "memory");
 }
 
-// kType: storage of the state; E: state values a lane holds of a row (8 E >=
-// N); V: values of one copy; kDepth: row steps copied ahead.
-template <int kType, int E, int V, int kDepth>
+// kType: storage of the state; L: lanes of a row; E: state values a lane holds
+// of it (L E >= N); V: values of one copy; kDepth: row steps copied ahead.
+template <int kType, int L, int E, int V, int kDepth>
 __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(const ssd_step_params a, const StepPlan plan) {
     using StT = typename Stored<kType>::T;
-    constexpr int kChunks = E / V;
+    constexpr int kChunks = E / V, kStepGroups = kStepThreads / L;     // rows worked on at a time
     constexpr bool k8bit = kType == SSD_E4M3 || kType == SSD_I8;
     constexpr bool kAsync = V * sizeof(StT) >= 4;       // narrower shares are loaded when they are needed
-    __shared__ __align__(16) float s_b[8 * E], s_c[8 * E], s_x[kStepMaxRows], s_y[kStepMaxRows];
+    __shared__ __align__(16) float s_b[L * E], s_c[L * E], s_x[kStepMaxRows], s_y[kStepMaxRows];
     __shared__ float s_dx[kStepMaxRows], s_keep[kStepMaxRows];     // dt' x; decay (times the row's scale)
     __shared__ float s_scale[k8bit ? kStepMaxRows : 1];
+    __shared__ __align__(16) uint32_t s_keys[20];
     __shared__ Pack<StT, V> s_raw[kAsync ? kDepth * kChunks * kStepThreads : 1];
 
     const int N = a.dstate, P = a.headdim, H = a.nheads;
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
     const int run = blockIdx.x % plan.runs;
     const int g = (blockIdx.x / plan.runs) % a.ngroups;
     const int b = blockIdx.x / plan.runs / a.ngroups;
-    const int tid = threadIdx.x, lane8 = tid & 7, grp = tid >> 3;
+    const int tid = threadIdx.x, lane = tid % L, grp = tid / L;
     const int r0 = g * rows_g + run * plan.rows;        // the CTA's rows of the request: r0 .. r0 + rows - 1
     const int rows = min(plan.rows, rows_g - run * plan.rows);
     const bool bf16 = a.io_dtype == SSD_BF16;
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
             const int r = t + grp;
 #pragma unroll
             for (int k = 0; k < kChunks; ++k) {
-                const int n = (k * 8 + lane8) * V;
+                const int n = (k * L + lane) * V;
                 const bool live = r < rows && n < N && pos > 0;
                 copy_async<V * (int)sizeof(StT)>(&s_raw[(stage * kChunks + k) * kStepThreads + tid],
                                                  live ? cache + (int64_t)r * N + n : cache, live);
@@ -183,7 +183,8 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
         }
         return h0;
     };
-    for (int i = N + tid; i < 8 * E; i += kStepThreads) s_b[i] = s_c[i] = 0.f;
+    if (a.sr_seed && tid < 20) round_keys(*a.sr_seed, tid, s_keys);
+    for (int i = N + tid; i < L * E; i += kStepThreads) s_b[i] = s_c[i] = 0.f;
     const int h0 = bf16 ? convolve(__nv_bfloat16{}) : convolve(float{});
     __syncthreads();
     {
@@ -216,11 +217,10 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
     for (int k = 0; k < kChunks; ++k)
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int e = k * V + j, n = (k * 8 + lane8) * V + j;
+            const int e = k * V + j, n = (k * L + lane) * V + j;
             (e & 1 ? bv[e / 2].y : bv[e / 2].x) = s_b[n];
             (e & 1 ? cv[e / 2].y : cv[e / 2].x) = s_c[n];
         }
-    const uint64_t seed = a.sr_seed ? *a.sr_seed : 0;
     int stage = 0;
 #pragma unroll 1
     for (int t = 0; t < rows; t += kStepGroups) {
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
         if constexpr (kAsync) asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
 #pragma unroll
         for (int k = 0; k < kChunks; ++k) {
-            const int n = (k * 8 + lane8) * V;
+            const int n = (k * L + lane) * V;
             if (n >= N) continue;       // past the row: an infinite x must not meet a zero there
             Pack<StT, V> now{};
             if constexpr (kAsync) now = s_raw[(stage * kChunks + k) * kStepThreads + tid];
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
             if constexpr (V == 1) {
                 st[k] = fmaf(keep, st[k], dx * (k & 1 ? bv[k / 2].y : bv[k / 2].x));
                 acc.x = fmaf(k & 1 ? cv[k / 2].y : cv[k / 2].x, st[k], acc.x);
-                if (k8bit) big = max_abs(big, st[k]);
+                if (k8bit) big = max_abs(big, st[k], st[k]);
             } else {
 #pragma unroll
                 for (int e = k * V; e < (k + 1) * V; e += 2) {
@@ -252,23 +252,23 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
                     acc = fma2(cv[e / 2], s, acc);
                     st[e] = s.x;
                     st[e + 1] = s.y;
-                    if (k8bit) big = max_abs(max_abs(big, s.x), s.y);
+                    if (k8bit) big = max_abs(big, s.x, s.y);
                 }
             }
         }
         // the values are in registers: their places take the rows kDepth steps on
         copy_rows(t + kDepth * kStepGroups, stage);
         stage = stage + 1 == kDepth ? 0 : stage + 1;
-        const float sum = sum8(acc.x + acc.y);
-        if (lane8 == 0 && live) s_y[r] = sum;
+        const float sum = lanes_sum<L>(acc.x + acc.y);
+        if (lane == 0 && live) s_y[r] = sum;
         float inv = 0.f, sc = 0.f;
         if constexpr (k8bit) {
-            row_scale(max8(big), code_limit<kType>(), &inv, &sc);
-            if (lane8 == 0 && live) s_scale[r] = sc;
+            row_scale(lanes_max<L>(big), code_limit<kType>(), &inv, &sc);
+            if (lane == 0 && live) s_scale[r] = sc;
         }
 #pragma unroll
         for (int k = 0; k < kChunks; ++k) {
-            const int n = (k * 8 + lane8) * V;
+            const int n = (k * L + lane) * V;
             if (!live || n >= N) continue;
             const float *v = st + k * V;
             const uint64_t e = (uint64_t)(row0 + r) * N + n;
@@ -285,10 +285,10 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
                         if constexpr (V >= 4) {         // e is a multiple of 4
-                            if (j % 4 == 0) w = sr_block(seed, (e + j) >> 2, 0u);
+                            if (j % 4 == 0) w = sr_keyed(s_keys, (e + j) >> 2, 0u);
                             p.v[j] = sr_f16_fast(v[j], sr_word(w, j % 4));
                         } else {
-                            w = sr_block(seed, (e + j) >> 2, 0u);
+                            w = sr_keyed(s_keys, (e + j) >> 2, 0u);
                             p.v[j] = sr_f16_fast(v[j], sr_word(w, (uint32_t)(e + j) & 3u));
                         }
                     }
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
                     for (int j = 0; j < V; ++j) p.v[j] = __float2half_rn(v[j]);
                 }
             } else {
-                p = a.sr_seed ? encode8_sr<kType, V>(v, inv, seed, e) : encode8<kType, V>(v, inv);
+                p = a.sr_seed ? encode8_sr<kType, V>(v, inv, s_keys, e) : encode8<kType, V>(v, inv);
             }
             store_pack<StT, V>(cache + (int64_t)r * N + n, p);
         }
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
     }
 }
 
-template <int kType, int E, int V>
+template <int kType, int L, int E, int V>
 cudaError_t launch_step(const ssd_step_params &p, cudaStream_t stream) {
     constexpr int size = (int)sizeof(typename Stored<kType>::T);
     // steps in flight: 24 KB of a CTA's states, at least two, at most six
@@ -327,9 +327,12 @@ cudaError_t launch_step(const ssd_step_params &p, cudaStream_t stream) {
     constexpr int kDepth = kFit < 2 ? 2 : kFit > 6 ? 6 : kFit;
     StepPlan plan;
     const int rows_g = p.nheads / p.ngroups * p.headdim;
-    // long runs share the convolution of B and C; short ones fill the GPU
-    const int64_t share = (int64_t)rows_g * p.ngroups * p.batch / (152 * 12);
-    plan.rows = share >= kStepMaxRows ? kStepMaxRows : share >= 128 ? 128 : share >= 64 ? 64 : 32;
+    // the shortest runs that are all resident at once; long ones share the
+    // convolution of B and C
+    plan.rows = 32;
+    while (plan.rows < kStepMaxRows &&
+           (int64_t)(rows_g + plan.rows - 1) / plan.rows * p.ngroups * p.batch > 152 * (E == 32 ? 4 : 6))
+        plan.rows *= 2;
     plan.runs = (rows_g + plan.rows - 1) / plan.rows;
     const int io = p.io_dtype == SSD_F32 ? 4 : 2, vec = 4 * io;
     plan.vec4 = p.width == 4 && p.dstate % 4 == 0 && rows_g % 4 == 0 && p.xbc_stride % 4 == 0 &&
@@ -337,25 +340,32 @@ cudaError_t launch_step(const ssd_step_params &p, cudaStream_t stream) {
                 aligned_to(p.weight, 16);
     const int64_t grid = (int64_t)p.batch * p.ngroups * plan.runs;
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    step_kernel<kType, E, V, kDepth><<<(unsigned)grid, kStepThreads, 0, stream>>>(p, plan);
+    step_kernel<kType, L, E, V, kDepth><<<(unsigned)grid, kStepThreads, 0, stream>>>(p, plan);
     return cudaGetLastError();
 }
 
-template <int kType, int E>
+template <int kType, int L, int E>
 cudaError_t launch_step_vec(const ssd_step_params &p, cudaStream_t stream) {
     constexpr int size = (int)sizeof(typename Stored<kType>::T);
-    const int v = state_vector(p.dstate, size, p.state_cache);
-    if constexpr (16 / size <= E) if (v == 16 / size) return launch_step<kType, E, 16 / size>(p, stream);
-    if constexpr (8 / size >= 4 && 8 / size <= E) if (v == 8 / size) return launch_step<kType, E, 8 / size>(p, stream);
-    if constexpr (4 <= E) if (v == 4) return launch_step<kType, E, 4>(p, stream);
-    return launch_step<kType, E, 1>(p, stream);
+    const int v = state_vector(p.dstate, size, p.state_cache, L);
+    if constexpr (16 / size <= E) if (v == 16 / size) return launch_step<kType, L, E, 16 / size>(p, stream);
+    if constexpr (8 / size >= 4 && 8 / size <= E) if (v == 8 / size) return launch_step<kType, L, E, 8 / size>(p, stream);
+    if constexpr (4 <= E) if (v == 4) return launch_step<kType, L, E, 4>(p, stream);
+    return launch_step<kType, L, E, 1>(p, stream);
 }
 
+// fp32: 16 values a lane keep enough bytes in flight.  Narrower types are
+// bound by instructions, of which a row has some whatever its length: 32 values a lane.
 template <int kType>
 cudaError_t launch_step_type(const ssd_step_params &p, cudaStream_t stream) {
-    if (p.dstate <= 64) return launch_step_vec<kType, 8>(p, stream);
-    if (p.dstate <= 128) return launch_step_vec<kType, 16>(p, stream);
-    return launch_step_vec<kType, 32>(p, stream);
+    if constexpr (kType == SSD_F32) {
+        if (p.dstate <= 64) return launch_step_vec<kType, 8, 8>(p, stream);
+        if (p.dstate <= 128) return launch_step_vec<kType, 8, 16>(p, stream);
+    } else {
+        if (p.dstate <= 64) return launch_step_vec<kType, 4, 16>(p, stream);
+        if (p.dstate <= 128) return launch_step_vec<kType, 4, 32>(p, stream);
+    }
+    return launch_step_vec<kType, 8, 32>(p, stream);
 }
 
 }  // namespace
