@@ -31,10 +31,22 @@ constexpr int kStepThreads = 128;
 constexpr int kStepMaxRows = 256;                  // of one CTA
 
 struct StepPlan {
-    int rows;          // rows of a CTA, a multiple of 16
-    int runs;          // CTAs of a group
-    int vec4;          // four channels of xbc, weight, bias and ring make aligned vectors, width 4
+    int rows_g;        // rows of a group
+    int rows;          // rows of a CTA, a multiple of 32
+    int channels;
+    int vec4;          // four channels and four rows make aligned vectors, width 4
+    uint32_t p_mul;    // x / P = x p_mul >> p_shift for 0 <= x < 2^31
+    int p_shift;
 };
+
+// floor(x / P) for all 0 <= x < 2^31: with 2^s >= P and m = ceil(2^(31+s) / P),
+// m P - 2^(31+s) < 2^s, so x m / 2^(31+s) exceeds x / P by less than 1 / P.
+inline void set_divisor(StepPlan &plan, int P) {
+    int s = 0;
+    while ((1LL << s) < P) ++s;
+    plan.p_mul = (uint32_t)(((1ULL << (31 + s)) + P - 1) / P);
+    plan.p_shift = 31 + s;
+}
 
 // One channel's convolution at position pos.
 template <typename IoT>
@@ -56,8 +68,8 @@ __device__ __forceinline__ float conv_channel(const ssd_step_params &a, const Io
 
 // Four neighbouring channels, width 4, all loads issued together.
 template <typename IoT>
-__device__ __forceinline__ void conv_channels4(const ssd_step_params &a, const IoT *xbc, IoT *ring, int channels,
-                                               int c, int pos, int row, bool keep, float *dst) {
+__device__ __forceinline__ float4 conv_channels4(const ssd_step_params &a, const IoT *xbc, IoT *ring, int channels,
+                                                 int c, int pos, int row, bool keep) {
     const Pack<IoT, 16> w = load_pack<IoT, 16>(static_cast<const IoT *>(a.weight) + (int64_t)c * 4);
     Pack<IoT, 4> in[4], bias{};
     in[0] = load_pack<IoT, 4>(xbc + c);
@@ -69,14 +81,25 @@ __device__ __forceinline__ void conv_channels4(const ssd_step_params &a, const I
         if (k <= pos) in[k] = load_pack<IoT, 4>(ring + (int64_t)r * channels + c);
     }
     if (a.bias) bias = load_pack<IoT, 4>(static_cast<const IoT *>(a.bias) + c);
+    float u[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         float acc = to_float(bias.v[j]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) acc = fmaf(to_float(w.v[4 * j + 3 - k]), to_float(in[k].v[j]), acc);
-        dst[j] = a.activation ? silu(acc) : acc;
+        u[j] = a.activation ? silu(acc) : acc;
     }
     if (keep) store_pack<IoT, 4>(ring + (int64_t)row * channels + c, in[0]);
+    return make_float4(u[0], u[1], u[2], u[3]);
+}
+
+// dt' and the decay exp(dt' A) of a head
+template <typename IoT>
+__device__ __forceinline__ float2 head_terms(const ssd_step_params &a, int b, int h) {
+    float dt = to_float(static_cast<const IoT *>(a.dt)[(int64_t)b * a.dt_stride + h]);
+    if (a.dt_bias) dt += a.dt_bias[h];
+    if (a.dt_softplus) dt = softplus(dt);
+    return make_float2(dt, expf(dt * a.A[h]));
 }
 
 // A thread's share of a row, kBytes of it, into its own place in shared memory;
@@ -99,20 +122,17 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
     constexpr int kChunks = E / V, kStepGroups = kStepThreads / L;     // rows worked on at a time
     constexpr bool k8bit = kType == SSD_E4M3 || kType == SSD_I8;
     constexpr bool kAsync = V * sizeof(StT) >= 4;       // narrower shares are loaded when they are needed
-    __shared__ __align__(16) float s_b[L * E], s_c[L * E], s_x[kStepMaxRows], s_y[kStepMaxRows];
-    __shared__ float s_dx[kStepMaxRows], s_keep[kStepMaxRows];     // dt' x; decay (times the row's scale)
+    // of each row: D x, later y; dt' x; the decay, times its scale
+    __shared__ __align__(16) float s_b[L * E], s_c[L * E], s_y[kStepMaxRows], s_dx[kStepMaxRows], s_keep[kStepMaxRows];
     __shared__ float s_scale[k8bit ? kStepMaxRows : 1];
     __shared__ __align__(16) uint32_t s_keys[20];
     __shared__ Pack<StT, V> s_raw[kAsync ? kDepth * kChunks * kStepThreads : 1];
 
     const int N = a.dstate, P = a.headdim, H = a.nheads;
-    const int rows_g = H / a.ngroups * P;               // rows of a group
-    const int run = blockIdx.x % plan.runs;
-    const int g = (blockIdx.x / plan.runs) % a.ngroups;
-    const int b = blockIdx.x / plan.runs / a.ngroups;
+    const int b = blockIdx.x, g = blockIdx.y, run = blockIdx.z;
     const int tid = threadIdx.x, lane = tid % L, grp = tid / L;
-    const int r0 = g * rows_g + run * plan.rows;        // the CTA's rows of the request: r0 .. r0 + rows - 1
-    const int rows = min(plan.rows, rows_g - run * plan.rows);
+    const int r0 = g * plan.rows_g + run * plan.rows;        // the CTA's rows of the request: r0 .. r0 + rows - 1
+    const int rows = min(plan.rows, plan.rows_g - run * plan.rows);
     const bool bf16 = a.io_dtype == SSD_BF16;
 
     const int slot = a.slot_idx[(int64_t)b * (a.slot_idx_stride ? a.slot_idx_stride : 1)];
@@ -150,65 +170,57 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) copy_rows(d * kStepGroups, d);
 
-    // ---- convolution -------------------------------------------------------
-    const int channels = H * P + 2 * a.ngroups * N;
+    // ---- convolution, and what each row takes from it and from its head -----
+    const int channels = plan.channels;
     const int ring_row = pos % a.conv_rows;
-    const int cb = H * P + g * N, cc = H * P + (a.ngroups + g) * N;     // first channels of B and C
+    const int cb = H * P + g * N, cc = cb + a.ngroups * N;      // first channels of B and C
     auto convolve = [&](auto io) {
         using IoT = decltype(io);
         const IoT *xbc = static_cast<const IoT *>(a.xbc) + (int64_t)b * a.xbc_stride;
         IoT *ring = static_cast<IoT *>(a.conv_cache) + (int64_t)slot * a.conv_rows * channels;
+        auto head_of = [&](int row) { return (int)((uint64_t)(uint32_t)row * plan.p_mul >> plan.p_shift); };
         if (plan.vec4) {
             for (int i = 4 * tid; i < 2 * N + rows; i += 4 * kStepThreads) {
-                const int c = i < N ? cb + i : i < 2 * N ? cc + i - N : r0 + i - 2 * N;
-                float *dst = i < N ? s_b + i : i < 2 * N ? s_c + i - N : s_x + i - 2 * N;
-                conv_channels4<IoT>(a, xbc, ring, channels, c, pos, ring_row, i >= 2 * N || run == 0, dst);
+                if (i < 2 * N) {
+                    const int c = i < N ? cb + i : cc + i - N;
+                    *reinterpret_cast<float4 *>(i < N ? s_b + i : s_c + i - N) =
+                        conv_channels4<IoT>(a, xbc, ring, channels, c, pos, ring_row, run == 0);
+                } else {
+                    const int r = i - 2 * N, h = head_of(r0 + r);
+                    float4 sc = make_float4(1.f, 1.f, 1.f, 1.f);
+                    if (k8bit) sc = *reinterpret_cast<const float4 *>(a.state_scale + row0 + r);
+                    const float2 ht = head_terms<IoT>(a, b, h);
+                    const float dh = a.D ? a.D[h] : 0.f;
+                    const float4 x = conv_channels4<IoT>(a, xbc, ring, channels, r0 + r, pos, ring_row, true);
+                    const float dt = ht.x, keep = pos > 0 ? ht.y : 0.f;
+                    if (pos == 0) sc = make_float4(0.f, 0.f, 0.f, 0.f);
+                    *reinterpret_cast<float4 *>(s_dx + r) = make_float4(dt * x.x, dt * x.y, dt * x.z, dt * x.w);
+                    *reinterpret_cast<float4 *>(s_y + r) = make_float4(dh * x.x, dh * x.y, dh * x.z, dh * x.w);
+                    *reinterpret_cast<float4 *>(s_keep + r) =
+                        make_float4(keep * sc.x, keep * sc.y, keep * sc.z, keep * sc.w);
+                }
             }
         } else {
             for (int i = tid; i < 2 * N + rows; i += kStepThreads) {
                 const int c = i < N ? cb + i : i < 2 * N ? cc + i - N : r0 + i - 2 * N;
-                float *dst = i < N ? s_b + i : i < 2 * N ? s_c + i - N : s_x + i - 2 * N;
-                *dst = conv_channel<IoT>(a, xbc, ring, channels, c, pos, ring_row);
+                const float u = conv_channel<IoT>(a, xbc, ring, channels, c, pos, ring_row);
                 if (i >= 2 * N || run == 0) ring[(int64_t)ring_row * channels + c] = xbc[c];
+                if (i < 2 * N) {
+                    *(i < N ? s_b + i : s_c + i - N) = u;
+                } else {
+                    const int r = i - 2 * N, h = head_of(r0 + r);
+                    const float2 ht = head_terms<IoT>(a, b, h);
+                    s_dx[r] = ht.x * u;
+                    s_y[r] = a.D ? a.D[h] * u : 0.f;
+                    s_keep[r] = pos > 0 ? (k8bit ? ht.y * a.state_scale[row0 + r] : ht.y) : 0.f;
+                }
             }
         }
-        // dt' and decay, kept per row
-        const int h0 = r0 / P, h1 = (r0 + rows - 1) / P;
-        for (int h = h0 + tid; h <= h1; h += kStepThreads) {
-            float dt = to_float(static_cast<const IoT *>(a.dt)[(int64_t)b * a.dt_stride + h]);
-            if (a.dt_bias) dt += a.dt_bias[h];
-            if (a.dt_softplus) dt = softplus(dt);
-            s_dx[h - h0] = dt;
-            s_keep[h - h0] = expf(dt * a.A[h]);
-        }
-        return h0;
     };
     if (a.sr_seed && tid < 20) round_keys(*a.sr_seed, tid, s_keys);
     for (int i = N + tid; i < L * E; i += kStepThreads) s_b[i] = s_c[i] = 0.f;
-    const int h0 = bf16 ? convolve(__nv_bfloat16{}) : convolve(float{});
-    __syncthreads();
-    {
-        float dx[kStepMaxRows / kStepThreads], keep[kStepMaxRows / kStepThreads];
-#pragma unroll
-        for (int k = 0; k < kStepMaxRows / kStepThreads; ++k) {
-            const int i = tid + k * kStepThreads;
-            if (i < rows) {
-                const int h = (r0 + i) / P - h0;
-                dx[k] = s_dx[h] * s_x[i];
-                keep[k] = s_keep[h];
-                if (k8bit) keep[k] *= pos > 0 ? a.state_scale[row0 + i] : 0.f;
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kStepMaxRows / kStepThreads; ++k) {
-            const int i = tid + k * kStepThreads;
-            if (i < rows) {
-                s_dx[i] = dx[k];
-                s_keep[i] = keep[k];
-            }
-        }
-    }
+    if (bf16) convolve(__nv_bfloat16{});
+    else convolve(float{});
     __syncthreads();
 
     // ---- update and read-out -----------------------------------------------
@@ -260,7 +272,7 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
         copy_rows(t + kDepth * kStepGroups, stage);
         stage = stage + 1 == kDepth ? 0 : stage + 1;
         const float sum = lanes_sum<L>(acc.x + acc.y);
-        if (lane == 0 && live) s_y[r] = sum;
+        if (lane == 0 && live) s_y[r] += sum;
         float inv = 0.f, sc = 0.f;
         if constexpr (k8bit) {
             row_scale(lanes_max<L>(big), code_limit<kType>(), &inv, &sc);
@@ -308,7 +320,7 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
     // ---- y ------------------------------------------------------------------
     for (int i = tid; i < rows; i += kStepThreads) {
         if (k8bit) a.state_scale[row0 + i] = s_scale[i];
-        float y = s_y[i] + (a.D ? a.D[(r0 + i) / P] * s_x[i] : 0.f);
+        float y = s_y[i];
         if (bf16) {
             if (a.z) y *= silu(__bfloat162float(static_cast<const __nv_bfloat16 *>(a.z)[(int64_t)b * a.z_stride + r0 + i]));
             static_cast<__nv_bfloat16 *>(a.out_y)[y0 + i] = __float2bfloat16_rn(y);
@@ -326,21 +338,23 @@ cudaError_t launch_step(const ssd_step_params &p, cudaStream_t stream) {
     constexpr int kFit = 24576 / (kStepThreads * E * size);
     constexpr int kDepth = kFit < 2 ? 2 : kFit > 6 ? 6 : kFit;
     StepPlan plan;
-    const int rows_g = p.nheads / p.ngroups * p.headdim;
+    const int rows_g = plan.rows_g = p.nheads / p.ngroups * p.headdim;
+    plan.channels = p.nheads * p.headdim + 2 * p.ngroups * p.dstate;
+    set_divisor(plan, p.headdim);
     // the shortest runs that are all resident at once; long ones share the
     // convolution of B and C
     plan.rows = 32;
     while (plan.rows < kStepMaxRows &&
            (int64_t)(rows_g + plan.rows - 1) / plan.rows * p.ngroups * p.batch > 152 * (E == 32 ? 4 : 6))
         plan.rows *= 2;
-    plan.runs = (rows_g + plan.rows - 1) / plan.rows;
+    const int runs = (rows_g + plan.rows - 1) / plan.rows;
     const int io = p.io_dtype == SSD_F32 ? 4 : 2, vec = 4 * io;
-    plan.vec4 = p.width == 4 && p.dstate % 4 == 0 && rows_g % 4 == 0 && p.xbc_stride % 4 == 0 &&
+    plan.vec4 = p.width == 4 && p.dstate % 4 == 0 && p.headdim % 4 == 0 && p.xbc_stride % 4 == 0 &&
                 aligned_to(p.xbc, vec) && aligned_to(p.conv_cache, vec) && aligned_to(p.bias, vec) &&
-                aligned_to(p.weight, 16);
-    const int64_t grid = (int64_t)p.batch * p.ngroups * plan.runs;
-    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    step_kernel<kType, L, E, V, kDepth><<<(unsigned)grid, kStepThreads, 0, stream>>>(p, plan);
+                aligned_to(p.weight, 16) && aligned_to(p.state_scale, 16);
+    if (p.ngroups > 65535 || runs > 65535) return cudaErrorInvalidConfiguration;
+    const dim3 grid((unsigned)p.batch, (unsigned)p.ngroups, (unsigned)runs);
+    step_kernel<kType, L, E, V, kDepth><<<grid, kStepThreads, 0, stream>>>(p, plan);
     return cudaGetLastError();
 }
 
