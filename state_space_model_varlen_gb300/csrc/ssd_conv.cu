@@ -4,12 +4,15 @@
 //
 // Each value is read once and written once: the kernel is bound by HBM.  A CTA
 // owns a tile of tokens and of channels; a thread owns V neighbouring channels
-// (16 bytes) and walks the tile's tokens with the last W - 1 inputs in
-// registers, so a tile reads W - 1 tokens more than it writes.
+// and walks the tile's tokens in groups of eight, whose inputs are loaded
+// together one group ahead, with the last W - 1 inputs in registers.  A tile
+// reads W - 1 tokens more than it writes.
 //
-// Sequence boundaries are worked out once per CTA: every thread looks at some
-// of the sequences and marks the tile's tokens in shared memory; the walk then
-// reads one record per token.
+// Sequence boundaries are worked out once per CTA, while the first group's
+// inputs are on their way: every thread looks at some of the sequences and
+// marks the tile's tokens in shared memory.  A group whose tokens all have
+// their W - 1 predecessors in this call slides the window; any other loads
+// every tap of every token from where it lies, four tokens at a time.
 //
 // The convolution cache is updated in place by other CTAs than those that
 // read it, unless one thread does both: the CTA whose tile holds a sequence's
@@ -22,53 +25,91 @@ namespace ssd {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kMaxTile = 32;       // tokens of a tile
+constexpr int kMaxTile = 64;       // tokens of a tile
+constexpr int kGroup = 8;          // tokens whose inputs are loaded together
+constexpr int kSlow = 4;           // tokens of a group at a boundary taken together
 
 struct Token {
     int local;      // token of its sequence, -1: no valid sequence
     int row;        // its row of the ring
     int slot;       // -1: no cache
-    int past;       // min(position, W - 1) << 1 | this token is written to the ring here
+    int past;       // min(position, W - 1)
 };
+constexpr int kSlides = 1, kKeeps = 2;      // of a group: every token has its window here; some go to the ring
 
+// dt of the tile's tokens widened to fp32
+template <typename IoT>
+__device__ __forceinline__ void widen_dt(const ssd_conv_params &a, int64_t t0, int nt) {
+    const IoT *dt = static_cast<const IoT *>(a.dt);
+    for (int h = threadIdx.x; h < a.nheads; h += kThreads) {
+        for (int i = 0; i < nt; i += kGroup) {
+            float v[kGroup];
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j)
+                if (i + j < nt) v[j] = to_float(dt[(t0 + i + j) * a.dt_stride + h]);
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j)
+                if (i + j < nt) a.out_dt[(t0 + i + j) * a.nheads + h] = v[j];
+        }
+    }
+}
+
+// kW: the width, or 0 for one that only a.width tells (then no group slides).
 template <typename IoT, int V, int kW>
-__global__ void __launch_bounds__(kThreads) conv_kernel(const ssd_conv_params a, int tile, int ctiles) {
+__global__ void __launch_bounds__(kThreads) conv_kernel(const ssd_conv_params a, int tile, int dt_column) {
     __shared__ int seq_of[kMaxTile];
     __shared__ Token token[kMaxTile];
+    __shared__ uint8_t keep[kMaxTile];             // the token goes to the ring here
+    __shared__ int group[kMaxTile / kGroup];
     __shared__ int tail_seq;
+    constexpr int kM = kW ? kW : SSD_CONV_MAX_WIDTH;
+    constexpr int kPast = kW > 1 ? kW - 1 : 1;      // inputs a sliding window keeps
     const int W = kW ? kW : a.width;
     const int64_t t0 = (int64_t)blockIdx.x * tile;
     const int nt = (int)min((int64_t)tile, a.total_tokens - t0);
-    const int ct = blockIdx.y;
-
-    // the last column of CTAs widens dt
-    if (ct == ctiles) {
-        const IoT *dt = static_cast<const IoT *>(a.dt);
-        for (int i = threadIdx.x; i < nt * a.nheads; i += kThreads) {
-            const int64_t t = t0 + i / a.nheads;
-            const int h = i % a.nheads;
-            a.out_dt[t * a.nheads + h] = to_float(dt[t * a.dt_stride + h]);
-        }
+    const int ct = (int)blockIdx.y - dt_column;
+    if (ct < 0) {
+        widen_dt<IoT>(a, t0, nt);
         return;
+    }
+    const bool reporter = ct == 0 && a.device_status != nullptr;
+
+    // ---- the first group's inputs and the window before it -----------------
+    const int c = (ct * kThreads + threadIdx.x) * V;
+    const bool mine = c < a.channels;
+    const IoT *x = static_cast<const IoT *>(a.xbc) + t0 * a.xbc_stride + c;    // of the tile's first token
+    Pack<IoT, V> next[kGroup], prev[kPast];
+    auto load_group = [&](int i0) {
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j)
+            if (mine && i0 + j < nt) next[j] = load_pack<IoT, V>(x + (i0 + j) * a.xbc_stride);
+    };
+    if constexpr (kW > 1) {
+        load_group(0);
+#pragma unroll
+        for (int m = 1; m < kW; ++m)
+            if (mine && t0 >= m) prev[m - 1] = load_pack<IoT, V>(x - m * a.xbc_stride);
     }
 
     // ---- the tile's tokens -------------------------------------------------
-    if (threadIdx.x < tile) seq_of[threadIdx.x] = -1;
+    if (threadIdx.x < kMaxTile) seq_of[threadIdx.x] = -1;
+    if (threadIdx.x < kMaxTile / kGroup) group[threadIdx.x] = kW > 1 ? kSlides : 0;
     if (threadIdx.x == 0) tail_seq = -1;
     __syncthreads();
     for (int s = threadIdx.x; s < a.num_seqs; s += kThreads) {
         const int64_t b = a.cu_seqlens[s], e = a.cu_seqlens[s + 1];
         if (b < 0 || e < b || e > a.total_tokens) {
-            if (t0 == 0 && ct == 0 && a.device_status) atomicOr(a.device_status, SSD_DEV_BAD_SEQLENS);
+            if (t0 == 0 && reporter) atomicOr(a.device_status, SSD_DEV_BAD_SEQLENS);
             continue;
         }
         const int64_t lo = max(b, t0), hi = min(e, t0 + nt);
         for (int64_t t = lo; t < hi; ++t) seq_of[t - t0] = s;
     }
     __syncthreads();
-    if (threadIdx.x < nt) {
-        const int s = seq_of[threadIdx.x];
+    if (threadIdx.x < kMaxTile) {
+        const int s = (int)threadIdx.x < nt ? seq_of[threadIdx.x] : -1;
         Token k = {-1, 0, -1, 0};
+        bool kept = false;
         if (s >= 0) {
             const int64_t b = a.cu_seqlens[s], e = a.cu_seqlens[s + 1];
             const int64_t local = t0 + threadIdx.x - b;
@@ -78,11 +119,11 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ssd_conv_params a,
             if (a.conv_cache != nullptr) {
                 slot = a.slot_idx[s * (a.slot_idx_stride ? a.slot_idx_stride : 1)];
                 ok = slot >= 0 && slot < a.num_slots;
-                if (!ok && local == 0 && ct == 0 && a.device_status) atomicOr(a.device_status, SSD_DEV_BAD_SLOT);
+                if (!ok && local == 0 && reporter) atomicOr(a.device_status, SSD_DEV_BAD_SLOT);
             }
             if (start < 0) {
                 ok = false;
-                if (local == 0 && ct == 0 && a.device_status) atomicOr(a.device_status, SSD_DEV_BAD_POS);
+                if (local == 0 && reporter) atomicOr(a.device_status, SSD_DEV_BAD_POS);
             }
             if (ok) {
                 const int64_t pos = start + local;
@@ -90,19 +131,20 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ssd_conv_params a,
                 k.local = (int)min(local, (int64_t)0x7fffffff);
                 k.slot = slot;
                 k.row = slot >= 0 ? (int)(pos % a.conv_rows) : 0;
-                const bool keep = slot >= 0 && begins_here && t0 + threadIdx.x >= e - (W - 1);
-                k.past = (int)min(pos, (int64_t)(W - 1)) << 1 | (keep ? 1 : 0);
+                k.past = (int)min(pos, (int64_t)(W - 1));
+                kept = slot >= 0 && begins_here && t0 + threadIdx.x >= e - (W - 1);
                 // the tile's last sequence goes on after it: its end is kept below
-                if (slot >= 0 && begins_here && threadIdx.x == nt - 1 && e > t0 + nt) tail_seq = s;
+                if (slot >= 0 && begins_here && (int)threadIdx.x == nt - 1 && e > t0 + nt) tail_seq = s;
             }
         }
         token[threadIdx.x] = k;
+        keep[threadIdx.x] = kept;
+        if (k.local < W - 1) atomicAnd(&group[threadIdx.x / kGroup], ~kSlides);
+        if (kept) atomicOr(&group[threadIdx.x / kGroup], kKeeps);
     }
     __syncthreads();
+    if (!mine) return;
 
-    const int c = (ct * kThreads + threadIdx.x) * V;
-    if (c >= a.channels) return;
-    const IoT *x = static_cast<const IoT *>(a.xbc) + c;
     IoT *ring = static_cast<IoT *>(a.conv_cache) + c;
     // where this thread's channels go
     IoT *out;
@@ -117,107 +159,140 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ssd_conv_params a,
         out = static_cast<IoT *>(a.out2) + (c - a.split0 - a.split1);
         ostride = a.channels - a.split0 - a.split1;
     }
+    out += t0 * ostride;
 
-    constexpr int kM = kW ? kW : SSD_CONV_MAX_WIDTH;
-    float w[kM][V], bias[V];
+    float w[kM][V], bias[V];        // w[k]: the tap of the token k before
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         bias[j] = a.bias ? to_float(static_cast<const IoT *>(a.bias)[c + j]) : 0.f;
 #pragma unroll
-        for (int k = 0; k < kM; ++k)     // w[k]: the tap of the token k before
+        for (int k = 0; k < kM; ++k)
             w[k][j] = k < W ? to_float(static_cast<const IoT *>(a.weight)[(int64_t)(c + j) * W + (W - 1 - k)]) : 0.f;
     }
+    auto finish = [&](float *acc, int i) {
+        Pack<IoT, V> u;
+#pragma unroll
+        for (int j = 0; j < V; ++j) u.v[j] = from_float<IoT>(a.activation ? silu(acc[j]) : acc[j]);
+        store_pack<IoT, V>(out + i * ostride, u);
+    };
 
-    // win[k]: the input k tokens before the current one
-    float win[kM][V];
+    for (int i0 = 0; i0 < nt; i0 += kGroup) {
+        const int what = group[i0 / kGroup];
+        if constexpr (kW > 1) {
+            Pack<IoT, V> now[kGroup];
 #pragma unroll
-    for (int k = 0; k < kM; ++k)
+            for (int j = 0; j < kGroup; ++j) now[j] = next[j];
+            load_group(i0 + kGroup);
+            if (what & kSlides) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) win[k][j] = 0.f;
-
-    for (int i = 0; i < nt; ++i) {
-        const Token k = token[i];
-        if (k.local < 0) continue;
-        const int64_t t = t0 + i;
-        const Pack<IoT, V> now = load_pack<IoT, V>(x + t * a.xbc_stride);
+                for (int i = 0; i < kGroup; ++i) {
+                    float acc[V];
 #pragma unroll
-        for (int m = kM - 1; m > 0; --m)
+                    for (int j = 0; j < V; ++j) acc[j] = bias[j];
 #pragma unroll
-            for (int j = 0; j < V; ++j) win[m][j] = win[m - 1][j];
+                    for (int m = 0; m < kW; ++m)
 #pragma unroll
-        for (int j = 0; j < V; ++j) win[0][j] = to_float(now.v[j]);
-        if (k.local == 0 || i == 0) {
-            // the window's past: from the sequence's tokens, the ring, or zero
-#pragma unroll
-            for (int m = 1; m < kM; ++m) {
-                if (m >= W) break;
-#pragma unroll
-                for (int j = 0; j < V; ++j) win[m][j] = 0.f;
-                const IoT *src = nullptr;
-                if (m <= k.local) {
-                    src = x + (t - m) * a.xbc_stride;
-                } else if (m <= (k.past >> 1) && k.slot >= 0) {
-                    int row = k.row - m;
-                    if (row < 0) row += a.conv_rows;
-                    src = ring + ((int64_t)k.slot * a.conv_rows + row) * a.channels;
+                        for (int j = 0; j < V; ++j)
+                            acc[j] = fmaf(w[m][j], to_float(i >= m ? now[i - m].v[j] : prev[m - i - 1].v[j]), acc[j]);
+                    finish(acc, i0 + i);
                 }
-                if (src) {
-                    const Pack<IoT, V> p = load_pack<IoT, V>(src);
+            }
 #pragma unroll
-                    for (int j = 0; j < V; ++j) win[m][j] = to_float(p.v[j]);
+            for (int m = 0; m < kW - 1; ++m) prev[m] = now[kGroup - 1 - m];
+        }
+        if (!(what & kSlides)) {
+            for (int s0 = i0; s0 < min(i0 + kGroup, nt); s0 += kSlow) {
+                Pack<IoT, V> tap[kSlow][kM];
+#pragma unroll
+                for (int i = 0; i < kSlow; ++i) {
+                    const Token k = token[s0 + i];
+#pragma unroll
+                    for (int m = 0; m < kM; ++m) {
+                        tap[i][m] = Pack<IoT, V>{};
+                        if (m >= W || k.local < 0) continue;
+                        const IoT *src = nullptr;
+                        if (m <= k.local) {
+                            src = x + (int64_t)(s0 + i - m) * a.xbc_stride;
+                        } else if (m <= k.past && k.slot >= 0) {
+                            int row = k.row - m;
+                            if (row < 0) row += a.conv_rows;
+                            src = ring + ((int64_t)k.slot * a.conv_rows + row) * a.channels;
+                        }
+                        if (src) tap[i][m] = load_pack<IoT, V>(src);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kSlow; ++i) {
+                    if (token[s0 + i].local < 0) continue;
+                    float acc[V];
+#pragma unroll
+                    for (int j = 0; j < V; ++j) acc[j] = bias[j];
+#pragma unroll
+                    for (int m = 0; m < kM; ++m)
+                        if (m < W)
+#pragma unroll
+                            for (int j = 0; j < V; ++j) acc[j] = fmaf(w[m][j], to_float(tap[i][m].v[j]), acc[j]);
+                    finish(acc, s0 + i);
                 }
             }
         }
-        Pack<IoT, V> u;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            float acc = bias[j];
-#pragma unroll
-            for (int m = 0; m < kM; ++m)
-                if (m < W) acc = fmaf(w[m][j], win[m][j], acc);
-            u.v[j] = from_float<IoT>(a.activation ? silu(acc) : acc);
+        if (what & kKeeps) {
+            for (int i = i0; i < min(i0 + kGroup, nt); ++i) {
+                if (!keep[i]) continue;
+                const Token k = token[i];
+                store_pack<IoT, V>(ring + ((int64_t)k.slot * a.conv_rows + k.row) * a.channels,
+                                   load_pack<IoT, V>(x + i * a.xbc_stride));
+            }
         }
-        store_pack<IoT, V>(out + t * ostride, u);
-        if (k.past & 1) store_pack<IoT, V>(ring + ((int64_t)k.slot * a.conv_rows + k.row) * a.channels, now);
     }
 
     // the end of the sequence that begins in this tile and passes it
     const int s = tail_seq;
     if (s >= 0) {
         const Token k = token[nt - 1];
-        const int64_t e = a.cu_seqlens[s + 1];
-        for (int64_t t = max(t0 + nt, e - (W - 1)); t < e; ++t) {
-            const int row = (int)((k.row + (t - (t0 + nt - 1))) % a.conv_rows);
+        const int64_t e = (int64_t)a.cu_seqlens[s + 1] - t0;       // tokens from the tile's first
+        for (int64_t i = max((int64_t)nt, e - (W - 1)); i < e; ++i) {
+            const int row = (int)((k.row + (i - (nt - 1))) % a.conv_rows);
             store_pack<IoT, V>(ring + ((int64_t)k.slot * a.conv_rows + row) * a.channels,
-                               load_pack<IoT, V>(x + t * a.xbc_stride));
+                               load_pack<IoT, V>(x + i * a.xbc_stride));
         }
     }
 }
 
 template <typename IoT, int V>
 cudaError_t launch(const ssd_conv_params &p, cudaStream_t stream) {
-    const int tile = kMaxTile;
+    const int ctiles = (p.channels + kThreads * V - 1) / (kThreads * V), dt = p.dt != nullptr ? 1 : 0;
+    // long tiles read fewer tokens twice; short ones fill the GPU
+    int tile = kMaxTile;
+    while (tile > kGroup && (p.total_tokens + tile - 1) / tile * ctiles < 152 * 8) tile /= 2;
     const int64_t tiles = (p.total_tokens + tile - 1) / tile;
-    const int ctiles = (p.channels + kThreads * V - 1) / (kThreads * V);
-    if (tiles > 0x7fffffff || ctiles + 1 > 65535) return cudaErrorInvalidConfiguration;
-    const dim3 grid((unsigned)tiles, (unsigned)(ctiles + (p.dt != nullptr ? 1 : 0)));
-    if (p.width == 4)
-        conv_kernel<IoT, V, 4><<<grid, kThreads, 0, stream>>>(p, tile, ctiles);
-    else
-        conv_kernel<IoT, V, 0><<<grid, kThreads, 0, stream>>>(p, tile, ctiles);
+    if (tiles > 0x7fffffff || ctiles + dt > 65535) return cudaErrorInvalidConfiguration;
+    const dim3 grid((unsigned)tiles, (unsigned)(ctiles + dt));
+    switch (p.width) {
+        case 2: conv_kernel<IoT, V, 2><<<grid, kThreads, 0, stream>>>(p, tile, dt); break;
+        case 3: conv_kernel<IoT, V, 3><<<grid, kThreads, 0, stream>>>(p, tile, dt); break;
+        case 4: conv_kernel<IoT, V, 4><<<grid, kThreads, 0, stream>>>(p, tile, dt); break;
+        default: conv_kernel<IoT, V, 0><<<grid, kThreads, 0, stream>>>(p, tile, dt);
+    }
     return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_conv(const ssd_conv_params &p, cudaStream_t stream) {
-    const int io = p.io_dtype == SSD_F32 ? 4 : 2, v = 16 / io;
+    const int io = p.io_dtype == SSD_F32 ? 4 : 2;
     const int rest = p.channels - p.split0 - p.split1;
-    const bool wide = p.channels % v == 0 && p.xbc_stride % v == 0 && p.split0 % v == 0 && p.split1 % v == 0 &&
-                      rest % v == 0 && aligned_to(p.xbc, 16) && aligned_to(p.conv_cache, 16) &&
-                      aligned_to(p.out0, 16) && aligned_to(p.out1, 16) && aligned_to(p.out2, 16);
-    if (p.io_dtype == SSD_F32) return wide ? launch<float, 4>(p, stream) : launch<float, 1>(p, stream);
-    return wide ? launch<__nv_bfloat16, 8>(p, stream) : launch<__nv_bfloat16, 1>(p, stream);
+    auto can = [&](int v) {
+        const size_t bytes = (size_t)v * io;
+        return p.channels % v == 0 && p.xbc_stride % v == 0 && p.split0 % v == 0 && p.split1 % v == 0 &&
+               rest % v == 0 && aligned_to(p.xbc, bytes) && aligned_to(p.conv_cache, bytes) &&
+               aligned_to(p.out0, bytes) && aligned_to(p.out1, bytes) && aligned_to(p.out2, bytes);
+    };
+    if (p.io_dtype == SSD_F32)
+        return can(4) ? launch<float, 4>(p, stream) : can(2) ? launch<float, 2>(p, stream) : launch<float, 1>(p, stream);
+    return can(4)   ? launch<__nv_bfloat16, 4>(p, stream)
+           : can(2) ? launch<__nv_bfloat16, 2>(p, stream)
+                    : launch<__nv_bfloat16, 1>(p, stream);
 }
 
 }  // namespace ssd
