@@ -27,7 +27,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kMaxTile = 64;       // tokens of a tile
 constexpr int kGroup = 8;          // tokens whose inputs are loaded together
-constexpr int kSlow = 4;           // tokens of a group at a boundary taken together
+constexpr int kSlow = 2;           // tokens of a group at a boundary taken together
 
 struct Token {
     int local;      // token of its sequence, -1: no valid sequence
@@ -54,9 +54,35 @@ __device__ __forceinline__ void widen_dt(const ssd_conv_params &a, int64_t t0, i
     }
 }
 
+// acc += w x over a thread's channels, and the finished value
+template <typename IoT, int V>
+__device__ __forceinline__ void accumulate(float2 (&acc)[(V + 1) / 2], const float2 (&w)[(V + 1) / 2], const Pack<IoT, V> &x) {
+    if constexpr (V == 1) {
+        acc[0].x = fmaf(w[0].x, to_float(x.v[0]), acc[0].x);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) acc[j] = fma2(w[j], pair_of<V>(x, j), acc[j]);
+    }
+}
+template <typename IoT, int V>
+__device__ __forceinline__ Pack<IoT, V> finished(const float2 (&acc)[(V + 1) / 2], int activation) {
+    Pack<IoT, V> u;
+    if constexpr (V == 1) {
+        u.v[0] = from_float<IoT>(activation ? silu(acc[0].x) : acc[0].x);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) set_pair<V>(u, j, activation ? silu2(acc[j]) : acc[j]);
+    }
+    return u;
+}
+
+// CTAs of an SM that the registers should leave room for
+template <typename IoT, int V, int kW>
+constexpr int kMinCtas = kW == 0 ? 2 : V * sizeof(IoT) > 8 ? 4 : 6;
+
 // kW: the width, or 0 for one that only a.width tells (then no group slides).
 template <typename IoT, int V, int kW>
-__global__ void __launch_bounds__(kThreads) conv_kernel(const ssd_conv_params a, int tile, int dt_column) {
+__global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(const ssd_conv_params a, int tile, int dt_column) {
     __shared__ int seq_of[kMaxTile];
     __shared__ Token token[kMaxTile];
     __shared__ uint8_t keep[kMaxTile];             // the token goes to the ring here
@@ -161,20 +187,19 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ssd_conv_params a,
     }
     out += t0 * ostride;
 
-    float w[kM][V], bias[V];        // w[k]: the tap of the token k before
+    constexpr int kPairs = (V + 1) / 2;
+    float2 w[kM][kPairs], bias[kPairs];        // w[k]: the tap of the token k before
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        bias[j] = a.bias ? to_float(static_cast<const IoT *>(a.bias)[c + j]) : 0.f;
+        const float bj = a.bias ? to_float(static_cast<const IoT *>(a.bias)[c + j]) : 0.f;
+        (j & 1 ? bias[j / 2].y : bias[j / 2].x) = bj;
 #pragma unroll
-        for (int k = 0; k < kM; ++k)
-            w[k][j] = k < W ? to_float(static_cast<const IoT *>(a.weight)[(int64_t)(c + j) * W + (W - 1 - k)]) : 0.f;
+        for (int k = 0; k < kM; ++k) {
+            const float wk =
+                k < W ? to_float(static_cast<const IoT *>(a.weight)[(int64_t)(c + j) * W + (W - 1 - k)]) : 0.f;
+            (j & 1 ? w[k][j / 2].y : w[k][j / 2].x) = wk;
+        }
     }
-    auto finish = [&](float *acc, int i) {
-        Pack<IoT, V> u;
-#pragma unroll
-        for (int j = 0; j < V; ++j) u.v[j] = from_float<IoT>(a.activation ? silu(acc[j]) : acc[j]);
-        store_pack<IoT, V>(out + i * ostride, u);
-    };
 
     for (int i0 = 0; i0 < nt; i0 += kGroup) {
         const int what = group[i0 / kGroup];
@@ -186,15 +211,12 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ssd_conv_params a,
             if (what & kSlides) {
 #pragma unroll
                 for (int i = 0; i < kGroup; ++i) {
-                    float acc[V];
+                    float2 acc[kPairs];
 #pragma unroll
-                    for (int j = 0; j < V; ++j) acc[j] = bias[j];
+                    for (int j = 0; j < kPairs; ++j) acc[j] = bias[j];
 #pragma unroll
-                    for (int m = 0; m < kW; ++m)
-#pragma unroll
-                        for (int j = 0; j < V; ++j)
-                            acc[j] = fmaf(w[m][j], to_float(i >= m ? now[i - m].v[j] : prev[m - i - 1].v[j]), acc[j]);
-                    finish(acc, i0 + i);
+                    for (int m = 0; m < kW; ++m) accumulate<IoT, V>(acc, w[m], i >= m ? now[i - m] : prev[m - i - 1]);
+                    store_pack<IoT, V>(out + (i0 + i) * ostride, finished<IoT, V>(acc, a.activation));
                 }
             }
 #pragma unroll
@@ -224,15 +246,13 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ssd_conv_params a,
 #pragma unroll
                 for (int i = 0; i < kSlow; ++i) {
                     if (token[s0 + i].local < 0) continue;
-                    float acc[V];
+                    float2 acc[kPairs];
 #pragma unroll
-                    for (int j = 0; j < V; ++j) acc[j] = bias[j];
+                    for (int j = 0; j < kPairs; ++j) acc[j] = bias[j];
 #pragma unroll
                     for (int m = 0; m < kM; ++m)
-                        if (m < W)
-#pragma unroll
-                            for (int j = 0; j < V; ++j) acc[j] = fmaf(w[m][j], to_float(tap[i][m].v[j]), acc[j]);
-                    finish(acc, s0 + i);
+                        if (m < W) accumulate<IoT, V>(acc, w[m], tap[i][m]);
+                    store_pack<IoT, V>(out + (s0 + i) * ostride, finished<IoT, V>(acc, a.activation));
                 }
             }
         }

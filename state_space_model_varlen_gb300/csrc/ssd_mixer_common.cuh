@@ -29,8 +29,19 @@ template <typename T, int V> __device__ __forceinline__ void store_pack(T *dst, 
     *reinterpret_cast<Pack<T, V> *>(dst) = p;
 }
 
-// v sigmoid(v).  ex2 and rcp approximations: about 2^-21 relative error.
-__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.f + __expf(-v)); }
+// v sigmoid(v) through the ex2 and rcp approximations: about 2^-21 relative
+// error.  Where e^-v overflows the reciprocal of infinity gives the right 0.
+__device__ __forceinline__ float ex2_approx(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float rcp_approx(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float silu(float v) { return v * rcp_approx(1.f + ex2_approx(v * -1.4426950408889634f)); }
 
 // softplus(z) = log(1 + e^z) in the overflow-safe form max(z,0) + log1p(e^-|z|)
 __device__ __forceinline__ float softplus(float z) { return fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))); }
@@ -54,6 +65,39 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     float2 o;
     memcpy(&o, &r, 8);
     return o;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t r, x, y;
+    memcpy(&x, &a, 8);
+    memcpy(&y, &b, 8);
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    float2 o;
+    memcpy(&o, &r, 8);
+    return o;
+}
+__device__ __forceinline__ float2 silu2(float2 v) {
+    const float2 e = mul2(v, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+    const float2 d = add2(make_float2(ex2_approx(e.x), ex2_approx(e.y)), make_float2(1.f, 1.f));
+    return mul2(v, make_float2(rcp_approx(d.x), rcp_approx(d.y)));
+}
+
+// Elements 2 i, 2 i + 1 of a pack as floats, and back.
+template <int V> __device__ __forceinline__ float2 pair_of(const Pack<float, V> &p, int i) {
+    return make_float2(p.v[2 * i], p.v[2 * i + 1]);
+}
+template <int V> __device__ __forceinline__ float2 pair_of(const Pack<__nv_bfloat16, V> &p, int i) {
+    uint32_t w;
+    memcpy(&w, p.v + 2 * i, 4);
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <int V> __device__ __forceinline__ void set_pair(Pack<float, V> &p, int i, float2 f) {
+    p.v[2 * i] = f.x;
+    p.v[2 * i + 1] = f.y;
+}
+template <int V> __device__ __forceinline__ void set_pair(Pack<__nv_bfloat16, V> &p, int i, float2 f) {
+    const __nv_bfloat162 b = __float22bfloat162_rn(f);
+    memcpy(p.v + 2 * i, &b, 4);
 }
 
 // ---------------------------------------------------------------------------
