@@ -4,9 +4,10 @@
 //
 // Each value is read once and written once: the kernel is bound by HBM.  A CTA
 // owns a tile of tokens and of channels; a thread owns V neighbouring channels
-// and walks the tile's tokens in groups of eight, whose inputs are loaded
-// together one group ahead, with the last W - 1 inputs in registers.  A tile
-// reads W - 1 tokens more than it writes.
+// and walks the tile's tokens in groups of eight with the last W - 1 inputs in
+// registers.  It copies its own share of the inputs into shared memory
+// asynchronously, a few groups ahead, and alone reads it back.  A tile reads
+// W - 1 tokens more than it writes.
 //
 // Sequence boundaries are worked out once per CTA, while the first group's
 // inputs are on their way: every thread looks at some of the sequences and
@@ -54,14 +55,25 @@ __device__ __forceinline__ void widen_dt(const ssd_conv_params &a, int64_t t0, i
     }
 }
 
-// acc += w x over a thread's channels, and the finished value
+// A thread's channels as pairs of floats (V = 1: the first of one), acc += w x
+// over them, and the finished values.
 template <typename IoT, int V>
-__device__ __forceinline__ void accumulate(float2 (&acc)[(V + 1) / 2], const float2 (&w)[(V + 1) / 2], const Pack<IoT, V> &x) {
+__device__ __forceinline__ void widen(const Pack<IoT, V> &x, float2 (&f)[(V + 1) / 2]) {
     if constexpr (V == 1) {
-        acc[0].x = fmaf(w[0].x, to_float(x.v[0]), acc[0].x);
+        f[0].x = to_float(x.v[0]);
     } else {
 #pragma unroll
-        for (int j = 0; j < V / 2; ++j) acc[j] = fma2(w[j], pair_of<V>(x, j), acc[j]);
+        for (int j = 0; j < V / 2; ++j) f[j] = pair_of<V>(x, j);
+    }
+}
+template <int V>
+__device__ __forceinline__ void accumulate(float2 (&acc)[(V + 1) / 2], const float2 (&w)[(V + 1) / 2],
+                                           const float2 (&x)[(V + 1) / 2]) {
+    if constexpr (V == 1) {
+        acc[0].x = fmaf(w[0].x, x[0].x, acc[0].x);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) acc[j] = fma2(w[j], x[j], acc[j]);
     }
 }
 template <typename IoT, int V>
@@ -90,6 +102,12 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
     __shared__ int tail_seq;
     constexpr int kM = kW ? kW : SSD_CONV_MAX_WIDTH;
     constexpr int kPast = kW > 1 ? kW - 1 : 1;      // inputs a sliding window keeps
+    constexpr int kPairs = (V + 1) / 2;
+    // groups copied ahead: 24 KB of a CTA's inputs; two-byte shares are loaded one group ahead instead
+    constexpr int kBytes = V * (int)sizeof(IoT);
+    constexpr bool kAsync = kBytes >= 4 && kW > 1;
+    constexpr int kDepth = kBytes >= 16 ? 2 : kBytes == 8 ? 3 : 4;
+    __shared__ Pack<IoT, V> s_x[kAsync ? kDepth * kGroup * kThreads : 1];
     const int W = kW ? kW : a.width;
     const int64_t t0 = (int64_t)blockIdx.x * tile;
     const int nt = (int)min((int64_t)tile, a.total_tokens - t0);
@@ -105,16 +123,26 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
     const bool mine = c < a.channels;
     const IoT *x = static_cast<const IoT *>(a.xbc) + t0 * a.xbc_stride + c;    // of the tile's first token
     Pack<IoT, V> next[kGroup], prev[kPast];
-    auto load_group = [&](int i0) {
+    auto load_group = [&](int i0, int stage) {
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j)
-            if (mine && i0 + j < nt) next[j] = load_pack<IoT, V>(x + (i0 + j) * a.xbc_stride);
+        for (int j = 0; j < kGroup; ++j) {
+            const bool live = mine && i0 + j < nt;
+            if constexpr (kAsync)
+                copy_async<kBytes>(&s_x[(stage * kGroup + j) * kThreads + threadIdx.x],
+                                   live ? x + (i0 + j) * a.xbc_stride : static_cast<const IoT *>(a.xbc), live);
+            else if (live)
+                next[j] = load_pack<IoT, V>(x + (i0 + j) * a.xbc_stride);
+        }
+        if constexpr (kAsync) commit_async();
     };
     if constexpr (kW > 1) {
-        load_group(0);
 #pragma unroll
-        for (int m = 1; m < kW; ++m)
+        for (int d = 0; d < (kAsync ? kDepth : 1); ++d) load_group(d * kGroup, d);
+#pragma unroll
+        for (int m = 1; m < kW; ++m) {
+            prev[m - 1] = Pack<IoT, V>{};
             if (mine && t0 >= m) prev[m - 1] = load_pack<IoT, V>(x - m * a.xbc_stride);
+        }
     }
 
     // ---- the tile's tokens -------------------------------------------------
@@ -169,7 +197,10 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
         if (kept) atomicOr(&group[threadIdx.x / kGroup], kKeeps);
     }
     __syncthreads();
-    if (!mine) return;
+    if (!mine) {
+        if constexpr (kAsync) wait_async<0>();
+        return;
+    }
 
     IoT *ring = static_cast<IoT *>(a.conv_cache) + c;
     // where this thread's channels go
@@ -187,40 +218,73 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
     }
     out += t0 * ostride;
 
-    constexpr int kPairs = (V + 1) / 2;
     float2 w[kM][kPairs], bias[kPairs];        // w[k]: the tap of the token k before
+    if constexpr (kW > 0 && V > 1) {
+        const Pack<IoT, V * kM> pw = load_pack<IoT, V * kM>(static_cast<const IoT *>(a.weight) + (int64_t)c * kM);
+        Pack<IoT, V> pb{};
+        if (a.bias) pb = load_pack<IoT, V>(static_cast<const IoT *>(a.bias) + c);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const float bj = a.bias ? to_float(static_cast<const IoT *>(a.bias)[c + j]) : 0.f;
-        (j & 1 ? bias[j / 2].y : bias[j / 2].x) = bj;
+        for (int j = 0; j < V / 2; ++j) {
+            bias[j] = pair_of<V>(pb, j);
 #pragma unroll
-        for (int k = 0; k < kM; ++k) {
-            const float wk =
-                k < W ? to_float(static_cast<const IoT *>(a.weight)[(int64_t)(c + j) * W + (W - 1 - k)]) : 0.f;
-            (j & 1 ? w[k][j / 2].y : w[k][j / 2].x) = wk;
+            for (int k = 0; k < kM; ++k)
+                w[k][j] = make_float2(to_float(pw.v[2 * j * kM + kM - 1 - k]), to_float(pw.v[(2 * j + 1) * kM + kM - 1 - k]));
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float bj = a.bias ? to_float(static_cast<const IoT *>(a.bias)[c + j]) : 0.f;
+            (j & 1 ? bias[j / 2].y : bias[j / 2].x) = bj;
+#pragma unroll
+            for (int k = 0; k < kM; ++k) {
+                const float wk =
+                    k < W ? to_float(static_cast<const IoT *>(a.weight)[(int64_t)(c + j) * W + (W - 1 - k)]) : 0.f;
+                (j & 1 ? w[k][j / 2].y : w[k][j / 2].x) = wk;
+            }
         }
     }
 
+    float2 win[kPast][kPairs];          // win[m]: the input m + 1 tokens before
+#pragma unroll
+    for (int m = 0; m < kPast; ++m) widen<IoT, V>(prev[m], win[m]);
+    int stage = 0;
+#pragma unroll 1
     for (int i0 = 0; i0 < nt; i0 += kGroup) {
         const int what = group[i0 / kGroup];
         if constexpr (kW > 1) {
             Pack<IoT, V> now[kGroup];
+            if constexpr (kAsync) wait_async<kDepth - 1>();
 #pragma unroll
-            for (int j = 0; j < kGroup; ++j) now[j] = next[j];
-            load_group(i0 + kGroup);
+            for (int i = 0; i < kGroup; ++i)
+                now[i] = kAsync ? s_x[(stage * kGroup + i) * kThreads + threadIdx.x] : next[i];
+            if constexpr (!kAsync) load_group(i0 + kGroup, 0);
             if (what & kSlides) {
 #pragma unroll
                 for (int i = 0; i < kGroup; ++i) {
-                    float2 acc[kPairs];
+                    float2 acc[kPairs], f[kPairs];
+                    widen<IoT, V>(now[i], f);
 #pragma unroll
                     for (int j = 0; j < kPairs; ++j) acc[j] = bias[j];
+                    accumulate<V>(acc, w[0], f);
 #pragma unroll
-                    for (int m = 0; m < kW; ++m) accumulate<IoT, V>(acc, w[m], i >= m ? now[i - m] : prev[m - i - 1]);
+                    for (int m = 1; m < kW; ++m) accumulate<V>(acc, w[m], win[m - 1]);
                     store_pack<IoT, V>(out + (i0 + i) * ostride, finished<IoT, V>(acc, a.activation));
-                }
-            }
 #pragma unroll
-            for (int m = 0; m < kW - 1; ++m) prev[m] = now[kGroup - 1 - m];
+                    for (int j = 0; j < kPairs; ++j) {
+#pragma unroll
+                        for (int m = kPast - 1; m > 0; --m) win[m][j] = win[m - 1][j];
+                        win[0][j] = f[j];
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int m = 0; m < kPast; ++m) widen<IoT, V>(now[kGroup - 1 - m], win[m]);
+            }
+            // the group is in registers: its place takes the one kDepth groups on
+            if constexpr (kAsync) {
+                load_group(i0 + kDepth * kGroup, stage);
+                stage = stage + 1 == kDepth ? 0 : stage + 1;
+            }
         }
         if (!(what & kSlides)) {
             for (int s0 = i0; s0 < min(i0 + kGroup, nt); s0 += kSlow) {
@@ -251,7 +315,11 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
                     for (int j = 0; j < kPairs; ++j) acc[j] = bias[j];
 #pragma unroll
                     for (int m = 0; m < kM; ++m)
-                        if (m < W) accumulate<IoT, V>(acc, w[m], tap[i][m]);
+                        if (m < W) {
+                            float2 f[kPairs];
+                            widen<IoT, V>(tap[i][m], f);
+                            accumulate<V>(acc, w[m], f);
+                        }
                     store_pack<IoT, V>(out + (s0 + i) * ostride, finished<IoT, V>(acc, a.activation));
                 }
             }
@@ -266,6 +334,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
         }
     }
 
+    if constexpr (kAsync) wait_async<0>();
     // the end of the sequence that begins in this tile and passes it
     const int s = tail_seq;
     if (s >= 0) {
@@ -306,7 +375,8 @@ cudaError_t launch_conv(const ssd_conv_params &p, cudaStream_t stream) {
         const size_t bytes = (size_t)v * io;
         return p.channels % v == 0 && p.xbc_stride % v == 0 && p.split0 % v == 0 && p.split1 % v == 0 &&
                rest % v == 0 && aligned_to(p.xbc, bytes) && aligned_to(p.conv_cache, bytes) &&
-               aligned_to(p.out0, bytes) && aligned_to(p.out1, bytes) && aligned_to(p.out2, bytes);
+               aligned_to(p.out0, bytes) && aligned_to(p.out1, bytes) && aligned_to(p.out2, bytes) &&
+               aligned_to(p.weight, 16) && aligned_to(p.bias, bytes);
     };
     if (p.io_dtype == SSD_F32)
         return can(4) ? launch<float, 4>(p, stream) : can(2) ? launch<float, 2>(p, stream) : launch<float, 1>(p, stream);

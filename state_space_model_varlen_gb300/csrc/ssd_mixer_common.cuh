@@ -20,13 +20,32 @@ template <> __device__ __forceinline__ float from_float<float>(float v) { return
 template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
 // V consecutive elements moved together (one instruction up to 16 bytes).
-template <typename T, int V> struct alignas(sizeof(T) * V <= 16 ? sizeof(T) * V : 16) Pack { T v[V]; };
+constexpr int pack_align(int bytes) { return bytes % 16 == 0 ? 16 : bytes & -bytes; }
+template <typename T, int V> struct alignas(pack_align(sizeof(T) * V)) Pack { T v[V]; };
 
 template <typename T, int V> __device__ __forceinline__ Pack<T, V> load_pack(const T *src) {
     return *reinterpret_cast<const Pack<T, V> *>(src);
 }
 template <typename T, int V> __device__ __forceinline__ void store_pack(T *dst, const Pack<T, V> &p) {
     *reinterpret_cast<Pack<T, V> *>(dst) = p;
+}
+
+// kBytes (4, 8 or 16) from global to shared memory, asynchronously; zeros where
+// `live` is false (src is then any valid address, not read).  A thread that
+// reads its own copies back needs no barrier, only wait_async.
+template <int kBytes>
+__device__ __forceinline__ void copy_async(void *dst, const void *src, bool live) {
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst);
+    const int n = live ? kBytes : 0;
+    if constexpr (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(src), "n"(kBytes), "r"(n) : "memory");
+}
+__device__ __forceinline__ void commit_async() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all but the thread's newest kPending groups of copies have landed
+template <int kPending> __device__ __forceinline__ void wait_async() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 
 // v sigmoid(v) through the ex2 and rcp approximations: about 2^-21 relative

@@ -102,18 +102,6 @@ __device__ __forceinline__ float2 head_terms(const ssd_step_params &a, int b, in
     return make_float2(dt, expf(dt * a.A[h]));
 }
 
-// A thread's share of a row, kBytes of it, into its own place in shared memory;
-// zeros where `live` is false.
-template <int kBytes>
-__device__ __forceinline__ void copy_async(void *dst, const void *src, bool live) {
-    const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst);
-    const int n = live ? kBytes : 0;
-    if constexpr (kBytes == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(n) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(src), "n"(kBytes), "r"(n) : "memory");
-}
-
 // kType: storage of the state; L: lanes of a row; E: state values a lane holds
 // of it (L E >= N); V: values of one copy; kDepth: row steps copied ahead.
 template <int kType, int L, int E, int V, int kDepth>
@@ -164,7 +152,7 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
                 copy_async<V * (int)sizeof(StT)>(&s_raw[(stage * kChunks + k) * kStepThreads + tid],
                                                  live ? cache + (int64_t)r * N + n : cache, live);
             }
-            asm volatile("cp.async.commit_group;" ::: "memory");
+            commit_async();
         }
     };
 #pragma unroll
@@ -244,7 +232,7 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
         float2 acc = make_float2(0.f, 0.f);
         float st[E];
         float big = 0.f;
-        if constexpr (kAsync) asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+        if constexpr (kAsync) wait_async<kDepth - 1>();
 #pragma unroll
         for (int k = 0; k < kChunks; ++k) {
             const int n = (k * L + lane) * V;
@@ -314,7 +302,7 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
             store_pack<StT, V>(cache + (int64_t)r * N + n, p);
         }
     }
-    if constexpr (kAsync) asm volatile("cp.async.wait_all;" ::: "memory");
+    if constexpr (kAsync) wait_async<0>();
     __syncthreads();
 
     // ---- y ------------------------------------------------------------------
