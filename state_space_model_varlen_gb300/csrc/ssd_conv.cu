@@ -9,11 +9,14 @@
 // asynchronously, a few groups ahead, and alone reads it back.  A tile reads
 // W - 1 tokens more than it writes.
 //
-// Sequence boundaries are worked out once per CTA, while the first group's
-// inputs are on their way: every thread looks at some of the sequences and
-// marks the tile's tokens in shared memory.  A group whose tokens all have
-// their W - 1 predecessors in this call slides the window; any other loads
-// every tap of every token from where it lies, four tokens at a time.
+// Sequence boundaries are worked out once per CTA, while the first groups'
+// inputs are on their way: every thread looks at some of the sequences, and
+// those that meet the tile leave a record at their first token in it.  A group
+// whose tokens all have their W - 1 predecessors in this call slides the
+// window.  In any other, batches of short sequences copy what the tokens lack
+// from the ring all at once (kShort); batches of long ones, where such groups
+// are few, load every tap from where it lies, two tokens at a time, which
+// leaves the shared memory to the inputs.
 //
 // The convolution cache is updated in place by other CTAs than those that
 // read it, unless one thread does both: the CTA whose tile holds a sequence's
@@ -28,13 +31,17 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kMaxTile = 64;       // tokens of a tile
 constexpr int kGroup = 8;          // tokens whose inputs are loaded together
-constexpr int kSlow = 2;           // tokens of a group at a boundary taken together
+constexpr int kSlow = 2;           // tokens whose taps are loaded together at a boundary
 
 struct Token {
     int local;      // token of its sequence, -1: no valid sequence
     int row;        // its row of the ring
     int slot;       // -1: no cache
     int past;       // min(position, W - 1)
+};
+struct Sequence {
+    int64_t begin, end;
+    int start, slot;    // slot -1: no cache
 };
 constexpr int kSlides = 1, kKeeps = 2;      // of a group: every token has its window here; some go to the ring
 
@@ -90,24 +97,26 @@ __device__ __forceinline__ Pack<IoT, V> finished(const float2 (&acc)[(V + 1) / 2
 
 // CTAs of an SM that the registers should leave room for
 template <typename IoT, int V, int kW>
-constexpr int kMinCtas = kW == 0 ? 2 : V * sizeof(IoT) > 8 ? 4 : 6;
+constexpr int kMinCtas = kW == 0 ? 3 : 5;
 
 // kW: the width, or 0 for one that only a.width tells (then no group slides).
-template <typename IoT, int V, int kW>
+template <typename IoT, int V, int kW, bool kShort>
 __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(const ssd_conv_params a, int tile, int dt_column) {
-    __shared__ int seq_of[kMaxTile];
+    __shared__ Sequence sequence[kMaxTile];        // at the sequence's first token in the tile
+    __shared__ uint32_t firsts[kMaxTile / 32];      // where there are any
     __shared__ Token token[kMaxTile];
     __shared__ uint8_t keep[kMaxTile];             // the token goes to the ring here
     __shared__ int group[kMaxTile / kGroup];
-    __shared__ int tail_seq;
+    __shared__ int64_t tail;                       // where that sequence ends, from the tile's first token; 0: none
     constexpr int kM = kW ? kW : SSD_CONV_MAX_WIDTH;
     constexpr int kPast = kW > 1 ? kW - 1 : 1;      // inputs a sliding window keeps
     constexpr int kPairs = (V + 1) / 2;
-    // groups copied ahead: 24 KB of a CTA's inputs; two-byte shares are loaded one group ahead instead
+    // groups copied ahead; two-byte shares are loaded one group ahead instead
     constexpr int kBytes = V * (int)sizeof(IoT);
     constexpr bool kAsync = kBytes >= 4 && kW > 1;
-    constexpr int kDepth = kBytes >= 16 ? 2 : kBytes == 8 ? 3 : 4;
+    constexpr int kDepth = kBytes < 8 ? 4 : kShort ? 2 : 3;
     __shared__ Pack<IoT, V> s_x[kAsync ? kDepth * kGroup * kThreads : 1];
+    __shared__ Pack<IoT, V> s_old[kAsync && kShort ? kGroup * kPast * kThreads : 1];
     const int W = kW ? kW : a.width;
     const int64_t t0 = (int64_t)blockIdx.x * tile;
     const int nt = (int)min((int64_t)tile, a.total_tokens - t0);
@@ -118,20 +127,37 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
     }
     const bool reporter = ct == 0 && a.device_status != nullptr;
 
-    // ---- the first group's inputs and the window before it -----------------
+    // ---- every load that depends on nothing: sequences, inputs, weights -----
+    auto look_up = [&](int s) {
+        Sequence q = {a.cu_seqlens[s], a.cu_seqlens[s + 1], 0, -1};
+        if (a.start_pos) q.start = a.start_pos[s];
+        if (a.conv_cache) q.slot = a.slot_idx[s * (a.slot_idx_stride ? a.slot_idx_stride : 1)];
+        return q;
+    };
+    Sequence seq{};
+    if ((int)threadIdx.x < a.num_seqs) seq = look_up(threadIdx.x);
     const int c = (ct * kThreads + threadIdx.x) * V;
     const bool mine = c < a.channels;
     const IoT *x = static_cast<const IoT *>(a.xbc) + t0 * a.xbc_stride + c;    // of the tile's first token
     Pack<IoT, V> next[kGroup], prev[kPast];
     auto load_group = [&](int i0, int stage) {
+        const IoT *src = x + i0 * a.xbc_stride;
+        if (mine && i0 + kGroup <= nt) {
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j) {
-            const bool live = mine && i0 + j < nt;
-            if constexpr (kAsync)
-                copy_async<kBytes>(&s_x[(stage * kGroup + j) * kThreads + threadIdx.x],
-                                   live ? x + (i0 + j) * a.xbc_stride : static_cast<const IoT *>(a.xbc), live);
-            else if (live)
-                next[j] = load_pack<IoT, V>(x + (i0 + j) * a.xbc_stride);
+            for (int j = 0; j < kGroup; ++j, src += a.xbc_stride) {
+                if constexpr (kAsync) copy_async<kBytes>(&s_x[(stage * kGroup + j) * kThreads + threadIdx.x], src, true);
+                else next[j] = load_pack<IoT, V>(src);
+            }
+        } else if (mine && i0 < nt) {
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j, src += a.xbc_stride) {
+                const bool live = i0 + j < nt;
+                if constexpr (kAsync)
+                    copy_async<kBytes>(&s_x[(stage * kGroup + j) * kThreads + threadIdx.x],
+                                       live ? src : static_cast<const IoT *>(a.xbc), live);
+                else if (live)
+                    next[j] = load_pack<IoT, V>(src);
+            }
         }
         if constexpr (kAsync) commit_async();
     };
@@ -145,51 +171,64 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
         }
     }
 
+    Pack<IoT, V * kM> pw{};
+    Pack<IoT, V> pb{};
+    if constexpr (kW > 0 && V > 1) {
+        if (mine) {
+            pw = load_pack<IoT, V * kM>(static_cast<const IoT *>(a.weight) + (int64_t)c * kM);
+            if (a.bias) pb = load_pack<IoT, V>(static_cast<const IoT *>(a.bias) + c);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            if (mine && a.bias) pb.v[j] = static_cast<const IoT *>(a.bias)[c + j];
+#pragma unroll
+            for (int k = 0; k < kM; ++k)        // as a width of kM with leading zeros
+                if (mine && k < W)
+                    pw.v[j * kM + kM - 1 - k] = static_cast<const IoT *>(a.weight)[(int64_t)(c + j) * W + (W - 1 - k)];
+        }
+    }
+
     // ---- the tile's tokens -------------------------------------------------
-    if (threadIdx.x < kMaxTile) seq_of[threadIdx.x] = -1;
+    if (threadIdx.x < kMaxTile / 32) firsts[threadIdx.x] = 0;
     if (threadIdx.x < kMaxTile / kGroup) group[threadIdx.x] = kW > 1 ? kSlides : 0;
-    if (threadIdx.x == 0) tail_seq = -1;
+    if (threadIdx.x == 0) tail = 0;
     __syncthreads();
     for (int s = threadIdx.x; s < a.num_seqs; s += kThreads) {
-        const int64_t b = a.cu_seqlens[s], e = a.cu_seqlens[s + 1];
-        if (b < 0 || e < b || e > a.total_tokens) {
-            if (t0 == 0 && reporter) atomicOr(a.device_status, SSD_DEV_BAD_SEQLENS);
-            continue;
+        const Sequence q = s == (int)threadIdx.x ? seq : look_up(s);
+        int bad = 0;
+        if (q.begin < 0 || q.end < q.begin || q.end > a.total_tokens) bad = SSD_DEV_BAD_SEQLENS;
+        else if (q.end > q.begin && a.conv_cache && (q.slot < 0 || q.slot >= a.num_slots)) bad = SSD_DEV_BAD_SLOT;
+        else if (q.end > q.begin && q.start < 0) bad = SSD_DEV_BAD_POS;
+        if (bad) {
+            if (blockIdx.x == 0 && reporter) atomicOr(a.device_status, bad);
+        } else if (q.begin < t0 + nt && q.end > t0 && q.end > q.begin) {
+            const int first = (int)(max(q.begin, t0) - t0);
+            sequence[first] = q;
+            atomicOr(&firsts[first / 32], 1u << (first % 32));
         }
-        const int64_t lo = max(b, t0), hi = min(e, t0 + nt);
-        for (int64_t t = lo; t < hi; ++t) seq_of[t - t0] = s;
     }
     __syncthreads();
     if (threadIdx.x < kMaxTile) {
-        const int s = (int)threadIdx.x < nt ? seq_of[threadIdx.x] : -1;
+        const int i = threadIdx.x;
+        // the last first token up to this one
+        uint32_t below = firsts[i / 32] & (0xffffffffu >> (31 - i % 32));
+        int first = below ? (i & ~31) + 31 - __clz(below) : -1;
+        for (int word = i / 32 - 1; first < 0 && word >= 0; --word)
+            if (firsts[word]) first = word * 32 + 31 - __clz(firsts[word]);
         Token k = {-1, 0, -1, 0};
         bool kept = false;
-        if (s >= 0) {
-            const int64_t b = a.cu_seqlens[s], e = a.cu_seqlens[s + 1];
-            const int64_t local = t0 + threadIdx.x - b;
-            const int start = a.start_pos ? a.start_pos[s] : 0;
-            int slot = -1;
-            bool ok = true;
-            if (a.conv_cache != nullptr) {
-                slot = a.slot_idx[s * (a.slot_idx_stride ? a.slot_idx_stride : 1)];
-                ok = slot >= 0 && slot < a.num_slots;
-                if (!ok && local == 0 && reporter) atomicOr(a.device_status, SSD_DEV_BAD_SLOT);
-            }
-            if (start < 0) {
-                ok = false;
-                if (local == 0 && reporter) atomicOr(a.device_status, SSD_DEV_BAD_POS);
-            }
-            if (ok) {
-                const int64_t pos = start + local;
-                const bool begins_here = b >= t0;
-                k.local = (int)min(local, (int64_t)0x7fffffff);
-                k.slot = slot;
-                k.row = slot >= 0 ? (int)(pos % a.conv_rows) : 0;
-                k.past = (int)min(pos, (int64_t)(W - 1));
-                kept = slot >= 0 && begins_here && t0 + threadIdx.x >= e - (W - 1);
-                // the tile's last sequence goes on after it: its end is kept below
-                if (slot >= 0 && begins_here && (int)threadIdx.x == nt - 1 && e > t0 + nt) tail_seq = s;
-            }
+        if (i < nt && first >= 0 && sequence[first].end > t0 + i) {
+            const Sequence q = sequence[first];
+            const int64_t local = t0 + i - q.begin, pos = q.start + local;
+            const bool begins_here = q.begin >= t0;
+            k.local = (int)min(local, (int64_t)0x7fffffff);
+            k.slot = q.slot;
+            k.row = q.slot >= 0 ? (int)(pos % a.conv_rows) : 0;
+            k.past = (int)min(pos, (int64_t)(W - 1));
+            kept = q.slot >= 0 && begins_here && t0 + i >= q.end - (W - 1);
+            // the tile's last sequence goes on after it: its end is kept below
+            if (q.slot >= 0 && begins_here && i == nt - 1 && q.end > t0 + nt) tail = q.end - t0;
         }
         token[threadIdx.x] = k;
         keep[threadIdx.x] = kept;
@@ -219,30 +258,53 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
     out += t0 * ostride;
 
     float2 w[kM][kPairs], bias[kPairs];        // w[k]: the tap of the token k before
-    if constexpr (kW > 0 && V > 1) {
-        const Pack<IoT, V * kM> pw = load_pack<IoT, V * kM>(static_cast<const IoT *>(a.weight) + (int64_t)c * kM);
-        Pack<IoT, V> pb{};
-        if (a.bias) pb = load_pack<IoT, V>(static_cast<const IoT *>(a.bias) + c);
 #pragma unroll
-        for (int j = 0; j < V / 2; ++j) {
-            bias[j] = pair_of<V>(pb, j);
+    for (int j = 0; j < V; ++j) {
+        (j & 1 ? bias[j / 2].y : bias[j / 2].x) = to_float(pb.v[j]);
 #pragma unroll
-            for (int k = 0; k < kM; ++k)
-                w[k][j] = make_float2(to_float(pw.v[2 * j * kM + kM - 1 - k]), to_float(pw.v[(2 * j + 1) * kM + kM - 1 - k]));
-        }
-    } else {
+        for (int k = 0; k < kM; ++k)
+            (j & 1 ? w[k][j / 2].y : w[k][j / 2].x) = to_float(pw.v[j * kM + kM - 1 - k]);
+    }
+    // the group of tokens i0 .., every tap from where it lies
+    auto boundary = [&](int i0) {
+#pragma unroll 1
+        for (int s0 = i0; s0 < min(i0 + kGroup, nt); s0 += kSlow) {
+            Pack<IoT, V> tap[kSlow][kM];
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float bj = a.bias ? to_float(static_cast<const IoT *>(a.bias)[c + j]) : 0.f;
-            (j & 1 ? bias[j / 2].y : bias[j / 2].x) = bj;
+            for (int i = 0; i < kSlow; ++i) {
+                const Token k = token[s0 + i];
 #pragma unroll
-            for (int k = 0; k < kM; ++k) {
-                const float wk =
-                    k < W ? to_float(static_cast<const IoT *>(a.weight)[(int64_t)(c + j) * W + (W - 1 - k)]) : 0.f;
-                (j & 1 ? w[k][j / 2].y : w[k][j / 2].x) = wk;
+                for (int m = 0; m < kM; ++m) {
+                    tap[i][m] = Pack<IoT, V>{};
+                    if (m >= W || k.local < 0) continue;
+                    const IoT *src = nullptr;
+                    if (m <= k.local) {
+                        src = x + (int64_t)(s0 + i - m) * a.xbc_stride;
+                    } else if (m <= k.past && k.slot >= 0) {
+                        int row = k.row - m;
+                        if (row < 0) row += a.conv_rows;
+                        src = ring + ((int64_t)k.slot * a.conv_rows + row) * a.channels;
+                    }
+                    if (src) tap[i][m] = load_pack<IoT, V>(src);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kSlow; ++i) {
+                if (token[s0 + i].local < 0) continue;
+                float2 acc[kPairs];
+#pragma unroll
+                for (int j = 0; j < kPairs; ++j) acc[j] = bias[j];
+#pragma unroll
+                for (int m = 0; m < kM; ++m)
+                    if (m < W) {
+                        float2 f[kPairs];
+                        widen<IoT, V>(tap[i][m], f);
+                        accumulate<V>(acc, w[m], f);
+                    }
+                store_pack<IoT, V>(out + (s0 + i) * ostride, finished<IoT, V>(acc, a.activation));
             }
         }
-    }
+    };
 
     float2 win[kPast][kPairs];          // win[m]: the input m + 1 tokens before
 #pragma unroll
@@ -258,27 +320,83 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
             for (int i = 0; i < kGroup; ++i)
                 now[i] = kAsync ? s_x[(stage * kGroup + i) * kThreads + threadIdx.x] : next[i];
             if constexpr (!kAsync) load_group(i0 + kGroup, 0);
+            // a token's value from its input and the W - 1 before it, and the window moved on
+            auto one = [&](int i, bool write, auto before) {
+                float2 acc[kPairs], f[kPairs];
+                widen<IoT, V>(now[i], f);
+#pragma unroll
+                for (int j = 0; j < kPairs; ++j) acc[j] = bias[j];
+                accumulate<V>(acc, w[0], f);
+#pragma unroll
+                for (int m = 1; m < kW; ++m) {
+                    float2 g[kPairs];
+                    before(m, g);
+                    accumulate<V>(acc, w[m], g);
+                }
+                if (write) store_pack<IoT, V>(out + (i0 + i) * ostride, finished<IoT, V>(acc, a.activation));
+#pragma unroll
+                for (int j = 0; j < kPairs; ++j) {
+#pragma unroll
+                    for (int m = kPast - 1; m > 0; --m) win[m][j] = win[m - 1][j];
+                    win[0][j] = f[j];
+                }
+            };
             if (what & kSlides) {
 #pragma unroll
-                for (int i = 0; i < kGroup; ++i) {
-                    float2 acc[kPairs], f[kPairs];
-                    widen<IoT, V>(now[i], f);
+                for (int i = 0; i < kGroup; ++i)
+                    one(i, true, [&](int m, float2 (&g)[kPairs]) {
 #pragma unroll
-                    for (int j = 0; j < kPairs; ++j) acc[j] = bias[j];
-                    accumulate<V>(acc, w[0], f);
-#pragma unroll
-                    for (int m = 1; m < kW; ++m) accumulate<V>(acc, w[m], win[m - 1]);
-                    store_pack<IoT, V>(out + (i0 + i) * ostride, finished<IoT, V>(acc, a.activation));
-#pragma unroll
-                    for (int j = 0; j < kPairs; ++j) {
-#pragma unroll
-                        for (int m = kPast - 1; m > 0; --m) win[m][j] = win[m - 1][j];
-                        win[0][j] = f[j];
-                    }
-                }
-            } else {
+                        for (int j = 0; j < kPairs; ++j) g[j] = win[m - 1][j];
+                    });
+            } else if constexpr (!kShort) {
+                boundary(i0);
 #pragma unroll
                 for (int m = 0; m < kPast; ++m) widen<IoT, V>(now[kGroup - 1 - m], win[m]);
+            } else {
+                Pack<IoT, V> old[kAsync ? 1 : kGroup][kPast];
+#pragma unroll
+                for (int i = 0; i < kGroup; ++i) {
+                    const Token k = token[i0 + i];
+#pragma unroll
+                    for (int m = 1; m < kW; ++m) {
+                        const bool live = k.local >= 0 && m > k.local && m <= k.past && k.slot >= 0;
+                        int row = k.row - m;
+                        if (row < 0) row += a.conv_rows;
+                        const IoT *src = live ? ring + ((int64_t)k.slot * a.conv_rows + row) * a.channels
+                                              : static_cast<const IoT *>(a.xbc);
+                        if constexpr (kAsync) {
+                            copy_async<kBytes>(&s_old[(i * kPast + m - 1) * kThreads + threadIdx.x], src, live);
+                        } else {
+                            old[i][m - 1] = Pack<IoT, V>{};
+                            if (live) old[i][m - 1] = load_pack<IoT, V>(src);
+                        }
+                    }
+                }
+                if constexpr (kAsync) {
+                    commit_async();
+                    wait_async<0>();
+                }
+#pragma unroll
+                for (int i = 0; i < kGroup; ++i) {
+                    const int local = token[i0 + i].local;
+                    one(i, local >= 0, [&](int m, float2 (&g)[kPairs]) {
+                        widen<IoT, V>(kAsync ? s_old[(i * kPast + m - 1) * kThreads + threadIdx.x] : old[kAsync ? 0 : i][m - 1], g);
+#pragma unroll
+                        for (int j = 0; j < kPairs; ++j) {
+                            g[j].x = m <= local ? win[m - 1][j].x : g[j].x;
+                            if (V > 1) g[j].y = m <= local ? win[m - 1][j].y : g[j].y;
+                        }
+                    });
+                }
+            }
+            // after the group's taps are read: a short sequence writes rows that it read
+            if (what & kKeeps) {
+#pragma unroll
+                for (int i = 0; i < kGroup; ++i) {
+                    const Token k = token[i0 + i];
+                    if (keep[i0 + i])
+                        store_pack<IoT, V>(ring + ((int64_t)k.slot * a.conv_rows + k.row) * a.channels, now[i]);
+                }
             }
             // the group is in registers: its place takes the one kDepth groups on
             if constexpr (kAsync) {
@@ -286,45 +404,8 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
                 stage = stage + 1 == kDepth ? 0 : stage + 1;
             }
         }
-        if (!(what & kSlides)) {
-            for (int s0 = i0; s0 < min(i0 + kGroup, nt); s0 += kSlow) {
-                Pack<IoT, V> tap[kSlow][kM];
-#pragma unroll
-                for (int i = 0; i < kSlow; ++i) {
-                    const Token k = token[s0 + i];
-#pragma unroll
-                    for (int m = 0; m < kM; ++m) {
-                        tap[i][m] = Pack<IoT, V>{};
-                        if (m >= W || k.local < 0) continue;
-                        const IoT *src = nullptr;
-                        if (m <= k.local) {
-                            src = x + (int64_t)(s0 + i - m) * a.xbc_stride;
-                        } else if (m <= k.past && k.slot >= 0) {
-                            int row = k.row - m;
-                            if (row < 0) row += a.conv_rows;
-                            src = ring + ((int64_t)k.slot * a.conv_rows + row) * a.channels;
-                        }
-                        if (src) tap[i][m] = load_pack<IoT, V>(src);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < kSlow; ++i) {
-                    if (token[s0 + i].local < 0) continue;
-                    float2 acc[kPairs];
-#pragma unroll
-                    for (int j = 0; j < kPairs; ++j) acc[j] = bias[j];
-#pragma unroll
-                    for (int m = 0; m < kM; ++m)
-                        if (m < W) {
-                            float2 f[kPairs];
-                            widen<IoT, V>(tap[i][m], f);
-                            accumulate<V>(acc, w[m], f);
-                        }
-                    store_pack<IoT, V>(out + (s0 + i) * ostride, finished<IoT, V>(acc, a.activation));
-                }
-            }
-        }
-        if (what & kKeeps) {
+        if constexpr (kW <= 1) boundary(i0);
+        if (kW <= 1 && (what & kKeeps)) {
             for (int i = i0; i < min(i0 + kGroup, nt); ++i) {
                 if (!keep[i]) continue;
                 const Token k = token[i];
@@ -336,14 +417,19 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
 
     if constexpr (kAsync) wait_async<0>();
     // the end of the sequence that begins in this tile and passes it
-    const int s = tail_seq;
-    if (s >= 0) {
+    const int64_t e = tail;
+    if (e > 0) {
         const Token k = token[nt - 1];
-        const int64_t e = (int64_t)a.cu_seqlens[s + 1] - t0;       // tokens from the tile's first
-        for (int64_t i = max((int64_t)nt, e - (W - 1)); i < e; ++i) {
-            const int row = (int)((k.row + (i - (nt - 1))) % a.conv_rows);
-            store_pack<IoT, V>(ring + ((int64_t)k.slot * a.conv_rows + row) * a.channels,
-                               load_pack<IoT, V>(x + i * a.xbc_stride));
+        const int64_t i0 = max((int64_t)nt, e - (W - 1));
+        Pack<IoT, V> last[kM];
+#pragma unroll
+        for (int m = 0; m < kM; ++m)
+            if (i0 + m < e) last[m] = load_pack<IoT, V>(x + (i0 + m) * a.xbc_stride);
+#pragma unroll
+        for (int m = 0; m < kM; ++m) {
+            if (i0 + m >= e) break;
+            const int row = (int)((k.row + (i0 + m - (nt - 1))) % a.conv_rows);
+            store_pack<IoT, V>(ring + ((int64_t)k.slot * a.conv_rows + row) * a.channels, last[m]);
         }
     }
 }
@@ -351,17 +437,30 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
 template <typename IoT, int V>
 cudaError_t launch(const ssd_conv_params &p, cudaStream_t stream) {
     const int ctiles = (p.channels + kThreads * V - 1) / (kThreads * V), dt = p.dt != nullptr ? 1 : 0;
-    // long tiles read fewer tokens twice; short ones fill the GPU
-    int tile = kMaxTile;
-    while (tile > kGroup && (p.total_tokens + tile - 1) / tile * ctiles < 152 * 8) tile /= 2;
+    // the tile whose waves of CTAs take the least, a CTA's own start counted as
+    // 24 tokens: long tiles for long batches, one wave of shorter ones below that
+    int tile = kGroup;
+    int64_t least = INT64_MAX;
+    const int64_t resident = 152 * kMinCtas<IoT, V, 4>;
+    for (int t = kGroup; t <= kMaxTile; t += kGroup) {
+        const int64_t ctas = (p.total_tokens + t - 1) / t * ctiles, cost = (ctas + resident - 1) / resident * (t + 24);
+        if (cost <= least) {
+            least = cost;
+            tile = t;
+        }
+    }
     const int64_t tiles = (p.total_tokens + tile - 1) / tile;
     if (tiles > 0x7fffffff || ctiles + dt > 65535) return cudaErrorInvalidConfiguration;
     const dim3 grid((unsigned)tiles, (unsigned)(ctiles + dt));
+    // mean length below 64: many groups hold a sequence's first token (201
+    // sequences, 1,311 tokens: 16 us so, 19 us the other way; 61,773 tokens in 32: 434 and 413)
+    const bool brief = p.total_tokens < 64LL * p.num_seqs;
+    auto run = [&](auto kernel) { kernel<<<grid, kThreads, 0, stream>>>(p, tile, dt); };
     switch (p.width) {
-        case 2: conv_kernel<IoT, V, 2><<<grid, kThreads, 0, stream>>>(p, tile, dt); break;
-        case 3: conv_kernel<IoT, V, 3><<<grid, kThreads, 0, stream>>>(p, tile, dt); break;
-        case 4: conv_kernel<IoT, V, 4><<<grid, kThreads, 0, stream>>>(p, tile, dt); break;
-        default: conv_kernel<IoT, V, 0><<<grid, kThreads, 0, stream>>>(p, tile, dt);
+        case 2: brief ? run(conv_kernel<IoT, V, 2, true>) : run(conv_kernel<IoT, V, 2, false>); break;
+        case 3: brief ? run(conv_kernel<IoT, V, 3, true>) : run(conv_kernel<IoT, V, 3, false>); break;
+        case 4: brief ? run(conv_kernel<IoT, V, 4, true>) : run(conv_kernel<IoT, V, 4, false>); break;
+        default: run(conv_kernel<IoT, V, 0, false>);
     }
     return cudaGetLastError();
 }
@@ -378,8 +477,8 @@ cudaError_t launch_conv(const ssd_conv_params &p, cudaStream_t stream) {
                aligned_to(p.out0, bytes) && aligned_to(p.out1, bytes) && aligned_to(p.out2, bytes) &&
                aligned_to(p.weight, 16) && aligned_to(p.bias, bytes);
     };
-    if (p.io_dtype == SSD_F32)
-        return can(4) ? launch<float, 4>(p, stream) : can(2) ? launch<float, 2>(p, stream) : launch<float, 1>(p, stream);
+    // eight bytes a thread: more would not leave room for the ring's share of a group
+    if (p.io_dtype == SSD_F32) return can(2) ? launch<float, 2>(p, stream) : launch<float, 1>(p, stream);
     return can(4)   ? launch<__nv_bfloat16, 4>(p, stream)
            : can(2) ? launch<__nv_bfloat16, 2>(p, stream)
                     : launch<__nv_bfloat16, 1>(p, stream);

@@ -2,79 +2,185 @@
 //
 //   out = rms(y SiLU(z)) w   or   rms(y) w SiLU(z)
 //
-// Each value is read once and written once: bound by HBM.  One CTA takes one
-// group of one row and keeps its values in registers between the sum of
-// squares and the scaling.
+// Each value is read once and written once: bound by HBM.  One warp takes a
+// short group of one row, one CTA a longer one; either holds the group in
+// registers between the sum of squares and the scaling, all its loads issued
+// together.  Groups of more than 2,048 vectors are read twice (from L2 the
+// second time).
 #include "ssd_mixer_common.cuh"
 #include "ssd_mixer_internal.h"
 
 namespace ssd {
 namespace {
 
+constexpr int kChunks = 4;                  // vectors of a thread
+constexpr int kItemWarps = 4;               // warps of a CTA that takes a group with each
+
+// one group of one row
+template <typename IoT> struct Item {
+    const IoT *y, *z, *w;
+    IoT *out;
+    __device__ Item(const ssd_gated_norm_params &a, int64_t item, int groups) {
+        const int64_t row = item / groups;
+        const int c0 = (int)(item % groups) * a.group_size;
+        y = static_cast<const IoT *>(a.y) + row * a.y_stride + c0;
+        z = a.z ? static_cast<const IoT *>(a.z) + row * a.z_stride + c0 : nullptr;
+        w = a.weight ? static_cast<const IoT *>(a.weight) + c0 : nullptr;
+        out = static_cast<IoT *>(a.out) + row * a.out_stride + c0;
+    }
+};
+
+// What is normed of a vector: y, or y SiLU(z).  (V = 1: the first of a pair.)
 template <typename IoT, int V>
-__global__ void __launch_bounds__(256) gated_norm_kernel(const ssd_gated_norm_params a, int groups) {
-    __shared__ float part[8];
-    const int64_t row = blockIdx.x / groups;
-    const int c0 = (int)(blockIdx.x % groups) * a.group_size;
-    const IoT *y = static_cast<const IoT *>(a.y) + row * a.y_stride + c0;
-    const IoT *z = a.z ? static_cast<const IoT *>(a.z) + row * a.z_stride + c0 : nullptr;
-    const IoT *w = a.weight ? static_cast<const IoT *>(a.weight) + c0 : nullptr;
-    IoT *out = static_cast<IoT *>(a.out) + row * a.out_stride + c0;
-    auto value = [&](int c, float (&v)[V], float (&gate)[V]) {
-        const Pack<IoT, V> py = load_pack<IoT, V>(y + c);
-        Pack<IoT, V> pz;
-        if (z) pz = load_pack<IoT, V>(z + c);
+__device__ __forceinline__ void normed(const Pack<IoT, V> &y, const Pack<IoT, V> &z, bool gated, float2 (&v)[(V + 1) / 2]) {
+    if constexpr (V == 1) {
+        v[0].x = to_float(y.v[0]);
+        if (gated) v[0].x *= silu(to_float(z.v[0]));
+    } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            v[j] = to_float(py.v[j]);
-            gate[j] = z ? silu(to_float(pz.v[j])) : 1.f;
-            if (!a.norm_before_gate) {
-                v[j] *= gate[j];
-                gate[j] = 1.f;
-            }
+        for (int j = 0; j < V / 2; ++j) {
+            v[j] = pair_of<V>(y, j);
+            if (gated) v[j] = mul2(v[j], silu2(pair_of<V>(z, j)));
         }
-    };
-    float sum = 0.f;
-    for (int c = threadIdx.x * V; c < a.group_size; c += blockDim.x * V) {
-        float v[V], gate[V];
-        value(c, v, gate);
+    }
+}
+template <int V> __device__ __forceinline__ void add_squares(float2 &sum, const float2 (&v)[(V + 1) / 2]) {
+    if constexpr (V == 1) {
+        sum.x = fmaf(v[0].x, v[0].x, sum.x);
+    } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) sum = fmaf(v[j], v[j], sum);
+        for (int j = 0; j < V / 2; ++j) sum = fma2(v[j], v[j], sum);
+    }
+}
+// v r w, times SiLU(z) where the gate comes after the norm
+template <typename IoT, int V>
+__device__ __forceinline__ Pack<IoT, V> scaled(const float2 (&v)[(V + 1) / 2], float r, const Pack<IoT, V> &w, bool weighted,
+                                               const Pack<IoT, V> &z, bool gated) {
+    Pack<IoT, V> o;
+    if constexpr (V == 1) {
+        float f = v[0].x * r;
+        if (weighted) f *= to_float(w.v[0]);
+        if (gated) f *= silu(to_float(z.v[0]));
+        o.v[0] = from_float<IoT>(f);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) {
+            float2 f = mul2(v[j], make_float2(r, r));
+            if (weighted) f = mul2(f, pair_of<V>(w, j));
+            if (gated) f = mul2(f, silu2(pair_of<V>(z, j)));
+            set_pair<V>(o, j, f);
+        }
+    }
+    return o;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+// over the CTA, whose warps leave their sums in part
+__device__ __forceinline__ float cta_sum(float v, float *part) {
+    v = warp_sum(v);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = (threadIdx.x & 31) < blockDim.x / 32 ? part[threadIdx.x & 31] : 0.f;
+    return warp_sum(v);
+}
+
+// kWarp: each warp an item; else the CTA one item, a thread kChunks vectors at most.
+template <typename IoT, int V, bool kWarp>
+__global__ void __launch_bounds__(kWarp ? 32 * kItemWarps : 512) gated_norm_kernel(const ssd_gated_norm_params a, int groups, int64_t items) {
+    __shared__ float part[32];
+    const int64_t id = kWarp ? (int64_t)blockIdx.x * kItemWarps + threadIdx.x / 32 : blockIdx.x;
+    if (id >= items) return;
+    const Item<IoT> it(a, id, groups);
+    const int at = (kWarp ? threadIdx.x & 31 : threadIdx.x) * V, step = (kWarp ? 32 : blockDim.x) * V;
+    const bool after = it.z && a.norm_before_gate, before = it.z && !a.norm_before_gate;
+    Pack<IoT, V> y[kChunks], z[kChunks], w[kChunks];
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) {
+        const int c = at + k * step;
+        y[k] = z[k] = w[k] = Pack<IoT, V>{};
+        if (c < a.group_size) {
+            y[k] = load_pack<IoT, V>(it.y + c);
+            if (it.z) z[k] = load_pack<IoT, V>(it.z + c);
+        }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
-    __syncthreads();
-    sum = 0.f;
-    for (int i = 0; i < (int)blockDim.x / 32; ++i) sum += part[i];
-    const float r = 1.f / sqrtf(sum / (float)a.group_size + a.eps);
-    for (int c = threadIdx.x * V; c < a.group_size; c += blockDim.x * V) {
-        float v[V], gate[V];
-        value(c, v, gate);
-        Pack<IoT, V> po;
+    for (int k = 0; k < kChunks; ++k)
+        if (it.w && at + k * step < a.group_size) w[k] = load_pack<IoT, V>(it.w + at + k * step);
+    float2 v[kChunks][(V + 1) / 2], two = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            po.v[j] = from_float<IoT>(v[j] * r * (w ? to_float(w[c + j]) : 1.f) * gate[j]);
-        store_pack<IoT, V>(out + c, po);
+    for (int k = 0; k < kChunks; ++k) {
+        normed<IoT, V>(y[k], z[k], before, v[k]);
+        add_squares<V>(two, v[k]);
+    }
+    const float sum = kWarp ? warp_sum(two.x + two.y) : cta_sum(two.x + two.y, part);
+    const float r = 1.f / sqrtf(sum / (float)a.group_size + a.eps);
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) {
+        const int c = at + k * step;
+        if (c < a.group_size) store_pack<IoT, V>(it.out + c, scaled<IoT, V>(v[k], r, w[k], it.w != nullptr, z[k], after));
+    }
+}
+
+template <typename IoT, int V>
+__global__ void __launch_bounds__(1024) gated_norm_long_kernel(const ssd_gated_norm_params a, int groups) {
+    __shared__ float part[32];
+    const Item<IoT> it(a, blockIdx.x, groups);
+    const bool after = it.z && a.norm_before_gate, before = it.z && !a.norm_before_gate;
+    float2 two = make_float2(0.f, 0.f);
+    float r = 0.f;
+    for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 4
+        for (int c = threadIdx.x * V; c < a.group_size; c += blockDim.x * V) {
+            Pack<IoT, V> y = load_pack<IoT, V>(it.y + c), z{}, w{};
+            if (it.z) z = load_pack<IoT, V>(it.z + c);
+            float2 v[(V + 1) / 2];
+            normed<IoT, V>(y, z, before, v);
+            if (pass) {
+                if (it.w) w = load_pack<IoT, V>(it.w + c);
+                store_pack<IoT, V>(it.out + c, scaled<IoT, V>(v, r, w, it.w != nullptr, z, after));
+            } else {
+                add_squares<V>(two, v);
+            }
+        }
+        if (!pass) r = 1.f / sqrtf(cta_sum(two.x + two.y, part) / (float)a.group_size + a.eps);
     }
 }
 
 template <typename IoT, int V>
 cudaError_t launch(const ssd_gated_norm_params &p, cudaStream_t stream) {
     const int groups = p.columns / p.group_size;
-    if (p.rows * groups > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    gated_norm_kernel<IoT, V><<<(unsigned)(p.rows * groups), 256, 0, stream>>>(p, groups);
+    const int64_t items = p.rows * groups;
+    if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const int vectors = (p.group_size + V - 1) / V;
+    if (vectors <= 32 * kChunks) {
+        gated_norm_kernel<IoT, V, true>
+            <<<(unsigned)((items + kItemWarps - 1) / kItemWarps), 32 * kItemWarps, 0, stream>>>(p, groups, items);
+    } else if (vectors <= 512 * kChunks) {
+        const int warps = (vectors + 32 * kChunks - 1) / (32 * kChunks);
+        gated_norm_kernel<IoT, V, false><<<(unsigned)items, 32 * warps, 0, stream>>>(p, groups, items);
+    } else {
+        gated_norm_long_kernel<IoT, V><<<(unsigned)items, 1024, 0, stream>>>(p, groups);
+    }
     return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_gated_norm(const ssd_gated_norm_params &p, cudaStream_t stream) {
-    const int io = p.io_dtype == SSD_F32 ? 4 : 2, v = 16 / io;
-    const bool wide = p.group_size % v == 0 && p.y_stride % v == 0 && p.out_stride % v == 0 && p.z_stride % v == 0 &&
-                      aligned_to(p.y, 16) && aligned_to(p.z, 16) && aligned_to(p.out, 16);
-    if (p.io_dtype == SSD_F32) return wide ? launch<float, 4>(p, stream) : launch<float, 1>(p, stream);
-    return wide ? launch<__nv_bfloat16, 8>(p, stream) : launch<__nv_bfloat16, 1>(p, stream);
+    const int io = p.io_dtype == SSD_F32 ? 4 : 2;
+    auto can = [&](int v) {
+        const size_t bytes = (size_t)v * io;
+        return p.group_size % v == 0 && p.y_stride % v == 0 && p.out_stride % v == 0 && p.z_stride % v == 0 &&
+               aligned_to(p.y, bytes) && aligned_to(p.z, bytes) && aligned_to(p.out, bytes) && aligned_to(p.weight, bytes);
+    };
+    if (p.io_dtype == SSD_F32) return can(4) ? launch<float, 4>(p, stream) : launch<float, 1>(p, stream);
+    return can(8)   ? launch<__nv_bfloat16, 8>(p, stream)
+           : can(4) ? launch<__nv_bfloat16, 4>(p, stream)
+                    : launch<__nv_bfloat16, 1>(p, stream);
 }
 
 }  // namespace ssd
