@@ -115,11 +115,12 @@ ssd_status ssd_step(const ssd_step_params *params, struct CUstream_st *stream) {
     const ssd_status v = check(params);
     if (v != SSD_OK || params->batch == 0) return v;
     switch (params->state_dtype) {
-        case SSD_F32: return done(ssd::launch_step_32(*params, stream));
-        case SSD_BF16:
-        case SSD_F16: return done(ssd::launch_step_16(*params, stream));
+        case SSD_F32: return done(ssd::launch_step_f32(*params, stream));
+        case SSD_BF16: return done(ssd::launch_step_bf16(*params, stream));
+        case SSD_F16: return done(ssd::launch_step_f16(*params, stream));
+        case SSD_E4M3: return done(ssd::launch_step_e4m3(*params, stream));
     }
-    return done(ssd::launch_step_8(*params, stream));
+    return done(ssd::launch_step_i8(*params, stream));
 }
 
 ssd_status ssd_gated_norm(const ssd_gated_norm_params *params, struct CUstream_st *stream) {

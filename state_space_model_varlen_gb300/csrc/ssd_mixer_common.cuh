@@ -197,16 +197,16 @@ __device__ __forceinline__ __half sr_f16_fast(float v, uint32_t r) {
 // ---- nearest ---------------------------------------------------------------
 template <int kType> __device__ __forceinline__ uint32_t encode4(const float *h, float inv) {
     if constexpr (kType == SSD_E4M3) {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(h[0], inv), __fmul_rn(h[1], inv)),
-                                                     __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(h[2], inv), __fmul_rn(h[3], inv)),
-                                                     __NV_SATFINITE, __NV_E4M3);
+        const float2 inv2 = make_float2(inv, inv);
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(mul2(make_float2(h[0], h[1]), inv2), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(mul2(make_float2(h[2], h[3]), inv2), __NV_SATFINITE, __NV_E4M3);
         return __byte_perm(lo, hi, 0x5410);
     } else {
         // 1.5 2^23 + v, whose rounding is the rounding to an integer
-        uint32_t t[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) t[i] = __float_as_uint(__fadd_rn(__fmul_rn(h[i], inv), 12582912.f));
+        const float2 inv2 = make_float2(inv, inv), magic = make_float2(12582912.f, 12582912.f);
+        const float2 lo = add2(mul2(make_float2(h[0], h[1]), inv2), magic);
+        const float2 hi = add2(mul2(make_float2(h[2], h[3]), inv2), magic);
+        const uint32_t t[4] = {__float_as_uint(lo.x), __float_as_uint(lo.y), __float_as_uint(hi.x), __float_as_uint(hi.y)};
         return __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
     }
 }
@@ -272,9 +272,9 @@ template <int kType> __device__ __forceinline__ uint32_t encode4_sr(const float 
         // values 0, 2 and 1, 3 as pairs of fp16, doubled with the random bits
         // doubled: the high byte of each half then holds the seven bits that stay
         // (fp16's top exponent bit is 0 below 2); the sign comes from the fp16
-        const float s = inv * 0.00390625f;
-        const __half2 even = __floats2half2_rn(__fmul_rn(h[0], s), __fmul_rn(h[2], s));
-        const __half2 odd = __floats2half2_rn(__fmul_rn(h[1], s), __fmul_rn(h[3], s));
+        const float2 s2 = make_float2(inv * 0.00390625f, inv * 0.00390625f);
+        const float2 lo = mul2(make_float2(h[0], h[1]), s2), hi = mul2(make_float2(h[2], h[3]), s2);
+        const __half2 even = __floats2half2_rn(lo.x, hi.x), odd = __floats2half2_rn(lo.y, hi.y);
         uint32_t fe, fo;
         memcpy(&fe, &even, 4);
         memcpy(&fo, &odd, 4);

@@ -13,10 +13,12 @@ cudaError_t launch_conv(const ssd_conv_params &p, cudaStream_t stream);
 cudaError_t launch_gated_norm(const ssd_gated_norm_params &p, cudaStream_t stream);
 cudaError_t launch_state_store(const ssd_state_params &p, cudaStream_t stream);
 cudaError_t launch_state_load(const ssd_state_params &p, cudaStream_t stream);
-// The step, one translation unit per state storage size.
-cudaError_t launch_step_32(const ssd_step_params &p, cudaStream_t stream);
-cudaError_t launch_step_16(const ssd_step_params &p, cudaStream_t stream);
-cudaError_t launch_step_8(const ssd_step_params &p, cudaStream_t stream);
+// The step, one translation unit for each type of the state cache.
+cudaError_t launch_step_f32(const ssd_step_params &p, cudaStream_t stream);
+cudaError_t launch_step_bf16(const ssd_step_params &p, cudaStream_t stream);
+cudaError_t launch_step_f16(const ssd_step_params &p, cudaStream_t stream);
+cudaError_t launch_step_e4m3(const ssd_step_params &p, cudaStream_t stream);
+cudaError_t launch_step_i8(const ssd_step_params &p, cudaStream_t stream);
 
 inline bool aligned_to(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) % bytes) == 0; }
 

@@ -28,7 +28,7 @@ namespace ssd {
 namespace {
 
 constexpr int kStepThreads = 128;
-constexpr int kStepMaxRows = 256;                  // of one CTA
+constexpr int kStepMaxRows = 512;                  // of one CTA
 
 struct StepPlan {
     int rows_g;        // rows of a group
@@ -103,8 +103,9 @@ __device__ __forceinline__ float2 head_terms(const ssd_step_params &a, int b, in
 }
 
 // kType: storage of the state; L: lanes of a row; E: state values a lane holds
-// of it (L E >= N); V: values of one copy; kDepth: row steps copied ahead.
-template <int kType, int L, int E, int V, int kDepth>
+// of it (L E >= N); V: values of one copy; kDepth: row steps copied ahead; kSr:
+// stochastic rounding.
+template <int kType, int L, int E, int V, int kDepth, bool kSr>
 __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(const ssd_step_params a, const StepPlan plan) {
     using StT = typename Stored<kType>::T;
     constexpr int kChunks = E / V, kStepGroups = kStepThreads / L;     // rows worked on at a time
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
     // of each row: D x, later y; dt' x; the decay, times its scale
     __shared__ __align__(16) float s_b[L * E], s_c[L * E], s_y[kStepMaxRows], s_dx[kStepMaxRows], s_keep[kStepMaxRows];
     __shared__ float s_scale[k8bit ? kStepMaxRows : 1];
-    __shared__ __align__(16) uint32_t s_keys[20];
+    __shared__ __align__(16) uint32_t s_keys[kSr ? 20 : 1];
     __shared__ Pack<StT, V> s_raw[kAsync ? kDepth * kChunks * kStepThreads : 1];
 
     const int N = a.dstate, P = a.headdim, H = a.nheads;
@@ -141,22 +142,25 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
     // ---- the state's first copies ------------------------------------------
     const int64_t row0 = (int64_t)slot * H * P + r0;    // row of the cache
     StT *cache = static_cast<StT *>(a.state_cache) + row0 * N;
-    // the rows t .. t + 15, to the stage's places
-    auto copy_rows = [&](int t, int stage) {
+    // the next kStepGroups rows, to the stage's places; none at position 0
+    const StT *ahead = cache + (int64_t)grp * N + lane * V;
+    int ahead_rows = (pos > 0 ? rows : 0) - grp;        // how many from this thread's next on
+    auto copy_rows = [&](int stage) {
         if constexpr (kAsync) {
-            const int r = t + grp;
+            const bool live = ahead_rows > 0;
+            const StT *src = live ? ahead : cache;
 #pragma unroll
-            for (int k = 0; k < kChunks; ++k) {
-                const int n = (k * L + lane) * V;
-                const bool live = r < rows && n < N && pos > 0;
+            for (int k = 0; k < kChunks; ++k)
                 copy_async<V * (int)sizeof(StT)>(&s_raw[(stage * kChunks + k) * kStepThreads + tid],
-                                                 live ? cache + (int64_t)r * N + n : cache, live);
-            }
+                                                 (k * L + lane) * V < N ? src + k * L * V : cache,
+                                                 live && (k * L + lane) * V < N);
             commit_async();
+            ahead += kStepGroups * N;
+            ahead_rows -= kStepGroups;
         }
     };
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d) copy_rows(d * kStepGroups, d);
+    for (int d = 0; d < kDepth; ++d) copy_rows(d);
 
     // ---- convolution, and what each row takes from it and from its head -----
     const int channels = plan.channels;
@@ -205,7 +209,7 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
             }
         }
     };
-    if (a.sr_seed && tid < 20) round_keys(*a.sr_seed, tid, s_keys);
+    if (kSr && tid < 20) round_keys(*a.sr_seed, tid, s_keys);
     for (int i = N + tid; i < L * E; i += kStepThreads) s_b[i] = s_c[i] = 0.f;
     if (bf16) convolve(__nv_bfloat16{});
     else convolve(float{});
@@ -222,12 +226,13 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
             (e & 1 ? cv[e / 2].y : cv[e / 2].x) = s_c[n];
         }
     int stage = 0;
+    StT *dst = cache + (int64_t)grp * N + lane * V;
+    uint64_t e0 = (uint64_t)(row0 + grp) * N + lane * V;        // flat index of the thread's first value
 #pragma unroll 1
-    for (int t = 0; t < rows; t += kStepGroups) {
+    for (int t = 0; t < rows; t += kStepGroups, dst += kStepGroups * N, e0 += kStepGroups * N) {
         const int r = t + grp;
         const bool live = r < rows;
-        const float dx = live ? s_dx[r] : 0.f;
-        const float keep = live ? s_keep[r] : 0.f;
+        const float dx = s_dx[r], keep = s_keep[r];     // whatever they are past the last row
         const float2 dx2 = make_float2(dx, dx), keep2 = make_float2(keep, keep);
         float2 acc = make_float2(0.f, 0.f);
         float st[E];
@@ -239,7 +244,7 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
             if (n >= N) continue;       // past the row: an infinite x must not meet a zero there
             Pack<StT, V> now{};
             if constexpr (kAsync) now = s_raw[(stage * kChunks + k) * kStepThreads + tid];
-            else if (live && pos > 0) now = load_pack<StT, V>(cache + (int64_t)r * N + n);
+            else if (live && pos > 0) now = load_pack<StT, V>(dst + k * L * V);
             decode<kType, V>(now, st + k * V);
             if constexpr (V == 1) {
                 st[k] = fmaf(keep, st[k], dx * (k & 1 ? bv[k / 2].y : bv[k / 2].x));
@@ -257,7 +262,7 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
             }
         }
         // the values are in registers: their places take the rows kDepth steps on
-        copy_rows(t + kDepth * kStepGroups, stage);
+        copy_rows(stage);
         stage = stage + 1 == kDepth ? 0 : stage + 1;
         const float sum = lanes_sum<L>(acc.x + acc.y);
         if (lane == 0 && live) s_y[r] += sum;
@@ -271,7 +276,7 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
             const int n = (k * L + lane) * V;
             if (!live || n >= N) continue;
             const float *v = st + k * V;
-            const uint64_t e = (uint64_t)(row0 + r) * N + n;
+            const uint64_t e = e0 + k * L * V;
             Pack<StT, V> p;
             if constexpr (kType == SSD_F32) {
 #pragma unroll
@@ -280,7 +285,7 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
 #pragma unroll
                 for (int j = 0; j < V; ++j) p.v[j] = __float2bfloat16_rn(v[j]);
             } else if constexpr (kType == SSD_F16) {
-                if (a.sr_seed) {
+                if constexpr (kSr) {
                     uint4 w = make_uint4(0, 0, 0, 0);
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
@@ -297,9 +302,10 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
                     for (int j = 0; j < V; ++j) p.v[j] = __float2half_rn(v[j]);
                 }
             } else {
-                p = a.sr_seed ? encode8_sr<kType, V>(v, inv, s_keys, e) : encode8<kType, V>(v, inv);
+                if constexpr (kSr) p = encode8_sr<kType, V>(v, inv, s_keys, e);
+                else p = encode8<kType, V>(v, inv);
             }
-            store_pack<StT, V>(cache + (int64_t)r * N + n, p);
+            store_pack<StT, V>(dst + k * L * V, p);
         }
     }
     if constexpr (kAsync) wait_async<0>();
@@ -329,12 +335,20 @@ cudaError_t launch_step(const ssd_step_params &p, cudaStream_t stream) {
     const int rows_g = plan.rows_g = p.nheads / p.ngroups * p.headdim;
     plan.channels = p.nheads * p.headdim + 2 * p.ngroups * p.dstate;
     set_divisor(plan, p.headdim);
-    // the shortest runs that are all resident at once; long ones share the
-    // convolution of B and C
-    plan.rows = 32;
-    while (plan.rows < kStepMaxRows &&
-           (int64_t)(rows_g + plan.rows - 1) / plan.rows * p.ngroups * p.batch > 152 * (E == 32 ? 4 : 6))
-        plan.rows *= 2;
+    // the run whose waves of CTAs take the least, a CTA's own start counted as 64
+    // rows: long runs share the convolution of B and C, short ones fill the GPU
+    constexpr int kMinRows = kStepThreads / L < 32 ? 32 : kStepThreads / L;
+    const int64_t resident = 152 * (E == 32 ? 4 : 6);
+    int64_t least = INT64_MAX;
+    for (int rows = kMinRows; rows <= kStepMaxRows; rows += 32) {
+        const int64_t ctas = (int64_t)((rows_g + rows - 1) / rows) * p.ngroups * p.batch;
+        const int64_t cost = (ctas + resident - 1) / resident * (rows + 64);
+        if (cost < least) {
+            least = cost;
+            plan.rows = rows;
+        }
+        if (rows >= rows_g) break;
+    }
     const int runs = (rows_g + plan.rows - 1) / plan.rows;
     const int io = p.io_dtype == SSD_F32 ? 4 : 2, vec = 4 * io;
     plan.vec4 = p.width == 4 && p.dstate % 4 == 0 && p.headdim % 4 == 0 && p.xbc_stride % 4 == 0 &&
@@ -342,7 +356,12 @@ cudaError_t launch_step(const ssd_step_params &p, cudaStream_t stream) {
                 aligned_to(p.weight, 16) && aligned_to(p.state_scale, 16);
     if (p.ngroups > 65535 || runs > 65535) return cudaErrorInvalidConfiguration;
     const dim3 grid((unsigned)p.batch, (unsigned)p.ngroups, (unsigned)runs);
-    step_kernel<kType, L, E, V, kDepth><<<grid, kStepThreads, 0, stream>>>(p, plan);
+    if constexpr (kType == SSD_F32 || kType == SSD_BF16) {
+        step_kernel<kType, L, E, V, kDepth, false><<<grid, kStepThreads, 0, stream>>>(p, plan);
+    } else {
+        if (p.sr_seed) step_kernel<kType, L, E, V, kDepth, true><<<grid, kStepThreads, 0, stream>>>(p, plan);
+        else step_kernel<kType, L, E, V, kDepth, false><<<grid, kStepThreads, 0, stream>>>(p, plan);
+    }
     return cudaGetLastError();
 }
 
