@@ -45,7 +45,8 @@ extern "C" {
 /* 8-bit storage of a state cache, beside SSD_F32, SSD_BF16 and SSD_F16.  The
  * N values of a state row [slot, h, p, :] are codes times one fp32 scale:
  *   m = max |h_n|;  inv = (1 / m) lim;  code_n = round(h_n inv);
- *   scale = m (1 / lim)           (each operation rounded to fp32)
+ *   scale = m (1 / lim)           (each operation rounded to fp32; in
+ *   ssd_step inv may be two units of its last place from that)
  * with lim 448 (E4M3, codes are e4m3 numbers) or 127 (I8, codes are signed
  * integers).  A row with m < 2^-100 is held as zeros with scale 0; a row with
  * an infinity or a NaN gets the scale NaN, so that it reads back as NaN.

@@ -173,15 +173,21 @@ __device__ __forceinline__ void decode(const Pack<typename Stored<kType>::T, V> 
 }
 
 // What a row's largest magnitude makes of its scale: inv multiplies the
-// values, scale multiplies the codes.
+// values, scale multiplies the codes.  kExact: inv is (1 / m) limit with both
+// operations rounded; else through the reciprocal approximation, within two
+// units of its last place, where that neither over- nor underflows.
+template <bool kExact>
 __device__ __forceinline__ void row_scale(float m, float limit, float *inv, float *scale) {
-    *inv = __fmul_rn(__frcp_rn(m), limit);
     *scale = __fmul_rn(m, 1.f / limit);
-    if (!(m < __int_as_float(0x7f800000))) {    // an infinity or a NaN in the row
+    if (!kExact && m < 1.329227995784916e+36f && m >= 7.888609052210118e-31f) {    // 2^120, 2^-100
+        *inv = rcp_approx(m) * limit;
+    } else if (!(m < __int_as_float(0x7f800000))) {     // an infinity or a NaN in the row
         *inv = 0.f;
         *scale = __int_as_float(0x7fffffff);
-    } else if (m < 7.888609052210118e-31f) {    // 2^-100
+    } else if (m < 7.888609052210118e-31f) {
         *inv = *scale = 0.f;
+    } else {
+        *inv = __fmul_rn(__frcp_rn(m), limit);
     }
 }
 

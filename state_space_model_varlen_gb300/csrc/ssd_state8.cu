@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kThreads) store_kernel(const ssd_state_params 
                 else if (V == 1) big = max_abs(big, v[k][j], v[k][j]);
             }
         float inv, scale;
-        row_scale(lanes_max<8>(big), code_limit<kType>(), &inv, &scale);
+        row_scale<true>(lanes_max<8>(big), code_limit<kType>(), &inv, &scale);
         if (r >= per) continue;
         if (lane == 0) a.state_scale[row] = scale;
         uint8_t *dst = static_cast<uint8_t *>(a.state_cache) + row * N;

@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
         if (lane == 0 && live) s_y[r] += sum;
         float inv = 0.f, sc = 0.f;
         if constexpr (k8bit) {
-            row_scale(lanes_max<L>(big), code_limit<kType>(), &inv, &sc);
+            row_scale<false>(lanes_max<L>(big), code_limit<kType>(), &inv, &sc);
             if (lane == 0 && live) s_scale[r] = sc;
         }
 #pragma unroll
@@ -328,8 +328,9 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
 template <int kType, int L, int E, int V>
 cudaError_t launch_step(const ssd_step_params &p, cudaStream_t stream) {
     constexpr int size = (int)sizeof(typename Stored<kType>::T);
-    // steps in flight: 24 KB of a CTA's states, at least two, at most six
-    constexpr int kFit = 24576 / (kStepThreads * E * size);
+    // steps in flight: 24 KB of a CTA's states (12 KB of 8-bit ones, whose CTAs
+    // compute longer on them: 109 us so, 114 with 24 KB), at least two, at most six
+    constexpr int kFit = (size == 1 ? 12288 : 24576) / (kStepThreads * E * size);
     constexpr int kDepth = kFit < 2 ? 2 : kFit > 6 ? 6 : kFit;
     StepPlan plan;
     const int rows_g = plan.rows_g = p.nheads / p.ngroups * p.headdim;
