@@ -117,6 +117,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
     constexpr int kDepth = kBytes < 8 ? 4 : kShort ? 2 : 3;
     __shared__ Pack<IoT, V> s_x[kAsync ? kDepth * kGroup * kThreads : 1];
     __shared__ Pack<IoT, V> s_old[kAsync && kShort ? kGroup * kPast * kThreads : 1];
+    await_previous();
     const int W = kW ? kW : a.width;
     const int64_t t0 = (int64_t)blockIdx.x * tile;
     const int nt = (int)min((int64_t)tile, a.total_tokens - t0);
@@ -455,14 +456,13 @@ cudaError_t launch(const ssd_conv_params &p, cudaStream_t stream) {
     // mean length below 64: many groups hold a sequence's first token (201
     // sequences, 1,311 tokens: 16 us so, 19 us the other way; 61,773 tokens in 32: 434 and 413)
     const bool brief = p.total_tokens < 64LL * p.num_seqs;
-    auto run = [&](auto kernel) { kernel<<<grid, kThreads, 0, stream>>>(p, tile, dt); };
+    auto run = [&](auto kernel) { return enqueue(kernel, grid, kThreads, stream, p, tile, dt); };
     switch (p.width) {
-        case 2: brief ? run(conv_kernel<IoT, V, 2, true>) : run(conv_kernel<IoT, V, 2, false>); break;
-        case 3: brief ? run(conv_kernel<IoT, V, 3, true>) : run(conv_kernel<IoT, V, 3, false>); break;
-        case 4: brief ? run(conv_kernel<IoT, V, 4, true>) : run(conv_kernel<IoT, V, 4, false>); break;
-        default: run(conv_kernel<IoT, V, 0, false>);
+        case 2: return brief ? run(conv_kernel<IoT, V, 2, true>) : run(conv_kernel<IoT, V, 2, false>);
+        case 3: return brief ? run(conv_kernel<IoT, V, 3, true>) : run(conv_kernel<IoT, V, 3, false>);
+        case 4: return brief ? run(conv_kernel<IoT, V, 4, true>) : run(conv_kernel<IoT, V, 4, false>);
     }
-    return cudaGetLastError();
+    return run(conv_kernel<IoT, V, 0, false>);
 }
 
 }  // namespace

@@ -92,6 +92,7 @@ __device__ __forceinline__ float cta_sum(float v, float *part) {
 template <typename IoT, int V, bool kWarp>
 __global__ void __launch_bounds__(kWarp ? 32 * kItemWarps : 512) gated_norm_kernel(const ssd_gated_norm_params a, int groups, int64_t items) {
     __shared__ float part[32];
+    await_previous();
     const int64_t id = kWarp ? (int64_t)blockIdx.x * kItemWarps + threadIdx.x / 32 : blockIdx.x;
     if (id >= items) return;
     const Item<IoT> it(a, id, groups);
@@ -128,6 +129,7 @@ __global__ void __launch_bounds__(kWarp ? 32 * kItemWarps : 512) gated_norm_kern
 template <typename IoT, int V>
 __global__ void __launch_bounds__(1024) gated_norm_long_kernel(const ssd_gated_norm_params a, int groups) {
     __shared__ float part[32];
+    await_previous();
     const Item<IoT> it(a, blockIdx.x, groups);
     const bool after = it.z && a.norm_before_gate, before = it.z && !a.norm_before_gate;
     float2 two = make_float2(0.f, 0.f);
@@ -156,16 +158,13 @@ cudaError_t launch(const ssd_gated_norm_params &p, cudaStream_t stream) {
     const int64_t items = p.rows * groups;
     if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const int vectors = (p.group_size + V - 1) / V;
-    if (vectors <= 32 * kChunks) {
-        gated_norm_kernel<IoT, V, true>
-            <<<(unsigned)((items + kItemWarps - 1) / kItemWarps), 32 * kItemWarps, 0, stream>>>(p, groups, items);
-    } else if (vectors <= 512 * kChunks) {
-        const int warps = (vectors + 32 * kChunks - 1) / (32 * kChunks);
-        gated_norm_kernel<IoT, V, false><<<(unsigned)items, 32 * warps, 0, stream>>>(p, groups, items);
-    } else {
-        gated_norm_long_kernel<IoT, V><<<(unsigned)items, 1024, 0, stream>>>(p, groups);
-    }
-    return cudaGetLastError();
+    if (vectors <= 32 * kChunks)
+        return enqueue(gated_norm_kernel<IoT, V, true>, dim3((unsigned)((items + kItemWarps - 1) / kItemWarps)),
+                       32 * kItemWarps, stream, p, groups, items);
+    if (vectors <= 512 * kChunks)
+        return enqueue(gated_norm_kernel<IoT, V, false>, dim3((unsigned)items),
+                       32 * ((vectors + 32 * kChunks - 1) / (32 * kChunks)), stream, p, groups, items);
+    return enqueue(gated_norm_long_kernel<IoT, V>, dim3((unsigned)items), 1024, stream, p, groups);
 }
 
 }  // namespace

@@ -19,6 +19,13 @@ template <typename T> __device__ __forceinline__ T from_float(float v);
 template <> __device__ __forceinline__ float from_float<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+// First statement of every kernel: waits until all work before it in the stream
+// is done and visible.  (No kernel lets the next one start early: its CTAs then
+// held places of this one's, 20.6 for 19.7 us of two convolutions back to back.)
+__device__ __forceinline__ void await_previous() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // V consecutive elements moved together (one instruction up to 16 bytes).
 constexpr int pack_align(int bytes) { return bytes % 16 == 0 ? 16 : bytes & -bytes; }
 template <typename T, int V> struct alignas(pack_align(sizeof(T) * V)) Pack { T v[V]; };

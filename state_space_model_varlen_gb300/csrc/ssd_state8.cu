@@ -26,6 +26,7 @@ __device__ __forceinline__ int checked_slot(const ssd_state_params &a, int s, bo
 template <typename DnT, int kType, int E, int V>
 __global__ void __launch_bounds__(kThreads) store_kernel(const ssd_state_params a, int blocks) {
     __shared__ __align__(16) uint32_t keys[20];
+    await_previous();
     const int s = blockIdx.x / blocks, N = a.dstate;
     const int64_t per = (int64_t)a.nheads * a.headdim;
     const int64_t r0 = (int64_t)(blockIdx.x % blocks) * kTile + (threadIdx.x >> 3);
@@ -74,6 +75,7 @@ __global__ void __launch_bounds__(kThreads) store_kernel(const ssd_state_params 
 
 template <typename DnT, int kType, int E, int V>
 __global__ void __launch_bounds__(kThreads) load_kernel(const ssd_state_params a, int blocks) {
+    await_previous();
     const int s = blockIdx.x / blocks, N = a.dstate;
     const int64_t per = (int64_t)a.nheads * a.headdim;
     const int64_t r0 = (int64_t)(blockIdx.x % blocks) * kTile + (threadIdx.x >> 3);
@@ -120,10 +122,8 @@ template <bool kStore, typename DnT, int kType, int E, int V>
 cudaError_t launch(const ssd_state_params &p, cudaStream_t stream) {
     const int64_t per = (int64_t)p.nheads * p.headdim, blocks = (per + kTile - 1) / kTile;
     if (p.num_states * blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    const unsigned grid = (unsigned)(p.num_states * blocks);
-    if (kStore) store_kernel<DnT, kType, E, V><<<grid, kThreads, 0, stream>>>(p, (int)blocks);
-    else load_kernel<DnT, kType, E, V><<<grid, kThreads, 0, stream>>>(p, (int)blocks);
-    return cudaGetLastError();
+    return enqueue(kStore ? store_kernel<DnT, kType, E, V> : load_kernel<DnT, kType, E, V>,
+                   dim3((unsigned)(p.num_states * blocks)), kThreads, stream, p, (int)blocks);
 }
 
 template <bool kStore, typename DnT, int kType, int V>

@@ -117,6 +117,7 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
     __shared__ __align__(16) uint32_t s_keys[kSr ? 20 : 1];
     __shared__ Pack<StT, V> s_raw[kAsync ? kDepth * kChunks * kStepThreads : 1];
 
+    await_previous();
     const int N = a.dstate, P = a.headdim, H = a.nheads;
     const int b = blockIdx.x, g = blockIdx.y, run = blockIdx.z;
     const int tid = threadIdx.x, lane = tid % L, grp = tid / L;
@@ -357,13 +358,9 @@ cudaError_t launch_step(const ssd_step_params &p, cudaStream_t stream) {
                 aligned_to(p.weight, 16) && aligned_to(p.state_scale, 16);
     if (p.ngroups > 65535 || runs > 65535) return cudaErrorInvalidConfiguration;
     const dim3 grid((unsigned)p.batch, (unsigned)p.ngroups, (unsigned)runs);
-    if constexpr (kType == SSD_F32 || kType == SSD_BF16) {
-        step_kernel<kType, L, E, V, kDepth, false><<<grid, kStepThreads, 0, stream>>>(p, plan);
-    } else {
-        if (p.sr_seed) step_kernel<kType, L, E, V, kDepth, true><<<grid, kStepThreads, 0, stream>>>(p, plan);
-        else step_kernel<kType, L, E, V, kDepth, false><<<grid, kStepThreads, 0, stream>>>(p, plan);
-    }
-    return cudaGetLastError();
+    if constexpr (kType != SSD_F32 && kType != SSD_BF16)
+        if (p.sr_seed) return enqueue(step_kernel<kType, L, E, V, kDepth, true>, grid, kStepThreads, stream, p, plan);
+    return enqueue(step_kernel<kType, L, E, V, kDepth, false>, grid, kStepThreads, stream, p, plan);
 }
 
 template <int kType, int L, int E>
