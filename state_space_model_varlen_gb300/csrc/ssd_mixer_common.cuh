@@ -142,9 +142,13 @@ template <int kType> constexpr float code_limit() { return kType == SSD_I8 ? 127
 // Four codes, packed low to high, as floats without their scale.
 template <int kType> __device__ __forceinline__ void decode4(uint32_t w, float *out) {
     if constexpr (kType == SSD_E4M3) {
-        const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
-        const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-        const float2 f0 = __half22float2(__half2(lo)), f1 = __half22float2(__half2(hi));
+        uint32_t lo, hi;
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}" : "=r"(lo), "=r"(hi) : "r"(w));
+        __half2 h0, h1;
+        memcpy(&h0, &lo, 4);
+        memcpy(&h1, &hi, 4);
+        const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
         out[0] = f0.x;
         out[1] = f0.y;
         out[2] = f1.x;
@@ -198,22 +202,32 @@ __device__ __forceinline__ void row_scale(float m, float limit, float *inv, floa
     }
 }
 
-// sr_f16 with the dropped bits as an integer where fp16 is normal: there
-// (|v| - |lo|) / spacing is the 13 dropped bits over 2^13.
+// sr_f16 with the dropped part as an integer: where fp16 is normal,
+// (|v| - |lo|) / spacing is the 13 dropped bits over 2^13; below, the fraction
+// of |v| in units of 2^-24.  From 2^16 on (and for what is not finite) the general form.
+static __device__ __noinline__ uint32_t sr_f16_large(float v, uint32_t r) { return __half_as_ushort(sr_f16(v, r)); }
 __device__ __forceinline__ __half sr_f16_fast(float v, uint32_t r) {
-    const uint32_t bits = __float_as_uint(v), a = bits & 0x7fffffffu;
-    if (a < 0x38800000u || a >= 0x47800000u) return sr_f16(v, r);       // below 2^-14, from 2^16 on, inf, NaN
-    const uint32_t h = ((a - 0x38000000u) >> 13) + ((a << 19) > r ? 1u : 0u);
-    return __ushort_as_half((unsigned short)(h | (bits >> 16 & 0x8000u)));
+    const uint32_t bits = __float_as_uint(v), a = bits & 0x7fffffffu, sign = bits >> 16 & 0x8000u;
+    uint32_t h = ((a - 0x38000000u) >> 13) + ((a << 19) > r ? 1u : 0u) | sign;
+    if (a < 0x38800000u) {                              // 2^-14
+        const float u = __uint_as_float(a) * 16777216.f;
+        const uint32_t lo = (uint32_t)u;
+        h = lo + (__float2uint_ru((u - (float)lo) * 4294967296.f) > r ? 1u : 0u) | sign;
+    } else if (a >= 0x47800000u) {
+        h = sr_f16_large(v, r);
+    }
+    return __ushort_as_half((unsigned short)h);
 }
 
 // ---- nearest ---------------------------------------------------------------
 template <int kType> __device__ __forceinline__ uint32_t encode4(const float *h, float inv) {
     if constexpr (kType == SSD_E4M3) {
         const float2 inv2 = make_float2(inv, inv);
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(mul2(make_float2(h[0], h[1]), inv2), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(mul2(make_float2(h[2], h[3]), inv2), __NV_SATFINITE, __NV_E4M3);
-        return __byte_perm(lo, hi, 0x5410);
+        const float2 v0 = mul2(make_float2(h[0], h[1]), inv2), v1 = mul2(make_float2(h[2], h[3]), inv2);
+        uint32_t w;
+        asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+            "mov.b32 %0, {l, h};\n\t}" : "=r"(w) : "f"(v0.x), "f"(v0.y), "f"(v1.x), "f"(v1.y));
+        return w;
     } else {
         // 1.5 2^23 + v, whose rounding is the rounding to an integer
         const float2 inv2 = make_float2(inv, inv), magic = make_float2(12582912.f, 12582912.f);
