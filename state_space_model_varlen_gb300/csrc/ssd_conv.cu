@@ -18,10 +18,12 @@
 // are few, load every tap from where it lies, two tokens at a time, which
 // leaves the shared memory to the inputs.
 //
-// The convolution cache is updated in place by other CTAs than those that
-// read it, unless one thread does both: the CTA whose tile holds a sequence's
-// first token, which reads the ring, also writes the sequence's last inputs to
-// it, afterwards, also where those lie in later tiles.
+// The convolution cache is updated in place, so one thread does all that a
+// sequence reads and writes of a channel's ring: the CTA whose tile holds the
+// sequence's first token.  It computes the sequence's first W - 1 tokens, the
+// only ones that need the ring, also where they pass the tile's end (the next
+// tile leaves them out), and afterwards writes the sequence's last inputs,
+// also where those lie in later tiles.
 #include "ssd_mixer_common.cuh"
 #include "ssd_mixer_internal.h"
 
@@ -30,11 +32,12 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kMaxTile = 64;       // tokens of a tile
+constexpr int kRecords = kMaxTile + SSD_CONV_MAX_WIDTH;       // and those after it that it may take over
 constexpr int kGroup = 8;          // tokens whose inputs are loaded together
 constexpr int kSlow = 2;           // tokens whose taps are loaded together at a boundary
 
 struct Token {
-    int local;      // token of its sequence, -1: no valid sequence
+    int local;      // token of its sequence, -1: none of this CTA's
     int row;        // its row of the ring
     int slot;       // -1: no cache
     int past;       // min(position, W - 1)
@@ -104,9 +107,10 @@ template <typename IoT, int V, int kW, bool kShort>
 __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(const ssd_conv_params a, int tile, int dt_column) {
     __shared__ Sequence sequence[kMaxTile];        // at the sequence's first token in the tile
     __shared__ uint32_t firsts[kMaxTile / 32];      // where there are any
-    __shared__ Token token[kMaxTile];
+    __shared__ Token token[kRecords];
     __shared__ uint8_t keep[kMaxTile];             // the token goes to the ring here
     __shared__ int group[kMaxTile / kGroup];
+    __shared__ int after;                          // tokens after the tile that are this CTA's
     __shared__ int64_t tail;                       // where that sequence ends, from the tile's first token; 0: none
     constexpr int kM = kW ? kW : SSD_CONV_MAX_WIDTH;
     constexpr int kPast = kW > 1 ? kW - 1 : 1;      // inputs a sliding window keeps
@@ -193,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
     // ---- the tile's tokens -------------------------------------------------
     if (threadIdx.x < kMaxTile / 32) firsts[threadIdx.x] = 0;
     if (threadIdx.x < kMaxTile / kGroup) group[threadIdx.x] = kW > 1 ? kSlides : 0;
-    if (threadIdx.x == 0) tail = 0;
+    if (threadIdx.x == 0) tail = after = 0;
     __syncthreads();
     for (int s = threadIdx.x; s < a.num_seqs; s += kThreads) {
         const Sequence q = s == (int)threadIdx.x ? seq : look_up(s);
@@ -210,31 +214,37 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
         }
     }
     __syncthreads();
-    if (threadIdx.x < kMaxTile) {
+    if (threadIdx.x < kRecords) {
         const int i = threadIdx.x;
-        // the last first token up to this one
-        uint32_t below = firsts[i / 32] & (0xffffffffu >> (31 - i % 32));
-        int first = below ? (i & ~31) + 31 - __clz(below) : -1;
-        for (int word = i / 32 - 1; first < 0 && word >= 0; --word)
+        // the last first token up to this one (a token after the tile: up to the tile's last)
+        const int to = min(i, nt - 1);
+        const uint32_t below = firsts[to / 32] & (0xffffffffu >> (31 - to % 32));
+        int first = below ? (to & ~31) + 31 - __clz(below) : -1;
+        for (int word = to / 32 - 1; first < 0 && word >= 0; --word)
             if (firsts[word]) first = word * 32 + 31 - __clz(firsts[word]);
         Token k = {-1, 0, -1, 0};
         bool kept = false;
-        if (i < nt && first >= 0 && sequence[first].end > t0 + i) {
+        if (first >= 0 && sequence[first].end > t0 + i) {
             const Sequence q = sequence[first];
             const int64_t local = t0 + i - q.begin, pos = q.start + local;
             const bool begins_here = q.begin >= t0;
-            k.local = (int)min(local, (int64_t)0x7fffffff);
-            k.slot = q.slot;
-            k.row = q.slot >= 0 ? (int)(pos % a.conv_rows) : 0;
-            k.past = (int)min(pos, (int64_t)(W - 1));
-            kept = q.slot >= 0 && begins_here && t0 + i >= q.end - (W - 1);
-            // the tile's last sequence goes on after it: its end is kept below
-            if (q.slot >= 0 && begins_here && i == nt - 1 && q.end > t0 + nt) tail = q.end - t0;
+            if (i < nt ? begins_here || local >= W - 1 : begins_here && local < W - 1) {
+                k.local = (int)min(local, (int64_t)0x7fffffff);
+                k.slot = q.slot;
+                k.row = q.slot >= 0 ? (int)(pos % a.conv_rows) : 0;
+                k.past = (int)min(pos, (int64_t)(W - 1));
+                kept = i < nt && q.slot >= 0 && begins_here && t0 + i >= q.end - (W - 1);
+                // the tile's last sequence goes on after it: its end is kept below
+                if (q.slot >= 0 && begins_here && i == nt - 1 && q.end > t0 + nt) tail = q.end - t0;
+                if (i >= nt) atomicMax(&after, i + 1 - nt);
+            }
         }
-        token[threadIdx.x] = k;
-        keep[threadIdx.x] = kept;
-        if (k.local < W - 1) atomicAnd(&group[threadIdx.x / kGroup], ~kSlides);
-        if (kept) atomicOr(&group[threadIdx.x / kGroup], kKeeps);
+        token[i] = k;
+        if (i < kMaxTile) {
+            keep[i] = kept;
+            if (k.local < W - 1) atomicAnd(&group[i / kGroup], ~kSlides);
+            if (kept) atomicOr(&group[i / kGroup], kKeeps);
+        }
     }
     __syncthreads();
     if (!mine) {
@@ -266,10 +276,10 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
         for (int k = 0; k < kM; ++k)
             (j & 1 ? w[k][j / 2].y : w[k][j / 2].x) = to_float(pw.v[j * kM + kM - 1 - k]);
     }
-    // the group of tokens i0 .., every tap from where it lies
-    auto boundary = [&](int i0) {
+    // the tokens from .. to - 1, every tap from where it lies
+    auto boundary = [&](int from, int to) {
 #pragma unroll 1
-        for (int s0 = i0; s0 < min(i0 + kGroup, nt); s0 += kSlow) {
+        for (int s0 = from; s0 < to; s0 += kSlow) {
             Pack<IoT, V> tap[kSlow][kM];
 #pragma unroll
             for (int i = 0; i < kSlow; ++i) {
@@ -277,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
 #pragma unroll
                 for (int m = 0; m < kM; ++m) {
                     tap[i][m] = Pack<IoT, V>{};
-                    if (m >= W || k.local < 0) continue;
+                    if (m >= W || k.local < 0 || s0 + i >= to) continue;
                     const IoT *src = nullptr;
                     if (m <= k.local) {
                         src = x + (int64_t)(s0 + i - m) * a.xbc_stride;
@@ -291,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
             }
 #pragma unroll
             for (int i = 0; i < kSlow; ++i) {
-                if (token[s0 + i].local < 0) continue;
+                if (token[s0 + i].local < 0 || s0 + i >= to) continue;
                 float2 acc[kPairs];
 #pragma unroll
                 for (int j = 0; j < kPairs; ++j) acc[j] = bias[j];
@@ -350,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
                         for (int j = 0; j < kPairs; ++j) g[j] = win[m - 1][j];
                     });
             } else if constexpr (!kShort) {
-                boundary(i0);
+                boundary(i0, min(i0 + kGroup, nt));
 #pragma unroll
                 for (int m = 0; m < kPast; ++m) widen<IoT, V>(now[kGroup - 1 - m], win[m]);
             } else {
@@ -405,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
                 stage = stage + 1 == kDepth ? 0 : stage + 1;
             }
         }
-        if constexpr (kW <= 1) boundary(i0);
+        if constexpr (kW <= 1) boundary(i0, min(i0 + kGroup, nt));
         if (kW <= 1 && (what & kKeeps)) {
             for (int i = i0; i < min(i0 + kGroup, nt); ++i) {
                 if (!keep[i]) continue;
@@ -417,6 +427,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
     }
 
     if constexpr (kAsync) wait_async<0>();
+    boundary(nt, nt + after);
     // the end of the sequence that begins in this tile and passes it
     const int64_t e = tail;
     if (e > 0) {

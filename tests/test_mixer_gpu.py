@@ -147,6 +147,40 @@ def test_conv_in_pieces_is_the_whole(cuts):
     assert torch.equal(ring[q][last], whole["ring"][q][last])
 
 
+@pytest.mark.parametrize("W", [4, 7])
+def test_conv_ring_in_place_where_sequences_begin_at_a_tiles_end(W):
+    """Sequences of 12 tokens with W or 12 ring rows, so that the rows a sequence writes last are among those its first
+    tokens read, beginning at every distance (mod 4) from a tile's end, in more CTAs than run at a time."""
+    lens, C = [7] + [12] * 900, 10_240
+    c = _conv_case(lens, C - 512, 256, W, "bf16", seed=W, start=lambda s: 5 + s, rows=12 if W == 7 else 4)
+    keep, st = _conv_run(c)
+    assert st == 0
+    at = np.unique(np.concatenate([np.arange(3, C, 128), np.arange(C - 3, C)]))
+    want, err, ring = R.conv(_np(c["xbc"])[:, at], _np(c["w"])[at], _np(c["bias"])[at], True, c["cu"],
+                             c["start"].cpu().numpy(), c["slot"].cpu().numpy(), _np(keep)[:, :, at])
+    R.check(_np(_torch().cat(c["out"], 1))[:, at], want, err, "bf16", "convolution")
+    np.testing.assert_array_equal(_np(c["ring"])[:, :, at], ring)
+
+
+@pytest.mark.parametrize("n", [1, 2, 7, 8, 9, 23, 24, 25, 40, 56, 63, 64, 65])
+def test_conv_sequences_across_tile_ends(n):
+    """A sequence that begins n tokens into the batch, whatever the tile, and others of one to five tokens after it."""
+    c = _conv_case([n, 9, 1, 2, 3, 4, 5, 30], 64, 16, 4, "bf16", seed=n, start=lambda s: 3 * s)
+    keep, st = _conv_run(c)
+    assert st == 0
+    _conv_check(c, keep, "bf16")
+
+
+def test_conv_fresh_sequences_do_not_read_the_ring():
+    c = _conv_case([1, 3, 40, 2], 64, 16, 4, "bf16", start=lambda s: 0)
+    c["ring"].fill_(float("nan"))
+    keep, st = _conv_run(c)
+    got = np.concatenate([_np(o) for o in c["out"]], 1)
+    want, err, _ = R.conv(_np(c["xbc"]), _np(c["w"]), _np(c["bias"]), True, c["cu"], None, None, None)
+    assert st == 0
+    R.check(got, want, err, "bf16", "convolution")
+
+
 def test_conv_bad_metadata_is_reported_and_skipped():
     torch = _torch()
     for what, flag in (("cu", binding.SSD_DEV_BAD_SEQLENS), ("slot", binding.SSD_DEV_BAD_SLOT),
