@@ -34,7 +34,7 @@ struct StepPlan {
     int rows_g;        // rows of a group
     int rows;          // rows of a CTA, a multiple of 32
     int channels;
-    int vec4;          // four channels and four rows make aligned vectors, width 4
+    int vec4;          // four channels and four rows make aligned vectors, and the width is 2, 3 or 4
     uint32_t p_mul;    // x / P = x p_mul >> p_shift for 0 <= x < 2^31
     int p_shift;
 };
@@ -66,15 +66,15 @@ __device__ __forceinline__ float conv_channel(const ssd_step_params &a, const Io
     return a.activation ? silu(acc) : acc;
 }
 
-// Four neighbouring channels, width 4, all loads issued together.
-template <typename IoT>
+// Four neighbouring channels, all loads issued together.
+template <typename IoT, int kW>
 __device__ __forceinline__ float4 conv_channels4(const ssd_step_params &a, const IoT *xbc, IoT *ring, int channels,
                                                  int c, int pos, int row, bool keep) {
-    const Pack<IoT, 16> w = load_pack<IoT, 16>(static_cast<const IoT *>(a.weight) + (int64_t)c * 4);
-    Pack<IoT, 4> in[4], bias{};
+    const Pack<IoT, 4 * kW> w = load_pack<IoT, 4 * kW>(static_cast<const IoT *>(a.weight) + (int64_t)c * kW);
+    Pack<IoT, 4> in[kW], bias{};
     in[0] = load_pack<IoT, 4>(xbc + c);
 #pragma unroll
-    for (int k = 1; k < 4; ++k) {
+    for (int k = 1; k < kW; ++k) {
         int r = row - k;
         if (r < 0) r += a.conv_rows;
         in[k] = Pack<IoT, 4>{};
@@ -86,7 +86,7 @@ __device__ __forceinline__ float4 conv_channels4(const ssd_step_params &a, const
     for (int j = 0; j < 4; ++j) {
         float acc = to_float(bias.v[j]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) acc = fmaf(to_float(w.v[4 * j + 3 - k]), to_float(in[k].v[j]), acc);
+        for (int k = 0; k < kW; ++k) acc = fmaf(to_float(w.v[kW * j + kW - 1 - k]), to_float(in[k].v[j]), acc);
         u[j] = a.activation ? silu(acc) : acc;
     }
     if (keep) store_pack<IoT, 4>(ring + (int64_t)row * channels + c, in[0]);
@@ -172,19 +172,24 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
         const IoT *xbc = static_cast<const IoT *>(a.xbc) + (int64_t)b * a.xbc_stride;
         IoT *ring = static_cast<IoT *>(a.conv_cache) + (int64_t)slot * a.conv_rows * channels;
         auto head_of = [&](int row) { return (int)((uint64_t)(uint32_t)row * plan.p_mul >> plan.p_shift); };
+        auto four = [&](int c, bool keep) {
+            if (a.width == 4) return conv_channels4<IoT, 4>(a, xbc, ring, channels, c, pos, ring_row, keep);
+            if (a.width == 3) return conv_channels4<IoT, 3>(a, xbc, ring, channels, c, pos, ring_row, keep);
+            return conv_channels4<IoT, 2>(a, xbc, ring, channels, c, pos, ring_row, keep);
+        };
         if (plan.vec4) {
             for (int i = 4 * tid; i < 2 * N + rows; i += 4 * kStepThreads) {
                 if (i < 2 * N) {
                     const int c = i < N ? cb + i : cc + i - N;
                     *reinterpret_cast<float4 *>(i < N ? s_b + i : s_c + i - N) =
-                        conv_channels4<IoT>(a, xbc, ring, channels, c, pos, ring_row, run == 0);
+                        four(c, run == 0);
                 } else {
                     const int r = i - 2 * N, h = head_of(r0 + r);
                     float4 sc = make_float4(1.f, 1.f, 1.f, 1.f);
                     if (k8bit) sc = *reinterpret_cast<const float4 *>(a.state_scale + row0 + r);
                     const float2 ht = head_terms<IoT>(a, b, h);
                     const float dh = a.D ? a.D[h] : 0.f;
-                    const float4 x = conv_channels4<IoT>(a, xbc, ring, channels, r0 + r, pos, ring_row, true);
+                    const float4 x = four(r0 + r, true);
                     const float dt = ht.x, keep = pos > 0 ? ht.y : 0.f;
                     if (pos == 0) sc = make_float4(0.f, 0.f, 0.f, 0.f);
                     *reinterpret_cast<float4 *>(s_dx + r) = make_float4(dt * x.x, dt * x.y, dt * x.z, dt * x.w);
@@ -353,7 +358,7 @@ cudaError_t launch_step(const ssd_step_params &p, cudaStream_t stream) {
     }
     const int runs = (rows_g + plan.rows - 1) / plan.rows;
     const int io = p.io_dtype == SSD_F32 ? 4 : 2, vec = 4 * io;
-    plan.vec4 = p.width == 4 && p.dstate % 4 == 0 && p.headdim % 4 == 0 && p.xbc_stride % 4 == 0 &&
+    plan.vec4 = p.width >= 2 && p.width <= 4 && p.dstate % 4 == 0 && p.headdim % 4 == 0 && p.xbc_stride % 4 == 0 &&
                 aligned_to(p.xbc, vec) && aligned_to(p.conv_cache, vec) && aligned_to(p.bias, vec) &&
                 aligned_to(p.weight, 16) && aligned_to(p.state_scale, 16);
     if (p.ngroups > 65535 || runs > 65535) return cudaErrorInvalidConfiguration;
