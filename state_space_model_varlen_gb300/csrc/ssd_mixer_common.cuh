@@ -69,10 +69,15 @@ __device__ __forceinline__ float rcp_approx(float v) {
 }
 __device__ __forceinline__ float silu(float v) { return v * rcp_approx(1.f + ex2_approx(v * -1.4426950408889634f)); }
 
+// v / (1 + e^-v), each operation rounded by itself
+__device__ __forceinline__ float silu_stepwise(float v) { return __fdiv_rn(v, __fadd_rn(1.f, expf(-v))); }
+
 // softplus(z) = log(1 + e^z) in the overflow-safe form max(z,0) + log1p(e^-|z|)
 __device__ __forceinline__ float softplus(float z) { return fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))); }
 
-// Two fp32 operations in one instruction, each rounded as by itself.
+// Two fp32 operations in one instruction.  (ptxas merges a packed product and a
+// packed sum into one fused operation; where the product's own rounding
+// matters, the sum is two scalar __fadd_rn.)
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     uint64_t r, x, y, z;
     memcpy(&x, &a, 8);
@@ -230,10 +235,10 @@ template <int kType> __device__ __forceinline__ uint32_t encode4(const float *h,
         return w;
     } else {
         // 1.5 2^23 + v, whose rounding is the rounding to an integer
-        const float2 inv2 = make_float2(inv, inv), magic = make_float2(12582912.f, 12582912.f);
-        const float2 lo = add2(mul2(make_float2(h[0], h[1]), inv2), magic);
-        const float2 hi = add2(mul2(make_float2(h[2], h[3]), inv2), magic);
-        const uint32_t t[4] = {__float_as_uint(lo.x), __float_as_uint(lo.y), __float_as_uint(hi.x), __float_as_uint(hi.y)};
+        const float2 inv2 = make_float2(inv, inv);
+        const float2 lo = mul2(make_float2(h[0], h[1]), inv2), hi = mul2(make_float2(h[2], h[3]), inv2);
+        const uint32_t t[4] = {__float_as_uint(__fadd_rn(lo.x, 12582912.f)), __float_as_uint(__fadd_rn(lo.y, 12582912.f)),
+                               __float_as_uint(__fadd_rn(hi.x, 12582912.f)), __float_as_uint(__fadd_rn(hi.y, 12582912.f))};
         return __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
     }
 }

@@ -19,6 +19,12 @@
 // The convolution cache is a ring, so the row the call writes (pos mod rows)
 // is none of those its other CTAs read, and they need no order among them.
 // Every CTA convolves its group's B and C for itself (from L2).
+//
+// With fp32 activations and a cache below fp32, everything that leads to the
+// stored state is rounded operation by operation, sums from the oldest tap on:
+// a plain fp32 program then stores the same bits.  (A stored value that is
+// rounded the other way is off by 2^-4 to 2^-9 of itself, which fp32 outputs of
+// later steps would show.)  With bf16 activations products and sums are fused.
 #pragma once
 
 #include "ssd_mixer_common.cuh"
@@ -48,22 +54,32 @@ inline void set_divisor(StepPlan &plan, int P) {
     plan.p_shift = 31 + s;
 }
 
+// acc + w x, fused or (fp32 activations) operation by operation
+template <typename IoT> __device__ __forceinline__ float tap(float acc, float w, float x) {
+    return sizeof(IoT) == 4 ? __fadd_rn(acc, __fmul_rn(w, x)) : fmaf(w, x, acc);
+}
+template <typename IoT> __device__ __forceinline__ float convolved(float acc, float bias, int activation) {
+    acc = __fadd_rn(acc, bias);
+    if (!activation) return acc;
+    return sizeof(IoT) == 4 ? silu_stepwise(acc) : silu(acc);
+}
+
 // One channel's convolution at position pos.
 template <typename IoT>
 __device__ __forceinline__ float conv_channel(const ssd_step_params &a, const IoT *xbc, const IoT *ring, int channels,
                                               int c, int pos, int row) {
     const IoT *w = static_cast<const IoT *>(a.weight) + (int64_t)c * a.width;
-    float acc = a.bias ? to_float(static_cast<const IoT *>(a.bias)[c]) : 0.f;
-    acc = fmaf(to_float(w[a.width - 1]), to_float(xbc[c]), acc);
+    float acc = 0.f;
 #pragma unroll
-    for (int k = 1; k < SSD_CONV_MAX_WIDTH; ++k) {
+    for (int k = SSD_CONV_MAX_WIDTH - 1; k > 0; --k) {
         if (k < a.width && k <= pos) {
             int r = row - k;
             if (r < 0) r += a.conv_rows;
-            acc = fmaf(to_float(w[a.width - 1 - k]), to_float(ring[(int64_t)r * channels + c]), acc);
+            acc = tap<IoT>(acc, to_float(w[a.width - 1 - k]), to_float(ring[(int64_t)r * channels + c]));
         }
     }
-    return a.activation ? silu(acc) : acc;
+    acc = tap<IoT>(acc, to_float(w[a.width - 1]), to_float(xbc[c]));
+    return convolved<IoT>(acc, a.bias ? to_float(static_cast<const IoT *>(a.bias)[c]) : 0.f, a.activation);
 }
 
 // Four neighbouring channels, all loads issued together.
@@ -84,10 +100,10 @@ __device__ __forceinline__ float4 conv_channels4(const ssd_step_params &a, const
     float u[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        float acc = to_float(bias.v[j]);
+        float acc = 0.f;
 #pragma unroll
-        for (int k = 0; k < kW; ++k) acc = fmaf(to_float(w.v[kW * j + kW - 1 - k]), to_float(in[k].v[j]), acc);
-        u[j] = a.activation ? silu(acc) : acc;
+        for (int k = kW - 1; k >= 0; --k) acc = tap<IoT>(acc, to_float(w.v[kW * j + kW - 1 - k]), to_float(in[k].v[j]));
+        u[j] = convolved<IoT>(acc, to_float(bias.v[j]), a.activation);
     }
     if (keep) store_pack<IoT, 4>(ring + (int64_t)row * channels + c, in[0]);
     return make_float4(u[0], u[1], u[2], u[3]);
@@ -99,7 +115,7 @@ __device__ __forceinline__ float2 head_terms(const ssd_step_params &a, int b, in
     float dt = to_float(static_cast<const IoT *>(a.dt)[(int64_t)b * a.dt_stride + h]);
     if (a.dt_bias) dt += a.dt_bias[h];
     if (a.dt_softplus) dt = softplus(dt);
-    return make_float2(dt, expf(dt * a.A[h]));
+    return make_float2(dt, expf(__fmul_rn(dt, a.A[h])));
 }
 
 // kType: storage of the state; L: lanes of a row; E: state values a lane holds
@@ -111,9 +127,9 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
     constexpr int kChunks = E / V, kStepGroups = kStepThreads / L;     // rows worked on at a time
     constexpr bool k8bit = kType == SSD_E4M3 || kType == SSD_I8;
     constexpr bool kAsync = V * sizeof(StT) >= 4;       // narrower shares are loaded when they are needed
-    // of each row: D x, later y; dt' x; the decay, times its scale
+    // of each row: D x, later y; dt' x; the decay, times its scale where that is fused
     __shared__ __align__(16) float s_b[L * E], s_c[L * E], s_y[kStepMaxRows], s_dx[kStepMaxRows], s_keep[kStepMaxRows];
-    __shared__ float s_scale[k8bit ? kStepMaxRows : 1];
+    __shared__ __align__(16) float s_scale[k8bit ? kStepMaxRows : 4];       // of each row: the old scale, then the new one
     __shared__ __align__(16) uint32_t s_keys[kSr ? 20 : 1];
     __shared__ Pack<StT, V> s_raw[kAsync ? kDepth * kChunks * kStepThreads : 1];
 
@@ -124,6 +140,7 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
     const int r0 = g * plan.rows_g + run * plan.rows;        // the CTA's rows of the request: r0 .. r0 + rows - 1
     const int rows = min(plan.rows, plan.rows_g - run * plan.rows);
     const bool bf16 = a.io_dtype == SSD_BF16;
+    const bool stepwise = kType != SSD_F32 && !bf16;
 
     const int slot = a.slot_idx[(int64_t)b * (a.slot_idx_stride ? a.slot_idx_stride : 1)];
     const int pos = a.pos[b];
@@ -192,6 +209,10 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
                     const float4 x = four(r0 + r, true);
                     const float dt = ht.x, keep = pos > 0 ? ht.y : 0.f;
                     if (pos == 0) sc = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (k8bit && stepwise) {
+                        *reinterpret_cast<float4 *>(s_scale + r) = sc;
+                        sc = make_float4(1.f, 1.f, 1.f, 1.f);
+                    }
                     *reinterpret_cast<float4 *>(s_dx + r) = make_float4(dt * x.x, dt * x.y, dt * x.z, dt * x.w);
                     *reinterpret_cast<float4 *>(s_y + r) = make_float4(dh * x.x, dh * x.y, dh * x.z, dh * x.w);
                     *reinterpret_cast<float4 *>(s_keep + r) =
@@ -210,7 +231,9 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
                     const float2 ht = head_terms<IoT>(a, b, h);
                     s_dx[r] = ht.x * u;
                     s_y[r] = a.D ? a.D[h] * u : 0.f;
-                    s_keep[r] = pos > 0 ? (k8bit ? ht.y * a.state_scale[row0 + r] : ht.y) : 0.f;
+                    const float sc = k8bit && pos > 0 ? a.state_scale[row0 + r] : 1.f, keep = pos > 0 ? ht.y : 0.f;
+                    if (k8bit) s_scale[r] = sc;
+                    s_keep[r] = k8bit && !stepwise ? keep * sc : keep;
                 }
             }
         }
@@ -252,7 +275,17 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
             if constexpr (kAsync) now = s_raw[(stage * kChunks + k) * kStepThreads + tid];
             else if (live && pos > 0) now = load_pack<StT, V>(dst + k * L * V);
             decode<kType, V>(now, st + k * V);
-            if constexpr (V == 1) {
+            if (stepwise) {
+                const float sc = k8bit ? s_scale[r] : 1.f;
+#pragma unroll
+                for (int e = k * V; e < (k + 1) * V; ++e) {
+                    const float b = e & 1 ? bv[e / 2].y : bv[e / 2].x, c = e & 1 ? cv[e / 2].y : cv[e / 2].x;
+                    if (k8bit) st[e] = __fmul_rn(st[e], sc);
+                    st[e] = __fadd_rn(__fmul_rn(keep, st[e]), __fmul_rn(dx, b));
+                    acc.x = fmaf(c, st[e], acc.x);
+                    if (k8bit) big = max_abs(big, st[e], st[e]);
+                }
+            } else if constexpr (V == 1) {
                 st[k] = fmaf(keep, st[k], dx * (k & 1 ? bv[k / 2].y : bv[k / 2].x));
                 acc.x = fmaf(k & 1 ? cv[k / 2].y : cv[k / 2].x, st[k], acc.x);
                 if (k8bit) big = max_abs(big, st[k], st[k]);
@@ -274,7 +307,9 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
         if (lane == 0 && live) s_y[r] += sum;
         float inv = 0.f, sc = 0.f;
         if constexpr (k8bit) {
-            row_scale<false>(lanes_max<L>(big), code_limit<kType>(), &inv, &sc);
+            const float most = lanes_max<L>(big);
+            if (stepwise) row_scale<true>(most, code_limit<kType>(), &inv, &sc);
+            else row_scale<false>(most, code_limit<kType>(), &inv, &sc);
             if (lane == 0 && live) s_scale[r] = sc;
         }
 #pragma unroll

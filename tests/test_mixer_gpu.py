@@ -371,6 +371,44 @@ def test_step_stochastic_rounding(H, P, N, kind):
     _step_check(c, before)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f16", "e4m3", "i8"])
+@pytest.mark.parametrize("B,H,P,N,G,W", [(6, 4, 64, 128, 2, 4), (5, 3, 50, 100, 1, 2), (4, 2, 7, 37, 1, 4)])
+def test_step_fp32_activations_store_the_bits_of_a_plain_program(B, H, P, N, G, W, kind):
+    """fp32 activations, a narrower cache: every operation rounds by itself, so elementwise torch operations in the
+    formula's order (taps summed from the oldest, bias last) give the stored states bit for bit, step after step."""
+    torch = _torch()
+    c = _step_case(B, H, P, N, G, W, "f32", kind, seed=21)
+    c["A"] = -torch.rand(H, device="cuda") - 0.5
+    lim = R.LIM.get(kind)
+    for _ in range(3):
+        q, pos = c["slot"].long(), c["pos"].long()
+        u = torch.zeros_like(c["xbc"])
+        for k in range(W - 1, -1, -1):
+            x = c["xbc"] if k == 0 else c["ring"][q, (pos - k) % W] * (pos >= k)[:, None]
+            u = u + c["w"][:, W - 1 - k] * x
+        u = u + c["bias"]
+        u = u / (1.0 + torch.exp(-u))
+        x = u[:, :H * P].view(B, H, P)
+        Bm = u[:, H * P:H * P + G * N].view(B, G, N).repeat_interleave(H // G, 1)
+        dt = c["dt"] + c["dt_bias"]
+        dt = dt.clamp(min=0) + torch.log1p(torch.exp(-dt.abs()))
+        h = c["state"].view(torch.uint8)[q].view(_t(kind)).float()
+        if lim:
+            h = h * c["scale"][q][..., None]
+        h = torch.where((pos > 0)[:, None, None, None], h, 0.0)
+        h = torch.exp(dt * c["A"])[..., None, None] * h + (dt[..., None] * x)[..., None] * Bm[:, :, None]
+        if lim:
+            m = h.abs().amax(-1)
+            v = h * (torch.reciprocal(m) * lim)[..., None]
+            want = v.to(torch.float8_e4m3fn) if kind == "e4m3" else torch.round(v).to(torch.int8)
+        else:
+            want = h.to(_t(kind))
+        _step_run(c)
+        got = c["state"].view(torch.uint8)[q].view(_t(kind))
+        assert np.array_equal(_bits(got), _bits(want))
+        c["pos"] += 1
+
+
 def test_step_padding_and_bad_requests():
     torch = _torch()
     for kind in ("f32", "e4m3"):
