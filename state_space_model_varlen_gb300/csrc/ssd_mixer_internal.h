@@ -41,10 +41,10 @@ cudaError_t enqueue(void (*kernel)(Params...), dim3 grid, int threads, cudaStrea
 inline bool aligned_to(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) % bytes) == 0; }
 
 // The widest vector of a state row, in elements of `size` bytes: 16 bytes
-// where the row's bytes and the base allow it, then 8, then 4 elements, then 1.
+// where the row's bytes and the base allow it, then 4 elements, then 1.
 // `lanes` lanes share a row, so rows of fewer vectors take narrower ones.
 inline int state_vector(int n, int size, const void *base, int lanes) {
-    for (int v : {16 / size, 8 / size, 4})
+    for (int v : {16 / size, 4})
         if (v >= 4 && n % v == 0 && (n / v >= lanes || v == 4) && aligned_to(base, (size_t)v * size)) return v;
     return 1;
 }

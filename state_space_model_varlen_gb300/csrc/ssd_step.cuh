@@ -120,8 +120,8 @@ __device__ __forceinline__ float2 head_terms(const ssd_step_params &a, int b, in
 
 // kType: storage of the state; L: lanes of a row; E: state values a lane holds
 // of it (L E >= N); V: values of one copy; kDepth: row steps copied ahead; kSr:
-// stochastic rounding.
-template <int kType, int L, int E, int V, int kDepth, bool kSr>
+// stochastic rounding; stepwise: see above.
+template <int kType, int L, int E, int V, int kDepth, bool kSr, bool stepwise>
 __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(const ssd_step_params a, const StepPlan plan) {
     using StT = typename Stored<kType>::T;
     constexpr int kChunks = E / V, kStepGroups = kStepThreads / L;     // rows worked on at a time
@@ -139,8 +139,7 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
     const int tid = threadIdx.x, lane = tid % L, grp = tid / L;
     const int r0 = g * plan.rows_g + run * plan.rows;        // the CTA's rows of the request: r0 .. r0 + rows - 1
     const int rows = min(plan.rows, plan.rows_g - run * plan.rows);
-    const bool bf16 = a.io_dtype == SSD_BF16;
-    const bool stepwise = kType != SSD_F32 && !bf16;
+    const bool bf16 = kType == SSD_F32 ? a.io_dtype == SSD_BF16 : !stepwise;
 
     const int slot = a.slot_idx[(int64_t)b * (a.slot_idx_stride ? a.slot_idx_stride : 1)];
     const int pos = a.pos[b];
@@ -240,8 +239,10 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
     };
     if (kSr && tid < 20) round_keys(*a.sr_seed, tid, s_keys);
     for (int i = N + tid; i < L * E; i += kStepThreads) s_b[i] = s_c[i] = 0.f;
-    if (bf16) convolve(__nv_bfloat16{});
-    else convolve(float{});
+    if constexpr (kType == SSD_F32 || !stepwise)
+        if (bf16) convolve(__nv_bfloat16{});
+    if constexpr (kType == SSD_F32 || stepwise)
+        if (!bf16) convolve(float{});
     __syncthreads();
 
     // ---- update and read-out -----------------------------------------------
@@ -275,15 +276,23 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
             if constexpr (kAsync) now = s_raw[(stage * kChunks + k) * kStepThreads + tid];
             else if (live && pos > 0) now = load_pack<StT, V>(dst + k * L * V);
             decode<kType, V>(now, st + k * V);
-            if (stepwise) {
+            if constexpr (stepwise && V == 1) {
+                if (k8bit) st[k] = __fmul_rn(st[k], s_scale[r]);
+                st[k] = __fadd_rn(__fmul_rn(keep, st[k]), __fmul_rn(dx, k & 1 ? bv[k / 2].y : bv[k / 2].x));
+                acc.x = fmaf(k & 1 ? cv[k / 2].y : cv[k / 2].x, st[k], acc.x);
+                if (k8bit) big = max_abs(big, st[k], st[k]);
+            } else if constexpr (stepwise) {
                 const float sc = k8bit ? s_scale[r] : 1.f;
 #pragma unroll
-                for (int e = k * V; e < (k + 1) * V; ++e) {
-                    const float b = e & 1 ? bv[e / 2].y : bv[e / 2].x, c = e & 1 ? cv[e / 2].y : cv[e / 2].x;
-                    if (k8bit) st[e] = __fmul_rn(st[e], sc);
-                    st[e] = __fadd_rn(__fmul_rn(keep, st[e]), __fmul_rn(dx, b));
-                    acc.x = fmaf(c, st[e], acc.x);
-                    if (k8bit) big = max_abs(big, st[e], st[e]);
+                for (int e = k * V; e < (k + 1) * V; e += 2) {
+                    float2 s = make_float2(st[e], st[e + 1]);
+                    if (k8bit) s = mul2(s, make_float2(sc, sc));
+                    const float2 old = mul2(keep2, s), add = mul2(dx2, bv[e / 2]);
+                    s = make_float2(__fadd_rn(old.x, add.x), __fadd_rn(old.y, add.y));
+                    acc = fma2(cv[e / 2], s, acc);
+                    st[e] = s.x;
+                    st[e + 1] = s.y;
+                    if (k8bit) big = max_abs(big, s.x, s.y);
                 }
             } else if constexpr (V == 1) {
                 st[k] = fmaf(keep, st[k], dx * (k & 1 ? bv[k / 2].y : bv[k / 2].x));
@@ -308,8 +317,7 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
         float inv = 0.f, sc = 0.f;
         if constexpr (k8bit) {
             const float most = lanes_max<L>(big);
-            if (stepwise) row_scale<true>(most, code_limit<kType>(), &inv, &sc);
-            else row_scale<false>(most, code_limit<kType>(), &inv, &sc);
+            row_scale<stepwise>(most, code_limit<kType>(), &inv, &sc);
             if (lane == 0 && live) s_scale[r] = sc;
         }
 #pragma unroll
@@ -398,9 +406,16 @@ cudaError_t launch_step(const ssd_step_params &p, cudaStream_t stream) {
                 aligned_to(p.weight, 16) && aligned_to(p.state_scale, 16);
     if (p.ngroups > 65535 || runs > 65535) return cudaErrorInvalidConfiguration;
     const dim3 grid((unsigned)p.batch, (unsigned)p.ngroups, (unsigned)runs);
+    auto run = [&](auto kernel) { return enqueue(kernel, grid, kStepThreads, stream, p, plan); };
+    const bool f32 = p.io_dtype == SSD_F32;
+    if constexpr (kType == SSD_F32) return run(step_kernel<kType, L, E, V, kDepth, false, false>);
     if constexpr (kType != SSD_F32 && kType != SSD_BF16)
-        if (p.sr_seed) return enqueue(step_kernel<kType, L, E, V, kDepth, true>, grid, kStepThreads, stream, p, plan);
-    return enqueue(step_kernel<kType, L, E, V, kDepth, false>, grid, kStepThreads, stream, p, plan);
+        if (p.sr_seed)
+            return f32 ? run(step_kernel<kType, L, E, V, kDepth, true, true>)
+                       : run(step_kernel<kType, L, E, V, kDepth, true, false>);
+    if constexpr (kType != SSD_F32)
+        return f32 ? run(step_kernel<kType, L, E, V, kDepth, false, true>)
+                   : run(step_kernel<kType, L, E, V, kDepth, false, false>);
 }
 
 template <int kType, int L, int E>
@@ -408,7 +423,6 @@ cudaError_t launch_step_vec(const ssd_step_params &p, cudaStream_t stream) {
     constexpr int size = (int)sizeof(typename Stored<kType>::T);
     const int v = state_vector(p.dstate, size, p.state_cache, L);
     if constexpr (16 / size <= E) if (v == 16 / size) return launch_step<kType, L, E, 16 / size>(p, stream);
-    if constexpr (8 / size >= 4 && 8 / size <= E) if (v == 8 / size) return launch_step<kType, L, E, 8 / size>(p, stream);
     if constexpr (4 <= E) if (v == 4) return launch_step<kType, L, E, 4>(p, stream);
     return launch_step<kType, L, E, 1>(p, stream);
 }
