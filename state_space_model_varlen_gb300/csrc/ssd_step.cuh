@@ -36,6 +36,10 @@ namespace {
 constexpr int kStepThreads = 128;
 constexpr int kStepMaxRows = 512;                  // of one CTA
 
+// CTAs of an SM that the registers leave room for
+template <int kType, int E>
+constexpr int kStepCtas = E == 32 ? 4 : kType == SSD_E4M3 || kType == SSD_I8 ? 5 : 6;
+
 struct StepPlan {
     int rows_g;        // rows of a group
     int rows;          // rows of a CTA, a multiple of 32
@@ -122,7 +126,7 @@ __device__ __forceinline__ float2 head_terms(const ssd_step_params &a, int b, in
 // of it (L E >= N); V: values of one copy; kDepth: row steps copied ahead; kSr:
 // stochastic rounding; stepwise: see above.
 template <int kType, int L, int E, int V, int kDepth, bool kSr, bool stepwise>
-__global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(const ssd_step_params a, const StepPlan plan) {
+__global__ void __launch_bounds__(kStepThreads, kStepCtas<kType, E>) step_kernel(const ssd_step_params a, const StepPlan plan) {
     using StT = typename Stored<kType>::T;
     constexpr int kChunks = E / V, kStepGroups = kStepThreads / L;     // rows worked on at a time
     constexpr bool k8bit = kType == SSD_E4M3 || kType == SSD_I8;
@@ -377,9 +381,9 @@ __global__ void __launch_bounds__(kStepThreads, E == 32 ? 4 : 6) step_kernel(con
 template <int kType, int L, int E, int V>
 cudaError_t launch_step(const ssd_step_params &p, cudaStream_t stream) {
     constexpr int size = (int)sizeof(typename Stored<kType>::T);
-    // steps in flight: 24 KB of a CTA's states (12 KB of 8-bit ones, whose CTAs
-    // compute longer on them: 109 us so, 114 with 24 KB), at least two, at most six
-    constexpr int kFit = (size == 1 ? 12288 : 24576) / (kStepThreads * E * size);
+    // steps in flight: 24 KB of a CTA's states (8 KB of 8-bit ones, whose CTAs
+    // compute longer on them), at least two, at most six
+    constexpr int kFit = (size == 1 ? 8192 : 24576) / (kStepThreads * E * size);
     constexpr int kDepth = kFit < 2 ? 2 : kFit > 6 ? 6 : kFit;
     StepPlan plan;
     const int rows_g = plan.rows_g = p.nheads / p.ngroups * p.headdim;
@@ -388,7 +392,7 @@ cudaError_t launch_step(const ssd_step_params &p, cudaStream_t stream) {
     // the run whose waves of CTAs take the least, a CTA's own start counted as 64
     // rows: long runs share the convolution of B and C, short ones fill the GPU
     constexpr int kMinRows = kStepThreads / L < 32 ? 32 : kStepThreads / L;
-    const int64_t resident = 152 * (E == 32 ? 4 : 6);
+    const int64_t resident = 152 * kStepCtas<kType, E>;
     int64_t least = INT64_MAX;
     for (int rows = kMinRows; rows <= kStepMaxRows; rows += 32) {
         const int64_t ctas = (int64_t)((rows_g + rows - 1) / rows) * p.ngroups * p.batch;
@@ -427,17 +431,16 @@ cudaError_t launch_step_vec(const ssd_step_params &p, cudaStream_t stream) {
     return launch_step<kType, L, E, 1>(p, stream);
 }
 
-// fp32: 16 values a lane keep enough bytes in flight.  Narrower types are
-// bound by instructions, of which a row has some whatever its length: 32 values a lane.
+// Eight lanes a row; four where a row of up to 64 narrow values would leave
+// eight with less than a vector each.  (128 values a row, 128 requests, four lanes
+// of 32 values instead: bf16 89 for 86 us, e4m3 68 for 64.)
 template <int kType>
 cudaError_t launch_step_type(const ssd_step_params &p, cudaStream_t stream) {
-    if constexpr (kType == SSD_F32) {
-        if (p.dstate <= 64) return launch_step_vec<kType, 8, 8>(p, stream);
-        if (p.dstate <= 128) return launch_step_vec<kType, 8, 16>(p, stream);
-    } else {
-        if (p.dstate <= 64) return launch_step_vec<kType, 4, 16>(p, stream);
-        if (p.dstate <= 128) return launch_step_vec<kType, 4, 32>(p, stream);
+    if (p.dstate <= 64) {
+        if constexpr (kType == SSD_F32) return launch_step_vec<kType, 8, 8>(p, stream);
+        else return launch_step_vec<kType, 4, 16>(p, stream);
     }
+    if (p.dstate <= 128) return launch_step_vec<kType, 8, 16>(p, stream);
     return launch_step_vec<kType, 8, 32>(p, stream);
 }
 
