@@ -76,6 +76,8 @@ class MixerError(SSDError):
 
 
 def _stream(t, stream):
+    if not t.is_cuda:
+        raise ValueError("the mixer operators run on CUDA tensors")
     return (_torch().cuda.current_stream(t.device) if stream is None else stream).cuda_stream
 
 
@@ -114,6 +116,12 @@ def _shape(t, want, what):
         raise ValueError("%s must have the shape %s, not %s" % (what, tuple(want), tuple(t.shape)))
 
 
+def _one_device(*tensors):
+    where = {t.device for t in tensors if t is not None}
+    if len(where) > 1:
+        raise ValueError("the tensors of a call must be on one device, not on %s" % sorted(map(str, where)))
+
+
 def _seed_ptr(t):
     torch = _torch()
     if t is None:
@@ -131,6 +139,8 @@ def _positions(t, n, what):
 
 
 def _slots(p, t, n):
+    if t is None:
+        raise ValueError("slot_idx is missing")
     _shape(t, (n,), "slot_idx")
     p.slot_idx, p.slot_idx_stride = _index_ptr(t)
     if n > 1 and t.stride(0) <= 0:
@@ -146,6 +156,8 @@ def make_conv_params(xbc, weight, cu_seqlens, out_x, out_B=None, out_C=None, *, 
     """Fill ``ssd_conv_params``.  ``xbc`` [T, channels] may be a column range of a wider tensor; the channels go to
     ``out_x``, ``out_B`` and ``out_C`` ([T, ...], dense) in that order."""
     torch = _torch()
+    _one_device(xbc, weight, cu_seqlens, out_x, out_B, out_C, bias, conv_cache, slot_idx, start_pos, dt, out_dt,
+                device_status)
     T, C = xbc.shape
     S = cu_seqlens.shape[0] - 1
     p = ConvParams()
@@ -169,8 +181,6 @@ def make_conv_params(xbc, weight, cu_seqlens, out_x, out_B=None, out_C=None, *, 
         _shape(conv_cache, (conv_cache.shape[0], conv_cache.shape[1], C), "conv_cache")
         p.conv_cache = _ptr(conv_cache, xbc.dtype)
         p.num_slots, p.conv_rows = conv_cache.shape[0], conv_cache.shape[1]
-        if slot_idx is None:
-            raise ValueError("a convolution cache needs slot_idx")
         _slots(p, slot_idx, S)
     p.start_pos = _positions(start_pos, S, "start_pos")
     if (dt is None) != (out_dt is None):
@@ -221,6 +231,8 @@ def make_step_params(xbc, dt, weight, A, conv_cache, state_cache, pos, slot_idx,
     """Fill ``ssd_step_params``: one token for each row of ``xbc``.  ``xbc``, ``z`` and ``dt`` may be column ranges of
     one in-projection output; ``sr_seed`` is a one-element int64 device tensor."""
     torch = _torch()
+    _one_device(xbc, dt, weight, A, conv_cache, state_cache, pos, slot_idx, out_y, z, conv_bias, dt_bias, D,
+                state_scale, sr_seed, device_status)
     H, P, N = state_cache.shape[1:]
     B, C = xbc.shape
     if C != H * P + 2 * ngroups * N:
@@ -273,6 +285,7 @@ def step(xbc, dt, weight, A, conv_cache, state_cache, pos, slot_idx, *, ngroups,
 # ---------------------------------------------------------------------------
 def make_norm_params(y, weight, out, *, z=None, group_size=None, eps=1e-5, norm_before_gate=False) -> GatedNormParams:
     """Fill ``ssd_gated_norm_params``.  ``y``, ``z`` and ``out`` are [rows, columns] or [rows, H, P]."""
+    _one_device(y, weight, out, z)
     p = GatedNormParams()
     columns = _row_numel(y)
     p.rows, p.columns = y.shape[0], columns
@@ -310,6 +323,7 @@ def make_state_params(states, state_cache, state_scale, slot_idx, *, has_init=No
                       device_status=None) -> StateParams:
     """Fill ``ssd_state_params``: dense ``states`` [n, H, P, N] and the slots of an 8-bit cache."""
     torch = _torch()
+    _one_device(states, state_cache, state_scale, slot_idx, has_init, sr_seed, device_status)
     n, H, P, N = states.shape
     p = StateParams()
     p.num_states, p.nheads, p.headdim, p.dstate = n, H, P, N

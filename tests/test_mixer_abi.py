@@ -153,6 +153,20 @@ def test_binding_refuses_wrong_tensors():
         mixer.make_state_params(t(2, 1, 8, 8), t(3, 1, 8, 8, dtype=torch.int16), t(3, 1, 8), t(2, dtype=i32))
 
 
+def test_binding_refuses_tensors_elsewhere():
+    import torch
+    t = torch.zeros
+    i32 = torch.int32
+    with pytest.raises(ValueError, match="CUDA"):
+        mixer.gated_rms_norm(t(3, 8))
+    with pytest.raises(ValueError, match="one device"):
+        mixer.make_norm_params(t(3, 8), t(8, device="meta"), t(3, 8))
+    with pytest.raises(ValueError, match="one device"):
+        mixer.make_state_params(t(2, 1, 8, 8), t(3, 1, 8, 8, dtype=torch.int8), t(3, 1, 8, device="meta"), t(2, dtype=i32))
+    with pytest.raises(ValueError, match="slot_idx"):
+        mixer.make_state_params(t(2, 1, 8, 8), t(3, 1, 8, 8, dtype=torch.int8), t(3, 1, 8), None)
+
+
 # ---- the reference's own pieces --------------------------------------------
 def test_reference_e4m3_grid_is_torchs():
     import torch
