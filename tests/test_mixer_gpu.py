@@ -516,6 +516,64 @@ def test_step_on_another_stream_and_in_a_graph():
     assert torch.equal(a["y"], b["y"]) and np.array_equal(_bits(a["state"]), _bits(b["state"]))
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_order_with_copies_other_streams_and_plain_kernels(captured):
+    """Each operator is set up while the work before it drains: it must still see all of it, whatever that is (a copy,
+    a fill, a kernel of another stream joined by an event, one of these operators), and what follows must see its own."""
+    torch = _torch()
+    T, H, P = 20_000, 4, 64
+    d = Draw(3)
+    src, big = d.randn(T, H * P, dtype="bf16"), d.randn(1500, 1500)
+    y, z = torch.zeros_like(src), torch.zeros_like(src)
+    a, b, e = (torch.zeros_like(src) for _ in range(3))
+    states, back = d.randn(40, H, P, 128), torch.zeros(40, H, P, 128, device="cuda")
+    cache = torch.zeros(40, H, P, 128, dtype=torch.int8, device="cuda")
+    scale, slot = torch.zeros(40, H, P, device="cuda"), _i32(range(40))
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def body():
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            for _ in range(6):
+                big @ big                                   # keeps the side stream busy before it writes z
+            z.copy_(src)
+        y.fill_(3.0)
+        y.copy_(src)
+        here.wait_stream(side)
+        mixer.gated_rms_norm(y, z=z, group_size=P, out=a)   # after the join
+        mixer.gated_rms_norm(a, z=z, group_size=P, out=b)   # after one of its own kind
+        back.zero_()
+        mixer.state_store(states, cache, scale, slot)
+        mixer.state_load(cache, scale, slot, states=back)
+        e.copy_(b)                                          # a copy after it
+        e.mul_(2.0)
+        y.zero_()                                           # overwrites what the norm read
+
+    with torch.cuda.stream(main):
+        body()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in (a, b, e, back)]
+        for t in (a, b, e, back, scale):
+            t.zero_()
+        torch.cuda.synchronize()
+        if captured:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=main):
+                body()
+            for _ in range(5):
+                g.replay()
+        else:
+            for _ in range(5):
+                body()
+        torch.cuda.synchronize()
+    for t, w in zip((a, b, e, back), want):
+        assert torch.equal(t, w)
+    ref, err = R.norm(_np(src[:50]), _np(src[:50]), None, P, 1e-5, False)
+    R.check(_np(a[:50]), ref, err, "bf16", "norm")
+    assert torch.equal(e, b * 2.0) and torch.equal(back, cache.float() * scale[..., None])
+
+
 # ---------------------------------------------------------------------------
 # gated norm
 # ---------------------------------------------------------------------------
