@@ -2,19 +2,20 @@
 //
 //   out = rms(y SiLU(z)) w   or   rms(y) w SiLU(z)
 //
-// Each value is read once and written once: bound by HBM.  One warp takes a
-// short group of one row, one CTA a longer one; either holds the group in
+// Each value is read once and written once: bound by HBM.  Four to 32 lanes
+// take a short group of one row, a CTA a longer one; either holds the group in
 // registers between the sum of squares and the scaling, all its loads issued
-// together.  Groups of more than 2,048 vectors are read twice (from L2 the
-// second time).
+// together.  Groups past what a CTA holds are read twice (from L2 the second
+// time).
 #include "ssd_mixer_common.cuh"
 #include "ssd_mixer_internal.h"
 
 namespace ssd {
 namespace {
 
-constexpr int kChunks = 4;                  // vectors of a thread
-constexpr int kItemWarps = 4;               // warps of a CTA that takes a group with each
+constexpr int kItemThreads = 128;           // of a CTA that takes several groups
+// the most threads of a CTA that takes one group: what the registers allow
+template <int V> constexpr int kThreads = V == 1 ? 1024 : 512;
 
 // one group of one row
 template <typename IoT> struct Item {
@@ -88,41 +89,48 @@ __device__ __forceinline__ float cta_sum(float v, float *part) {
     return warp_sum(v);
 }
 
-// kWarp: each warp an item; else the CTA one item, a thread kChunks vectors at most.
-template <typename IoT, int V, bool kWarp>
-__global__ void __launch_bounds__(kWarp ? 32 * kItemWarps : 512) gated_norm_kernel(const ssd_gated_norm_params a, int groups, int64_t items) {
+// kLanes: lanes of an item, or 0: the CTA takes one; C: vectors of a thread at most.
+template <typename IoT, int V, int kLanes, int C>
+__global__ void __launch_bounds__(kLanes ? kItemThreads : kThreads<V>)
+    gated_norm_kernel(const ssd_gated_norm_params a, int groups, int64_t items) {
     __shared__ float part[32];
     await_previous();
-    const int64_t id = kWarp ? (int64_t)blockIdx.x * kItemWarps + threadIdx.x / 32 : blockIdx.x;
-    if (id >= items) return;
-    const Item<IoT> it(a, id, groups);
-    const int at = (kWarp ? threadIdx.x & 31 : threadIdx.x) * V, step = (kWarp ? 32 : blockDim.x) * V;
+    constexpr int L = kLanes ? kLanes : 32;
+    const int64_t id = kLanes ? ((int64_t)blockIdx.x * kItemThreads + threadIdx.x) / L : blockIdx.x;
+    const bool live = id < items;               // past the last item: lanes that only take part in the sums
+    const Item<IoT> it(a, live ? id : 0, groups);
+    const int size = live ? a.group_size : 0;
+    const int at = (kLanes ? threadIdx.x % L : threadIdx.x) * V, step = (kLanes ? L : blockDim.x) * V;
     const bool after = it.z && a.norm_before_gate, before = it.z && !a.norm_before_gate;
-    Pack<IoT, V> y[kChunks], z[kChunks], w[kChunks];
+    Pack<IoT, V> y[C], z[C], w[C];
 #pragma unroll
-    for (int k = 0; k < kChunks; ++k) {
+    for (int k = 0; k < C; ++k) {
         const int c = at + k * step;
         y[k] = z[k] = w[k] = Pack<IoT, V>{};
-        if (c < a.group_size) {
+        if (c < size) {
             y[k] = load_pack<IoT, V>(it.y + c);
             if (it.z) z[k] = load_pack<IoT, V>(it.z + c);
         }
     }
+    // weights ahead of the sum too, unless they would take single elements a register each
+    if constexpr (V > 1)
 #pragma unroll
-    for (int k = 0; k < kChunks; ++k)
-        if (it.w && at + k * step < a.group_size) w[k] = load_pack<IoT, V>(it.w + at + k * step);
-    float2 v[kChunks][(V + 1) / 2], two = make_float2(0.f, 0.f);
+        for (int k = 0; k < C; ++k)
+            if (it.w && at + k * step < size) w[k] = load_pack<IoT, V>(it.w + at + k * step);
+    float2 v[C][(V + 1) / 2], two = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < kChunks; ++k) {
+    for (int k = 0; k < C; ++k) {
         normed<IoT, V>(y[k], z[k], before, v[k]);
         add_squares<V>(two, v[k]);
     }
-    const float sum = kWarp ? warp_sum(two.x + two.y) : cta_sum(two.x + two.y, part);
+    const float sum = kLanes ? lanes_sum<L>(two.x + two.y) : cta_sum(two.x + two.y, part);
     const float r = 1.f / sqrtf(sum / (float)a.group_size + a.eps);
 #pragma unroll
-    for (int k = 0; k < kChunks; ++k) {
+    for (int k = 0; k < C; ++k) {
         const int c = at + k * step;
-        if (c < a.group_size) store_pack<IoT, V>(it.out + c, scaled<IoT, V>(v[k], r, w[k], it.w != nullptr, z[k], after));
+        if (c >= size) continue;
+        if (V == 1 && it.w) w[k] = load_pack<IoT, V>(it.w + c);
+        store_pack<IoT, V>(it.out + c, scaled<IoT, V>(v[k], r, w[k], it.w != nullptr, z[k], after));
     }
 }
 
@@ -158,12 +166,25 @@ cudaError_t launch(const ssd_gated_norm_params &p, cudaStream_t stream) {
     const int64_t items = p.rows * groups;
     if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const int vectors = (p.group_size + V - 1) / V;
-    if (vectors <= 32 * kChunks)
-        return enqueue(gated_norm_kernel<IoT, V, true>, dim3((unsigned)((items + kItemWarps - 1) / kItemWarps)),
-                       32 * kItemWarps, stream, p, groups, items);
-    if (vectors <= 512 * kChunks)
-        return enqueue(gated_norm_kernel<IoT, V, false>, dim3((unsigned)items),
-                       32 * ((vectors + 32 * kChunks - 1) / (32 * kChunks)), stream, p, groups, items);
+    auto shared = [&](auto kernel, int lanes) {
+        const int64_t per = kItemThreads / lanes;
+        return enqueue(kernel, dim3((unsigned)((items + per - 1) / per)), kItemThreads, stream, p, groups, items);
+    };
+    if (vectors <= 4) return shared(gated_norm_kernel<IoT, V, 4, 1>, 4);
+    if (vectors <= 8) return shared(gated_norm_kernel<IoT, V, 8, 1>, 8);
+    if (vectors <= 16) return shared(gated_norm_kernel<IoT, V, 16, 1>, 16);
+    if (vectors <= 32) return shared(gated_norm_kernel<IoT, V, 32, 1>, 32);
+    if (vectors <= 128) return shared(gated_norm_kernel<IoT, V, 32, 4>, 32);
+    auto whole = [&](auto kernel, int chunks) {
+        return enqueue(kernel, dim3((unsigned)items), 32 * ((vectors + 32 * chunks - 1) / (32 * chunks)), stream, p, groups,
+                       items);
+    };
+    if constexpr (V == 1) {
+        if (vectors <= kThreads<V> * 10) return whole(gated_norm_kernel<IoT, V, 0, 10>, 10);
+    } else {
+        if (vectors <= kThreads<V> * 4) return whole(gated_norm_kernel<IoT, V, 0, 4>, 4);
+        if (vectors <= kThreads<V> * 8) return whole(gated_norm_kernel<IoT, V, 0, 8>, 8);
+    }
     return enqueue(gated_norm_long_kernel<IoT, V>, dim3((unsigned)items), 1024, stream, p, groups);
 }
 

@@ -323,29 +323,42 @@ template <int kType> __device__ __forceinline__ uint32_t encode4_sr(const float 
     }
 }
 
-// V values of flat elements e0 .. (a multiple of V where V >= 4).
+// The random bytes of a row of n codes that begins at flat element e0, written
+// to `bytes` (16-byte aligned, rand_blocks(n) blocks) by the L lanes that share
+// the row; element e0 + i has byte (e0 & 15) + i.  Whole warps call it.
+constexpr int rand_blocks(int n) { return (n + 30) / 16; }
+template <int L>
+__device__ __forceinline__ void row_bytes(uint4 *bytes, const uint32_t *keys, uint64_t e0, int n, int lane) {
+    __syncwarp();           // the row before has been read
+    const int blocks = ((int)(e0 & 15) + n + 15) >> 4;
+    for (int i = lane; i < blocks; i += L) bytes[i] = sr_keyed(keys, (e0 >> 4) + i, 2u);
+    __syncwarp();
+}
+
+// V values of flat elements e0 .. as codes.  V = 16 is a whole Philox block
+// (e0 a multiple of 16); fewer read their bytes at `bytes`, see row_bytes.
 template <int kType, int V>
-__device__ __forceinline__ Pack<uint8_t, V> encode8_sr(const float *h, float inv, const uint32_t *keys, uint64_t e0) {
+__device__ __forceinline__ Pack<uint8_t, V> encode8_sr(const float *h, float inv, const uint32_t *keys, uint64_t e0,
+                                                       const uint8_t *bytes) {
     Pack<uint8_t, V> out;
-    if constexpr (V >= 4) {
-        const uint4 r = sr_keyed(keys, e0 >> 4, 2u);
-        uint32_t word[4] = {r.x, r.y, r.z, r.w}, w[V / 4];
-        if constexpr (V == 8) {
-            word[0] = (e0 & 8) ? r.z : r.x;
-            word[1] = (e0 & 8) ? r.w : r.y;
-        } else if constexpr (V == 4) {
-            word[0] = sr_word(r, (uint32_t)(e0 >> 2) & 3u);
+    if constexpr (V >= 4) {         // e0 is a multiple of V: whole words
+        uint32_t word[V / 4], w[V / 4];
+        if constexpr (V == 16) {
+            const uint4 r = sr_keyed(keys, e0 >> 4, 2u);
+            word[0] = r.x;
+            word[1] = r.y;
+            word[2] = r.z;
+            word[3] = r.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < V / 4; ++j) word[j] = *reinterpret_cast<const uint32_t *>(bytes + 4 * j);
         }
 #pragma unroll
         for (int j = 0; j < V; j += 4) w[j / 4] = encode4_sr<kType>(h + j, inv, word[j / 4]);
         memcpy(out.v, w, V);
     } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const uint64_t e = e0 + (uint64_t)j;
-            const uint32_t word = sr_word(sr_keyed(keys, e >> 4, 2u), (uint32_t)(e >> 2) & 3u);
-            out.v[j] = encode1_sr<kType>(h[j], inv, (word >> (8 * ((uint32_t)e & 3u))) & 0xffu);
-        }
+        for (int j = 0; j < V; ++j) out.v[j] = encode1_sr<kType>(h[j], inv, bytes[j]);
     }
     return out;
 }

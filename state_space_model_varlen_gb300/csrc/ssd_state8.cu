@@ -26,6 +26,7 @@ __device__ __forceinline__ int checked_slot(const ssd_state_params &a, int s, bo
 template <typename DnT, int kType, int E, int V>
 __global__ void __launch_bounds__(kThreads) store_kernel(const ssd_state_params a, int blocks) {
     __shared__ __align__(16) uint32_t keys[20];
+    __shared__ uint4 s_rand[kGroups * rand_blocks(8 * E)];
     await_previous();
     const int s = blockIdx.x / blocks, N = a.dstate;
     const int64_t per = (int64_t)a.nheads * a.headdim;
@@ -60,6 +61,8 @@ __global__ void __launch_bounds__(kThreads) store_kernel(const ssd_state_params 
             }
         float inv, scale;
         row_scale<true>(lanes_max<8>(big), code_limit<kType>(), &inv, &scale);
+        uint4 *rand = s_rand + (threadIdx.x >> 3) * rand_blocks(8 * E);
+        if (a.sr_seed) row_bytes<8>(rand, keys, (uint64_t)row * N, N, lane);
         if (r >= per) continue;
         if (lane == 0) a.state_scale[row] = scale;
         uint8_t *dst = static_cast<uint8_t *>(a.state_cache) + row * N;
@@ -67,7 +70,9 @@ __global__ void __launch_bounds__(kThreads) store_kernel(const ssd_state_params 
         for (int k = 0; k < E / V; ++k) {
             const int n = (k * 8 + lane) * V;
             if (n >= N) continue;
-            store_pack<uint8_t, V>(dst + n, a.sr_seed ? encode8_sr<kType, V>(v[k], inv, keys, (uint64_t)(row * N + n))
+            store_pack<uint8_t, V>(dst + n, a.sr_seed ? encode8_sr<kType, V>(v[k], inv, keys, (uint64_t)(row * N + n),
+                                                                            reinterpret_cast<const uint8_t *>(rand) +
+                                                                                (row * N & 15) + n)
                                                       : encode8<kType, V>(v[k], inv));
         }
     }

@@ -135,6 +135,8 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas<kType, E>) step_kernel
     __shared__ __align__(16) float s_b[L * E], s_c[L * E], s_y[kStepMaxRows], s_dx[kStepMaxRows], s_keep[kStepMaxRows];
     __shared__ __align__(16) float s_scale[k8bit ? kStepMaxRows : 4];       // of each row: the old scale, then the new one
     __shared__ __align__(16) uint32_t s_keys[kSr ? 20 : 1];
+    constexpr bool kRowBytes = kSr && k8bit && V < 16;       // random bytes by rows, not by lanes
+    __shared__ uint4 s_rand[kRowBytes ? kStepGroups * rand_blocks(L * E) : 1];
     __shared__ Pack<StT, V> s_raw[kAsync ? kDepth * kChunks * kStepThreads : 1];
 
     await_previous();
@@ -324,6 +326,8 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas<kType, E>) step_kernel
             row_scale<stepwise>(most, code_limit<kType>(), &inv, &sc);
             if (lane == 0 && live) s_scale[r] = sc;
         }
+        uint4 *rand = s_rand + (kRowBytes ? grp * rand_blocks(L * E) : 0);
+        if constexpr (kRowBytes) row_bytes<L>(rand, s_keys, e0 - lane * V, N, lane);
 #pragma unroll
         for (int k = 0; k < kChunks; ++k) {
             const int n = (k * L + lane) * V;
@@ -355,7 +359,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas<kType, E>) step_kernel
                     for (int j = 0; j < V; ++j) p.v[j] = __float2half_rn(v[j]);
                 }
             } else {
-                if constexpr (kSr) p = encode8_sr<kType, V>(v, inv, s_keys, e);
+                if constexpr (kSr) p = encode8_sr<kType, V>(v, inv, s_keys, e, reinterpret_cast<const uint8_t *>(rand) + ((e0 - lane * V) & 15) + n);
                 else p = encode8<kType, V>(v, inv);
             }
             store_pack<StT, V>(dst + k * L * V, p);
@@ -436,9 +440,13 @@ cudaError_t launch_step_vec(const ssd_step_params &p, cudaStream_t stream) {
 // of 32 values instead: bf16 89 for 86 us, e4m3 68 for 64.)
 template <int kType>
 cudaError_t launch_step_type(const ssd_step_params &p, cudaStream_t stream) {
-    if (p.dstate <= 64) {
-        if constexpr (kType == SSD_F32) return launch_step_vec<kType, 8, 8>(p, stream);
-        else return launch_step_vec<kType, 4, 16>(p, stream);
+    if (p.dstate <= 16) return launch_step_vec<kType, 4, 4>(p, stream);
+    if constexpr (kType == SSD_F32) {
+        if (p.dstate <= 32) return launch_step_vec<kType, 8, 4>(p, stream);
+        if (p.dstate <= 64) return launch_step_vec<kType, 8, 8>(p, stream);
+    } else {
+        if (p.dstate <= 32) return launch_step_vec<kType, 4, 8>(p, stream);
+        if (p.dstate <= 64) return launch_step_vec<kType, 4, 16>(p, stream);
     }
     if (p.dstate <= 128) return launch_step_vec<kType, 8, 16>(p, stream);
     return launch_step_vec<kType, 8, 32>(p, stream);
