@@ -24,13 +24,15 @@
 // only ones that need the ring, also where they pass the tile's end (the next
 // tile leaves them out), and afterwards writes the sequence's last inputs,
 // also where those lie in later tiles.
+#include <algorithm>
+
 #include "ssd_mixer_common.cuh"
 #include "ssd_mixer_internal.h"
 
 namespace ssd {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 128;       // of a CTA at most: fewer where the channels do not fill them
 constexpr int kMaxTile = 64;       // tokens of a tile
 constexpr int kRecords = kMaxTile + SSD_CONV_MAX_WIDTH;       // and those after it that it may take over
 constexpr int kGroup = 8;          // tokens whose inputs are loaded together
@@ -52,7 +54,7 @@ constexpr int kSlides = 1, kKeeps = 2;      // of a group: every token has its w
 template <typename IoT>
 __device__ __forceinline__ void widen_dt(const ssd_conv_params &a, int64_t t0, int nt) {
     const IoT *dt = static_cast<const IoT *>(a.dt);
-    for (int h = threadIdx.x; h < a.nheads; h += kThreads) {
+    for (int h = threadIdx.x; h < a.nheads; h += blockDim.x) {
         for (int i = 0; i < nt; i += kGroup) {
             float v[kGroup];
 #pragma unroll
@@ -103,7 +105,9 @@ template <typename IoT, int V, int kW>
 constexpr int kMinCtas = kW == 0 ? 3 : 5;
 
 // kW: the width, or 0 for one that only a.width tells (then no group slides).
-template <typename IoT, int V, int kW, bool kShort>
+// kSplit: only the rows of xbc are not aligned to V elements: they are loaded
+// one element at a time, everything else V together.
+template <typename IoT, int V, int kW, bool kShort, bool kSplit>
 __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(const ssd_conv_params a, int tile, int dt_column) {
     __shared__ Sequence sequence[kMaxTile];        // at the sequence's first token in the tile
     __shared__ uint32_t firsts[kMaxTile / 32];      // where there are any
@@ -117,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
     constexpr int kPairs = (V + 1) / 2;
     // groups copied ahead; two-byte shares are loaded one group ahead instead
     constexpr int kBytes = V * (int)sizeof(IoT);
-    constexpr bool kAsync = kBytes >= 4 && kW > 1;
+    constexpr bool kAsync = kBytes >= 4 && kW > 1 && !kSplit;
     constexpr int kDepth = kBytes < 8 ? 4 : kShort ? 2 : 3;
     __shared__ Pack<IoT, V> s_x[kAsync ? kDepth * kGroup * kThreads : 1];
     __shared__ Pack<IoT, V> s_old[kAsync && kShort ? kGroup * kPast * kThreads : 1];
@@ -141,17 +145,27 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
     };
     Sequence seq{};
     if ((int)threadIdx.x < a.num_seqs) seq = look_up(threadIdx.x);
-    const int c = (ct * kThreads + threadIdx.x) * V;
+    const int c = (ct * blockDim.x + threadIdx.x) * V;
     const bool mine = c < a.channels;
     const IoT *x = static_cast<const IoT *>(a.xbc) + t0 * a.xbc_stride + c;    // of the tile's first token
     Pack<IoT, V> next[kGroup], prev[kPast];
+    auto load_x = [](const IoT *src) {
+        if constexpr (kSplit) {
+            Pack<IoT, V> p;
+#pragma unroll
+            for (int j = 0; j < V; ++j) p.v[j] = src[j];
+            return p;
+        } else {
+            return load_pack<IoT, V>(src);
+        }
+    };
     auto load_group = [&](int i0, int stage) {
         const IoT *src = x + i0 * a.xbc_stride;
         if (mine && i0 + kGroup <= nt) {
 #pragma unroll
             for (int j = 0; j < kGroup; ++j, src += a.xbc_stride) {
                 if constexpr (kAsync) copy_async<kBytes>(&s_x[(stage * kGroup + j) * kThreads + threadIdx.x], src, true);
-                else next[j] = load_pack<IoT, V>(src);
+                else next[j] = load_x(src);
             }
         } else if (mine && i0 < nt) {
 #pragma unroll
@@ -161,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
                     copy_async<kBytes>(&s_x[(stage * kGroup + j) * kThreads + threadIdx.x],
                                        live ? src : static_cast<const IoT *>(a.xbc), live);
                 else if (live)
-                    next[j] = load_pack<IoT, V>(src);
+                    next[j] = load_x(src);
             }
         }
         if constexpr (kAsync) commit_async();
@@ -172,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
 #pragma unroll
         for (int m = 1; m < kW; ++m) {
             prev[m - 1] = Pack<IoT, V>{};
-            if (mine && t0 >= m) prev[m - 1] = load_pack<IoT, V>(x - m * a.xbc_stride);
+            if (mine && t0 >= m) prev[m - 1] = load_x(x - m * a.xbc_stride);
         }
     }
 
@@ -195,11 +209,12 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
     }
 
     // ---- the tile's tokens -------------------------------------------------
+    static_assert(kMaxTile / kGroup <= 32 && kMaxTile / 32 <= 32, "the smallest CTA has a warp");
     if (threadIdx.x < kMaxTile / 32) firsts[threadIdx.x] = 0;
     if (threadIdx.x < kMaxTile / kGroup) group[threadIdx.x] = kW > 1 ? kSlides : 0;
     if (threadIdx.x == 0) tail = after = 0;
     __syncthreads();
-    for (int s = threadIdx.x; s < a.num_seqs; s += kThreads) {
+    for (int s = threadIdx.x; s < a.num_seqs; s += blockDim.x) {
         const Sequence q = s == (int)threadIdx.x ? seq : look_up(s);
         int bad = 0;
         if (q.begin < 0 || q.end < q.begin || q.end > a.total_tokens) bad = SSD_DEV_BAD_SEQLENS;
@@ -214,8 +229,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
         }
     }
     __syncthreads();
-    if (threadIdx.x < kRecords) {
-        const int i = threadIdx.x;
+    for (int i = threadIdx.x; i < kRecords; i += blockDim.x) {
         // the last first token up to this one (a token after the tile: up to the tile's last)
         const int to = min(i, nt - 1);
         const uint32_t below = firsts[to / 32] & (0xffffffffu >> (31 - to % 32));
@@ -288,15 +302,13 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
                 for (int m = 0; m < kM; ++m) {
                     tap[i][m] = Pack<IoT, V>{};
                     if (m >= W || k.local < 0 || s0 + i >= to) continue;
-                    const IoT *src = nullptr;
                     if (m <= k.local) {
-                        src = x + (int64_t)(s0 + i - m) * a.xbc_stride;
+                        tap[i][m] = load_x(x + (int64_t)(s0 + i - m) * a.xbc_stride);
                     } else if (m <= k.past && k.slot >= 0) {
                         int row = k.row - m;
                         if (row < 0) row += a.conv_rows;
-                        src = ring + ((int64_t)k.slot * a.conv_rows + row) * a.channels;
+                        tap[i][m] = load_pack<IoT, V>(ring + ((int64_t)k.slot * a.conv_rows + row) * a.channels);
                     }
-                    if (src) tap[i][m] = load_pack<IoT, V>(src);
                 }
             }
 #pragma unroll
@@ -421,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
                 if (!keep[i]) continue;
                 const Token k = token[i];
                 store_pack<IoT, V>(ring + ((int64_t)k.slot * a.conv_rows + k.row) * a.channels,
-                                   load_pack<IoT, V>(x + i * a.xbc_stride));
+                                   load_x(x + i * a.xbc_stride));
             }
         }
     }
@@ -436,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
         Pack<IoT, V> last[kM];
 #pragma unroll
         for (int m = 0; m < kM; ++m)
-            if (i0 + m < e) last[m] = load_pack<IoT, V>(x + (i0 + m) * a.xbc_stride);
+            if (i0 + m < e) last[m] = load_x(x + (i0 + m) * a.xbc_stride);
 #pragma unroll
         for (int m = 0; m < kM; ++m) {
             if (i0 + m >= e) break;
@@ -446,14 +458,16 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
     }
 }
 
-template <typename IoT, int V>
+template <typename IoT, int V, bool kSplit>
 cudaError_t launch(const ssd_conv_params &p, cudaStream_t stream) {
-    const int ctiles = (p.channels + kThreads * V - 1) / (kThreads * V), dt = p.dt != nullptr ? 1 : 0;
+    const int lanes = (p.channels + V - 1) / V, ctiles = (lanes + kThreads - 1) / kThreads, dt = p.dt != nullptr ? 1 : 0;
+    const int threads = ((lanes + ctiles - 1) / ctiles + 31) / 32 * 32;
     // the tile whose waves of CTAs take the least, a CTA's own start counted as
     // 24 tokens: long tiles for long batches, one wave of shorter ones below that
     int tile = kGroup;
     int64_t least = INT64_MAX;
-    const int64_t resident = 152 * kMinCtas<IoT, V, 4>;
+    // what the registers leave room for, at most the eight of the shared memory
+    const int64_t resident = 152LL * std::min(8, kMinCtas<IoT, V, 4> * kThreads / threads);
     for (int t = kGroup; t <= kMaxTile; t += kGroup) {
         const int64_t ctas = (p.total_tokens + t - 1) / t * ctiles, cost = (ctas + resident - 1) / resident * (t + 24);
         if (cost <= least) {
@@ -467,14 +481,14 @@ cudaError_t launch(const ssd_conv_params &p, cudaStream_t stream) {
     // mean length below 64: many groups hold a sequence's first token (201
     // sequences, 1,311 tokens of 5,376 channels: 14 us so, 18 the other way; 61,773 tokens of
     // 10,240 channels in 32 sequences: 488 and 399)
-    const bool brief = p.total_tokens < 64LL * p.num_seqs;
-    auto run = [&](auto kernel) { return enqueue(kernel, grid, kThreads, stream, p, tile, dt); };
+    const bool brief = !kSplit && p.total_tokens < 64LL * p.num_seqs;
+    auto run = [&](auto kernel) { return enqueue(kernel, grid, threads, stream, p, tile, dt); };
     switch (p.width) {
-        case 2: return brief ? run(conv_kernel<IoT, V, 2, true>) : run(conv_kernel<IoT, V, 2, false>);
-        case 3: return brief ? run(conv_kernel<IoT, V, 3, true>) : run(conv_kernel<IoT, V, 3, false>);
-        case 4: return brief ? run(conv_kernel<IoT, V, 4, true>) : run(conv_kernel<IoT, V, 4, false>);
+        case 2: return brief ? run(conv_kernel<IoT, V, 2, !kSplit, kSplit>) : run(conv_kernel<IoT, V, 2, false, kSplit>);
+        case 3: return brief ? run(conv_kernel<IoT, V, 3, !kSplit, kSplit>) : run(conv_kernel<IoT, V, 3, false, kSplit>);
+        case 4: return brief ? run(conv_kernel<IoT, V, 4, !kSplit, kSplit>) : run(conv_kernel<IoT, V, 4, false, kSplit>);
     }
-    return run(conv_kernel<IoT, V, 0, false>);
+    return run(conv_kernel<IoT, V, 0, false, kSplit>);
 }
 
 }  // namespace
@@ -482,18 +496,19 @@ cudaError_t launch(const ssd_conv_params &p, cudaStream_t stream) {
 cudaError_t launch_conv(const ssd_conv_params &p, cudaStream_t stream) {
     const int io = p.io_dtype == SSD_F32 ? 4 : 2;
     const int rest = p.channels - p.split0 - p.split1;
-    auto can = [&](int v) {
+    auto rest_can = [&](int v) {
         const size_t bytes = (size_t)v * io;
-        return p.channels % v == 0 && p.xbc_stride % v == 0 && p.split0 % v == 0 && p.split1 % v == 0 &&
-               rest % v == 0 && aligned_to(p.xbc, bytes) && aligned_to(p.conv_cache, bytes) &&
-               aligned_to(p.out0, bytes) && aligned_to(p.out1, bytes) && aligned_to(p.out2, bytes) &&
-               aligned_to(p.weight, 16) && aligned_to(p.bias, bytes);
+        return p.channels % v == 0 && p.split0 % v == 0 && p.split1 % v == 0 && rest % v == 0 &&
+               aligned_to(p.conv_cache, bytes) && aligned_to(p.out0, bytes) && aligned_to(p.out1, bytes) &&
+               aligned_to(p.out2, bytes) && aligned_to(p.weight, 16) && aligned_to(p.bias, bytes);
     };
+    auto can = [&](int v) { return rest_can(v) && p.xbc_stride % v == 0 && aligned_to(p.xbc, (size_t)v * io); };
     // eight bytes a thread: more would not leave room for the ring's share of a group
-    if (p.io_dtype == SSD_F32) return can(2) ? launch<float, 2>(p, stream) : launch<float, 1>(p, stream);
-    return can(4)   ? launch<__nv_bfloat16, 4>(p, stream)
-           : can(2) ? launch<__nv_bfloat16, 2>(p, stream)
-                    : launch<__nv_bfloat16, 1>(p, stream);
+    if (p.io_dtype == SSD_F32) return can(2) ? launch<float, 2, false>(p, stream) : launch<float, 1, false>(p, stream);
+    if (can(4)) return launch<__nv_bfloat16, 4, false>(p, stream);
+    if (can(2)) return launch<__nv_bfloat16, 2, false>(p, stream);
+    if (rest_can(4)) return launch<__nv_bfloat16, 4, true>(p, stream);
+    return rest_can(2) ? launch<__nv_bfloat16, 2, true>(p, stream) : launch<__nv_bfloat16, 1, false>(p, stream);
 }
 
 }  // namespace ssd
