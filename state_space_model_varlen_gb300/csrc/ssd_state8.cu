@@ -23,10 +23,10 @@ __device__ __forceinline__ int checked_slot(const ssd_state_params &a, int s, bo
     return -1;
 }
 
-template <typename DnT, int kType, int E, int V>
+template <typename DnT, int kType, int E, int V, bool kSr>
 __global__ void __launch_bounds__(kThreads) store_kernel(const ssd_state_params a, int blocks) {
     __shared__ __align__(16) uint32_t keys[20];
-    __shared__ uint4 s_rand[kGroups * rand_blocks(8 * E)];
+    __shared__ uint4 s_rand[kSr ? kGroups * rand_blocks(8 * E) : 1];
     await_previous();
     const int s = blockIdx.x / blocks, N = a.dstate;
     const int64_t per = (int64_t)a.nheads * a.headdim;
@@ -43,10 +43,10 @@ __global__ void __launch_bounds__(kThreads) store_kernel(const ssd_state_params 
             if (r < per && n < N)
                 p[i][k] = load_pack<DnT, V>(static_cast<const DnT *>(a.states) + ((int64_t)s * per + r) * N + n);
         }
-    if (a.sr_seed && threadIdx.x < 20) round_keys(*a.sr_seed, threadIdx.x, keys);
+    if (kSr && threadIdx.x < 20) round_keys(*a.sr_seed, threadIdx.x, keys);
     const int slot = checked_slot(a, s, threadIdx.x == 0 && blockIdx.x % blocks == 0);
     if (slot < 0) return;
-    if (a.sr_seed) __syncthreads();
+    if constexpr (kSr) __syncthreads();
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         const int64_t r = r0 + i * kGroups, row = (int64_t)slot * per + r;
@@ -61,8 +61,8 @@ __global__ void __launch_bounds__(kThreads) store_kernel(const ssd_state_params 
             }
         float inv, scale;
         row_scale<true>(lanes_max<8>(big), code_limit<kType>(), &inv, &scale);
-        uint4 *rand = s_rand + (threadIdx.x >> 3) * rand_blocks(8 * E);
-        if (a.sr_seed) row_bytes<8>(rand, keys, (uint64_t)row * N, N, lane);
+        uint4 *rand = s_rand + (kSr ? (threadIdx.x >> 3) * rand_blocks(8 * E) : 0);
+        if constexpr (kSr) row_bytes<8>(rand, keys, (uint64_t)row * N, N, lane);
         if (r >= per) continue;
         if (lane == 0) a.state_scale[row] = scale;
         uint8_t *dst = static_cast<uint8_t *>(a.state_cache) + row * N;
@@ -70,10 +70,11 @@ __global__ void __launch_bounds__(kThreads) store_kernel(const ssd_state_params 
         for (int k = 0; k < E / V; ++k) {
             const int n = (k * 8 + lane) * V;
             if (n >= N) continue;
-            store_pack<uint8_t, V>(dst + n, a.sr_seed ? encode8_sr<kType, V>(v[k], inv, keys, (uint64_t)(row * N + n),
-                                                                            reinterpret_cast<const uint8_t *>(rand) +
-                                                                                (row * N & 15) + n)
-                                                      : encode8<kType, V>(v[k], inv));
+            const uint8_t *bytes = reinterpret_cast<const uint8_t *>(rand) + (row * N & 15) + n;
+            if constexpr (kSr)
+                store_pack<uint8_t, V>(dst + n, encode8_sr<kType, V>(v[k], inv, keys, (uint64_t)(row * N + n), bytes));
+            else
+                store_pack<uint8_t, V>(dst + n, encode8<kType, V>(v[k], inv));
         }
     }
 }
@@ -127,8 +128,12 @@ template <bool kStore, typename DnT, int kType, int E, int V>
 cudaError_t launch(const ssd_state_params &p, cudaStream_t stream) {
     const int64_t per = (int64_t)p.nheads * p.headdim, blocks = (per + kTile - 1) / kTile;
     if (p.num_states * blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    return enqueue(kStore ? store_kernel<DnT, kType, E, V> : load_kernel<DnT, kType, E, V>,
-                   dim3((unsigned)(p.num_states * blocks)), kThreads, stream, p, (int)blocks);
+    const dim3 grid((unsigned)(p.num_states * blocks));
+    auto run = [&](auto kernel) { return enqueue(kernel, grid, kThreads, stream, p, (int)blocks); };
+    if constexpr (kStore)
+        return p.sr_seed ? run(store_kernel<DnT, kType, E, V, true>) : run(store_kernel<DnT, kType, E, V, false>);
+    else
+        return run(load_kernel<DnT, kType, E, V>);
 }
 
 template <bool kStore, typename DnT, int kType, int V>
