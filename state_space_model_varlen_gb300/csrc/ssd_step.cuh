@@ -25,6 +25,11 @@
 // a plain fp32 program then stores the same bits.  (A stored value that is
 // rounded the other way is off by 2^-4 to 2^-9 of itself, which fp32 outputs of
 // later steps would show.)  With bf16 activations products and sums are fused.
+//
+// Measured, 128 requests of 128 heads x 64 rows x 128 values: fp32 cache 164 us,
+// 6.6 TB/s (98 % of the copy rate); bf16 86 us (94 %); e4m3 64 us to nearest and
+// 101 us stochastically (67 and 42 %), bound by instructions: Philox 22 us of
+// it, the conversions most of the rest.  One request, fp32: 3.3 us in a graph.
 #pragma once
 
 #include "ssd_mixer_common.cuh"
