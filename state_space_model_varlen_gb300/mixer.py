@@ -53,16 +53,15 @@ _entries = {}
 
 
 def _entry(name):
-    f = _entries.get(name)
-    if f is None:
-        f = getattr(binding.load(), name)
-        f.restype, f.argtypes = ctypes.c_int, [ctypes.POINTER(_STRUCTS[name]), ctypes.c_void_p]
-        _entries[name] = f
+    """The C function of that name, loading (and if needed building) the library at its first use."""
+    f = getattr(binding.load(), name)
+    f.restype, f.argtypes = ctypes.c_int, [ctypes.POINTER(_STRUCTS[name]), ctypes.c_void_p]
+    _entries[name] = f
     return f
 
 
 def _call(name, params, stream_ptr):
-    rc = _entry(name)(params, stream_ptr or None)
+    rc = (_entries.get(name) or _entry(name))(params, stream_ptr or None)
     if rc != SSD_OK:
         raise MixerError(name, rc)
 
