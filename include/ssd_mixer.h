@@ -136,6 +136,10 @@ ssd_status ssd_conv_varlen(const ssd_conv_params *params, struct CUstream_st *st
  * cache is rewritten in place, rounded to nearest even, or stochastically
  * with sr_seed (SSD_F16: the rule of ssd_scan_params.sr_seed with stream 0;
  * 8-bit: the rule above; other types ignore it).  Use a new seed each step.
+ * With SSD_F32 activations and a narrower cache, every operation up to the
+ * stored state is rounded to fp32 by itself, in the order of the formulas (taps
+ * from the oldest on, then the bias), so that a plain fp32 program stores the
+ * same bits; otherwise products and sums may be fused.
  * slot -1 marks a padding request (a batch of fixed size in a CUDA graph):
  * its y is zero and nothing else of it is read or written.
  * Layouts:
