@@ -45,8 +45,8 @@ extern "C" {
 /* 8-bit storage of a state cache, beside SSD_F32, SSD_BF16 and SSD_F16.  The
  * N values of a state row [slot, h, p, :] are codes times one fp32 scale:
  *   m = max |h_n|;  inv = (1 / m) lim;  code_n = round(h_n inv);
- *   scale = m (1 / lim)           (each operation rounded to fp32; in
- *   ssd_step inv may be two units of its last place from that)
+ *   scale = m (1 / lim)
+ * (each operation, also of the rules below, rounded to fp32 by itself).
  * with lim 448 (E4M3, codes are e4m3 numbers) or 127 (I8, codes are signed
  * integers).  A row with m < 2^-100 is held as zeros with scale 0; a row with
  * an infinity or a NaN gets the scale NaN, so that it reads back as NaN.
@@ -136,10 +136,11 @@ ssd_status ssd_conv_varlen(const ssd_conv_params *params, struct CUstream_st *st
  * cache is rewritten in place, rounded to nearest even, or stochastically
  * with sr_seed (SSD_F16: the rule of ssd_scan_params.sr_seed with stream 0;
  * 8-bit: the rule above; other types ignore it).  Use a new seed each step.
- * With SSD_F32 activations and a narrower cache, every operation up to the
- * stored state is rounded to fp32 by itself, in the order of the formulas (taps
- * from the oldest on, then the bias), so that a plain fp32 program stores the
- * same bits; otherwise products and sums may be fused.
+ * With an 8-bit cache, with an SSD_F16 cache and sr_seed, and with SSD_F32
+ * activations and any cache below fp32, every operation up to the stored state is
+ * rounded to fp32 by itself, in the order of the formulas (taps from the oldest
+ * on, then the bias; SiLU as v / (1 + e^-v)), so that a plain fp32 program stores
+ * the same bits; otherwise products and sums may be fused.
  * slot -1 marks a padding request (a batch of fixed size in a CUDA graph):
  * its y is zero and nothing else of it is read or written.
  * Layouts:

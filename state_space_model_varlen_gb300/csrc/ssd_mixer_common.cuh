@@ -188,19 +188,14 @@ __device__ __forceinline__ void decode(const Pack<typename Stored<kType>::T, V> 
     }
 }
 
-// What a row's largest magnitude makes of its scale: inv multiplies the
-// values, scale multiplies the codes.  kExact: inv is (1 / m) limit with both
-// operations rounded; else through the reciprocal approximation, within two
-// units of its last place, where that neither over- nor underflows.
-template <bool kExact>
+// What a row's largest magnitude makes of its scale: inv = (1 / m) limit, with
+// both operations rounded, multiplies the values; scale multiplies the codes.
 __device__ __forceinline__ void row_scale(float m, float limit, float *inv, float *scale) {
     *scale = __fmul_rn(m, 1.f / limit);
-    if (!kExact && m < 1.329227995784916e+36f && m >= 7.888609052210118e-31f) {    // 2^120, 2^-100
-        *inv = rcp_approx(m) * limit;
-    } else if (!(m < __int_as_float(0x7f800000))) {     // an infinity or a NaN in the row
+    if (!(m < __int_as_float(0x7f800000))) {            // an infinity or a NaN in the row
         *inv = 0.f;
         *scale = __int_as_float(0x7fffffff);
-    } else if (m < 7.888609052210118e-31f) {
+    } else if (m < 7.888609052210118e-31f) {            // 2^-100
         *inv = *scale = 0.f;
     } else {
         *inv = __fmul_rn(__frcp_rn(m), limit);
@@ -292,9 +287,9 @@ template <int kType> __device__ __forceinline__ uint8_t encode1_sr(float h, floa
         return (uint8_t)((((f & 0x7fffu) + (byte & 0x7fu)) >> 7) | ((f >> 8) & 0x80u));
     } else {
         // floor(h inv + u), u = (byte + 1/2) / 256 (the mantissa of 128 + u, exactly), as
-        // the low byte of the sum with 1.5 2^23 rounded down
+        // the low byte of the sum with 1.5 2^23 rounded down; product and sum each rounded
         const float u = __uint_as_float(0x43000080u | (byte << 8)) - 128.f;
-        return (uint8_t)__float_as_uint(__fadd_rd(__fmaf_rn(h, inv, u), 12582912.f));
+        return (uint8_t)__float_as_uint(__fadd_rd(__fadd_rn(__fmul_rn(h, inv), u), 12582912.f));
     }
 }
 
@@ -313,11 +308,14 @@ template <int kType> __device__ __forceinline__ uint32_t encode4_sr(const float 
         const uint32_t xe = 2u * fe + ((word << 1) & 0x00fe00feu), xo = 2u * fo + ((word >> 7) & 0x00fe00feu);
         return __byte_perm((fe & 0x80008000u) | (xe & 0x7f007f00u), (fo & 0x80008000u) | (xo & 0x7f007f00u), 0x7351);
     } else {
+        const float2 inv2 = make_float2(inv, inv);
+        const float2 lo = mul2(make_float2(h[0], h[1]), inv2), hi = mul2(make_float2(h[2], h[3]), inv2);
+        const float v[4] = {lo.x, lo.y, hi.x, hi.y};
         uint32_t t[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float u = __uint_as_float(__byte_perm(word, 0x43000080u, 0x7604 | (i << 4))) - 128.f;
-            t[i] = __float_as_uint(__fadd_rd(__fmaf_rn(h[i], inv, u), 12582912.f));
+            t[i] = __float_as_uint(__fadd_rd(__fadd_rn(v[i], u), 12582912.f));
         }
         return __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
     }

@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kThreads) store_kernel(const ssd_state_params 
                 else if (V == 1) big = max_abs(big, v[k][j], v[k][j]);
             }
         float inv, scale;
-        row_scale<true>(lanes_max<8>(big), code_limit<kType>(), &inv, &scale);
+        row_scale(lanes_max<8>(big), code_limit<kType>(), &inv, &scale);
         uint4 *rand = s_rand + (kSr ? (threadIdx.x >> 3) * rand_blocks(8 * E) : 0);
         if constexpr (kSr) row_bytes<8>(rand, keys, (uint64_t)row * N, N, lane);
         if (r >= per) continue;

@@ -20,16 +20,20 @@
 // is none of those its other CTAs read, and they need no order among them.
 // Every CTA convolves its group's B and C for itself (from L2).
 //
-// With fp32 activations and a cache below fp32, everything that leads to the
-// stored state is rounded operation by operation, sums from the oldest tap on:
-// a plain fp32 program then stores the same bits.  (A stored value that is
-// rounded the other way is off by 2^-4 to 2^-9 of itself, which fp32 outputs of
-// later steps would show.)  With bf16 activations products and sums are fused.
+// Where a rounding of the last place can show in what a program sees later,
+// everything that leads to the stored state is rounded operation by operation,
+// sums from the oldest tap on, so that a plain fp32 program stores the same
+// bits: with every 8-bit cache (a code that tips moves the scale of its whole row
+// if it is the row's largest), with a seeded fp16 one, and with fp32 activations
+// and any cache below fp32 (a value that is rounded the other way is off by a
+// step of its type, which fp32 outputs of later steps show).  Otherwise, with
+// bf16 activations, products and sums are fused.
 //
 // Measured, 128 requests of 128 heads x 64 rows x 128 values: fp32 cache 164 us,
-// 6.6 TB/s (98 % of the copy rate); bf16 86 us (94 %); e4m3 64 us to nearest and
-// 101 us stochastically (67 and 42 %), bound by instructions: Philox 22 us of
-// it, the conversions most of the rest.  One request, fp32: 3.3 us in a graph.
+// 6.6 TB/s (98 % of the copy rate); bf16 86 us (94 %); e4m3 75 us to nearest and
+// 112 us stochastically (57 and 38 %), bound by instructions: Philox 22 us of
+// it, the roundings one by one 11, the conversions most of the rest.  One
+// request, fp32: 3.3 us in a graph.
 #pragma once
 
 #include "ssd_mixer_common.cuh"
@@ -63,18 +67,19 @@ inline void set_divisor(StepPlan &plan, int P) {
     plan.p_shift = 31 + s;
 }
 
-// acc + w x, fused or (fp32 activations) operation by operation
-template <typename IoT> __device__ __forceinline__ float tap(float acc, float w, float x) {
-    return sizeof(IoT) == 4 ? __fadd_rn(acc, __fmul_rn(w, x)) : fmaf(w, x, acc);
+// acc + w x, and the activation of the sum with its bias: fused and approximated,
+// or (plain) operation by operation
+template <bool plain> __device__ __forceinline__ float tap(float acc, float w, float x) {
+    return plain ? __fadd_rn(acc, __fmul_rn(w, x)) : fmaf(w, x, acc);
 }
-template <typename IoT> __device__ __forceinline__ float convolved(float acc, float bias, int activation) {
+template <bool plain> __device__ __forceinline__ float convolved(float acc, float bias, int activation) {
     acc = __fadd_rn(acc, bias);
     if (!activation) return acc;
-    return sizeof(IoT) == 4 ? silu_stepwise(acc) : silu(acc);
+    return plain ? silu_stepwise(acc) : silu(acc);
 }
 
 // One channel's convolution at position pos.
-template <typename IoT>
+template <typename IoT, bool plain>
 __device__ __forceinline__ float conv_channel(const ssd_step_params &a, const IoT *xbc, const IoT *ring, int channels,
                                               int c, int pos, int row) {
     const IoT *w = static_cast<const IoT *>(a.weight) + (int64_t)c * a.width;
@@ -84,15 +89,15 @@ __device__ __forceinline__ float conv_channel(const ssd_step_params &a, const Io
         if (k < a.width && k <= pos) {
             int r = row - k;
             if (r < 0) r += a.conv_rows;
-            acc = tap<IoT>(acc, to_float(w[a.width - 1 - k]), to_float(ring[(int64_t)r * channels + c]));
+            acc = tap<plain>(acc, to_float(w[a.width - 1 - k]), to_float(ring[(int64_t)r * channels + c]));
         }
     }
-    acc = tap<IoT>(acc, to_float(w[a.width - 1]), to_float(xbc[c]));
-    return convolved<IoT>(acc, a.bias ? to_float(static_cast<const IoT *>(a.bias)[c]) : 0.f, a.activation);
+    acc = tap<plain>(acc, to_float(w[a.width - 1]), to_float(xbc[c]));
+    return convolved<plain>(acc, a.bias ? to_float(static_cast<const IoT *>(a.bias)[c]) : 0.f, a.activation);
 }
 
 // Four neighbouring channels, all loads issued together.
-template <typename IoT, int kW>
+template <typename IoT, bool plain, int kW>
 __device__ __forceinline__ float4 conv_channels4(const ssd_step_params &a, const IoT *xbc, IoT *ring, int channels,
                                                  int c, int pos, int row, bool keep) {
     const Pack<IoT, 4 * kW> w = load_pack<IoT, 4 * kW>(static_cast<const IoT *>(a.weight) + (int64_t)c * kW);
@@ -111,8 +116,8 @@ __device__ __forceinline__ float4 conv_channels4(const ssd_step_params &a, const
     for (int j = 0; j < 4; ++j) {
         float acc = 0.f;
 #pragma unroll
-        for (int k = kW - 1; k >= 0; --k) acc = tap<IoT>(acc, to_float(w.v[kW * j + kW - 1 - k]), to_float(in[k].v[j]));
-        u[j] = convolved<IoT>(acc, to_float(bias.v[j]), a.activation);
+        for (int k = kW - 1; k >= 0; --k) acc = tap<plain>(acc, to_float(w.v[kW * j + kW - 1 - k]), to_float(in[k].v[j]));
+        u[j] = convolved<plain>(acc, to_float(bias.v[j]), a.activation);
     }
     if (keep) store_pack<IoT, 4>(ring + (int64_t)row * channels + c, in[0]);
     return make_float4(u[0], u[1], u[2], u[3]);
@@ -129,14 +134,16 @@ __device__ __forceinline__ float2 head_terms(const ssd_step_params &a, int b, in
 
 // kType: storage of the state; L: lanes of a row; E: state values a lane holds
 // of it (L E >= N); V: values of one copy; kDepth: row steps copied ahead; kSr:
-// stochastic rounding; stepwise: see above.
-template <int kType, int L, int E, int V, int kDepth, bool kSr, bool stepwise>
+// stochastic rounding; kF32Io: fp32 activations, else bf16 ones (an fp32 cache's
+// kernel takes either).
+template <int kType, int L, int E, int V, int kDepth, bool kSr, bool kF32Io>
 __global__ void __launch_bounds__(kStepThreads, kStepCtas<kType, E>) step_kernel(const ssd_step_params a, const StepPlan plan) {
     using StT = typename Stored<kType>::T;
     constexpr int kChunks = E / V, kStepGroups = kStepThreads / L;     // rows worked on at a time
     constexpr bool k8bit = kType == SSD_E4M3 || kType == SSD_I8;
+    constexpr bool stepwise = k8bit || kSr || (kF32Io && kType != SSD_F32);    // see above
     constexpr bool kAsync = V * sizeof(StT) >= 4;       // narrower shares are loaded when they are needed
-    // of each row: D x, later y; dt' x; the decay, times its scale where that is fused
+    // of each row: D x, later y; dt' x; the decay
     __shared__ __align__(16) float s_b[L * E], s_c[L * E], s_y[kStepMaxRows], s_dx[kStepMaxRows], s_keep[kStepMaxRows];
     __shared__ __align__(16) float s_scale[k8bit ? kStepMaxRows : 4];       // of each row: the old scale, then the new one
     __shared__ __align__(16) uint32_t s_keys[kSr ? 20 : 1];
@@ -150,7 +157,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas<kType, E>) step_kernel
     const int tid = threadIdx.x, lane = tid % L, grp = tid / L;
     const int r0 = g * plan.rows_g + run * plan.rows;        // the CTA's rows of the request: r0 .. r0 + rows - 1
     const int rows = min(plan.rows, plan.rows_g - run * plan.rows);
-    const bool bf16 = kType == SSD_F32 ? a.io_dtype == SSD_BF16 : !stepwise;
+    const bool bf16 = kType == SSD_F32 ? a.io_dtype == SSD_BF16 : !kF32Io;
 
     const int slot = a.slot_idx[(int64_t)b * (a.slot_idx_stride ? a.slot_idx_stride : 1)];
     const int pos = a.pos[b];
@@ -196,13 +203,14 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas<kType, E>) step_kernel
     const int cb = H * P + g * N, cc = cb + a.ngroups * N;      // first channels of B and C
     auto convolve = [&](auto io) {
         using IoT = decltype(io);
+        constexpr bool plain = stepwise || sizeof(IoT) == 4;
         const IoT *xbc = static_cast<const IoT *>(a.xbc) + (int64_t)b * a.xbc_stride;
         IoT *ring = static_cast<IoT *>(a.conv_cache) + (int64_t)slot * a.conv_rows * channels;
         auto head_of = [&](int row) { return (int)((uint64_t)(uint32_t)row * plan.p_mul >> plan.p_shift); };
         auto four = [&](int c, bool keep) {
-            if (a.width == 4) return conv_channels4<IoT, 4>(a, xbc, ring, channels, c, pos, ring_row, keep);
-            if (a.width == 3) return conv_channels4<IoT, 3>(a, xbc, ring, channels, c, pos, ring_row, keep);
-            return conv_channels4<IoT, 2>(a, xbc, ring, channels, c, pos, ring_row, keep);
+            if (a.width == 4) return conv_channels4<IoT, plain, 4>(a, xbc, ring, channels, c, pos, ring_row, keep);
+            if (a.width == 3) return conv_channels4<IoT, plain, 3>(a, xbc, ring, channels, c, pos, ring_row, keep);
+            return conv_channels4<IoT, plain, 2>(a, xbc, ring, channels, c, pos, ring_row, keep);
         };
         if (plan.vec4) {
             for (int i = 4 * tid; i < 2 * N + rows; i += 4 * kStepThreads) {
@@ -212,27 +220,23 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas<kType, E>) step_kernel
                         four(c, run == 0);
                 } else {
                     const int r = i - 2 * N, h = head_of(r0 + r);
-                    float4 sc = make_float4(1.f, 1.f, 1.f, 1.f);
+                    float4 sc{};
                     if (k8bit) sc = *reinterpret_cast<const float4 *>(a.state_scale + row0 + r);
                     const float2 ht = head_terms<IoT>(a, b, h);
                     const float dh = a.D ? a.D[h] : 0.f;
                     const float4 x = four(r0 + r, true);
                     const float dt = ht.x, keep = pos > 0 ? ht.y : 0.f;
                     if (pos == 0) sc = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (k8bit && stepwise) {
-                        *reinterpret_cast<float4 *>(s_scale + r) = sc;
-                        sc = make_float4(1.f, 1.f, 1.f, 1.f);
-                    }
+                    if (k8bit) *reinterpret_cast<float4 *>(s_scale + r) = sc;
                     *reinterpret_cast<float4 *>(s_dx + r) = make_float4(dt * x.x, dt * x.y, dt * x.z, dt * x.w);
                     *reinterpret_cast<float4 *>(s_y + r) = make_float4(dh * x.x, dh * x.y, dh * x.z, dh * x.w);
-                    *reinterpret_cast<float4 *>(s_keep + r) =
-                        make_float4(keep * sc.x, keep * sc.y, keep * sc.z, keep * sc.w);
+                    *reinterpret_cast<float4 *>(s_keep + r) = make_float4(keep, keep, keep, keep);
                 }
             }
         } else {
             for (int i = tid; i < 2 * N + rows; i += kStepThreads) {
                 const int c = i < N ? cb + i : i < 2 * N ? cc + i - N : r0 + i - 2 * N;
-                const float u = conv_channel<IoT>(a, xbc, ring, channels, c, pos, ring_row);
+                const float u = conv_channel<IoT, plain>(a, xbc, ring, channels, c, pos, ring_row);
                 if (i >= 2 * N || run == 0) ring[(int64_t)ring_row * channels + c] = xbc[c];
                 if (i < 2 * N) {
                     *(i < N ? s_b + i : s_c + i - N) = u;
@@ -241,18 +245,17 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas<kType, E>) step_kernel
                     const float2 ht = head_terms<IoT>(a, b, h);
                     s_dx[r] = ht.x * u;
                     s_y[r] = a.D ? a.D[h] * u : 0.f;
-                    const float sc = k8bit && pos > 0 ? a.state_scale[row0 + r] : 1.f, keep = pos > 0 ? ht.y : 0.f;
-                    if (k8bit) s_scale[r] = sc;
-                    s_keep[r] = k8bit && !stepwise ? keep * sc : keep;
+                    if (k8bit) s_scale[r] = pos > 0 ? a.state_scale[row0 + r] : 0.f;
+                    s_keep[r] = pos > 0 ? ht.y : 0.f;
                 }
             }
         }
     };
     if (kSr && tid < 20) round_keys(*a.sr_seed, tid, s_keys);
     for (int i = N + tid; i < L * E; i += kStepThreads) s_b[i] = s_c[i] = 0.f;
-    if constexpr (kType == SSD_F32 || !stepwise)
+    if constexpr (kType == SSD_F32 || !kF32Io)
         if (bf16) convolve(__nv_bfloat16{});
-    if constexpr (kType == SSD_F32 || stepwise)
+    if constexpr (kType == SSD_F32 || kF32Io)
         if (!bf16) convolve(float{});
     __syncthreads();
 
@@ -308,7 +311,6 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas<kType, E>) step_kernel
             } else if constexpr (V == 1) {
                 st[k] = fmaf(keep, st[k], dx * (k & 1 ? bv[k / 2].y : bv[k / 2].x));
                 acc.x = fmaf(k & 1 ? cv[k / 2].y : cv[k / 2].x, st[k], acc.x);
-                if (k8bit) big = max_abs(big, st[k], st[k]);
             } else {
 #pragma unroll
                 for (int e = k * V; e < (k + 1) * V; e += 2) {
@@ -316,7 +318,6 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas<kType, E>) step_kernel
                     acc = fma2(cv[e / 2], s, acc);
                     st[e] = s.x;
                     st[e + 1] = s.y;
-                    if (k8bit) big = max_abs(big, s.x, s.y);
                 }
             }
         }
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas<kType, E>) step_kernel
         float inv = 0.f, sc = 0.f;
         if constexpr (k8bit) {
             const float most = lanes_max<L>(big);
-            row_scale<stepwise>(most, code_limit<kType>(), &inv, &sc);
+            row_scale(most, code_limit<kType>(), &inv, &sc);
             if (lane == 0 && live) s_scale[r] = sc;
         }
         uint4 *rand = s_rand + (kRowBytes ? grp * rand_blocks(L * E) : 0);
