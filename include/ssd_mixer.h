@@ -19,7 +19,8 @@
  *
  * Common rules, as in ssd_scan.h: the caller owns every buffer; a call checks
  * its arguments on the host, enqueues exactly one kernel (none for an empty
- * batch) on `stream` and returns; nothing is allocated, synchronised or read
+ * batch) on `stream`, a stream of the calling thread's current device, on which
+ * the buffers lie too, and returns; nothing is allocated, synchronised or read
  * back, so a call may be captured in a CUDA graph; no call needs a workspace.
  * Invalid arguments return an error status and launch nothing.  Faults in
  * device-resident metadata make the kernel skip that request or sequence and

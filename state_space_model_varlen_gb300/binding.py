@@ -173,6 +173,22 @@ def _index_ptr(t):
     return t.data_ptr(), int(t.stride(0))
 
 
+def enqueue(entry, params, stream_ptr):
+    """``entry(params, stream)`` with the device of the block's tensors current: the library launches on the calling
+    thread's current device, and stream 0 is that device's.  A block filled by hand has no ``device`` and is the
+    caller's affair."""
+    device = getattr(params, "device", None)
+    if device is None:
+        return entry(params, stream_ptr or None)
+    if device.type != "cuda":
+        raise ValueError("the kernels run on CUDA tensors, not on the device %s" % device)
+    cuda = _torch().cuda
+    if device.index == cuda.current_device():
+        return entry(params, stream_ptr or None)
+    with cuda.device(device):
+        return entry(params, stream_ptr or None)
+
+
 def make_params(x, dt, A, B, C, cu_seqlens, *, dt_bias=None, D=None, state_cache=None,
                 slot_idx=None, has_init=None, write_final=True, out_y=None,
                 out_intermediate=None, dt_softplus=True, chunk_size=128, max_seqlen=0,

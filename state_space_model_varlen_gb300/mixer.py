@@ -4,7 +4,8 @@ norm) and the 8-bit state cache.
 
 Each operator has ``make_*_params`` (fills the argument block from torch
 tensors, no copies, no device reads: a serving loop keeps it), ``call_*`` (one
-call with such a block on a stream) and a function that does both and
+call with such a block on a stream of its tensors' device, whatever device is
+current; 0 is that device's default stream) and a function that does both and
 allocates its outputs.  Marshalling only: there is no fallback implementation.
 """
 from __future__ import annotations
@@ -61,7 +62,7 @@ def _entry(name):
 
 
 def _call(name, params, stream_ptr):
-    rc = (_entries.get(name) or _entry(name))(params, stream_ptr or None)
+    rc = binding.enqueue(_entries.get(name) or _entry(name), params, stream_ptr)
     if rc != SSD_OK:
         raise MixerError(name, rc)
 
@@ -77,7 +78,11 @@ class MixerError(SSDError):
 def _stream(t, stream):
     if not t.is_cuda:
         raise ValueError("the mixer operators run on CUDA tensors")
-    return (_torch().cuda.current_stream(t.device) if stream is None else stream).cuda_stream
+    if stream is None:
+        return _torch().cuda.current_stream(t.device).cuda_stream
+    if stream.device != t.device:
+        raise ValueError("the stream is of %s, the tensors are on %s" % (stream.device, t.device))
+    return stream.cuda_stream
 
 
 def _io(t):
@@ -119,6 +124,7 @@ def _one_device(*tensors):
     where = {t.device for t in tensors if t is not None}
     if len(where) > 1:
         raise ValueError("the tensors of a call must be on one device, not on %s" % sorted(map(str, where)))
+    return where.pop()
 
 
 def _seed_ptr(t):
@@ -155,11 +161,11 @@ def make_conv_params(xbc, weight, cu_seqlens, out_x, out_B=None, out_C=None, *, 
     """Fill ``ssd_conv_params``.  ``xbc`` [T, channels] may be a column range of a wider tensor; the channels go to
     ``out_x``, ``out_B`` and ``out_C`` ([T, ...], dense) in that order."""
     torch = _torch()
-    _one_device(xbc, weight, cu_seqlens, out_x, out_B, out_C, bias, conv_cache, slot_idx, start_pos, dt, out_dt,
-                device_status)
+    p = ConvParams()
+    p.device = _one_device(xbc, weight, cu_seqlens, out_x, out_B, out_C, bias, conv_cache, slot_idx, start_pos, dt,
+                           out_dt, device_status)
     T, C = xbc.shape
     S = cu_seqlens.shape[0] - 1
-    p = ConvParams()
     p.total_tokens, p.num_seqs, p.channels, p.width = T, S, C, weight.shape[-1]
     p.io_dtype, p.activation = _io(xbc), int(bool(activation))
     p.xbc, p.xbc_stride = _rows(xbc)
@@ -230,14 +236,14 @@ def make_step_params(xbc, dt, weight, A, conv_cache, state_cache, pos, slot_idx,
     """Fill ``ssd_step_params``: one token for each row of ``xbc``.  ``xbc``, ``z`` and ``dt`` may be column ranges of
     one in-projection output; ``sr_seed`` is a one-element int64 device tensor."""
     torch = _torch()
-    _one_device(xbc, dt, weight, A, conv_cache, state_cache, pos, slot_idx, out_y, z, conv_bias, dt_bias, D,
-                state_scale, sr_seed, device_status)
+    p = StepParams()
+    p.device = _one_device(xbc, dt, weight, A, conv_cache, state_cache, pos, slot_idx, out_y, z, conv_bias, dt_bias, D,
+                           state_scale, sr_seed, device_status)
     H, P, N = state_cache.shape[1:]
     B, C = xbc.shape
     if C != H * P + 2 * ngroups * N:
         raise ValueError("xbc has %d channels, %d heads of %d and %d groups of %d need %d"
                          % (C, H, P, ngroups, N, H * P + 2 * ngroups * N))
-    p = StepParams()
     p.batch, p.nheads, p.headdim, p.dstate, p.ngroups, p.width = B, H, P, N, ngroups, weight.shape[-1]
     p.io_dtype, p.state_dtype = _io(xbc), _state_code(state_cache)
     p.activation, p.dt_softplus = int(bool(activation)), int(bool(dt_softplus))
@@ -284,8 +290,8 @@ def step(xbc, dt, weight, A, conv_cache, state_cache, pos, slot_idx, *, ngroups,
 # ---------------------------------------------------------------------------
 def make_norm_params(y, weight, out, *, z=None, group_size=None, eps=1e-5, norm_before_gate=False) -> GatedNormParams:
     """Fill ``ssd_gated_norm_params``.  ``y``, ``z`` and ``out`` are [rows, columns] or [rows, H, P]."""
-    _one_device(y, weight, out, z)
     p = GatedNormParams()
+    p.device = _one_device(y, weight, out, z)
     columns = _row_numel(y)
     p.rows, p.columns = y.shape[0], columns
     p.group_size = columns if group_size is None else int(group_size)
@@ -322,9 +328,9 @@ def make_state_params(states, state_cache, state_scale, slot_idx, *, has_init=No
                       device_status=None) -> StateParams:
     """Fill ``ssd_state_params``: dense ``states`` [n, H, P, N] and the slots of an 8-bit cache."""
     torch = _torch()
-    _one_device(states, state_cache, state_scale, slot_idx, has_init, sr_seed, device_status)
-    n, H, P, N = states.shape
     p = StateParams()
+    p.device = _one_device(states, state_cache, state_scale, slot_idx, has_init, sr_seed, device_status)
+    n, H, P, N = states.shape
     p.num_states, p.nheads, p.headdim, p.dstate = n, H, P, N
     p.dense_dtype, p.state_dtype, p.num_slots = _io(states), _state_code(state_cache), state_cache.shape[0]
     _shape(state_cache, (state_cache.shape[0], H, P, N), "state_cache")

@@ -1,0 +1,95 @@
+"""On which device and stream the mixer operators' calls run, without a GPU: the
+library and torch's current device are stand-ins that record what they are
+given."""
+import contextlib
+
+import pytest
+import torch
+
+from state_space_model_varlen_gb300 import binding, mixer
+
+ENTRIES = {"ssd_conv_varlen": (mixer.ConvParams, mixer.call_conv), "ssd_step": (mixer.StepParams, mixer.call_step),
+           "ssd_gated_norm": (mixer.GatedNormParams, mixer.call_norm),
+           "ssd_state_store": (mixer.StateParams, mixer.call_state_store),
+           "ssd_state_load": (mixer.StateParams, mixer.call_state_load)}
+
+
+class Fake:
+    """A machine with several GPUs: the current one, and the (device, stream) of every launch."""
+
+    def __init__(self, monkeypatch, code=binding.SSD_OK):
+        self.current, self.launches, self.code = 0, [], code
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: self.current)
+        monkeypatch.setattr(torch.cuda, "device", self.device)
+
+    @contextlib.contextmanager
+    def device(self, device):
+        before, self.current = self.current, torch.device(device).index
+        try:
+            yield
+        finally:
+            self.current = before
+
+    def entry(self, params, stream):
+        self.launches.append((self.current, stream))
+        return self.code
+
+
+@pytest.mark.parametrize("name", sorted(ENTRIES))
+@pytest.mark.parametrize("stream", [0, 0x5000])
+def test_call_launches_on_the_device_of_its_tensors(monkeypatch, name, stream):
+    fake = Fake(monkeypatch)
+    monkeypatch.setitem(mixer._entries, name, fake.entry)
+    cls, call = ENTRIES[name]
+    p = cls()
+    for index in (1, 0, 2):
+        p.device = torch.device("cuda", index)
+        call(p, stream)
+        assert fake.launches[-1] == (index, stream or None) and fake.current == 0
+
+
+def test_device_is_put_back_after_a_refusal(monkeypatch):
+    fake = Fake(monkeypatch, binding.SSD_ERR_INVALID_ARG)
+    monkeypatch.setitem(mixer._entries, "ssd_gated_norm", fake.entry)
+    p = mixer.GatedNormParams()
+    p.device = torch.device("cuda", 1)
+    with pytest.raises(mixer.MixerError):
+        mixer.call_norm(p)
+    assert fake.launches == [(1, None)] and fake.current == 0
+
+
+def _blocks(device):
+    def t(*shape, dtype=torch.float32):
+        return torch.zeros(*shape, dtype=dtype, device=device)
+    i32 = torch.int32
+    states = (t(2, 1, 8, 8), t(3, 1, 8, 8, dtype=torch.int8), t(3, 1, 8), t(2, dtype=i32))
+    return [
+        (mixer.make_conv_params(t(5, 24), t(24, 4), t(2, dtype=i32), t(5, 1, 8), t(5, 1, 8), t(5, 1, 8)), mixer.call_conv),
+        (mixer.make_step_params(t(2, 24), t(2, 1), t(24, 4), t(1), t(3, 4, 24), t(3, 1, 8, 8), t(2, dtype=i32),
+                                t(2, dtype=i32), t(2, 1, 8), ngroups=1), mixer.call_step),
+        (mixer.make_norm_params(t(3, 8), t(8), t(3, 8)), mixer.call_norm),
+        (mixer.make_state_params(*states), mixer.call_state_store),
+        (mixer.make_state_params(*states), mixer.call_state_load)]
+
+
+def test_blocks_know_their_device_and_those_of_cpu_tensors_are_refused(monkeypatch):
+    for device in ("cpu", "meta"):
+        for p, call in _blocks(device):
+            assert p.device == torch.device(device)
+            with pytest.raises(ValueError, match="CUDA"):
+                call(p)
+
+
+def test_a_stream_of_another_device_is_refused():
+    class Tensor:
+        is_cuda, device = True, torch.device("cuda", 1)
+
+    class Stream:
+        cuda_stream = 0x7000
+
+        def __init__(self, index):
+            self.device = torch.device("cuda", index)
+
+    assert mixer._stream(Tensor, Stream(1)) == 0x7000
+    with pytest.raises(ValueError, match="stream"):
+        mixer._stream(Tensor, Stream(0))
