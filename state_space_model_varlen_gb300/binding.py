@@ -204,6 +204,7 @@ def make_params(x, dt, A, B, C, cu_seqlens, *, dt_bias=None, D=None, state_cache
     G, N = B.shape[1], B.shape[2]
     S = cu_seqlens.shape[0] - 1
     p = ScanParams()
+    p.device = x.device
     p.total_tokens, p.num_seqs, p.max_seqlen = T, S, int(max_seqlen)
     p.nheads, p.headdim, p.dstate, p.ngroups, p.chunk_size = H, P, N, G, int(chunk_size)
     p.io_dtype = _dtype_code(x, (SSD_F32, SSD_BF16))
@@ -261,7 +262,7 @@ def kernel_path(params: ScanParams) -> str:
 
 
 def call(params: ScanParams, stream_ptr: int = 0) -> None:
-    rc = load().ssd_scan_varlen(ctypes.byref(params), ctypes.c_void_p(stream_ptr or None))
+    rc = enqueue(load().ssd_scan_varlen, params, stream_ptr)
     if rc != SSD_OK:
         raise SSDError(rc)
 
@@ -272,7 +273,7 @@ def make_replay_params(scan: ScanParams, ring_x, ring_dt, ring_B, ring_window, r
     ``write_final=False``)."""
     torch = _torch()
     r = ReplayParams()
-    r.scan = scan
+    r.scan, r.device = scan, ring_x.device
     r.ring_x, r.ring_B = _ptr(ring_x), _ptr(ring_B)
     r.ring_dt = _ptr(ring_dt, torch.float32)
     r.ring_capacity = ring_x.shape[1]
@@ -284,7 +285,7 @@ def make_replay_params(scan: ScanParams, ring_x, ring_dt, ring_B, ring_window, r
 
 
 def call_replay(params: ReplayParams, stream_ptr: int = 0) -> None:
-    rc = load().ssd_replay_mtp(ctypes.byref(params), ctypes.c_void_p(stream_ptr or None))
+    rc = enqueue(load().ssd_replay_mtp, params, stream_ptr)
     if rc != SSD_OK:
         raise SSDError(rc)
 
@@ -298,7 +299,7 @@ def set_test_hooks(wait_cycles: int = 0, withhold_handover: int = -1,
 def call_noalloc(params: ScanParams, stream_ptr: int = 0) -> None:
     """``ssd_scan_varlen_noalloc``: the scan with the library's fixed scratch
     instead of ``params.workspace`` (for callers that cannot allocate)."""
-    rc = load().ssd_scan_varlen_noalloc(ctypes.byref(params), ctypes.c_void_p(stream_ptr or None))
+    rc = enqueue(load().ssd_scan_varlen_noalloc, params, stream_ptr)
     if rc != SSD_OK:
         raise SSDError(rc)
 

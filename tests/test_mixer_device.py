@@ -1,5 +1,5 @@
-"""On which device and stream the mixer operators' calls run, without a GPU: the
-library and torch's current device are stand-ins that record what they are
+"""On which device and stream the calls of the binding and of the mixer operators
+run, without a GPU: the library and torch's current device are stand-ins that record what they are
 given."""
 import contextlib
 
@@ -93,3 +93,36 @@ def test_a_stream_of_another_device_is_refused():
     assert mixer._stream(Tensor, Stream(1)) == 0x7000
     with pytest.raises(ValueError, match="stream"):
         mixer._stream(Tensor, Stream(0))
+
+
+@pytest.mark.parametrize("name,call,cls", [("ssd_scan_varlen", binding.call, binding.ScanParams),
+                                           ("ssd_scan_varlen_noalloc", binding.call_noalloc, binding.ScanParams),
+                                           ("ssd_replay_mtp", binding.call_replay, binding.ReplayParams)])
+@pytest.mark.parametrize("stream", [0, 0x5000])
+def test_scan_launches_on_the_device_of_its_tensors(monkeypatch, name, call, cls, stream):
+    fake = Fake(monkeypatch)
+
+    class Library:
+        pass
+
+    setattr(Library, name, staticmethod(fake.entry))
+    monkeypatch.setattr(binding, "load", lambda: Library)
+    p = cls()
+    for index in (1, 0, 2):
+        p.device = torch.device("cuda", index)
+        call(p, stream)
+        assert fake.launches[-1] == (index, stream or None) and fake.current == 0
+
+
+def test_scan_blocks_know_their_device():
+    for device in ("cpu", "meta"):
+        def t(*shape, dtype=torch.float32):
+            return torch.zeros(*shape, dtype=dtype, device=device)
+        cu = t(2, dtype=torch.int32)
+        p = binding.make_params(t(5, 1, 8), t(5, 1), t(1), t(5, 1, 8), t(5, 1, 8), cu, out_y=t(5, 1, 8))
+        one = t(1, dtype=torch.int32)
+        r = binding.make_replay_params(p, t(1, 4, 1, 8), t(1, 4, 1), t(1, 4, 1, 8), 4, one, one, one, one)
+        for block, call in ((p, binding.call), (p, binding.call_noalloc), (r, binding.call_replay)):
+            assert block.device == torch.device(device)
+            with pytest.raises(ValueError, match="CUDA"):
+                call(block)
