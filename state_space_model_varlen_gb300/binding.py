@@ -189,6 +189,20 @@ def enqueue(entry, params, stream_ptr):
         return entry(params, stream_ptr or None)
 
 
+def allocated(make, device, stream):
+    """The tensor ``make()``, whose memory a kernel on ``stream`` may write at once: it comes from that stream's part of
+    the allocator, where whatever used it before is done or ahead of the kernel.  The caller's current stream may use it
+    too (after the usual wait) and free it."""
+    if stream is None:
+        return make()
+    cuda = _torch().cuda
+    here = cuda.current_stream(device)
+    with cuda.stream(stream):
+        t = make()
+    t.record_stream(here)
+    return t
+
+
 def make_params(x, dt, A, B, C, cu_seqlens, *, dt_bias=None, D=None, state_cache=None,
                 slot_idx=None, has_init=None, write_final=True, out_y=None,
                 out_intermediate=None, dt_softplus=True, chunk_size=128, max_seqlen=0,
@@ -315,7 +329,7 @@ def ssd_scan_varlen(x, dt, A, B, C, cu_seqlens, *, dt_bias=None, D=None, state_c
     """
     torch = _torch()
     if out_y is None:
-        out_y = torch.empty_like(x)
+        out_y = allocated(lambda: torch.empty_like(x), x.device, stream)
     p = make_params(x, dt, A, B, C, cu_seqlens, dt_bias=dt_bias, D=D, state_cache=state_cache,
                     slot_idx=slot_idx, has_init=has_init, write_final=write_final, out_y=out_y,
                     out_intermediate=out_intermediate, dt_softplus=dt_softplus,
@@ -324,7 +338,7 @@ def ssd_scan_varlen(x, dt, A, B, C, cu_seqlens, *, dt_bias=None, D=None, state_c
     if workspace is None:
         need = workspace_size(p)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+            workspace = allocated(lambda: torch.empty(need, dtype=torch.uint8, device=x.device), x.device, stream)
             p.workspace, p.workspace_bytes = workspace.data_ptr(), need
     s = torch.cuda.current_stream(x.device) if stream is None else stream
     call(p, s.cuda_stream)

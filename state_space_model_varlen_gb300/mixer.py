@@ -216,11 +216,13 @@ def conv_varlen(xbc, weight, cu_seqlens, *, nheads, headdim, ngroups, dstate, bi
     """The short causal convolution of packed prompts; returns the scan's dense inputs (x, B, C, dt).  dt is None
     where none is given."""
     torch = _torch()
-    T = xbc.shape[0]
-    x = torch.empty(T, nheads, headdim, dtype=xbc.dtype, device=xbc.device)
-    B = torch.empty(T, ngroups, dstate, dtype=xbc.dtype, device=xbc.device)
-    C = torch.empty_like(B)
-    out_dt = None if dt is None else torch.empty(T, nheads, dtype=torch.float32, device=xbc.device)
+
+    def out(*shape, dtype=xbc.dtype):
+        return binding.allocated(lambda: torch.empty(xbc.shape[0], *shape, dtype=dtype, device=xbc.device), xbc.device,
+                                 stream)
+
+    x, B, C = out(nheads, headdim), out(ngroups, dstate), out(ngroups, dstate)
+    out_dt = None if dt is None else out(nheads, dtype=torch.float32)
     call_conv(make_conv_params(xbc, weight, cu_seqlens, x, B, C, bias=bias, activation=activation,
                                conv_cache=conv_cache, slot_idx=slot_idx, start_pos=start_pos, dt=dt, out_dt=out_dt,
                                device_status=device_status), _stream(xbc, stream))
@@ -279,7 +281,8 @@ def step(xbc, dt, weight, A, conv_cache, state_cache, pos, slot_idx, *, ngroups,
     """One token per request: convolution, state update, read-out and (with ``z``) gate; returns ``out_y``
     [batch, H, P].  Both caches are updated in place.  ``options`` are those of ``make_step_params``."""
     if out_y is None:
-        out_y = _torch().empty(xbc.shape[0], *state_cache.shape[1:3], dtype=xbc.dtype, device=xbc.device)
+        out_y = binding.allocated(lambda: _torch().empty(xbc.shape[0], *state_cache.shape[1:3], dtype=xbc.dtype,
+                                                         device=xbc.device), xbc.device, stream)
     call_step(make_step_params(xbc, dt, weight, A, conv_cache, state_cache, pos, slot_idx, out_y, ngroups=ngroups,
                                **options), _stream(xbc, stream))
     return out_y
@@ -315,7 +318,7 @@ def gated_rms_norm(y, weight=None, *, z=None, group_size=None, eps=1e-5, norm_be
                    stream=None):
     """RMS norm of ``y`` over groups of columns with the SiLU gate ``z``; returns ``out``."""
     if out is None:
-        out = _torch().empty(y.shape, dtype=y.dtype, device=y.device)
+        out = binding.allocated(lambda: _torch().empty(y.shape, dtype=y.dtype, device=y.device), y.device, stream)
     call_norm(make_norm_params(y, weight, out, z=z, group_size=group_size, eps=eps,
                                norm_before_gate=norm_before_gate), _stream(y, stream))
     return out
@@ -365,8 +368,9 @@ def state_load(state_cache, state_scale, slot_idx, *, states=None, dtype=None, h
     """Read slots of an 8-bit cache back into dense states (fp32 unless ``dtype`` or ``states`` says otherwise)."""
     torch = _torch()
     if states is None:
-        states = torch.empty(slot_idx.shape[0], *state_cache.shape[1:], dtype=dtype or torch.float32,
-                             device=state_cache.device)
+        states = binding.allocated(lambda: torch.empty(slot_idx.shape[0], *state_cache.shape[1:],
+                                                       dtype=dtype or torch.float32, device=state_cache.device),
+                                   state_cache.device, stream)
     call_state_load(make_state_params(states, state_cache, state_scale, slot_idx, has_init=has_init,
                                       device_status=device_status), _stream(states, stream))
     return states

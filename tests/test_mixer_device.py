@@ -2,6 +2,7 @@
 run, without a GPU: the library and torch's current device are stand-ins that record what they are
 given."""
 import contextlib
+from types import SimpleNamespace
 
 import pytest
 import torch
@@ -126,3 +127,59 @@ def test_scan_blocks_know_their_device():
             assert block.device == torch.device(device)
             with pytest.raises(ValueError, match="CUDA"):
                 call(block)
+
+
+class Memory:
+    """Stand-ins for torch's streams and allocator: what is allocated, on which stream, and for whose use."""
+
+    def __init__(self, monkeypatch):
+        self.current, self.made = "here", []
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: self.stream("here"))
+        monkeypatch.setattr(torch.cuda, "stream", self.switch)
+        for name in ("empty", "empty_like"):
+            monkeypatch.setattr(torch, name, self.make)
+        for module, names in ((mixer, ("make_conv_params", "make_step_params", "make_norm_params", "make_state_params",
+                                       "call_conv", "call_step", "call_norm", "call_state_load")),
+                              (binding, ("make_params", "call"))):
+            for name in names:
+                monkeypatch.setattr(module, name, lambda *args, **options: SimpleNamespace())
+        monkeypatch.setattr(binding, "workspace_size", lambda params: 256)
+
+    def stream(self, name):
+        return SimpleNamespace(name=name, cuda_stream=1, device=torch.device("cuda", 0))
+
+    @contextlib.contextmanager
+    def switch(self, stream):
+        before, self.current = self.current, stream.name
+        yield
+        self.current = before
+
+    def make(self, *args, **options):
+        t = SimpleNamespace(stream=self.current, users=[self.current], data_ptr=lambda: 0x1000)
+        t.record_stream = lambda stream: t.users.append(stream.name)
+        self.made.append(t)
+        return t
+
+
+def test_outputs_belong_to_the_stream_that_writes_them(monkeypatch):
+    """Memory of the current stream may still be read there when a kernel of another stream writes it: what a call
+    with stream= allocates comes from that stream, and the current one may free it."""
+    def tensor(*shape):
+        return SimpleNamespace(shape=shape, dtype=torch.float32, device=torch.device("cuda", 0), is_cuda=True)
+
+    memory = Memory(monkeypatch)
+    x = tensor(5, 1, 8)
+    for run, count in (
+            (lambda **k: mixer.conv_varlen(tensor(5, 24), None, None, nheads=1, headdim=8, ngroups=1, dstate=8,
+                                           dt=tensor(5, 1), **k), 4),
+            (lambda **k: mixer.step(tensor(5, 24), None, None, None, None, tensor(3, 1, 8, 8), None, None, ngroups=1,
+                                    **k), 1),
+            (lambda **k: mixer.gated_rms_norm(tensor(5, 8), **k), 1),
+            (lambda **k: mixer.state_load(tensor(3, 1, 8, 8), None, tensor(2), **k), 1),
+            (lambda **k: binding.ssd_scan_varlen(x, None, None, None, None, None, **k), 2)):
+        for name in ("side", "here"):
+            memory.made.clear()
+            monkeypatch.setattr(mixer, "_stream", lambda t, stream: 1)
+            run(**({} if name == "here" else {"stream": memory.stream(name)}))
+            assert [t.stream for t in memory.made] == [name] * count
+            assert all("here" in t.users for t in memory.made)
