@@ -3,7 +3,8 @@ Mamba2 mixer around the scan (packed convolution, single-token step, gated
 norm) and the 8-bit state cache.
 
 Each operator has ``make_*_params`` (fills the argument block from torch
-tensors, no copies, no device reads: a serving loop keeps it), ``call_*`` (one
+tensors, no copies, no device reads: a serving loop keeps it, and the block
+keeps its tensors), ``call_*`` (one
 call with such a block on a stream of its tensors' device, whatever device is
 current; 0 is that device's default stream) and a function that does both and
 allocates its outputs.  Marshalling only: there is no fallback implementation.
@@ -120,11 +121,12 @@ def _shape(t, want, what):
         raise ValueError("%s must have the shape %s, not %s" % (what, tuple(want), tuple(t.shape)))
 
 
-def _one_device(*tensors):
+def _hold(params, *tensors):
+    """The block's tensors, which live as long as it does, and their device."""
     where = {t.device for t in tensors if t is not None}
     if len(where) > 1:
         raise ValueError("the tensors of a call must be on one device, not on %s" % sorted(map(str, where)))
-    return where.pop()
+    params.device, params.tensors = where.pop(), tensors
 
 
 def _seed_ptr(t):
@@ -162,8 +164,8 @@ def make_conv_params(xbc, weight, cu_seqlens, out_x, out_B=None, out_C=None, *, 
     ``out_x``, ``out_B`` and ``out_C`` ([T, ...], dense) in that order."""
     torch = _torch()
     p = ConvParams()
-    p.device = _one_device(xbc, weight, cu_seqlens, out_x, out_B, out_C, bias, conv_cache, slot_idx, start_pos, dt,
-                           out_dt, device_status)
+    _hold(p, xbc, weight, cu_seqlens, out_x, out_B, out_C, bias, conv_cache, slot_idx, start_pos, dt, out_dt,
+          device_status)
     T, C = xbc.shape
     S = cu_seqlens.shape[0] - 1
     p.total_tokens, p.num_seqs, p.channels, p.width = T, S, C, weight.shape[-1]
@@ -239,8 +241,8 @@ def make_step_params(xbc, dt, weight, A, conv_cache, state_cache, pos, slot_idx,
     one in-projection output; ``sr_seed`` is a one-element int64 device tensor."""
     torch = _torch()
     p = StepParams()
-    p.device = _one_device(xbc, dt, weight, A, conv_cache, state_cache, pos, slot_idx, out_y, z, conv_bias, dt_bias, D,
-                           state_scale, sr_seed, device_status)
+    _hold(p, xbc, dt, weight, A, conv_cache, state_cache, pos, slot_idx, out_y, z, conv_bias, dt_bias, D, state_scale,
+          sr_seed, device_status)
     H, P, N = state_cache.shape[1:]
     B, C = xbc.shape
     if C != H * P + 2 * ngroups * N:
@@ -294,7 +296,7 @@ def step(xbc, dt, weight, A, conv_cache, state_cache, pos, slot_idx, *, ngroups,
 def make_norm_params(y, weight, out, *, z=None, group_size=None, eps=1e-5, norm_before_gate=False) -> GatedNormParams:
     """Fill ``ssd_gated_norm_params``.  ``y``, ``z`` and ``out`` are [rows, columns] or [rows, H, P]."""
     p = GatedNormParams()
-    p.device = _one_device(y, weight, out, z)
+    _hold(p, y, weight, out, z)
     columns = _row_numel(y)
     p.rows, p.columns = y.shape[0], columns
     p.group_size = columns if group_size is None else int(group_size)
@@ -332,7 +334,7 @@ def make_state_params(states, state_cache, state_scale, slot_idx, *, has_init=No
     """Fill ``ssd_state_params``: dense ``states`` [n, H, P, N] and the slots of an 8-bit cache."""
     torch = _torch()
     p = StateParams()
-    p.device = _one_device(states, state_cache, state_scale, slot_idx, has_init, sr_seed, device_status)
+    _hold(p, states, state_cache, state_scale, slot_idx, has_init, sr_seed, device_status)
     n, H, P, N = states.shape
     p.num_states, p.nheads, p.headdim, p.dstate = n, H, P, N
     p.dense_dtype, p.state_dtype, p.num_slots = _io(states), _state_code(state_cache), state_cache.shape[0]

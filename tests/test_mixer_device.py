@@ -2,6 +2,7 @@
 run, without a GPU: the library and torch's current device are stand-ins that record what they are
 given."""
 import contextlib
+import weakref
 from types import SimpleNamespace
 
 import pytest
@@ -79,6 +80,22 @@ def test_blocks_know_their_device_and_those_of_cpu_tensors_are_refused(monkeypat
             assert p.device == torch.device(device)
             with pytest.raises(ValueError, match="CUDA"):
                 call(p)
+
+
+def test_a_block_keeps_its_tensors():
+    """The addresses in a kept block stay those of its tensors, also of ones that the caller has let go."""
+    tensors = [torch.zeros(3, 8), torch.zeros(8), torch.zeros(3, 8), torch.zeros(3, 8)]
+    p = mixer.make_norm_params(*tensors[:3], z=tensors[3])
+    held = [weakref.ref(t) for t in tensors]
+    del tensors
+    assert [r().data_ptr() for r in held] == [p.y, p.weight, p.out, p.z]
+    del p
+    assert not any(r() for r in held)
+    has = torch.ones(2, dtype=torch.bool)
+    p = mixer.make_state_params(torch.zeros(2, 1, 8, 8), torch.zeros(3, 1, 8, 8, dtype=torch.int8), torch.zeros(3, 1, 8),
+                                torch.zeros(2, dtype=torch.int32), has_init=has)
+    has = weakref.ref(has)
+    assert has().data_ptr() == p.has_init
 
 
 def test_a_stream_of_another_device_is_refused():
