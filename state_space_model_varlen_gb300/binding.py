@@ -28,6 +28,7 @@ EXPORTED = ("ssd_replay_mtp", "ssd_scan_varlen", "ssd_scan_varlen_noalloc",
 
 class ScanParams(ctypes.Structure):
     """Mirror of ``ssd_scan_params``."""
+    device = None       # of the tensors, see block_device
     _fields_ = [
         ("total_tokens", ctypes.c_int64),
         ("num_seqs", ctypes.c_int32),
@@ -72,6 +73,7 @@ class ScanParams(ctypes.Structure):
 
 class ReplayParams(ctypes.Structure):
     """Mirror of ``ssd_replay_params``."""
+    device = None
     _fields_ = [
         ("scan", ScanParams),
         ("ring_x", ctypes.c_void_p),
@@ -173,11 +175,17 @@ def _index_ptr(t):
     return t.data_ptr(), int(t.stride(0))
 
 
+def block_device(device):
+    """What a block of tensors on ``device`` keeps as its ``device``: None where a launch need not look at the current
+    one, because there is no other (the look costs 0.8 us a call).  A block filled by hand has None too: its device is
+    the caller's affair."""
+    return None if device.type == "cuda" and _torch().cuda.device_count() == 1 else device
+
+
 def enqueue(entry, params, stream_ptr):
     """``entry(params, stream)`` with the device of the block's tensors current: the library launches on the calling
-    thread's current device, and stream 0 is that device's.  A block filled by hand has no ``device`` and is the
-    caller's affair."""
-    device = getattr(params, "device", None)
+    thread's current device, and stream 0 is that device's."""
+    device = params.device
     if device is None:
         return entry(params, stream_ptr or None)
     if device.type != "cuda":
@@ -218,7 +226,7 @@ def make_params(x, dt, A, B, C, cu_seqlens, *, dt_bias=None, D=None, state_cache
     G, N = B.shape[1], B.shape[2]
     S = cu_seqlens.shape[0] - 1
     p = ScanParams()
-    p.device = x.device
+    p.device = block_device(x.device)
     p.total_tokens, p.num_seqs, p.max_seqlen = T, S, int(max_seqlen)
     p.nheads, p.headdim, p.dstate, p.ngroups, p.chunk_size = H, P, N, G, int(chunk_size)
     p.io_dtype = _dtype_code(x, (SSD_F32, SSD_BF16))
@@ -287,7 +295,7 @@ def make_replay_params(scan: ScanParams, ring_x, ring_dt, ring_B, ring_window, r
     ``write_final=False``)."""
     torch = _torch()
     r = ReplayParams()
-    r.scan, r.device = scan, ring_x.device
+    r.scan, r.device = scan, block_device(ring_x.device)
     r.ring_x, r.ring_B = _ptr(ring_x), _ptr(ring_B)
     r.ring_dt = _ptr(ring_dt, torch.float32)
     r.ring_capacity = ring_x.shape[1]

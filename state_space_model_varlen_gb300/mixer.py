@@ -27,7 +27,8 @@ EXPORTED = ("ssd_conv_varlen", "ssd_gated_norm", "ssd_state_load", "ssd_state_st
 def _struct(name, fields):
     kinds = {"i32": ctypes.c_int32, "i64": ctypes.c_int64, "f32": ctypes.c_float, "p": ctypes.c_void_p}
     pairs = [(n, kinds[k]) for k, names in fields for n in names.split()]
-    return type(name, (ctypes.Structure,), {"_fields_": pairs, "__doc__": "Mirror of the C struct of this operator."})
+    return type(name, (ctypes.Structure,), {"_fields_": pairs, "__doc__": "Mirror of the C struct of this operator.",
+                                            "device": None})
 
 
 ConvParams = _struct("ConvParams", [
@@ -63,7 +64,8 @@ def _entry(name):
 
 
 def _call(name, params, stream_ptr):
-    rc = binding.enqueue(_entries.get(name) or _entry(name), params, stream_ptr)
+    entry = _entries.get(name) or _entry(name)
+    rc = entry(params, stream_ptr or None) if params.device is None else binding.enqueue(entry, params, stream_ptr)
     if rc != SSD_OK:
         raise MixerError(name, rc)
 
@@ -122,11 +124,11 @@ def _shape(t, want, what):
 
 
 def _hold(params, *tensors):
-    """The block's tensors, which live as long as it does, and their device."""
+    """The block's tensors, which live as long as it does, and their device (see ``binding.block_device``)."""
     where = {t.device for t in tensors if t is not None}
     if len(where) > 1:
         raise ValueError("the tensors of a call must be on one device, not on %s" % sorted(map(str, where)))
-    params.device, params.tensors = where.pop(), tensors
+    params.device, params.tensors = binding.block_device(where.pop()), tensors
 
 
 def _seed_ptr(t):

@@ -200,3 +200,10 @@ def test_outputs_belong_to_the_stream_that_writes_them(monkeypatch):
             run(**({} if name == "here" else {"stream": memory.stream(name)}))
             assert [t.stream for t in memory.made] == [name] * count
             assert all("here" in t.users for t in memory.made)
+
+
+@pytest.mark.parametrize("count,kept", [(1, None), (2, torch.device("cuda", 1))])
+def test_blocks_look_at_the_current_device_only_where_there_are_others(monkeypatch, count, kept):
+    monkeypatch.setattr(torch.cuda, "device_count", lambda: count)
+    assert binding.block_device(torch.device("cuda", 1)) == kept
+    assert binding.block_device(torch.device("cpu")) == torch.device("cpu")
