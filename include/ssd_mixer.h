@@ -84,7 +84,7 @@ extern "C" {
  * Channels [0, split0) go to out0, the next split1 to out1, the rest to out2,
  * each dense: the x, B and C of ssd_scan_varlen.  dt, in io_dtype, is widened
  * to the scan's fp32 out_dt by the same launch.
- * Tokens of no valid sequence are not written.
+ * Tokens of no valid sequence are written in no output.
  * Layouts:
  *   xbc    [T, channels]  io_dtype, row stride xbc_stride elements
  *   dt     [T, nheads]    io_dtype, row stride dt_stride, or NULL

@@ -55,9 +55,9 @@ struct Sequence {
 };
 constexpr int kSlides = 1, kKeeps = 2;      // of a group: every token has its window here; some go to the ring
 
-// dt of the tile's tokens widened to fp32
+// dt of the tile's tokens that are some valid sequence's, widened to fp32
 template <typename IoT>
-__device__ __forceinline__ void widen_dt(const ssd_conv_params &a, int64_t t0, int nt) {
+__device__ __forceinline__ void widen_dt(const ssd_conv_params &a, const Token *token, int64_t t0, int nt) {
     const IoT *dt = static_cast<const IoT *>(a.dt);
     for (int h = threadIdx.x; h < a.nheads; h += blockDim.x) {
         for (int i = 0; i < nt; i += kGroup) {
@@ -67,7 +67,7 @@ __device__ __forceinline__ void widen_dt(const ssd_conv_params &a, int64_t t0, i
                 if (i + j < nt) v[j] = to_float(dt[(t0 + i + j) * a.dt_stride + h]);
 #pragma unroll
             for (int j = 0; j < kGroup; ++j)
-                if (i + j < nt) a.out_dt[(t0 + i + j) * a.nheads + h] = v[j];
+                if (i + j < nt && token[i + j].local >= 0) a.out_dt[(t0 + i + j) * a.nheads + h] = v[j];
         }
     }
 }
@@ -134,11 +134,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
     const int W = kW ? kW : a.width;
     const int64_t t0 = (int64_t)blockIdx.x * tile;
     const int nt = (int)min((int64_t)tile, a.total_tokens - t0);
-    const int ct = (int)blockIdx.y - dt_column;
-    if (ct < 0) {
-        widen_dt<IoT>(a, t0, nt);
-        return;
-    }
+    const int ct = (int)blockIdx.y - dt_column;    // -1: dt alone, no channels
     const bool reporter = ct == 0 && a.device_status != nullptr;
 
     // ---- every load that depends on nothing: sequences, inputs, weights -----
@@ -150,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
     };
     Sequence seq{};
     if ((int)threadIdx.x < a.num_seqs) seq = look_up(threadIdx.x);
-    const int c = (ct * blockDim.x + threadIdx.x) * V;
+    const int c = ct < 0 ? a.channels : (ct * blockDim.x + threadIdx.x) * V;
     const bool mine = c < a.channels;
     const IoT *x = static_cast<const IoT *>(a.xbc) + t0 * a.xbc_stride + c;    // of the tile's first token
     Pack<IoT, V> next[kGroup], prev[kPast];
@@ -247,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
             const Sequence q = sequence[first];
             const int64_t local = t0 + i - q.begin, pos = q.start + local;
             const bool begins_here = q.begin >= t0;
-            if (i < nt ? begins_here || local >= W - 1 : begins_here && local < W - 1) {
+            if (i < nt ? begins_here || local >= W - 1 || ct < 0 : begins_here && local < W - 1) {
                 k.local = (int)min(local, (int64_t)0x7fffffff);
                 k.slot = q.slot;
                 k.row = q.slot >= 0 ? (int)(pos % a.conv_rows) : 0;
@@ -266,6 +262,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
         }
     }
     __syncthreads();
+    if (ct < 0) widen_dt<IoT>(a, token, t0, nt);
     if (!mine) {
         if constexpr (kAsync) wait_async<0>();
         return;
