@@ -464,12 +464,17 @@ template <typename IoT, int V, bool kSplit>
 cudaError_t launch(const ssd_conv_params &p, cudaStream_t stream) {
     const int lanes = (p.channels + V - 1) / V, ctiles = (lanes + kThreads - 1) / kThreads, dt = p.dt != nullptr ? 1 : 0;
     const int threads = ((lanes + ctiles - 1) / ctiles + 31) / 32 * 32;
+    // mean length below 64: many groups hold a sequence's first token (201
+    // sequences, 1,311 tokens of 5,376 channels: 14 us so, 18 the other way; 61,773 tokens of
+    // 10,240 channels in 32 sequences: 488 and 399)
+    const bool brief = !kSplit && p.total_tokens < 64LL * p.num_seqs;
     // the tile whose waves of CTAs take the least, a CTA's own start counted as
     // 24 tokens: long tiles for long batches, one wave of shorter ones below that
     int tile = kGroup;
     int64_t least = INT64_MAX;
-    // what the registers leave room for, at most the eight of the shared memory
-    const int64_t resident = 152LL * std::min(8, kMinCtas<IoT, V, 4> * kThreads / threads);
+    // what the registers leave room for, at most what the shared memory does: eight,
+    // with the ring's share of a group five (44 of 228 KB each)
+    const int64_t resident = 152LL * std::min(brief && p.width == 4 ? 5 : 8, kMinCtas<IoT, V, 4> * kThreads / threads);
     for (int t = kGroup; t <= kMaxTile; t += kGroup) {
         const int64_t ctas = (p.total_tokens + t - 1) / t * ctiles, cost = (ctas + resident - 1) / resident * (t + 24);
         if (cost <= least) {
@@ -480,10 +485,6 @@ cudaError_t launch(const ssd_conv_params &p, cudaStream_t stream) {
     const int64_t tiles = (p.total_tokens + tile - 1) / tile;
     if (tiles > 0x7fffffff || ctiles + dt > 65535) return cudaErrorInvalidConfiguration;
     const dim3 grid((unsigned)tiles, (unsigned)(ctiles + dt));
-    // mean length below 64: many groups hold a sequence's first token (201
-    // sequences, 1,311 tokens of 5,376 channels: 14 us so, 18 the other way; 61,773 tokens of
-    // 10,240 channels in 32 sequences: 488 and 399)
-    const bool brief = !kSplit && p.total_tokens < 64LL * p.num_seqs;
     auto run = [&](auto kernel) { return enqueue(kernel, grid, threads, stream, p, tile, dt); };
     switch (p.width) {
         case 2: return brief ? run(conv_kernel<IoT, V, 2, !kSplit, kSplit>) : run(conv_kernel<IoT, V, 2, false, kSplit>);
