@@ -55,19 +55,51 @@ struct Sequence {
 };
 constexpr int kSlides = 1, kKeeps = 2;      // of a group: every token has its window here; some go to the ring
 
-// dt of the tile's tokens that are some valid sequence's, widened to fp32
+// Sequence s as its metadata has it, and the status bits of what is wrong there.
+__device__ __forceinline__ Sequence look_up(const ssd_conv_params &a, int s) {
+    Sequence q = {a.cu_seqlens[s], a.cu_seqlens[s + 1], 0, -1};
+    if (a.start_pos) q.start = a.start_pos[s];
+    if (a.conv_cache) q.slot = a.slot_idx[s * (a.slot_idx_stride ? a.slot_idx_stride : 1)];
+    return q;
+}
+__device__ __forceinline__ int faults(const ssd_conv_params &a, const Sequence &q) {
+    if (q.begin < 0 || q.end < q.begin || q.end > a.total_tokens) return SSD_DEV_BAD_SEQLENS;
+    if (q.end > q.begin && a.conv_cache && (q.slot < 0 || q.slot >= a.num_slots)) return SSD_DEV_BAD_SLOT;
+    return q.end > q.begin && q.start < 0 ? SSD_DEV_BAD_POS : 0;
+}
+
+// dt of the tile's tokens that are some valid sequence's, widened to fp32.  The
+// first tokens' loads are on their way while the sequences are looked up.
 template <typename IoT>
-__device__ __forceinline__ void widen_dt(const ssd_conv_params &a, const Token *token, int64_t t0, int nt) {
-    const IoT *dt = static_cast<const IoT *>(a.dt);
+__device__ __forceinline__ void widen_dt(const ssd_conv_params &a, int64_t t0, int nt) {
+    __shared__ uint32_t live[kMaxTile / 32];
+    const IoT *dt = static_cast<const IoT *>(a.dt) + t0 * a.dt_stride;
+    float v[kGroup];
+    auto load = [&](int h, int i) {
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j)
+            if (i + j < nt) v[j] = to_float(dt[(i + j) * a.dt_stride + h]);
+    };
+    if ((int)threadIdx.x < a.nheads) load(threadIdx.x, 0);
+    if (threadIdx.x < kMaxTile / 32) live[threadIdx.x] = 0;
+    __syncthreads();
+    for (int s = threadIdx.x; s < a.num_seqs; s += blockDim.x) {
+        const Sequence q = look_up(a, s);
+        const int first = (int)max(q.begin - t0, (int64_t)0), end = (int)min(q.end - t0, (int64_t)nt);
+        if (faults(a, q) || end <= first) continue;
+        for (int w = first / 32; w * 32 < end; ++w) {
+            const int lo = max(first - w * 32, 0), n = min(end - w * 32, 32) - lo;
+            atomicOr(&live[w], (0xffffffffu >> (32 - n)) << lo);
+        }
+    }
+    __syncthreads();
     for (int h = threadIdx.x; h < a.nheads; h += blockDim.x) {
         for (int i = 0; i < nt; i += kGroup) {
-            float v[kGroup];
+            if (i > 0 || h >= (int)blockDim.x) load(h, i);
+            const uint32_t mask = live[i / 32] >> (i % 32);
 #pragma unroll
             for (int j = 0; j < kGroup; ++j)
-                if (i + j < nt) v[j] = to_float(dt[(t0 + i + j) * a.dt_stride + h]);
-#pragma unroll
-            for (int j = 0; j < kGroup; ++j)
-                if (i + j < nt && token[i + j].local >= 0) a.out_dt[(t0 + i + j) * a.nheads + h] = v[j];
+                if (mask >> j & 1) a.out_dt[(t0 + i + j) * a.nheads + h] = v[j];
         }
     }
 }
@@ -134,19 +166,17 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
     const int W = kW ? kW : a.width;
     const int64_t t0 = (int64_t)blockIdx.x * tile;
     const int nt = (int)min((int64_t)tile, a.total_tokens - t0);
-    const int ct = (int)blockIdx.y - dt_column;    // -1: dt alone, no channels
+    const int ct = (int)blockIdx.y - dt_column;
+    if (ct < 0) {
+        widen_dt<IoT>(a, t0, nt);
+        return;
+    }
     const bool reporter = ct == 0 && a.device_status != nullptr;
 
     // ---- every load that depends on nothing: sequences, inputs, weights -----
-    auto look_up = [&](int s) {
-        Sequence q = {a.cu_seqlens[s], a.cu_seqlens[s + 1], 0, -1};
-        if (a.start_pos) q.start = a.start_pos[s];
-        if (a.conv_cache) q.slot = a.slot_idx[s * (a.slot_idx_stride ? a.slot_idx_stride : 1)];
-        return q;
-    };
     Sequence seq{};
-    if ((int)threadIdx.x < a.num_seqs) seq = look_up(threadIdx.x);
-    const int c = ct < 0 ? a.channels : (ct * blockDim.x + threadIdx.x) * V;
+    if ((int)threadIdx.x < a.num_seqs) seq = look_up(a, threadIdx.x);
+    const int c = (ct * blockDim.x + threadIdx.x) * V;
     const bool mine = c < a.channels;
     const IoT *x = static_cast<const IoT *>(a.xbc) + t0 * a.xbc_stride + c;    // of the tile's first token
     Pack<IoT, V> next[kGroup], prev[kPast];
@@ -216,11 +246,8 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
     if (threadIdx.x == 0) tail = after = 0;
     __syncthreads();
     for (int s = threadIdx.x; s < a.num_seqs; s += blockDim.x) {
-        const Sequence q = s == (int)threadIdx.x ? seq : look_up(s);
-        int bad = 0;
-        if (q.begin < 0 || q.end < q.begin || q.end > a.total_tokens) bad = SSD_DEV_BAD_SEQLENS;
-        else if (q.end > q.begin && a.conv_cache && (q.slot < 0 || q.slot >= a.num_slots)) bad = SSD_DEV_BAD_SLOT;
-        else if (q.end > q.begin && q.start < 0) bad = SSD_DEV_BAD_POS;
+        const Sequence q = s == (int)threadIdx.x ? seq : look_up(a, s);
+        const int bad = faults(a, q);
         if (bad) {
             if (blockIdx.x == 0 && reporter) atomicOr(a.device_status, bad);
         } else if (q.begin < t0 + nt && q.end > t0 && q.end > q.begin) {
@@ -243,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
             const Sequence q = sequence[first];
             const int64_t local = t0 + i - q.begin, pos = q.start + local;
             const bool begins_here = q.begin >= t0;
-            if (i < nt ? begins_here || local >= W - 1 || ct < 0 : begins_here && local < W - 1) {
+            if (i < nt ? begins_here || local >= W - 1 : begins_here && local < W - 1) {
                 k.local = (int)min(local, (int64_t)0x7fffffff);
                 k.slot = q.slot;
                 k.row = q.slot >= 0 ? (int)(pos % a.conv_rows) : 0;
@@ -262,7 +289,6 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<IoT, V, kW>) conv_kernel(co
         }
     }
     __syncthreads();
-    if (ct < 0) widen_dt<IoT>(a, token, t0, nt);
     if (!mine) {
         if constexpr (kAsync) wait_async<0>();
         return;
@@ -465,8 +491,8 @@ cudaError_t launch(const ssd_conv_params &p, cudaStream_t stream) {
     const int lanes = (p.channels + V - 1) / V, ctiles = (lanes + kThreads - 1) / kThreads, dt = p.dt != nullptr ? 1 : 0;
     const int threads = ((lanes + ctiles - 1) / ctiles + 31) / 32 * 32;
     // mean length below 64: many groups hold a sequence's first token (201
-    // sequences, 1,311 tokens of 5,376 channels: 14 us so, 18 the other way; 61,773 tokens of
-    // 10,240 channels in 32 sequences: 488 and 399)
+    // sequences, 1,311 tokens of 5,376 channels: 16.8 us so, 22.3 the other way; 61,773
+    // tokens of 10,240 channels in 32 sequences: 492 and 399)
     const bool brief = !kSplit && p.total_tokens < 64LL * p.num_seqs;
     // the tile whose waves of CTAs take the least, a CTA's own start counted as
     // 24 tokens: long tiles for long batches, one wave of shorter ones below that

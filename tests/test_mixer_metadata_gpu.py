@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 @pytest.mark.parametrize("heads", [3, 130])
-@pytest.mark.parametrize("lens", [[40, 40, 40], [3, 70, 5, 1, 9, 2], [1] * 90, [300, 2, 200]])
+@pytest.mark.parametrize("lens", [[40, 40, 40], [3, 70, 5, 1, 9, 2], [1] * 90, [300, 2, 200], [0, 40, 0, 33, 0, 0, 25]])
 @pytest.mark.parametrize("what", ["padding", "slot", "start", "end"])
 def test_conv_writes_nothing_for_tokens_of_no_valid_sequence(lens, what, heads, io):
     """x, B, C and dt rows before and after the batch's sequences, and those of a faulty one, stay as they were."""
