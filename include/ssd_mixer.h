@@ -25,14 +25,18 @@
  * Invalid arguments return an error status and launch nothing.  Faults in
  * device-resident metadata make the kernel skip that request or sequence and
  * OR a bit into *device_status (if not NULL); the kernels never trap.  All
- * arithmetic is in fp32, rounded once where a value is stored.  Every pointer
- * must be aligned to its element type, else SSD_ERR_INVALID_ARG; 16-byte
- * aligned rows take the wide paths, others are computed as exactly.
+ * arithmetic is in fp32, rounded once where a value is stored.  SiLU goes through
+ * approximations of 2^v and 1 / v: relative error below 2^-20 + |v| 2^-23, zero
+ * below about v = -87.3 (results below 2^-119); ssd_step says where its
+ * convolution does not.  Every pointer must be aligned to its element type, else
+ * SSD_ERR_INVALID_ARG; 16-byte aligned rows take the wide paths, others are
+ * computed as exactly.
  *
  * Slots: slot_idx entry s is at slot_idx[s * slot_idx_stride] (0 = 1).  The
- * slots of one call must be distinct (entries of -1, ssd_step's padding, may
- * repeat); of two requests that name one slot it is unspecified what either
- * reads there and which one's write stays.
+ * slots of one call must be distinct (entries of -1 may repeat); of two requests
+ * that name one slot it is unspecified what either reads there and which one's
+ * write stays.  -1 marks padding in ssd_step alone; to the other entry points it
+ * is a bad slot like any that the cache does not have.
  */
 #ifndef SSD_MIXER_H_
 #define SSD_MIXER_H_
@@ -216,10 +220,11 @@ ssd_status ssd_gated_norm(const ssd_gated_norm_params *params, struct CUstream_s
 /* ------------------------------------------------------------------------
  * States [num_states, H, P, N] (SSD_F32 or SSD_BF16, dense) to and from
  * the slots of an 8-bit cache (state_cache [num_slots, H, P, N], state_scale
- * [num_slots, H, P]), in the form described at SSD_E4M3.  has_init (uint8
- * [num_states], NULL = all 1) is used by ssd_state_load alone: where it is 0
- * the state becomes zeros and the slot is not looked at.  sr_seed is used by
- * ssd_state_store alone.  dstate up to 256.                                */
+ * [num_slots, H, P]), in the form described at SSD_E4M3.  A state of a bad slot
+ * is skipped: the store writes nothing for it, the load leaves its part of
+ * states as it was.  has_init (uint8 [num_states], NULL = all 1) is used by
+ * ssd_state_load alone: where it is 0 the state becomes zeros and the slot is
+ * not looked at.  sr_seed is used by ssd_state_store alone.  dstate up to 256. */
 typedef struct {
     int32_t num_states;
     int32_t nheads, headdim, dstate;

@@ -55,8 +55,11 @@ template <int kPending> __device__ __forceinline__ void wait_async() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 
-// v sigmoid(v) through the ex2 and rcp approximations: about 2^-21 relative
-// error.  Where e^-v overflows the reciprocal of infinity gives the right 0.
+// v sigmoid(v) through the ex2 and rcp approximations, four instructions where
+// expf and a division take many: relative error below 2^-20 + |v| 2^-23, the
+// second part from the rounding of the exponent v log2(e) (2^-18 at v = -30).
+// Below about v = -87.3, where the result is below 2^-119, the reciprocal is
+// flushed and the result is zero.
 __device__ __forceinline__ float ex2_approx(float v) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));

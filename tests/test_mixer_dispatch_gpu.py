@@ -39,6 +39,25 @@ def test_conv_infinity_shows_in_its_window(io):
     assert np.isfinite(got).all()
 
 
+@pytest.mark.parametrize("channels", [64, 63])           # pairs and single values
+def test_silu_keeps_its_stated_error(channels):
+    """A convolution of width 1 with weight 1 is SiLU alone: relative error below 2^-20 + |v| 2^-23 down to -87, zero or
+    as exact below, and the limits at the infinities' side."""
+    torch = _torch()
+    v = torch.cat([torch.linspace(-87, 87, 63 * 64 * 40), torch.linspace(-1e-3, 1e-3, 63 * 64)]).cuda().view(-1, channels)
+    far = torch.tensor([-88.0, -100.0, -1e4, -3e38, 100.0, 3e38, 0.0, -0.0], device="cuda")[:, None].expand(8, channels)
+    x = torch.cat([v, far])
+    one = torch.ones(channels, 1, device="cuda")
+    out = torch.full_like(x, float("nan"))
+    cu = torch.tensor([0, x.shape[0]], dtype=torch.int32, device="cuda")
+    mixer.call_conv(mixer.make_conv_params(x, one, cu, out), torch.cuda.current_stream().cuda_stream)
+    got, a = _np(out), _np(x)
+    want = a * R.sigmoid(a)
+    assert np.all(np.abs(got - want) <= np.abs(want) * (2.0 ** -20 + np.abs(a) * 2.0 ** -23) + 2.0 ** -119)
+    near = np.abs(a) <= 87
+    assert np.all(np.abs(got - want)[near] <= (np.abs(want) * (2.0 ** -20 + np.abs(a) * 2.0 ** -23))[near])
+
+
 @pytest.mark.parametrize("kind,sr", [(k, None) for k in KINDS] + [("f16", 5), ("e4m3", 5), ("i8", 5)])
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 @pytest.mark.parametrize("B,H,P,N,G,W,pad", [
