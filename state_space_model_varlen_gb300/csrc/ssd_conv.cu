@@ -26,9 +26,9 @@
 // also where those lie in later tiles.
 //
 // Measured: 61,773 tokens of 10,240 bf16 channels in 32 prompts 399 us, 6.5 TB/s
-// (95 % of the copy rate); 2,232 tokens 22.5 us (floor 13.7); 200 single tokens
-// and a chunk of 1,111, 5,376 channels, 16.6 us (floor 4.2), where each group
-// with sequence starts is a memory round trip of its own.
+// (95 % of the copy rate); 2,232 tokens 22.4 us (floor 13.7); 200 single tokens
+// and a chunk of 1,111, 5,376 channels, 16.8 us (floor 4.2), where each group
+// with sequence starts, three of a tile, is a memory round trip of its own.
 #include <algorithm>
 
 #include "ssd_mixer_common.cuh"

@@ -31,9 +31,8 @@
 //
 // Measured, 128 requests of 128 heads x 64 rows x 128 values: fp32 cache 164 us,
 // 6.6 TB/s (98 % of the copy rate); bf16 86 us (94 %); e4m3 75 us to nearest and
-// 112 us stochastically (57 and 38 %), bound by instructions: Philox 22 us of
-// it, the roundings one by one 11, the conversions most of the rest.  One
-// request, fp32: 3.3 us in a graph.
+// 112 us stochastically (57 and 38 %), bound by instructions: Philox 21 us of
+// it, the roundings one by one 11.  One request, fp32: 3.3 us in a graph.
 #pragma once
 
 #include "ssd_mixer_common.cuh"
