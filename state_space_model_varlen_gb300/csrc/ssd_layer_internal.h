@@ -1,0 +1,17 @@
+// Internal declarations of the layer operators' translation units.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/ssd_layer.h"
+#include "ssd_mixer_internal.h"
+
+namespace ssd {
+
+// Each launches exactly one kernel; the arguments have been checked.
+cudaError_t launch_residual_norm(const ssd_residual_norm_params &p, cudaStream_t stream);
+cudaError_t launch_matvec4(const ssd_matvec4_params &p, cudaStream_t stream);
+cudaError_t launch_verify(const ssd_verify_params &p, cudaStream_t stream);
+
+}  // namespace ssd

@@ -1,0 +1,122 @@
+// Products of few rows with 4-bit weights.
+//
+//   out[r, o] = bias[o] + sum_k scale[o, g(k)] (code[o, k] - zero[o, g(k)]) x[r, k]
+//
+// The codes are read once for a tile of rows: bound by HBM for few rows.
+#include "ssd_layer_internal.h"
+#include "ssd_mixer_common.cuh"
+
+namespace ssd {
+namespace {
+
+template <int kType> __device__ __forceinline__ float stored_value(const void *p, int64_t i) {
+    using T = typename Stored<kType>::T;
+    float v;
+    decode<kType, 1>(load_pack<T, 1>(static_cast<const T *>(p) + i), &v);
+    return v;
+}
+// element i of an array of the types of x and scale
+__device__ __forceinline__ float value(const void *p, int64_t i, int type) {
+    switch (type) {
+        case SSD_F32: return stored_value<SSD_F32>(p, i);
+        case SSD_BF16: return stored_value<SSD_BF16>(p, i);
+        case SSD_F16: return stored_value<SSD_F16>(p, i);
+        case SSD_E4M3: return stored_value<SSD_E4M3>(p, i);
+    }
+    return stored_value<SSD_I8>(p, i);
+}
+__device__ __forceinline__ void put(void *p, int64_t i, int type, float v) {
+    if (type == SSD_F32) static_cast<float *>(p)[i] = v;
+    else static_cast<__nv_bfloat16 *>(p)[i] = from_float<__nv_bfloat16>(v);
+}
+
+// ---------------------------------------------------------------------------
+// Any sizes: a warp takes kOuts rows of weights, its lanes words of eight codes,
+// against eight rows of x that the CTA keeps in shared memory, 1,024 columns at a
+// time.  A weight is (code - zero) scale in fp32.
+// ---------------------------------------------------------------------------
+constexpr int kAnyWarps = 8, kOuts = 2, kAnyRows = 8, kAnyColumns = 1024, kAnyWords = kAnyColumns / 8;
+
+__global__ void __launch_bounds__(32 * kAnyWarps) matvec4_any_kernel(const ssd_matvec4_params a) {
+    __shared__ float4 xs[kAnyRows][2][kAnyWords];       // the halves of a word's columns apart: no bank conflicts
+    await_previous();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int K = a.in_features, groups = (K - 1) / a.group_size + 1, x_groups = a.x_scale ? (K - 1) / a.x_group + 1 : 0;
+    const int64_t bytes = ((int64_t)K + 1) / 2;
+    const int r0 = blockIdx.y * kAnyRows, o0 = (blockIdx.x * kAnyWarps + warp) * kOuts;
+    const int rows = min(kAnyRows, a.rows - r0);
+    const bool eights = a.group_size % 8 == 0;
+    float acc[kOuts][kAnyRows] = {};
+    for (int k0 = 0; k0 < K; k0 += kAnyColumns) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < kAnyRows * kAnyColumns; i += 32 * kAnyWarps) {
+            const int r = i / kAnyColumns, c = i % kAnyColumns;
+            const int64_t k = (int64_t)k0 + c;
+            float v = 0.f;
+            if (r < rows && k < K) {
+                v = value(a.x, (int64_t)(r0 + r) * a.x_stride + k, a.x_dtype);
+                if (a.x_scale) v *= a.x_scale[(int64_t)(r0 + r) * x_groups + k / a.x_group];
+            }
+            reinterpret_cast<float *>(&xs[r][(c >> 2) & 1][c >> 3])[c & 3] = v;
+        }
+        __syncthreads();
+        for (int w = lane; w < kAnyWords && k0 + 8 * w < K; w += 32) {
+            const int k = k0 + 8 * w;
+            float f[kOuts][8];
+#pragma unroll
+            for (int j = 0; j < kOuts; ++j) {
+                const int o = min(o0 + j, a.out_features - 1);
+                const uint8_t *src = a.weight + (int64_t)o * a.weight_stride + k / 2;
+                uint32_t word = 0;
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    if (k / 2 + b < bytes) word |= (uint32_t)src[b] << (8 * b);
+                const int64_t base = (int64_t)o * groups;
+                float s = 0.f, z = 8.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (i == 0 || !eights) {
+                        const int64_t g = base + min(k + i, K - 1) / a.group_size;
+                        s = value(a.scale, g, a.scale_dtype);
+                        if (a.zero) z = (float)a.zero[g];
+                    }
+                    f[j][i] = ((float)(word >> (4 * i) & 15u) - z) * s;
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < kAnyRows; ++r) {
+                if (r >= rows) break;
+                const float4 lo = xs[r][0][w], hi = xs[r][1][w];
+                const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+                for (int j = 0; j < kOuts; ++j)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (k + i < K) acc[j][r] = fmaf(f[j][i], v[i], acc[j][r]);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kOuts; ++j)
+#pragma unroll
+        for (int r = 0; r < kAnyRows; ++r) {
+            const float v = lanes_sum<32>(acc[j][r]);
+            const int o = o0 + j;
+            if (lane == 0 && r < rows && o < a.out_features)
+                put(a.out, (int64_t)(r0 + r) * a.out_stride + o, a.out_dtype,
+                    a.bias ? v + value(a.bias, o, a.out_dtype) : v);
+        }
+}
+
+cudaError_t launch_any(const ssd_matvec4_params &p, cudaStream_t stream) {
+    const int per = kAnyWarps * kOuts;
+    const dim3 grid((p.out_features - 1) / per + 1, (p.rows - 1) / kAnyRows + 1);
+    if (grid.y > 65535) return cudaErrorInvalidConfiguration;
+    return enqueue(matvec4_any_kernel, grid, 32 * kAnyWarps, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_matvec4(const ssd_matvec4_params &p, cudaStream_t stream) { return launch_any(p, stream); }
+
+}  // namespace ssd
