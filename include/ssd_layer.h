@@ -90,8 +90,10 @@ ssd_status ssd_residual_norm(const ssd_residual_norm_params *params, struct CUst
  * Codes are 0 .. 15, zero is 8 where it is NULL.  Code k of row o is the low
  * (k even) or high (k odd) half of byte k / 2 of the row.  x is fp32 or bf16, or
  * 8-bit codes times x_scale[r, k / x_group] (what ssd_residual_norm leaves).
- * All arithmetic is in fp32, each output is rounded once.  It is made for few
- * rows: more of them are computed as exactly, and read the weights again.
+ * All arithmetic is in fp32, each output is rounded once; a group's columns may be
+ * added before their scale is applied (15 |x| group_size has to be a fp32 number).
+ * It is made for few rows: more of them are computed as exactly, and read the
+ * weights again.
  * Layouts:
  *   x       [rows, in_features] x_dtype, row stride x_stride elements
  *   x_scale [rows, ceil(in_features / x_group)] fp32, dense (8-bit x alone)

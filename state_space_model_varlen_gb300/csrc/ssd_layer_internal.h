@@ -12,6 +12,8 @@ namespace ssd {
 // Each launches exactly one kernel; the arguments have been checked.
 cudaError_t launch_residual_norm(const ssd_residual_norm_params &p, cudaStream_t stream);
 cudaError_t launch_matvec4(const ssd_matvec4_params &p, cudaStream_t stream);
+// The tensor-core kernel of launch_matvec4, where it takes the call; false where it does not.
+bool launch_matvec4_mma(const ssd_matvec4_params &p, cudaStream_t stream, cudaError_t *error);
 cudaError_t launch_verify(const ssd_verify_params &p, cudaStream_t stream);
 
 }  // namespace ssd

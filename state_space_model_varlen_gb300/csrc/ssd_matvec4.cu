@@ -117,6 +117,9 @@ cudaError_t launch_any(const ssd_matvec4_params &p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_matvec4(const ssd_matvec4_params &p, cudaStream_t stream) { return launch_any(p, stream); }
+cudaError_t launch_matvec4(const ssd_matvec4_params &p, cudaStream_t stream) {
+    cudaError_t error;
+    return launch_matvec4_mma(p, stream, &error) ? error : launch_any(p, stream);
+}
 
 }  // namespace ssd

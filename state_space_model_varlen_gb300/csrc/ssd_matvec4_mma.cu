@@ -1,0 +1,461 @@
+// Products of few rows with 4-bit weights on the tensor cores, for rows of weights
+// in whole 16 bytes and groups of a multiple of 32 columns.
+//
+// A tile is 16 outputs; a warp multiplies it by 128 columns at a step
+// (mma.m16n8k16, weights as the 16 rows, rows of x as the columns).  code - zero is
+// an integer below 2^4 and exact in bf16, as are 8-bit activations; fp32 activations
+// become three bf16 parts of eight bits each, which together are exact.  Sums within
+// a group are the instruction's fp32 sums, the groups' scales are applied to them
+// in fp32.
+//
+// Bound by HBM: codes stream through a ring of asynchronous copies of each warp's
+// own, kStages steps deep; x is in shared memory for good.  The columns of a tile
+// are split over the warps of a CTA, and over a cluster of CTAs where there are few
+// tiles; the parts are added in a fixed order.
+#include "ssd_layer_internal.h"
+#include "ssd_mixer_common.cuh"
+
+namespace ssd {
+namespace {
+
+constexpr int kStages = 4, kMaxWarps = 8, kTile = 16, kStep = 128;
+constexpr int kSmemLimit = 227 * 1024;
+
+struct Plan {
+    ssd_matvec4_params p;
+    int row_tile;               // rows of x of a pass
+    int split;                  // CTAs of a cluster, which share a tile's columns
+    int warps;
+    int tiles, clusters;
+    int steps;                  // of a row: ceil(K / 128)
+    int per_warp;               // steps of a warp for one tile
+    int groups, x_groups;       // of a row
+    int group_blocks, x_group_blocks;   // 32-column blocks of a group
+    uint32_t group_magic, x_group_magic;        // floor(2^32 / blocks) + 1
+    int slice_x_groups;         // most x groups that a CTA's columns meet
+    int x_stride;               // bytes of a row of x in shared memory
+    int scale_slots;            // tiles whose scales are held
+    int scale_bytes, zero_bytes;        // of a tile
+    int off_x, off_xs, off_scale, off_zero, off_part, off_own, smem;
+};
+
+__device__ __forceinline__ int group_of(int block, int blocks, uint32_t magic) {
+    return blocks == 1 ? block : (int)__umulhi((uint32_t)block, magic);
+}
+
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Codes i and i + 4 of a word (at bits 4 i and 4 i + 16) less their zero, as bf16:
+// the code as the low bits of 128's mantissa, minus 128 + zero.  Exact.
+__device__ __forceinline__ uint32_t codes2(uint32_t word, int i, uint32_t zero) {
+    const uint32_t v = (word >> (4 * i) & 0x000f000fu) | 0x43004300u;
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(zero));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+__device__ __forceinline__ float scale_at(const uint8_t *scales, int i, int type) {
+    if (type == SSD_F32) return reinterpret_cast<const float *>(scales)[i];
+    const uint16_t h = reinterpret_cast<const uint16_t *>(scales)[i];
+    return type == SSD_BF16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
+}
+
+// eight consecutive values of a row of x
+__device__ __forceinline__ void load8(float (&v)[8], const ssd_matvec4_params &p, int64_t at, int live, bool wide) {
+    if (wide && live == 8) {
+        if (p.x_dtype == SSD_F32) {
+            const auto a = load_pack<float, 8>(static_cast<const float *>(p.x) + at);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = a.v[i];
+        } else if (p.x_dtype == SSD_BF16) {
+            decode<SSD_BF16, 8>(load_pack<__nv_bfloat16, 8>(static_cast<const __nv_bfloat16 *>(p.x) + at), v);
+        } else {
+            const auto a = load_pack<uint8_t, 8>(static_cast<const uint8_t *>(p.x) + at);
+            if (p.x_dtype == SSD_E4M3) decode<SSD_E4M3, 8>(a, v);
+            else decode<SSD_I8, 8>(a, v);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        v[i] = 0.f;
+        if (i >= live) continue;
+        const int64_t e = at + i;
+        if (p.x_dtype == SSD_F32) v[i] = static_cast<const float *>(p.x)[e];
+        else if (p.x_dtype == SSD_BF16) v[i] = to_float(static_cast<const __nv_bfloat16 *>(p.x)[e]);
+        else if (p.x_dtype == SSD_E4M3) decode<SSD_E4M3, 1>(load_pack<uint8_t, 1>(static_cast<const uint8_t *>(p.x) + e), v + i);
+        else decode<SSD_I8, 1>(load_pack<uint8_t, 1>(static_cast<const uint8_t *>(p.x) + e), v + i);
+    }
+}
+
+// The block of `bytes` at src into shared memory: asynchronously in 16 bytes where
+// it is aligned (its size always is), else byte by byte, at once.
+__device__ __forceinline__ void copy_block(uint8_t *dst, const uint8_t *src, int bytes, int live) {
+    if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
+        for (int i = threadIdx.x * 16; i < bytes; i += blockDim.x * 16) {
+            if (i + 16 <= live) {
+                copy_async<16>(dst + i, src + i, true);
+            } else {
+                for (int j = i; j < i + 16; ++j) dst[j] = j < live ? src[j] : 0;
+            }
+        }
+    } else {
+        for (int i = threadIdx.x; i < bytes; i += blockDim.x) dst[i] = i < live ? src[i] : 0;
+    }
+}
+
+// kCols: eights of columns (rows of x, or their parts) of a pass.  kBlocks: 32-column
+// blocks that certainly share their scales (1, 2, or 4: a step).
+template <int kCols, int kBlocks, bool kX8>
+__global__ void __launch_bounds__(32 * kMaxWarps, kCols <= 2 ? 3 : kCols == 4 ? 2 : 1) matvec4_mma_kernel(const __grid_constant__ Plan plan) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    constexpr int kPitch = kBlocks == 4 ? 64 : 80;      // bytes of a row of a stage: no bank conflicts in words of the quads
+    const ssd_matvec4_params &p = plan.p;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int rank = blockIdx.x % plan.split, cluster = blockIdx.x / plan.split;
+    const int r0 = blockIdx.y * plan.row_tile, rows = min(plan.row_tile, p.rows - r0);
+    const int parts = p.x_dtype == SSD_F32 ? 3 : 1, cols = rows * parts;
+    const int step0 = (int)((int64_t)plan.steps * rank / plan.split), step1 = (int)((int64_t)plan.steps * (rank + 1) / plan.split);
+    const int K = p.in_features, row_bytes = K / 2;
+    uint8_t *const ring = smem + warp * (kStages * kTile * kPitch);
+    uint8_t *const xs = smem + plan.off_x;
+    float *const xsc = reinterpret_cast<float *>(smem + plan.off_xs);
+    float *const part = reinterpret_cast<float *>(smem + plan.off_part);
+    float *const own = reinterpret_cast<float *>(smem + plan.off_own);
+    const int my_tiles = (plan.tiles - cluster + plan.clusters - 1) / plan.clusters;
+    const int total = my_tiles * plan.per_warp;
+    await_previous();
+
+    auto copy_scales = [&](int i) {             // of the CTA's tile i
+        const int64_t o0 = (int64_t)(cluster + i * plan.clusters) * kTile;
+        const int live = (int)min((int64_t)kTile, p.out_features - o0), slot = i % plan.scale_slots;
+        const int size = plan.scale_bytes / (kTile * plan.groups);
+        copy_block(smem + plan.off_scale + slot * plan.scale_bytes,
+                   static_cast<const uint8_t *>(p.scale) + o0 * plan.groups * size, plan.scale_bytes, live * plan.groups * size);
+        if (p.zero)
+            copy_block(smem + plan.off_zero + slot * plan.zero_bytes, p.zero + o0 * plan.groups, plan.zero_bytes, live * plan.groups);
+    };
+    // Step q of the warp's: its codes, and the scales of the next tile, which are
+    // then complete for all when the tile of this step has been added up.
+    auto issue = [&](int q) {
+        if (q < total) {
+            const int i = q / plan.per_warp, j = q - i * plan.per_warp;
+            const int step = step0 + j * plan.warps + warp;
+            const int64_t o0 = (int64_t)(cluster + i * plan.clusters) * kTile;
+            const int byte = step * (kStep / 2) + t * 16;
+            if (step < step1) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int64_t o = min(o0 + g + 8 * h, (int64_t)p.out_features - 1);
+                    copy_async<16>(ring + (q % kStages) * (kTile * kPitch) + (g + 8 * h) * kPitch + t * 16,
+                                   p.weight + o * p.weight_stride + (byte < row_bytes ? byte : 0), byte < row_bytes);
+                }
+            }
+            if (j == plan.per_warp - 1 && i + 1 < my_tiles) copy_scales(i + 1);
+        }
+        commit_async();
+    };
+
+    if (my_tiles > 0) copy_scales(0);
+#pragma unroll
+    for (int q = 0; q < kStages - 1; ++q) issue(q);
+
+    // x of the CTA's columns as bf16, in chunks of eight: values i and i + 4 side by
+    // side, as the codes of a word come; within a step the chunk that quad lane t reads
+    // with its j-th word at 4 j + t
+    {
+        const int chunks = (step1 - step0) * 16;
+        const int size = p.x_dtype == SSD_F32 ? 16 : p.x_dtype == SSD_BF16 ? 16 : 8;
+        const int elem = p.x_dtype == SSD_F32 ? 4 : p.x_dtype == SSD_BF16 ? 2 : 1;
+        const bool wide = (reinterpret_cast<uintptr_t>(p.x) % size) == 0 && (p.x_stride * elem) % size == 0;
+        for (int i = threadIdx.x; i < rows * chunks; i += blockDim.x) {
+            const int r = i / chunks, c = i - r * chunks;
+            const int64_t k = (int64_t)step0 * kStep + c * 8;
+            float v[8];
+            load8(v, p, (r0 + r) * p.x_stride + k, (int)max((int64_t)0, min((int64_t)8, K - k)), wide);
+            const int at = kBlocks == 4 ? (c & ~15) | (c & 3) << 2 | (c >> 2 & 3) : c;
+            for (int part = 0; part < parts; ++part) {
+                uint32_t u[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    u[j] = __float_as_uint(v[j]);
+                    if (v[j] != v[j]) u[j] = 0x7fc00000u;
+                    const float cut = __uint_as_float(u[j] & 0xffff0000u);
+                    v[j] = fabsf(cut) < __int_as_float(0x7f800000) ? v[j] - cut : 0.f;
+                }
+                const uint4 w = make_uint4(__byte_perm(u[0], u[4], 0x7632), __byte_perm(u[1], u[5], 0x7632),
+                                           __byte_perm(u[2], u[6], 0x7632), __byte_perm(u[3], u[7], 0x7632));
+                *reinterpret_cast<uint4 *>(xs + (part * rows + r) * plan.x_stride + at * 16) = w;
+            }
+        }
+        if constexpr (kX8) {
+            const int first = group_of(step0 * 4, plan.x_group_blocks, plan.x_group_magic);
+            for (int i = threadIdx.x; i < plan.slice_x_groups * kCols * 8; i += blockDim.x) {
+                const int r = i % (kCols * 8), x_group = first + i / (kCols * 8);
+                xsc[i] = r < rows && x_group < plan.x_groups ? p.x_scale[(int64_t)(r0 + r) * plan.x_groups + x_group] : 0.f;
+            }
+        }
+    }
+    wait_async<kStages - 2>();
+    __syncthreads();
+
+    const int first_x_group = kX8 ? group_of(step0 * 4, plan.x_group_blocks, plan.x_group_magic) : 0;
+    float sum[kCols][4];
+#pragma unroll
+    for (int n = 0; n < kCols; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[n][i] = 0.f;
+    int tile = 0, j = 0;
+    for (int q = 0; q < total; ++q) {
+        wait_async<kStages - 2>();
+        if constexpr (kBlocks < 4) __syncwarp();
+        issue(q + kStages - 1);
+        const int step = step0 + j * plan.warps + warp;
+        if (step < step1) {
+            const uint8_t *const codes = ring + (q % kStages) * (kTile * kPitch) + g * kPitch;
+            const uint8_t *const scales = smem + plan.off_scale + (tile % plan.scale_slots) * plan.scale_bytes;
+            const uint8_t *const zeros = smem + plan.off_zero + (tile % plan.scale_slots) * plan.zero_bytes;
+            const uint8_t *const x = xs + g * plan.x_stride + (step - step0) * (kStep * 2) + t * 16;
+            uint32_t lo[4], hi[4];
+            if constexpr (kBlocks == 4) {
+                *reinterpret_cast<uint4 *>(lo) = *reinterpret_cast<const uint4 *>(codes + t * 16);
+                *reinterpret_cast<uint4 *>(hi) = *reinterpret_cast<const uint4 *>(codes + 8 * kPitch + t * 16);
+            }
+#pragma unroll
+            for (int f = 0; f < 4 / kBlocks; ++f) {
+                const int block = step * 4 + f * kBlocks;
+                if (kBlocks < 4 && block * 32 >= K) break;
+                const int gi = group_of(block, plan.group_blocks, plan.group_magic);
+                uint32_t zlo = 0x43084308u, zhi = 0x43084308u;          // 128 + 8
+                if (p.zero) {
+                    zlo = 0x43004300u + zeros[g * plan.groups + gi] * 0x00010001u;
+                    zhi = 0x43004300u + zeros[(g + 8) * plan.groups + gi] * 0x00010001u;
+                }
+                float acc[kCols][4];
+#pragma unroll
+                for (int n = 0; n < kCols; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b) {
+                    const int w = f * kBlocks + b;
+                    if constexpr (kBlocks < 4) {
+                        lo[w] = *reinterpret_cast<const uint32_t *>(codes + w * 16 + t * 4);
+                        hi[w] = *reinterpret_cast<const uint32_t *>(codes + 8 * kPitch + w * 16 + t * 4);
+                    }
+                    const uint32_t a0[4] = {codes2(lo[w], 0, zlo), codes2(hi[w], 0, zhi), codes2(lo[w], 1, zlo), codes2(hi[w], 1, zhi)};
+                    const uint32_t a1[4] = {codes2(lo[w], 2, zlo), codes2(hi[w], 2, zhi), codes2(lo[w], 3, zlo), codes2(hi[w], 3, zhi)};
+#pragma unroll
+                    for (int n = 0; n < kCols; ++n) {
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (n * 8 + g < cols) v = *reinterpret_cast<const uint4 *>(x + n * 8 * plan.x_stride + w * 64);
+                        mma(acc[n], a0, v.x, v.y);
+                        mma(acc[n], a1, v.z, v.w);
+                    }
+                }
+                const float slo = scale_at(scales, g * plan.groups + gi, p.scale_dtype);
+                const float shi = scale_at(scales, (g + 8) * plan.groups + gi, p.scale_dtype);
+                const int xg = kX8 ? group_of(block, plan.x_group_blocks, plan.x_group_magic) - first_x_group : 0;
+#pragma unroll
+                for (int n = 0; n < kCols; ++n) {
+                    if constexpr (kX8) {
+                        const float2 s = *reinterpret_cast<const float2 *>(xsc + (xg * kCols + n) * 8 + 2 * t);
+                        sum[n][0] = fmaf(acc[n][0] * s.x, slo, sum[n][0]);
+                        sum[n][1] = fmaf(acc[n][1] * s.y, slo, sum[n][1]);
+                        sum[n][2] = fmaf(acc[n][2] * s.x, shi, sum[n][2]);
+                        sum[n][3] = fmaf(acc[n][3] * s.y, shi, sum[n][3]);
+                    } else {
+                        sum[n][0] = fmaf(acc[n][0], slo, sum[n][0]);
+                        sum[n][1] = fmaf(acc[n][1], slo, sum[n][1]);
+                        sum[n][2] = fmaf(acc[n][2], shi, sum[n][2]);
+                        sum[n][3] = fmaf(acc[n][3], shi, sum[n][3]);
+                    }
+                }
+            }
+        }
+        if (++j < plan.per_warp) continue;
+        // the tile's parts: of the warps, then of the cluster's CTAs.  Two buffers, so
+        // that one barrier a tile is enough.
+        j = 0;
+        constexpr int kWide = kCols * 8;
+        float *const mine = part + ((tile & 1) * plan.warps + warp) * (kTile * kWide);
+#pragma unroll
+        for (int n = 0; n < kCols; ++n) {
+            *reinterpret_cast<float2 *>(mine + g * kWide + n * 8 + 2 * t) = make_float2(sum[n][0], sum[n][1]);
+            *reinterpret_cast<float2 *>(mine + (g + 8) * kWide + n * 8 + 2 * t) = make_float2(sum[n][2], sum[n][3]);
+            sum[n][0] = sum[n][1] = sum[n][2] = sum[n][3] = 0.f;
+        }
+        __syncthreads();
+        const float *const all = part + (tile & 1) * plan.warps * (kTile * kWide);
+        const int64_t o0 = (int64_t)(cluster + tile * plan.clusters) * kTile;
+        auto finish = [&](int r, int o, float v) {
+            if (o0 + o >= p.out_features) return;
+            const int64_t at = (r0 + r) * p.out_stride + o0 + o;
+            if (p.out_dtype == SSD_F32) {
+                if (p.bias) v += static_cast<const float *>(p.bias)[o0 + o];
+                static_cast<float *>(p.out)[at] = v;
+            } else {
+                if (p.bias) v += to_float(static_cast<const __nv_bfloat16 *>(p.bias)[o0 + o]);
+                static_cast<__nv_bfloat16 *>(p.out)[at] = from_float<__nv_bfloat16>(v);
+            }
+        };
+        float *const own_now = own + (tile & 1) * (kTile * kWide);
+        for (int i = threadIdx.x; i < rows * kTile; i += blockDim.x) {
+            const int r = i / kTile, o = i % kTile;
+            float v = 0.f;
+            for (int part_ = 0; part_ < parts; ++part_)
+                for (int w = 0; w < plan.warps; ++w) v += all[(w * kTile + o) * kWide + part_ * rows + r];
+            if (plan.split == 1) finish(r, o, v);
+            else own_now[i] = v;
+        }
+        if (plan.split > 1) {
+            cluster_barrier();
+            const uint32_t local = (uint32_t)__cvta_generic_to_shared(own_now);
+            for (int i = rank * blockDim.x + threadIdx.x; i < rows * kTile; i += plan.split * blockDim.x) {
+                float v = 0.f;
+                for (int c = 0; c < plan.split; ++c) {
+                    uint32_t at;
+                    float f;
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(local + i * 4), "r"(c));
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(at) : "memory");
+                    v += f;
+                }
+                finish(i / kTile, i % kTile, v);
+            }
+        }
+        ++tile;
+    }
+    // no CTA leaves while another reads its part
+    if (plan.split > 1)
+        cluster_barrier();
+}
+
+int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
+int up(int v, int to) { return (v + to - 1) / to * to; }
+
+// Shared memory of a plan whose split, warps and rows are set.
+void lay_out(Plan &q, int col_tiles, int blocks) {
+    const int parts = q.p.x_dtype == SSD_F32 ? 3 : 1, slice = (q.steps - 1) / q.split + 1;
+    q.per_warp = (slice - 1) / q.warps + 1;
+    q.x_stride = up(slice * kStep * 2, 128) + 64;       // two rows of x beside one another in the banks
+    q.scale_slots = (kStages - 1) / q.per_warp + 2;
+    const int size = q.p.scale_dtype == SSD_F32 ? 4 : 2;
+    q.scale_bytes = kTile * q.groups * size;
+    q.zero_bytes = q.p.zero ? kTile * q.groups : 0;
+    q.slice_x_groups = q.p.x_scale ? slice * 4 / q.x_group_blocks + 2 : 0;
+    int at = q.warps * kStages * kTile * (blocks == 4 ? 64 : 80);
+    auto take = [&](int bytes) {
+        const int off = at;
+        at += up(bytes, 128);
+        return off;
+    };
+    q.off_x = take(q.row_tile * parts * q.x_stride);
+    q.off_xs = take(q.slice_x_groups * col_tiles * 8 * 4);
+    q.off_scale = take(q.scale_slots * q.scale_bytes);
+    q.off_zero = take(q.scale_slots * q.zero_bytes);
+    q.off_part = take(2 * q.warps * kTile * col_tiles * 8 * 4);
+    q.off_own = take(q.split > 1 ? 2 * kTile * col_tiles * 8 * 4 : 0);
+    q.smem = at;
+}
+
+template <int kCols, int kBlocks, bool kX8> cudaError_t run(const Plan &q, cudaStream_t stream) {
+    auto kernel = matvec4_mma_kernel<kCols, kBlocks, kX8>;
+    // the most that any plan takes, so that one call of a process and device is enough
+    static unsigned long long set = 0;          // bit d: device d (the first 64)
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    if (device >= 64 || !(__atomic_load_n(&set, __ATOMIC_ACQUIRE) >> device & 1)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+        if (e != cudaSuccess) return e;
+        if (device < 64) __atomic_fetch_or(&set, 1ull << device, __ATOMIC_RELEASE);
+    }
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)q.split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t config = {};
+    config.gridDim = dim3((unsigned)(q.clusters * q.split), (unsigned)((q.p.rows - 1) / q.row_tile + 1));
+    config.blockDim = dim3((unsigned)(32 * q.warps));
+    config.dynamicSmemBytes = (size_t)q.smem;
+    config.stream = stream;
+    config.attrs = attr;
+    config.numAttrs = 2;
+    return cudaLaunchKernelEx(&config, kernel, q);
+}
+
+template <int kCols, int kBlocks> cudaError_t run(const Plan &q, cudaStream_t stream) {
+    return q.p.x_scale ? run<kCols, kBlocks, true>(q, stream) : run<kCols, kBlocks, false>(q, stream);
+}
+
+template <int kCols> cudaError_t run(const Plan &q, int blocks, cudaStream_t stream) {
+    return blocks == 4   ? run<kCols, 4>(q, stream)
+           : blocks == 2 ? run<kCols, 2>(q, stream)
+                         : run<kCols, 1>(q, stream);
+}
+
+}  // namespace
+
+bool launch_matvec4_mma(const ssd_matvec4_params &p, cudaStream_t stream, cudaError_t *error) {
+    auto whole = [&](int group) { return group % 32 == 0 || group >= p.in_features; };
+    if (p.in_features % 32 != 0 || p.in_features > (1 << 20) || p.weight_stride % 16 != 0 || !aligned_to(p.weight, 16) ||
+        !whole(p.group_size) || (p.x_dtype > SSD_BF16 && !whole(p.x_group)))
+        return false;
+    Plan q = {};
+    q.p = p;
+    if (p.x_dtype <= SSD_BF16) q.p.x_scale = nullptr;
+    const int K = p.in_features, parts = p.x_dtype == SSD_F32 ? 3 : 1;
+    auto blocks_of = [&](int group) { return group >= K ? K / 32 : group / 32; };
+    q.groups = p.group_size >= K ? 1 : (K - 1) / p.group_size + 1;
+    q.group_blocks = blocks_of(p.group_size);
+    q.x_groups = !q.p.x_scale || p.x_group >= K ? 1 : (K - 1) / p.x_group + 1;
+    q.x_group_blocks = q.p.x_scale ? blocks_of(p.x_group) : 1;
+    auto magic = [](int blocks) { return (uint32_t)((1ull << 32) / blocks + 1); };
+    q.group_magic = magic(q.group_blocks);
+    q.x_group_magic = magic(q.x_group_blocks);
+    // blocks that share their scales wherever a step begins
+    const int wb = q.groups == 1 ? 4 : q.group_blocks, xb = q.x_groups == 1 ? 4 : q.x_group_blocks;
+    const int blocks = gcd(4, gcd(wb, xb));
+    q.tiles = (p.out_features - 1) / kTile + 1;
+    q.steps = (K - 1) / kStep + 1;
+    int col_tiles = 1;
+    while (col_tiles < 8 && col_tiles * 8 < p.rows * parts) col_tiles *= 2;
+    for (;; col_tiles /= 2) {
+        if (col_tiles == 0) return false;
+        q.row_tile = col_tiles * 8 / parts;
+        if (q.row_tile > p.rows) q.row_tile = p.rows;
+        // as many CTAs as are worth it, and more where a row of x would not fit
+        q.split = 1;
+        while (q.split < 8 && q.tiles * q.split < 304 && q.steps / (q.split * 2) >= kMaxWarps) q.split *= 2;
+        for (;; q.split *= 2) {
+            const int slice = (q.steps - 1) / q.split + 1;
+            q.warps = slice < kMaxWarps ? slice : kMaxWarps;
+            lay_out(q, col_tiles, blocks);
+            if (q.smem <= kSmemLimit || q.split == 8) break;
+        }
+        if (q.smem <= kSmemLimit) break;
+    }
+    if ((p.rows - 1) / q.row_tile + 1 > 65535) return false;
+    const int resident = kSmemLimit / (q.smem + 1024);
+    int clusters = 152 * (resident < 1 ? 1 : resident > 3 ? 3 : resident) / q.split;
+    if (clusters > q.tiles) clusters = q.tiles;
+    const int each = (q.tiles - 1) / clusters + 1;
+    q.clusters = (q.tiles - 1) / each + 1;
+    *error = col_tiles == 1   ? run<1>(q, blocks, stream)
+             : col_tiles == 2 ? run<2>(q, blocks, stream)
+             : col_tiles == 4 ? run<4>(q, blocks, stream)
+                              : run<8>(q, blocks, stream);
+    return true;
+}
+
+}  // namespace ssd
