@@ -1,7 +1,7 @@
 // Products of few rows with 4-bit weights on the tensor cores, for rows of weights
 // in whole 16 bytes and groups of a multiple of 32 columns.
 //
-// A tile is 16 outputs; a warp multiplies it by 128 columns at a step
+// A tile is 16 outputs, or 32 for few columns; a warp multiplies it by 128 columns at a step
 // (mma.m16n8k16, weights as the 16 rows, rows of x as the columns).  code - zero is
 // an integer below 2^4 and exact in bf16, as are 8-bit activations; fp32 activations
 // become three bf16 parts of eight bits each, which together are exact.  Sums within
@@ -18,7 +18,7 @@
 namespace ssd {
 namespace {
 
-constexpr int kStages = 4, kMaxWarps = 8, kTile = 16, kStep = 128;
+constexpr int kStages = 4, kMaxWarps = 8, kStep = 128;
 constexpr int kSmemLimit = 227 * 1024;
 
 struct Plan {
@@ -114,10 +114,14 @@ __device__ __forceinline__ void copy_block(uint8_t *dst, const uint8_t *src, int
 
 // kCols: eights of columns (rows of x, or their parts) of a pass.  kBlocks: 32-column
 // blocks that certainly share their scales (1, 2, or 4: a step).
+constexpr int mats(int cols) { return cols <= 2 ? 2 : 1; }         // sixteens of outputs of a tile
+constexpr int ctas(int cols) { return cols == 1 ? 3 : cols <= 4 ? 2 : 1; }
+constexpr int pitch(int blocks) { return blocks == 4 ? 64 : 80; }   // bytes of a row of a stage: no bank conflicts
+
 template <int kCols, int kBlocks, bool kX8>
-__global__ void __launch_bounds__(32 * kMaxWarps, kCols <= 2 ? 3 : kCols == 4 ? 2 : 1) matvec4_mma_kernel(const __grid_constant__ Plan plan) {
+__global__ void __launch_bounds__(32 * kMaxWarps, ctas(kCols)) matvec4_mma_kernel(const __grid_constant__ Plan plan) {
     extern __shared__ __align__(128) uint8_t smem[];
-    constexpr int kPitch = kBlocks == 4 ? 64 : 80;      // bytes of a row of a stage: no bank conflicts in words of the quads
+    constexpr int kMats = mats(kCols), kTile = 16 * kMats, kPitch = pitch(kBlocks), kWide = kCols * 8;
     const ssd_matvec4_params &p = plan.p;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int rank = blockIdx.x % plan.split, cluster = blockIdx.x / plan.split;
@@ -131,42 +135,56 @@ __global__ void __launch_bounds__(32 * kMaxWarps, kCols <= 2 ? 3 : kCols == 4 ? 
     float *const part = reinterpret_cast<float *>(smem + plan.off_part);
     float *const own = reinterpret_cast<float *>(smem + plan.off_own);
     const int my_tiles = (plan.tiles - cluster + plan.clusters - 1) / plan.clusters;
-    const int total = my_tiles * plan.per_warp;
+    const int scale_size = p.scale_dtype == SSD_F32 ? 4 : 2;
     await_previous();
 
-    auto copy_scales = [&](int i) {             // of the CTA's tile i
+    auto copy_scales = [&](int i, int slot) {           // of the CTA's tile i
         const int64_t o0 = (int64_t)(cluster + i * plan.clusters) * kTile;
-        const int live = (int)min((int64_t)kTile, p.out_features - o0), slot = i % plan.scale_slots;
-        const int size = plan.scale_bytes / (kTile * plan.groups);
+        const int live = (int)min((int64_t)kTile, p.out_features - o0);
         copy_block(smem + plan.off_scale + slot * plan.scale_bytes,
-                   static_cast<const uint8_t *>(p.scale) + o0 * plan.groups * size, plan.scale_bytes, live * plan.groups * size);
+                   static_cast<const uint8_t *>(p.scale) + o0 * plan.groups * scale_size, plan.scale_bytes,
+                   live * plan.groups * scale_size);
         if (p.zero)
             copy_block(smem + plan.off_zero + slot * plan.zero_bytes, p.zero + o0 * plan.groups, plan.zero_bytes, live * plan.groups);
     };
-    // Step q of the warp's: its codes, and the scales of the next tile, which are
-    // then complete for all when the tile of this step has been added up.
-    auto issue = [&](int q) {
-        if (q < total) {
-            const int i = q / plan.per_warp, j = q - i * plan.per_warp;
-            const int step = step0 + j * plan.warps + warp;
-            const int64_t o0 = (int64_t)(cluster + i * plan.clusters) * kTile;
-            const int byte = step * (kStep / 2) + t * 16;
-            if (step < step1) {
+    // The next step's codes, and with a tile's last step the scales of the next tile,
+    // which are then complete for all when this tile has been added up.
+    int to_tile = 0, to_j = 0, to_stage = 0, to_slot = 0;
+    const uint8_t *src[2 * kMats];                      // of the lane's 16 bytes of its rows
+    auto point = [&]() {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int64_t o = min(o0 + g + 8 * h, (int64_t)p.out_features - 1);
-                    copy_async<16>(ring + (q % kStages) * (kTile * kPitch) + (g + 8 * h) * kPitch + t * 16,
-                                   p.weight + o * p.weight_stride + (byte < row_bytes ? byte : 0), byte < row_bytes);
+        for (int h = 0; h < 2 * kMats; ++h) {
+            const int64_t o = min((int64_t)(cluster + to_tile * plan.clusters) * kTile + g + 8 * h, (int64_t)p.out_features - 1);
+            src[h] = p.weight + o * p.weight_stride + t * 16;
+        }
+    };
+    point();
+    auto issue = [&]() {
+        if (to_tile < my_tiles) {
+            const int step = step0 + to_j * plan.warps + warp, byte = step * (kStep / 2);
+            if (step < step1) {
+                const bool live = byte + t * 16 < row_bytes;
+                uint8_t *const dst = ring + to_stage * (kTile * kPitch) + g * kPitch + t * 16;
+#pragma unroll
+                for (int h = 0; h < 2 * kMats; ++h)
+                    copy_async<16>(dst + 8 * h * kPitch, live ? src[h] + byte : p.weight, live);
+            }
+            if (++to_j == plan.per_warp) {
+                to_j = 0;
+                if (++to_tile < my_tiles) {
+                    to_slot = to_slot + 1 == plan.scale_slots ? 0 : to_slot + 1;
+                    copy_scales(to_tile, to_slot);
+                    point();
                 }
             }
-            if (j == plan.per_warp - 1 && i + 1 < my_tiles) copy_scales(i + 1);
         }
+        to_stage = to_stage + 1 == kStages ? 0 : to_stage + 1;
         commit_async();
     };
 
-    if (my_tiles > 0) copy_scales(0);
-#pragma unroll
-    for (int q = 0; q < kStages - 1; ++q) issue(q);
+    if (my_tiles > 0) copy_scales(0, 0);
+#pragma unroll 1
+    for (int q = 0; q < kStages - 1; ++q) issue();
 
     // x of the CTA's columns as bf16, in chunks of eight: values i and i + 4 side by
     // side, as the codes of a word come; within a step the chunk that quad lane t reads
@@ -198,8 +216,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, kCols <= 2 ? 3 : kCols == 4 ? 
         }
         if constexpr (kX8) {
             const int first = group_of(step0 * 4, plan.x_group_blocks, plan.x_group_magic);
-            for (int i = threadIdx.x; i < plan.slice_x_groups * kCols * 8; i += blockDim.x) {
-                const int r = i % (kCols * 8), x_group = first + i / (kCols * 8);
+            for (int i = threadIdx.x; i < plan.slice_x_groups * kWide; i += blockDim.x) {
+                const int r = i % kWide, x_group = first + i / kWide;
                 xsc[i] = r < rows && x_group < plan.x_groups ? p.x_scale[(int64_t)(r0 + r) * plan.x_groups + x_group] : 0.f;
             }
         }
@@ -208,93 +226,119 @@ __global__ void __launch_bounds__(32 * kMaxWarps, kCols <= 2 ? 3 : kCols == 4 ? 
     __syncthreads();
 
     const int first_x_group = kX8 ? group_of(step0 * 4, plan.x_group_blocks, plan.x_group_magic) : 0;
-    float sum[kCols][4];
+    int row_at[2 * kMats];                              // of the lane's rows in a tile's scales
 #pragma unroll
-    for (int n = 0; n < kCols; ++n)
+    for (int h = 0; h < 2 * kMats; ++h) row_at[h] = (g + 8 * h) * plan.groups;
+    float sum[kMats][kCols][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum[n][i] = 0.f;
-    int tile = 0, j = 0;
-    for (int q = 0; q < total; ++q) {
-        wait_async<kStages - 2>();
-        if constexpr (kBlocks < 4) __syncwarp();
-        issue(q + kStages - 1);
-        const int step = step0 + j * plan.warps + warp;
-        if (step < step1) {
-            const uint8_t *const codes = ring + (q % kStages) * (kTile * kPitch) + g * kPitch;
-            const uint8_t *const scales = smem + plan.off_scale + (tile % plan.scale_slots) * plan.scale_bytes;
-            const uint8_t *const zeros = smem + plan.off_zero + (tile % plan.scale_slots) * plan.zero_bytes;
+    for (int m = 0; m < kMats; ++m)
+#pragma unroll
+        for (int n = 0; n < kCols; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[m][n][i] = 0.f;
+    int stage = 0, slot = 0;
+    for (int tile = 0; tile < my_tiles; ++tile) {
+        const uint8_t *const scales = smem + plan.off_scale + slot * plan.scale_bytes;
+        const uint8_t *const zeros = smem + plan.off_zero + slot * plan.zero_bytes;
+        slot = slot + 1 == plan.scale_slots ? 0 : slot + 1;
+        for (int j = 0; j < plan.per_warp; ++j) {
+            wait_async<kStages - 2>();
+            if constexpr (kBlocks < 4) __syncwarp();    // a lane reads what its neighbours copied
+            issue();
+            const int step = step0 + j * plan.warps + warp;
+            const uint8_t *const codes = ring + stage * (kTile * kPitch) + g * kPitch + (kBlocks == 4 ? t * 16 : t * 4);
+            stage = stage + 1 == kStages ? 0 : stage + 1;
+            if (step >= step1) continue;
             const uint8_t *const x = xs + g * plan.x_stride + (step - step0) * (kStep * 2) + t * 16;
-            uint32_t lo[4], hi[4];
+            uint32_t words[2 * kMats][4];
             if constexpr (kBlocks == 4) {
-                *reinterpret_cast<uint4 *>(lo) = *reinterpret_cast<const uint4 *>(codes + t * 16);
-                *reinterpret_cast<uint4 *>(hi) = *reinterpret_cast<const uint4 *>(codes + 8 * kPitch + t * 16);
+#pragma unroll
+                for (int h = 0; h < 2 * kMats; ++h)
+                    *reinterpret_cast<uint4 *>(words[h]) = *reinterpret_cast<const uint4 *>(codes + 8 * h * kPitch);
             }
 #pragma unroll
             for (int f = 0; f < 4 / kBlocks; ++f) {
                 const int block = step * 4 + f * kBlocks;
                 if (kBlocks < 4 && block * 32 >= K) break;
                 const int gi = group_of(block, plan.group_blocks, plan.group_magic);
-                uint32_t zlo = 0x43084308u, zhi = 0x43084308u;          // 128 + 8
-                if (p.zero) {
-                    zlo = 0x43004300u + zeros[g * plan.groups + gi] * 0x00010001u;
-                    zhi = 0x43004300u + zeros[(g + 8) * plan.groups + gi] * 0x00010001u;
-                }
-                float acc[kCols][4];
+                uint32_t zero[2 * kMats];               // 128 + zero, twice
 #pragma unroll
-                for (int n = 0; n < kCols; ++n)
+                for (int h = 0; h < 2 * kMats; ++h)
+                    zero[h] = p.zero ? 0x43004300u + zeros[row_at[h] + gi] * 0x00010001u : 0x43084308u;
+                float acc[kMats][kCols][4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+                for (int m = 0; m < kMats; ++m)
+#pragma unroll
+                    for (int n = 0; n < kCols; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
 #pragma unroll
                 for (int b = 0; b < kBlocks; ++b) {
                     const int w = f * kBlocks + b;
-                    if constexpr (kBlocks < 4) {
-                        lo[w] = *reinterpret_cast<const uint32_t *>(codes + w * 16 + t * 4);
-                        hi[w] = *reinterpret_cast<const uint32_t *>(codes + 8 * kPitch + w * 16 + t * 4);
+                    uint32_t a0[kMats][4], a1[kMats][4];
+#pragma unroll
+                    for (int m = 0; m < kMats; ++m) {
+                        uint32_t lo = words[2 * m][w], hi = words[2 * m + 1][w];
+                        if constexpr (kBlocks < 4) {
+                            lo = *reinterpret_cast<const uint32_t *>(codes + 16 * m * kPitch + w * 16);
+                            hi = *reinterpret_cast<const uint32_t *>(codes + (16 * m + 8) * kPitch + w * 16);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            a0[m][2 * i] = codes2(lo, i, zero[2 * m]);
+                            a0[m][2 * i + 1] = codes2(hi, i, zero[2 * m + 1]);
+                            a1[m][2 * i] = codes2(lo, i + 2, zero[2 * m]);
+                            a1[m][2 * i + 1] = codes2(hi, i + 2, zero[2 * m + 1]);
+                        }
                     }
-                    const uint32_t a0[4] = {codes2(lo[w], 0, zlo), codes2(hi[w], 0, zhi), codes2(lo[w], 1, zlo), codes2(hi[w], 1, zhi)};
-                    const uint32_t a1[4] = {codes2(lo[w], 2, zlo), codes2(hi[w], 2, zhi), codes2(lo[w], 3, zlo), codes2(hi[w], 3, zhi)};
 #pragma unroll
                     for (int n = 0; n < kCols; ++n) {
                         uint4 v = make_uint4(0, 0, 0, 0);
                         if (n * 8 + g < cols) v = *reinterpret_cast<const uint4 *>(x + n * 8 * plan.x_stride + w * 64);
-                        mma(acc[n], a0, v.x, v.y);
-                        mma(acc[n], a1, v.z, v.w);
+#pragma unroll
+                        for (int m = 0; m < kMats; ++m) {
+                            mma(acc[m][n], a0[m], v.x, v.y);
+                            mma(acc[m][n], a1[m], v.z, v.w);
+                        }
                     }
                 }
-                const float slo = scale_at(scales, g * plan.groups + gi, p.scale_dtype);
-                const float shi = scale_at(scales, (g + 8) * plan.groups + gi, p.scale_dtype);
+                float scale[2 * kMats];
+#pragma unroll
+                for (int h = 0; h < 2 * kMats; ++h) scale[h] = scale_at(scales, row_at[h] + gi, p.scale_dtype);
                 const int xg = kX8 ? group_of(block, plan.x_group_blocks, plan.x_group_magic) - first_x_group : 0;
 #pragma unroll
                 for (int n = 0; n < kCols; ++n) {
                     if constexpr (kX8) {
                         const float2 s = *reinterpret_cast<const float2 *>(xsc + (xg * kCols + n) * 8 + 2 * t);
-                        sum[n][0] = fmaf(acc[n][0] * s.x, slo, sum[n][0]);
-                        sum[n][1] = fmaf(acc[n][1] * s.y, slo, sum[n][1]);
-                        sum[n][2] = fmaf(acc[n][2] * s.x, shi, sum[n][2]);
-                        sum[n][3] = fmaf(acc[n][3] * s.y, shi, sum[n][3]);
-                    } else {
-                        sum[n][0] = fmaf(acc[n][0], slo, sum[n][0]);
-                        sum[n][1] = fmaf(acc[n][1], slo, sum[n][1]);
-                        sum[n][2] = fmaf(acc[n][2], shi, sum[n][2]);
-                        sum[n][3] = fmaf(acc[n][3], shi, sum[n][3]);
+#pragma unroll
+                        for (int m = 0; m < kMats; ++m) {
+                            acc[m][n][0] *= s.x;
+                            acc[m][n][1] *= s.y;
+                            acc[m][n][2] *= s.x;
+                            acc[m][n][3] *= s.y;
+                        }
                     }
+#pragma unroll
+                    for (int m = 0; m < kMats; ++m)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) sum[m][n][i] = fmaf(acc[m][n][i], scale[2 * m + i / 2], sum[m][n][i]);
                 }
             }
         }
-        if (++j < plan.per_warp) continue;
         // the tile's parts: of the warps, then of the cluster's CTAs.  Two buffers, so
         // that one barrier a tile is enough.
-        j = 0;
-        constexpr int kWide = kCols * 8;
+        const float *const all = part + (tile & 1) * plan.warps * (kTile * kWide);
         float *const mine = part + ((tile & 1) * plan.warps + warp) * (kTile * kWide);
 #pragma unroll
-        for (int n = 0; n < kCols; ++n) {
-            *reinterpret_cast<float2 *>(mine + g * kWide + n * 8 + 2 * t) = make_float2(sum[n][0], sum[n][1]);
-            *reinterpret_cast<float2 *>(mine + (g + 8) * kWide + n * 8 + 2 * t) = make_float2(sum[n][2], sum[n][3]);
-            sum[n][0] = sum[n][1] = sum[n][2] = sum[n][3] = 0.f;
-        }
+        for (int m = 0; m < kMats; ++m)
+#pragma unroll
+            for (int n = 0; n < kCols; ++n) {
+                float *const at = mine + (16 * m + g) * kWide + n * 8 + 2 * t;
+                *reinterpret_cast<float2 *>(at) = make_float2(sum[m][n][0], sum[m][n][1]);
+                *reinterpret_cast<float2 *>(at + 8 * kWide) = make_float2(sum[m][n][2], sum[m][n][3]);
+                sum[m][n][0] = sum[m][n][1] = sum[m][n][2] = sum[m][n][3] = 0.f;
+            }
         __syncthreads();
-        const float *const all = part + (tile & 1) * plan.warps * (kTile * kWide);
         const int64_t o0 = (int64_t)(cluster + tile * plan.clusters) * kTile;
         auto finish = [&](int r, int o, float v) {
             if (o0 + o >= p.out_features) return;
@@ -331,11 +375,9 @@ __global__ void __launch_bounds__(32 * kMaxWarps, kCols <= 2 ? 3 : kCols == 4 ? 
                 finish(i / kTile, i % kTile, v);
             }
         }
-        ++tile;
     }
     // no CTA leaves while another reads its part
-    if (plan.split > 1)
-        cluster_barrier();
+    if (plan.split > 1) cluster_barrier();
 }
 
 int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
@@ -343,6 +385,7 @@ int up(int v, int to) { return (v + to - 1) / to * to; }
 
 // Shared memory of a plan whose split, warps and rows are set.
 void lay_out(Plan &q, int col_tiles, int blocks) {
+    const int kTile = 16 * mats(col_tiles);
     const int parts = q.p.x_dtype == SSD_F32 ? 3 : 1, slice = (q.steps - 1) / q.split + 1;
     q.per_warp = (slice - 1) / q.warps + 1;
     q.x_stride = up(slice * kStep * 2, 128) + 64;       // two rows of x beside one another in the banks
@@ -351,7 +394,7 @@ void lay_out(Plan &q, int col_tiles, int blocks) {
     q.scale_bytes = kTile * q.groups * size;
     q.zero_bytes = q.p.zero ? kTile * q.groups : 0;
     q.slice_x_groups = q.p.x_scale ? slice * 4 / q.x_group_blocks + 2 : 0;
-    int at = q.warps * kStages * kTile * (blocks == 4 ? 64 : 80);
+    int at = q.warps * kStages * kTile * pitch(blocks);
     auto take = [&](int bytes) {
         const int off = at;
         at += up(bytes, 128);
@@ -426,7 +469,6 @@ bool launch_matvec4_mma(const ssd_matvec4_params &p, cudaStream_t stream, cudaEr
     // blocks that share their scales wherever a step begins
     const int wb = q.groups == 1 ? 4 : q.group_blocks, xb = q.x_groups == 1 ? 4 : q.x_group_blocks;
     const int blocks = gcd(4, gcd(wb, xb));
-    q.tiles = (p.out_features - 1) / kTile + 1;
     q.steps = (K - 1) / kStep + 1;
     int col_tiles = 1;
     while (col_tiles < 8 && col_tiles * 8 < p.rows * parts) col_tiles *= 2;
@@ -434,6 +476,7 @@ bool launch_matvec4_mma(const ssd_matvec4_params &p, cudaStream_t stream, cudaEr
         if (col_tiles == 0) return false;
         q.row_tile = col_tiles * 8 / parts;
         if (q.row_tile > p.rows) q.row_tile = p.rows;
+        q.tiles = (p.out_features - 1) / (16 * mats(col_tiles)) + 1;
         // as many CTAs as are worth it, and more where a row of x would not fit
         q.split = 1;
         while (q.split < 8 && q.tiles * q.split < 304 && q.steps / (q.split * 2) >= kMaxWarps) q.split *= 2;
@@ -447,7 +490,7 @@ bool launch_matvec4_mma(const ssd_matvec4_params &p, cudaStream_t stream, cudaEr
     }
     if ((p.rows - 1) / q.row_tile + 1 > 65535) return false;
     const int resident = kSmemLimit / (q.smem + 1024);
-    int clusters = 152 * (resident < 1 ? 1 : resident > 3 ? 3 : resident) / q.split;
+    int clusters = 152 * (resident < 1 ? 1 : resident > ctas(col_tiles) ? ctas(col_tiles) : resident) / q.split;
     if (clusters > q.tiles) clusters = q.tiles;
     const int each = (q.tiles - 1) / clusters + 1;
     q.clusters = (q.tiles - 1) / each + 1;
