@@ -18,7 +18,7 @@
 namespace ssd {
 namespace {
 
-constexpr int kStages = 4, kMaxWarps = 8, kStep = 128;
+constexpr int kStages = 3, kMaxWarps = 8, kStep = 128;
 constexpr int kSmemLimit = 227 * 1024;
 
 struct Plan {
@@ -48,12 +48,18 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// the same from zero
+__device__ __forceinline__ void mma_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 
 // Codes i and i + 4 of a word (at bits 4 i and 4 i + 16) less their zero, as bf16:
 // the code as the low bits of 128's mantissa, minus 128 + zero.  Exact.
 __device__ __forceinline__ uint32_t codes2(uint32_t word, int i, uint32_t zero) {
-    const uint32_t v = (word >> (4 * i) & 0x000f000fu) | 0x43004300u;
-    uint32_t r;
+    uint32_t v, r;              // and, or as one operation (the compiler makes two)
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(word >> (4 * i)), "r"(0x000f000fu), "r"(0x43004300u));
     asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(zero));
     return r;
 }
@@ -126,7 +132,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, ctas(kCols)) matvec4_mma_kerne
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int rank = blockIdx.x % plan.split, cluster = blockIdx.x / plan.split;
     const int r0 = blockIdx.y * plan.row_tile, rows = min(plan.row_tile, p.rows - r0);
-    const int parts = p.x_dtype == SSD_F32 ? 3 : 1, cols = rows * parts;
+    const int parts = p.x_dtype == SSD_F32 ? 3 : 1, cols = rows * parts, wide = (cols + 1) & ~1;
     const int step0 = (int)((int64_t)plan.steps * rank / plan.split), step1 = (int)((int64_t)plan.steps * (rank + 1) / plan.split);
     const int K = p.in_features, row_bytes = K / 2;
     uint8_t *const ring = smem + warp * (kStages * kTile * kPitch);
@@ -155,19 +161,20 @@ __global__ void __launch_bounds__(32 * kMaxWarps, ctas(kCols)) matvec4_mma_kerne
 #pragma unroll
         for (int h = 0; h < 2 * kMats; ++h) {
             const int64_t o = min((int64_t)(cluster + to_tile * plan.clusters) * kTile + g + 8 * h, (int64_t)p.out_features - 1);
-            src[h] = p.weight + o * p.weight_stride + t * 16;
+            src[h] = p.weight + o * p.weight_stride + (t * 16 < row_bytes ? t * 16 : 0);
         }
     };
     point();
+    uint8_t *const to = ring + g * kPitch + t * 16;
     auto issue = [&]() {
         if (to_tile < my_tiles) {
             const int step = step0 + to_j * plan.warps + warp, byte = step * (kStep / 2);
             if (step < step1) {
                 const bool live = byte + t * 16 < row_bytes;
-                uint8_t *const dst = ring + to_stage * (kTile * kPitch) + g * kPitch + t * 16;
+                const uint32_t at = live ? (uint32_t)byte : 0u;
+                uint8_t *const dst = to + to_stage * (kTile * kPitch);
 #pragma unroll
-                for (int h = 0; h < 2 * kMats; ++h)
-                    copy_async<16>(dst + 8 * h * kPitch, live ? src[h] + byte : p.weight, live);
+                for (int h = 0; h < 2 * kMats; ++h) copy_async<16>(dst + 8 * h * kPitch, src[h] + at, live);
             }
             if (++to_j == plan.per_warp) {
                 to_j = 0;
@@ -229,6 +236,10 @@ __global__ void __launch_bounds__(32 * kMaxWarps, ctas(kCols)) matvec4_mma_kerne
     int row_at[2 * kMats];                              // of the lane's rows in a tile's scales
 #pragma unroll
     for (int h = 0; h < 2 * kMats; ++h) row_at[h] = (g + 8 * h) * plan.groups;
+    // A column that is not there is computed from the last one and not looked at.
+    int x_at[kCols];
+#pragma unroll
+    for (int n = 0; n < kCols; ++n) x_at[n] = min(n * 8 + g, cols - 1) * plan.x_stride + t * 16;
     float sum[kMats][kCols][4];
 #pragma unroll
     for (int m = 0; m < kMats; ++m)
@@ -249,7 +260,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, ctas(kCols)) matvec4_mma_kerne
             const uint8_t *const codes = ring + stage * (kTile * kPitch) + g * kPitch + (kBlocks == 4 ? t * 16 : t * 4);
             stage = stage + 1 == kStages ? 0 : stage + 1;
             if (step >= step1) continue;
-            const uint8_t *const x = xs + g * plan.x_stride + (step - step0) * (kStep * 2) + t * 16;
+            const uint8_t *const x = xs + (step - step0) * (kStep * 2);
             uint32_t words[2 * kMats][4];
             if constexpr (kBlocks == 4) {
 #pragma unroll
@@ -266,12 +277,6 @@ __global__ void __launch_bounds__(32 * kMaxWarps, ctas(kCols)) matvec4_mma_kerne
                 for (int h = 0; h < 2 * kMats; ++h)
                     zero[h] = p.zero ? 0x43004300u + zeros[row_at[h] + gi] * 0x00010001u : 0x43084308u;
                 float acc[kMats][kCols][4];
-#pragma unroll
-                for (int m = 0; m < kMats; ++m)
-#pragma unroll
-                    for (int n = 0; n < kCols; ++n)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
 #pragma unroll
                 for (int b = 0; b < kBlocks; ++b) {
                     const int w = f * kBlocks + b;
@@ -293,11 +298,11 @@ __global__ void __launch_bounds__(32 * kMaxWarps, ctas(kCols)) matvec4_mma_kerne
                     }
 #pragma unroll
                     for (int n = 0; n < kCols; ++n) {
-                        uint4 v = make_uint4(0, 0, 0, 0);
-                        if (n * 8 + g < cols) v = *reinterpret_cast<const uint4 *>(x + n * 8 * plan.x_stride + w * 64);
+                        const uint4 v = *reinterpret_cast<const uint4 *>(x + x_at[n] + w * 64);
 #pragma unroll
                         for (int m = 0; m < kMats; ++m) {
-                            mma(acc[m][n], a0[m], v.x, v.y);
+                            if (b == 0) mma_first(acc[m][n], a0[m], v.x, v.y);
+                            else mma(acc[m][n], a0[m], v.x, v.y);
                             mma(acc[m][n], a1[m], v.z, v.w);
                         }
                     }
@@ -327,15 +332,17 @@ __global__ void __launch_bounds__(32 * kMaxWarps, ctas(kCols)) matvec4_mma_kerne
         }
         // the tile's parts: of the warps, then of the cluster's CTAs.  Two buffers, so
         // that one barrier a tile is enough.
-        const float *const all = part + (tile & 1) * plan.warps * (kTile * kWide);
-        float *const mine = part + ((tile & 1) * plan.warps + warp) * (kTile * kWide);
+        const float *const all = part + (tile & 1) * plan.warps * (kTile * wide);
+        float *const mine = part + ((tile & 1) * plan.warps + warp) * (kTile * wide);
 #pragma unroll
         for (int m = 0; m < kMats; ++m)
 #pragma unroll
             for (int n = 0; n < kCols; ++n) {
-                float *const at = mine + (16 * m + g) * kWide + n * 8 + 2 * t;
-                *reinterpret_cast<float2 *>(at) = make_float2(sum[m][n][0], sum[m][n][1]);
-                *reinterpret_cast<float2 *>(at + 8 * kWide) = make_float2(sum[m][n][2], sum[m][n][3]);
+                float *const at = mine + (16 * m + g) * wide + n * 8 + 2 * t;
+                if (n * 8 + 2 * t < wide) {
+                    *reinterpret_cast<float2 *>(at) = make_float2(sum[m][n][0], sum[m][n][1]);
+                    *reinterpret_cast<float2 *>(at + 8 * wide) = make_float2(sum[m][n][2], sum[m][n][3]);
+                }
                 sum[m][n][0] = sum[m][n][1] = sum[m][n][2] = sum[m][n][3] = 0.f;
             }
         __syncthreads();
@@ -351,12 +358,12 @@ __global__ void __launch_bounds__(32 * kMaxWarps, ctas(kCols)) matvec4_mma_kerne
                 static_cast<__nv_bfloat16 *>(p.out)[at] = from_float<__nv_bfloat16>(v);
             }
         };
-        float *const own_now = own + (tile & 1) * (kTile * kWide);
+        float *const own_now = own + (tile & 1) * (kTile * rows);
         for (int i = threadIdx.x; i < rows * kTile; i += blockDim.x) {
             const int r = i / kTile, o = i % kTile;
             float v = 0.f;
             for (int part_ = 0; part_ < parts; ++part_)
-                for (int w = 0; w < plan.warps; ++w) v += all[(w * kTile + o) * kWide + part_ * rows + r];
+                for (int w = 0; w < plan.warps; ++w) v += all[(w * kTile + o) * wide + part_ * rows + r];
             if (plan.split == 1) finish(r, o, v);
             else own_now[i] = v;
         }
@@ -404,8 +411,8 @@ void lay_out(Plan &q, int col_tiles, int blocks) {
     q.off_xs = take(q.slice_x_groups * col_tiles * 8 * 4);
     q.off_scale = take(q.scale_slots * q.scale_bytes);
     q.off_zero = take(q.scale_slots * q.zero_bytes);
-    q.off_part = take(2 * q.warps * kTile * col_tiles * 8 * 4);
-    q.off_own = take(q.split > 1 ? 2 * kTile * col_tiles * 8 * 4 : 0);
+    q.off_part = take(2 * q.warps * kTile * up(q.row_tile * parts, 2) * 4);
+    q.off_own = take(q.split > 1 ? 2 * kTile * q.row_tile * 4 : 0);
     q.smem = at;
 }
 
@@ -477,23 +484,35 @@ bool launch_matvec4_mma(const ssd_matvec4_params &p, cudaStream_t stream, cudaEr
         q.row_tile = col_tiles * 8 / parts;
         if (q.row_tile > p.rows) q.row_tile = p.rows;
         q.tiles = (p.out_features - 1) / (16 * mats(col_tiles)) + 1;
-        // as many CTAs as are worth it, and more where a row of x would not fit
-        q.split = 1;
-        while (q.split < 8 && q.tiles * q.split < 304 && q.steps / (q.split * 2) >= kMaxWarps) q.split *= 2;
-        for (;; q.split *= 2) {
+        // The split whose waves of tiles take the least, in steps of a warp: a tile ends
+        // with about one step's time for its parts' addition, two in a cluster.
+        Plan best = {};
+        double least = 0.0;
+        for (q.split = 1; q.split <= 8 && q.split <= q.steps; q.split *= 2) {
             const int slice = (q.steps - 1) / q.split + 1;
             q.warps = slice < kMaxWarps ? slice : kMaxWarps;
             lay_out(q, col_tiles, blocks);
-            if (q.smem <= kSmemLimit || q.split == 8) break;
+            if (q.smem > kSmemLimit) continue;
+            const int fit = kSmemLimit / (q.smem + 1024), most = ctas(col_tiles) * kMaxWarps / q.warps;
+            const int resident = fit < 1 ? 1 : fit < most ? fit : most;
+            q.clusters = 152 * resident / q.split;
+            if (q.clusters > q.tiles) q.clusters = q.tiles;
+            const int each = (q.tiles - 1) / q.clusters + 1;
+            q.clusters = (q.tiles - 1) / each + 1;
+            const int busy = (q.clusters * q.split - 1) / 152 + 1;      // CTAs of an SM
+            const int side = busy * q.warps < 16 ? 16 : busy * q.warps;     // fewer warps do not take their steps faster
+            const double cost = side * each * (q.per_warp + (q.split > 1 ? 2.0 : 1.0)) + busy * slice * q.row_tile * parts * 0.25;
+            if (best.split == 0 || cost < least) {
+                best = q;
+                least = cost;
+            }
         }
-        if (q.smem <= kSmemLimit) break;
+        if (best.split != 0) {
+            q = best;
+            break;
+        }
     }
     if ((p.rows - 1) / q.row_tile + 1 > 65535) return false;
-    const int resident = kSmemLimit / (q.smem + 1024);
-    int clusters = 152 * (resident < 1 ? 1 : resident > ctas(col_tiles) ? ctas(col_tiles) : resident) / q.split;
-    if (clusters > q.tiles) clusters = q.tiles;
-    const int each = (q.tiles - 1) / clusters + 1;
-    q.clusters = (q.tiles - 1) / each + 1;
     *error = col_tiles == 1   ? run<1>(q, blocks, stream)
              : col_tiles == 2 ? run<2>(q, blocks, stream)
              : col_tiles == 4 ? run<4>(q, blocks, stream)
