@@ -55,23 +55,24 @@ __device__ __forceinline__ void mma_first(float (&c)[4], const uint32_t (&a)[4],
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+// v in a register, which the compiler does not load or compute again at each use.
+__device__ __forceinline__ int kept(int v) {
+    int r;
+    asm volatile("mov.b32 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
 // Codes i and i + 4 of a word (at bits 4 i and 4 i + 16) less their zero, as bf16:
 // the code as the low bits of 128's mantissa, minus 128 + zero.  Exact.
-__device__ __forceinline__ uint32_t codes2(uint32_t word, int i, uint32_t zero) {
+__device__ __forceinline__ uint32_t codes2(uint32_t word, int i, uint32_t base, uint32_t zero) {
     uint32_t v, r;              // and, or as one operation (the compiler makes two)
-    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(word >> (4 * i)), "r"(0x000f000fu), "r"(0x43004300u));
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(word >> (4 * i)), "n"(0x000f000f), "r"(base));
     asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(zero));
     return r;
 }
 
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-
-__device__ __forceinline__ float scale_at(const uint8_t *scales, int i, int type) {
-    if (type == SSD_F32) return reinterpret_cast<const float *>(scales)[i];
-    const uint16_t h = reinterpret_cast<const uint16_t *>(scales)[i];
-    return type == SSD_BF16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
 }
 
 // eight consecutive values of a row of x
@@ -102,60 +103,66 @@ __device__ __forceinline__ void load8(float (&v)[8], const ssd_matvec4_params &p
     }
 }
 
-// The block of `bytes` at src into shared memory: asynchronously in 16 bytes where
-// it is aligned (its size always is), else byte by byte, at once.
-__device__ __forceinline__ void copy_block(uint8_t *dst, const uint8_t *src, int bytes, int live) {
-    if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
-        for (int i = threadIdx.x * 16; i < bytes; i += blockDim.x * 16) {
-            if (i + 16 <= live) {
-                copy_async<16>(dst + i, src + i, true);
-            } else {
-                for (int j = i; j < i + 16; ++j) dst[j] = j < live ? src[j] : 0;
-            }
-        }
+// The block of `bytes` (a multiple of 16) at src into shared memory, zeros behind the
+// first `live`: asynchronously in 16 bytes where src is aligned, else at once.
+__device__ __noinline__ void copy_ragged(uint8_t *dst, const uint8_t *src, int bytes, int live) {
+    for (int i = threadIdx.x; i < bytes; i += blockDim.x) dst[i] = i < live ? src[i] : 0;
+}
+__device__ __forceinline__ void copy_block(uint8_t *dst, const uint8_t *src, int bytes, int live, int thread) {
+    if (live == bytes && (reinterpret_cast<uintptr_t>(src) & 15) == 0) {
+#pragma unroll 1
+        for (int i = thread * 16; i < bytes; i += blockDim.x * 16) copy_async<16>(dst + i, src + i, true);
     } else {
-        for (int i = threadIdx.x; i < bytes; i += blockDim.x) dst[i] = i < live ? src[i] : 0;
+        copy_ragged(dst, src, bytes, live);
     }
 }
 
 // kCols: eights of columns (rows of x, or their parts) of a pass.  kBlocks: 32-column
 // blocks that certainly share their scales (1, 2, or 4: a step).
 constexpr int mats(int cols) { return cols <= 2 ? 2 : 1; }         // sixteens of outputs of a tile
-constexpr int ctas(int cols) { return cols == 1 ? 3 : cols <= 4 ? 2 : 1; }
+constexpr int ctas(int cols) { return cols <= 4 ? 2 : 1; }
 constexpr int pitch(int blocks) { return blocks == 4 ? 64 : 80; }   // bytes of a row of a stage: no bank conflicts
 
-template <int kCols, int kBlocks, bool kX8>
+template <int kCols, int kBlocks, bool kX8, bool kZero>
 __global__ void __launch_bounds__(32 * kMaxWarps, ctas(kCols)) matvec4_mma_kernel(const __grid_constant__ Plan plan) {
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int kMats = mats(kCols), kTile = 16 * kMats, kPitch = pitch(kBlocks), kWide = kCols * 8;
     const ssd_matvec4_params &p = plan.p;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int thread = kept(threadIdx.x), lane = thread & 31, g = lane >> 2, t = lane & 3;
+    const int warp = __shfl_sync(0xffffffffu, thread >> 5, 0);          // known to be the same in all lanes
+    const uint32_t base = (uint32_t)kept(0x43004300);                  // 128 in bf16, twice
+    const int scale_type = kept(p.scale_dtype);
     const int rank = blockIdx.x % plan.split, cluster = blockIdx.x / plan.split;
     const int r0 = blockIdx.y * plan.row_tile, rows = min(plan.row_tile, p.rows - r0);
     const int parts = p.x_dtype == SSD_F32 ? 3 : 1, cols = rows * parts, wide = (cols + 1) & ~1;
     const int step0 = (int)((int64_t)plan.steps * rank / plan.split), step1 = (int)((int64_t)plan.steps * (rank + 1) / plan.split);
-    const int K = p.in_features, row_bytes = K / 2;
+    const int K = p.in_features, row_bytes = kept(K / 2), warps = kept(plan.warps), per_warp = kept(plan.per_warp);
     uint8_t *const ring = smem + warp * (kStages * kTile * kPitch);
     uint8_t *const xs = smem + plan.off_x;
     float *const xsc = reinterpret_cast<float *>(smem + plan.off_xs);
     float *const part = reinterpret_cast<float *>(smem + plan.off_part);
     float *const own = reinterpret_cast<float *>(smem + plan.off_own);
     const int my_tiles = (plan.tiles - cluster + plan.clusters - 1) / plan.clusters;
-    const int scale_size = p.scale_dtype == SSD_F32 ? 4 : 2;
-    await_previous();
+        await_previous();
 
-    auto copy_scales = [&](int i, int slot) {           // of the CTA's tile i
-        const int64_t o0 = (int64_t)(cluster + i * plan.clusters) * kTile;
-        const int live = (int)min((int64_t)kTile, p.out_features - o0);
-        copy_block(smem + plan.off_scale + slot * plan.scale_bytes,
-                   static_cast<const uint8_t *>(p.scale) + o0 * plan.groups * scale_size, plan.scale_bytes,
-                   live * plan.groups * scale_size);
-        if (p.zero)
-            copy_block(smem + plan.off_zero + slot * plan.zero_bytes, p.zero + o0 * plan.groups, plan.zero_bytes, live * plan.groups);
+    // scales and zeros of the next tile whose codes are asked for
+    const int64_t tile_scales = (int64_t)plan.clusters * plan.scale_bytes, tile_zeros = (int64_t)plan.clusters * plan.zero_bytes;
+    const uint8_t *scale_src = static_cast<const uint8_t *>(p.scale) + (int64_t)cluster * plan.scale_bytes;
+    const uint8_t *zero_src = kZero ? p.zero + (int64_t)cluster * plan.zero_bytes : nullptr;
+    const int whole_tiles = p.out_features / kTile, whole_steps = K / kStep;
+    auto copy_scales = [&](int at, int slot) {          // of the tile that is number `at` of all
+        const int live = at < whole_tiles ? kTile : p.out_features - at * kTile;
+        copy_block(smem + plan.off_scale + slot * plan.scale_bytes, scale_src, plan.scale_bytes,
+                   live * (plan.scale_bytes / kTile), thread);
+        scale_src += tile_scales;
+        if (kZero) {
+            copy_block(smem + plan.off_zero + slot * plan.zero_bytes, zero_src, plan.zero_bytes, live * plan.groups, thread);
+            zero_src += tile_zeros;
+        }
     };
     // The next step's codes, and with a tile's last step the scales of the next tile,
     // which are then complete for all when this tile has been added up.
-    int to_tile = 0, to_j = 0, to_stage = 0, to_slot = 0;
+    int to_tile = 0, to_step = step0 + warp, to_j = 0, to_stage = 0, to_slot = 0;
     const uint8_t *src[2 * kMats];                      // of the lane's 16 bytes of its rows
     auto point = [&]() {
 #pragma unroll
@@ -166,22 +173,35 @@ __global__ void __launch_bounds__(32 * kMaxWarps, ctas(kCols)) matvec4_mma_kerne
     };
     point();
     uint8_t *const to = ring + g * kPitch + t * 16;
+    const int64_t jump = (int64_t)plan.clusters * kTile * p.weight_stride;
     auto issue = [&]() {
         if (to_tile < my_tiles) {
-            const int step = step0 + to_j * plan.warps + warp, byte = step * (kStep / 2);
-            if (step < step1) {
-                const bool live = byte + t * 16 < row_bytes;
-                const uint32_t at = live ? (uint32_t)byte : 0u;
+            if (to_step < step1) {
+                const int byte = to_step * (kStep / 2);
                 uint8_t *const dst = to + to_stage * (kTile * kPitch);
+                if (to_step < whole_steps) {
 #pragma unroll
-                for (int h = 0; h < 2 * kMats; ++h) copy_async<16>(dst + 8 * h * kPitch, src[h] + at, live);
+                    for (int h = 0; h < 2 * kMats; ++h) copy_async<16>(dst + 8 * h * kPitch, src[h] + byte, true);
+                } else {                                // the columns of the last step that are there
+                    const bool live = byte + t * 16 < row_bytes;
+#pragma unroll
+                    for (int h = 0; h < 2 * kMats; ++h) copy_async<16>(dst + 8 * h * kPitch, src[h] + (live ? byte : 0), live);
+                }
             }
-            if (++to_j == plan.per_warp) {
+            to_step += warps;
+            if (++to_j == per_warp) {
                 to_j = 0;
+                to_step = step0 + warp;
                 if (++to_tile < my_tiles) {
+                    const int at = cluster + to_tile * plan.clusters;
                     to_slot = to_slot + 1 == plan.scale_slots ? 0 : to_slot + 1;
-                    copy_scales(to_tile, to_slot);
-                    point();
+                    copy_scales(at, to_slot);
+                    if (at < whole_tiles) {
+#pragma unroll
+                        for (int h = 0; h < 2 * kMats; ++h) src[h] += jump;
+                    } else {
+                        point();
+                    }
                 }
             }
         }
@@ -189,7 +209,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, ctas(kCols)) matvec4_mma_kerne
         commit_async();
     };
 
-    if (my_tiles > 0) copy_scales(0, 0);
+    if (my_tiles > 0) copy_scales(cluster, 0);
 #pragma unroll 1
     for (int q = 0; q < kStages - 1; ++q) issue();
 
@@ -248,15 +268,17 @@ __global__ void __launch_bounds__(32 * kMaxWarps, ctas(kCols)) matvec4_mma_kerne
 #pragma unroll
             for (int i = 0; i < 4; ++i) sum[m][n][i] = 0.f;
     int stage = 0, slot = 0;
+    const uint32_t eight = (uint32_t)kept(0x43084308);  // 128 + 8
     for (int tile = 0; tile < my_tiles; ++tile) {
         const uint8_t *const scales = smem + plan.off_scale + slot * plan.scale_bytes;
         const uint8_t *const zeros = smem + plan.off_zero + slot * plan.zero_bytes;
         slot = slot + 1 == plan.scale_slots ? 0 : slot + 1;
-        for (int j = 0; j < plan.per_warp; ++j) {
+        int step = step0 + warp;
+#pragma unroll 1
+        for (int j = 0; j < per_warp; ++j, step += warps) {
             wait_async<kStages - 2>();
             if constexpr (kBlocks < 4) __syncwarp();    // a lane reads what its neighbours copied
             issue();
-            const int step = step0 + j * plan.warps + warp;
             const uint8_t *const codes = ring + stage * (kTile * kPitch) + g * kPitch + (kBlocks == 4 ? t * 16 : t * 4);
             stage = stage + 1 == kStages ? 0 : stage + 1;
             if (step >= step1) continue;
@@ -275,7 +297,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, ctas(kCols)) matvec4_mma_kerne
                 uint32_t zero[2 * kMats];               // 128 + zero, twice
 #pragma unroll
                 for (int h = 0; h < 2 * kMats; ++h)
-                    zero[h] = p.zero ? 0x43004300u + zeros[row_at[h] + gi] * 0x00010001u : 0x43084308u;
+                    zero[h] = kZero ? base + zeros[row_at[h] + gi] * 0x00010001u : eight;
                 float acc[kMats][kCols][4];
 #pragma unroll
                 for (int b = 0; b < kBlocks; ++b) {
@@ -290,10 +312,10 @@ __global__ void __launch_bounds__(32 * kMaxWarps, ctas(kCols)) matvec4_mma_kerne
                         }
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            a0[m][2 * i] = codes2(lo, i, zero[2 * m]);
-                            a0[m][2 * i + 1] = codes2(hi, i, zero[2 * m + 1]);
-                            a1[m][2 * i] = codes2(lo, i + 2, zero[2 * m]);
-                            a1[m][2 * i + 1] = codes2(hi, i + 2, zero[2 * m + 1]);
+                            a0[m][2 * i] = codes2(lo, i, base, zero[2 * m]);
+                            a0[m][2 * i + 1] = codes2(hi, i, base, zero[2 * m + 1]);
+                            a1[m][2 * i] = codes2(lo, i + 2, base, zero[2 * m]);
+                            a1[m][2 * i + 1] = codes2(hi, i + 2, base, zero[2 * m + 1]);
                         }
                     }
 #pragma unroll
@@ -308,8 +330,17 @@ __global__ void __launch_bounds__(32 * kMaxWarps, ctas(kCols)) matvec4_mma_kerne
                     }
                 }
                 float scale[2 * kMats];
+                if (scale_type == SSD_F32) {
 #pragma unroll
-                for (int h = 0; h < 2 * kMats; ++h) scale[h] = scale_at(scales, row_at[h] + gi, p.scale_dtype);
+                    for (int h = 0; h < 2 * kMats; ++h) scale[h] = reinterpret_cast<const float *>(scales)[row_at[h] + gi];
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2 * kMats; ++h) {
+                        const uint16_t v = reinterpret_cast<const uint16_t *>(scales)[row_at[h] + gi];
+                        const float bf16 = __uint_as_float((uint32_t)v << 16), f16 = __half2float(__ushort_as_half(v));
+                        scale[h] = scale_type == SSD_BF16 ? bf16 : f16;
+                    }
+                }
                 const int xg = kX8 ? group_of(block, plan.x_group_blocks, plan.x_group_magic) - first_x_group : 0;
 #pragma unroll
                 for (int n = 0; n < kCols; ++n) {
@@ -332,8 +363,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, ctas(kCols)) matvec4_mma_kerne
         }
         // the tile's parts: of the warps, then of the cluster's CTAs.  Two buffers, so
         // that one barrier a tile is enough.
-        const float *const all = part + (tile & 1) * plan.warps * (kTile * wide);
-        float *const mine = part + ((tile & 1) * plan.warps + warp) * (kTile * wide);
+        const float *const all = part + (tile & 1) * warps * (kTile * wide);
+        float *const mine = part + ((tile & 1) * warps + warp) * (kTile * wide);
 #pragma unroll
         for (int m = 0; m < kMats; ++m)
 #pragma unroll
@@ -346,31 +377,34 @@ __global__ void __launch_bounds__(32 * kMaxWarps, ctas(kCols)) matvec4_mma_kerne
                 sum[m][n][0] = sum[m][n][1] = sum[m][n][2] = sum[m][n][3] = 0.f;
             }
         __syncthreads();
-        const int64_t o0 = (int64_t)(cluster + tile * plan.clusters) * kTile;
-        auto finish = [&](int r, int o, float v) {
-            if (o0 + o >= p.out_features) return;
-            const int64_t at = (r0 + r) * p.out_stride + o0 + o;
+        const int o0 = (cluster + tile * plan.clusters) * kTile;
+        auto finish = [&](int i, float v) {             // output i of the tile's rows x kTile
+            const int r = i / kTile, o = o0 + i % kTile;
+            if (o >= p.out_features) return;
+            const int64_t at = (r0 + r) * p.out_stride + o;
             if (p.out_dtype == SSD_F32) {
-                if (p.bias) v += static_cast<const float *>(p.bias)[o0 + o];
+                if (p.bias) v += static_cast<const float *>(p.bias)[o];
                 static_cast<float *>(p.out)[at] = v;
             } else {
-                if (p.bias) v += to_float(static_cast<const __nv_bfloat16 *>(p.bias)[o0 + o]);
+                if (p.bias) v += to_float(static_cast<const __nv_bfloat16 *>(p.bias)[o]);
                 static_cast<__nv_bfloat16 *>(p.out)[at] = from_float<__nv_bfloat16>(v);
             }
         };
         float *const own_now = own + (tile & 1) * (kTile * rows);
-        for (int i = threadIdx.x; i < rows * kTile; i += blockDim.x) {
-            const int r = i / kTile, o = i % kTile;
+        for (int i = thread; i < rows * kTile; i += blockDim.x) {
+            const float *at = all + i % kTile * wide + i / kTile;
             float v = 0.f;
-            for (int part_ = 0; part_ < parts; ++part_)
-                for (int w = 0; w < plan.warps; ++w) v += all[(w * kTile + o) * wide + part_ * rows + r];
-            if (plan.split == 1) finish(r, o, v);
+            for (int w = 0; w < warps; ++w, at += kTile * wide) {
+                v += at[0];
+                if (parts == 3) v += at[rows] + at[2 * rows];
+            }
+            if (plan.split == 1) finish(i, v);
             else own_now[i] = v;
         }
         if (plan.split > 1) {
             cluster_barrier();
             const uint32_t local = (uint32_t)__cvta_generic_to_shared(own_now);
-            for (int i = rank * blockDim.x + threadIdx.x; i < rows * kTile; i += plan.split * blockDim.x) {
+            for (int i = rank * blockDim.x + thread; i < rows * kTile; i += plan.split * blockDim.x) {
                 float v = 0.f;
                 for (int c = 0; c < plan.split; ++c) {
                     uint32_t at;
@@ -379,7 +413,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, ctas(kCols)) matvec4_mma_kerne
                     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(at) : "memory");
                     v += f;
                 }
-                finish(i / kTile, i % kTile, v);
+                finish(i, v);
             }
         }
     }
@@ -416,8 +450,8 @@ void lay_out(Plan &q, int col_tiles, int blocks) {
     q.smem = at;
 }
 
-template <int kCols, int kBlocks, bool kX8> cudaError_t run(const Plan &q, cudaStream_t stream) {
-    auto kernel = matvec4_mma_kernel<kCols, kBlocks, kX8>;
+template <int kCols, int kBlocks, bool kX8, bool kZero> cudaError_t run(const Plan &q, cudaStream_t stream) {
+    auto kernel = matvec4_mma_kernel<kCols, kBlocks, kX8, kZero>;
     // the most that any plan takes, so that one call of a process and device is enough
     static unsigned long long set = 0;          // bit d: device d (the first 64)
     int device = 0;
@@ -445,7 +479,8 @@ template <int kCols, int kBlocks, bool kX8> cudaError_t run(const Plan &q, cudaS
 }
 
 template <int kCols, int kBlocks> cudaError_t run(const Plan &q, cudaStream_t stream) {
-    return q.p.x_scale ? run<kCols, kBlocks, true>(q, stream) : run<kCols, kBlocks, false>(q, stream);
+    if (q.p.zero) return q.p.x_scale ? run<kCols, kBlocks, true, true>(q, stream) : run<kCols, kBlocks, false, true>(q, stream);
+    return q.p.x_scale ? run<kCols, kBlocks, true, false>(q, stream) : run<kCols, kBlocks, false, false>(q, stream);
 }
 
 template <int kCols> cudaError_t run(const Plan &q, int blocks, cudaStream_t stream) {
