@@ -93,7 +93,8 @@ extern "C" {
 ssd_status ssd_residual_norm(const ssd_residual_norm_params *params, struct CUstream_st *stream) {
     const ssd_status v = check(params);
     if (v != SSD_OK || params->rows == 0) return v;
-    return done(ssd::launch_residual_norm(*params, stream));
+    return done(params->io_dtype == SSD_F32 ? ssd::launch_residual_norm_f32(*params, stream)
+                                            : ssd::launch_residual_norm_bf16(*params, stream));
 }
 
 ssd_status ssd_matvec4(const ssd_matvec4_params *params, struct CUstream_st *stream) {
