@@ -4,19 +4,24 @@
 //   draft i stands while u_i q_i(d_i) < p_i(d_i)
 //   w = max(p - q, 0) of the row where it stopped;  new = the lowest t with cum_t > u cum_V
 //
-// The sums decide which whole number comes out, so they are kept to about 48 bits:
+// The sums decide which whole number comes out, so they are kept to about 45 bits:
 // pairs of floats whose additions keep what rounding drops (Knuth's two-sum; for
 // p - q with p > q Dekker's shorter form), and doubles where there are few terms.
 // In doubles alone the additions of a 128-window batch would take longer than its
-// reads (two fp64 operations a clock and SM).  Bound by HBM: one row of p, and one
-// of q where a draft fell.
+// reads (two fp64 operations a clock and SM).
+//
+// A cluster of CTAs takes a window: each looks for the row where the window stops,
+// sums its part of it, and learns the others' sums through distributed shared
+// memory; the warp in whose part the random number falls reads that part again
+// (from L2).  Bound by HBM for many windows, one row of p and one of q where a draft
+// fell; for few by the chain of dependent reads in front of the row.
 #include "ssd_layer_internal.h"
 #include "ssd_mixer_common.cuh"
 
 namespace ssd {
 namespace {
 
-constexpr int kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kThreads = 512, kWarps = kThreads / 32, kLaneRun = 32;
 
 // s + c, s the rounded sum
 struct Sum {
@@ -29,28 +34,39 @@ struct Sum {
     __device__ double value() const { return (double)s + (double)c; }
 };
 
-__device__ __forceinline__ double warp_total(const Sum &a) {
-    double v = a.value();
+// The sum over the warp's lanes, in all of them.
+__device__ __forceinline__ double warp_total(Sum a) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+    for (int o = 16; o > 0; o >>= 1) a.add(__shfl_xor_sync(0xffffffffu, a.s, o), __shfl_xor_sync(0xffffffffu, a.c, o));
+    return __shfl_sync(0xffffffffu, a.value(), 0);
 }
 
 // Where w comes from: the target's row, less the draft's row or what was drafted.
 template <typename T> struct Weights {
     const T *p, *q;
     int without;                // token whose weight is 0, or -1
-    // w of token t as a rounded value and what its rounding dropped
-    __device__ float2 operator()(int t) const {
-        const float a = to_float(p[t]), b = q ? to_float(q[t]) : 0.f;
+    // w of token t with probabilities a and b as a rounded value and what its rounding dropped
+    __device__ static float2 of(float a, float b, bool out) {
         const float d = a - b;
         // 0 < d finite: a > b; b < 0 or not finite does not come with probabilities
-        return d > 0.f && d < __int_as_float(0x7f800000) && t != without ? make_float2(d, (a - d) - b) : make_float2(0.f, 0.f);
+        return d > 0.f && d < __int_as_float(0x7f800000) && !out ? make_float2(d, (a - d) - b) : make_float2(0.f, 0.f);
+    }
+    __device__ float2 operator()(int t) const { return of(to_float(p[t]), q ? to_float(q[t]) : 0.f, t == without); }
+    // adds the weights of tokens t .. t + N - 1
+    template <int N> __device__ void add(Sum &sum, int t) const {
+        const Pack<T, N> a = load_pack<T, N>(p + t);
+        Pack<T, N> b{};
+        if (q) b = load_pack<T, N>(q + t);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float2 v = of(to_float(a.v[i]), to_float(b.v[i]), t + i == without);
+            sum.add(v.x, v.y);
+        }
     }
 };
 
 template <typename T> struct Window {
-    int a, k, n;                // first token; drafts; drafts that stand
+    int first, k, n;            // first token; drafts; drafts that stand
     bool live;
     Weights<T> w;
 };
@@ -59,134 +75,234 @@ __device__ __forceinline__ void flag(int32_t *status, int bit) {
     if (status) atomicOr(status, bit);
 }
 
-template <typename T> __global__ void __launch_bounds__(kThreads) verify_kernel(const ssd_verify_params a) {
-    __shared__ Window<T> win;
-    __shared__ double part[kWarps];
-    __shared__ int found;
-    await_previous();
-    const int s = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, V = a.vocab;
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+__device__ __forceinline__ double load_of(const double *mine, int rank) {
+    uint32_t at;
+    double v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(mine)), "r"(rank));
+    asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(at) : "memory");
+    return v;
+}
+
+// The window's metadata and where it stops; one warp.  `report`: sets status bits.
+template <typename T> __device__ void find_stop(const ssd_verify_params &a, int s, bool report, Window<T> &win) {
+    const int lane = threadIdx.x & 31, V = a.vocab;
     const T *const target = static_cast<const T *>(a.target_probs), *const draft = static_cast<const T *>(a.draft_probs);
-    if (warp == 0) {
-        const int64_t first = a.cu_seqlens[s], end = a.cu_seqlens[s + 1];
-        const int64_t k = end - first - 1, d0 = first - s;
-        bool ok = true;
-        if (first < 0 || end < first || end > a.total_tokens || (k > 0 && (d0 < 0 || d0 + k > a.num_drafts))) {
-            if (lane == 0) flag(a.device_status, SSD_DEV_BAD_SEQLENS);
-            ok = false;
-        }
-        ok = ok && k >= 0;
-        int n = 0;
-        for (int base = 0; ok && base < k; base += 32) {
-            const int i = base + lane;
-            bool stands = true, bad = false;
-            if (i < k) {
-                const int tok = a.tokens[first + i + 1];
-                bad = tok < 0 || tok >= V;
-                if (!bad) {
-                    const double q = draft ? (double)to_float(draft[(d0 + i) * a.draft_stride + tok]) : 1.0;
-                    const double p = (double)to_float(target[(first + i) * a.target_stride + tok]);
-                    stands = (double)fminf(fmaxf(a.accept_u[d0 + i], 0.f), 1.f) * q < p;
-                }
-            }
-            const uint32_t stop = __ballot_sync(0xffffffffu, bad || !stands), wrong = __ballot_sync(0xffffffffu, bad);
-            if (stop) {
-                const int at = __ffs(stop) - 1;
-                n = base + at;
-                if (wrong >> at & 1) {
-                    if (lane == 0) flag(a.device_status, SSD_DEV_BAD_TOKEN);
-                    ok = false;
-                }
-                break;
-            }
-            n = (int)min((int64_t)base + 32, k);
-        }
-        if (lane == 0) {
-            win.live = ok;
-            win.a = (int)first;
-            win.k = (int)k;
-            win.n = n;
-            if (ok) {
-                win.w.p = target + (first + n) * a.target_stride;
-                win.w.q = draft && n < k ? draft + (d0 + n) * a.draft_stride : nullptr;
-                win.w.without = !draft && n < k ? a.tokens[first + n + 1] : -1;
-            }
-            found = -1;
-        }
+    const int64_t first = a.cu_seqlens[s], end = a.cu_seqlens[s + 1];
+    const int64_t k = end - first - 1, d0 = first - s;
+    bool ok = true;
+    if (first < 0 || end < first || end > a.total_tokens || (k > 0 && (d0 < 0 || d0 + k > a.num_drafts))) {
+        if (report && lane == 0) flag(a.device_status, SSD_DEV_BAD_SEQLENS);
+        ok = false;
     }
-    __syncthreads();
-    if (!win.live) return;
-    Weights<T> w = win.w;
-    const int first = win.a, k = win.k, n = win.n;
-    // a warp sums an unbroken part of the row
-    const int per = ((V - 1) / (32 * kWarps) + 1) * 32, lo = min(V, warp * per), hi = min(V, lo + per);
-    const float u_in = a.sample_u[s];
-    const double u = u_in > 0.f ? fmin((double)u_in, 1.0) : 0.0;
-    for (int attempt = 0; attempt < 2; ++attempt) {
-        Sum sum;
-        for (int t = lo + lane; t < hi; t += 32) {
-            const float2 v = w(t);
-            sum.add(v.x, v.y);
+    ok = ok && k >= 0;
+    int n = 0;
+    for (int base = 0; ok && base < k; base += 32) {
+        const int i = base + lane;
+        bool stands = true, bad = false;
+        if (i < k) {
+            const float u = a.accept_u[d0 + i];
+            const int tok = a.tokens[first + i + 1];
+            bad = tok < 0 || tok >= V;
+            if (!bad) {
+                const double q = draft ? (double)to_float(draft[(d0 + i) * a.draft_stride + tok]) : 1.0;
+                const double p = (double)to_float(target[(first + i) * a.target_stride + tok]);
+                stands = (double)fminf(fmaxf(u, 0.f), 1.f) * q < p;
+            }
         }
-        const double mine = warp_total(sum);
-        __syncthreads();
-        if (lane == 0) part[warp] = mine;
-        __syncthreads();
-        double total = 0.0;
-        for (int i = 0; i < kWarps; ++i) total += part[i];
-        if (total > 0.0) {
-            double goal = u * total;
-            double before = 0.0;
-            int owner = -1, last = -1;
-            for (int i = 0; i < kWarps && owner < 0; ++i) {
-                if (part[i] > 0.0) last = i;
-                if (before + part[i] > goal) owner = i;
-                else before += part[i];
-            }
-            if (owner < 0) {        // u = 1: the last token of any weight
-                owner = last;
-                goal = total * 2.0;
-                before = 0.0;
-            }
-            if (warp == owner) {
-                int at = -1, positive = -1;
-                for (int base = lo; base < hi && at < 0; base += 32) {
-                    const int t = base + lane;
-                    const float2 v = t < hi ? w(t) : make_float2(0.f, 0.f);
-                    double c = (double)v.x + (double)v.y;
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const double d = __shfl_up_sync(0xffffffffu, c, o);
-                        if (lane >= o) c += d;
-                    }
-                    const uint32_t some = __ballot_sync(0xffffffffu, v.x > 0.f);
-                    const uint32_t over = __ballot_sync(0xffffffffu, v.x > 0.f && before + c > goal);
-                    if (some) positive = base + 31 - __clz(some);
-                    if (over) at = base + __ffs(over) - 1;
-                    before += __shfl_sync(0xffffffffu, c, 31);
-                }
-                if (lane == 0) found = at < 0 ? positive : at;
+        const uint32_t stop = __ballot_sync(0xffffffffu, bad || !stands), wrong = __ballot_sync(0xffffffffu, bad);
+        if (stop) {
+            const int at = __ffs(stop) - 1;
+            n = base + at;
+            if (wrong >> at & 1) {
+                if (report && lane == 0) flag(a.device_status, SSD_DEV_BAD_TOKEN);
+                ok = false;
             }
             break;
         }
-        if (w.q == nullptr && w.without < 0) break;     // nothing in the target's row either
-        w.q = nullptr;
+        n = (int)min((int64_t)base + 32, k);
+    }
+    if (lane == 0) {
+        win.live = ok;
+        win.first = (int)first;
+        win.k = (int)k;
+        win.n = n;
+        if (ok) {
+            win.w.p = target + (first + n) * a.target_stride;
+            win.w.q = draft && n < k ? draft + (d0 + n) * a.draft_stride : nullptr;
+            win.w.without = !draft && n < k ? a.tokens[first + n + 1] : -1;
+        }
+    }
+}
+
+// The token of [lo, hi) where the sum, `before` ahead of lo, passes goal, or else the
+// last of any weight (-1 without one).  A lane takes kLaneRun tokens in a row.
+template <typename T, int N> __device__ int search(const Weights<T> &w, int lo, int hi, double before, double goal) {
+    const int lane = threadIdx.x & 31;
+    int positive = -1;
+    for (int base = lo; base < hi; base += 32 * kLaneRun) {
+        const int from = min(hi, base + lane * kLaneRun), to = min(hi, from + kLaneRun);
+        Sum sum;
+        int t = from;
+#pragma unroll 4
+        for (; t + N <= to; t += N) w.template add<N>(sum, t);
+        for (; t < to; ++t) w.template add<1>(sum, t);
+        const double mine = sum.value();
+        double c = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double d = __shfl_up_sync(0xffffffffu, c, o);
+            if (lane >= o) c += d;
+        }
+        const uint32_t some = __ballot_sync(0xffffffffu, mine > 0.0), over = some & __ballot_sync(0xffffffffu, before + c > goal);
+        const int at = over ? __ffs(over) - 1 : some ? 31 - __clz(some) : -1;
+        if (at >= 0) {          // the lane's tokens one after another; its last of any weight where nothing passes
+            int found = -1;
+            if (lane == at) {
+                const double left = over ? goal - (before + (c - mine)) : 2.0 * mine;
+                const float gs = (float)left, gc = (float)(left - (double)gs);
+                Sum so_far;
+                for (int i = from; i < to; ++i) {
+                    const float2 v = w(i);
+                    so_far.add(v.x, v.y);
+                    if (v.x > 0.f) {
+                        found = i;
+                        if ((so_far.s - gs) + (so_far.c - gc) > 0.f) break;
+                    }
+                }
+            }
+            positive = __shfl_sync(0xffffffffu, found, at);
+            if (over) return positive;
+        }
+        before += __shfl_sync(0xffffffffu, c, 31);
+    }
+    return positive;
+}
+
+template <typename T> __global__ void __launch_bounds__(kThreads) verify_kernel(const ssd_verify_params a, int split, int per) {
+    __shared__ Window<T> win;
+    __shared__ double part[kWarps], whole[8], totals[2];
+    __shared__ int found;
+    constexpr int N = 16 / sizeof(T);
+    await_previous();
+    const int s = blockIdx.x / split, rank = blockIdx.x % split, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, V = a.vocab;
+    if (warp == 0) find_stop(a, s, rank == 0, win);
+    const float u_in = a.sample_u[s];
+    const double u = u_in > 0.f ? fmin((double)u_in, 1.0) : 0.0;
+    __syncthreads();
+    if (!win.live) return;              // of all CTAs of the cluster
+    Weights<T> w = win.w;
+    const int first = win.first, k = win.k, n = win.n;
+    // a warp sums an unbroken part of the row
+    const int64_t begin = ((int64_t)rank * kWarps + warp) * per;
+    const int lo = (int)min((int64_t)V, begin), hi = (int)min((int64_t)V, begin + per);
+    for (int attempt = 0;; ++attempt) {
+        const bool wide = ((reinterpret_cast<uintptr_t>(w.p) | reinterpret_cast<uintptr_t>(w.q)) & 15) == 0;
+        Sum sum;
+        int t = lo;
+        if (wide) {
+#pragma unroll 4
+            for (int i = lo + lane * N; i + N <= hi; i += 32 * N) w.template add<N>(sum, i);
+            t = hi - (hi - lo) % N;
+        }
+#pragma unroll 8
+        for (int i = t + lane; i < hi; i += 32) w.template add<1>(sum, i);
+        const double mine = warp_total(sum);
+        if (lane == 0) part[warp] = mine;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            double v = 0.0;
+            for (int i = 0; i < kWarps; ++i) v += part[i];
+            totals[attempt] = v;        // of a first attempt it is still there when others read it late
+            found = -2;
+        }
+        __syncthreads();
+        if (split > 1) {
+            cluster_arrive();
+            cluster_wait();
+        }
+        if (threadIdx.x < split) whole[threadIdx.x] = split > 1 ? load_of(&totals[attempt], threadIdx.x) : totals[attempt];
+        __syncthreads();
+        double total = 0.0;
+        for (int i = 0; i < split; ++i) total += whole[i];
+        const bool last_try = attempt == 1 || (w.q == nullptr && w.without < 0);
+        if (total > 0.0 || last_try) {
+            // the CTA, then the warp, in whose part the goal lies; the last of any weight for u = 1
+            double goal = u * total, before = 0.0;
+            int owner = -1, last = 0;
+            for (int i = 0; i < split && owner < 0; ++i) {
+                if (whole[i] > 0.0) last = i;
+                if (before + whole[i] > goal) owner = i;
+                else before += whole[i];
+            }
+            if (owner < 0) {
+                owner = last;
+                goal = 4.0 * total;
+            }
+            if (rank == owner) {
+                int by = -1, last_warp = -1;
+                for (int i = 0; i < kWarps && by < 0; ++i) {
+                    if (part[i] > 0.0) last_warp = i;
+                    if (before + part[i] > goal) by = i;
+                    else before += part[i];
+                }
+                if (by < 0) {
+                    by = last_warp;
+                    goal = 4.0 * total;
+                }
+                if (by < 0) {
+                    if (threadIdx.x == 0) found = -1;
+                } else if (warp == by) {
+                    const int at = wide ? search<T, N>(w, lo, hi, before, goal) : search<T, 1>(w, lo, hi, before, goal);
+                    if (lane == 0) found = at;
+                }
+                __syncthreads();
+                for (int i = threadIdx.x; i <= k; i += kThreads)
+                    a.out_tokens[first + i] = i < n ? a.tokens[first + i + 1] : i == n ? found : -1;
+                if (threadIdx.x == 0) {
+                    if (found < 0) flag(a.device_status, SSD_DEV_BAD_PROBS);
+                    a.out_accepted[s] = n;
+                    if (a.ring_count) a.ring_count[s] += n + 1;
+                }
+            }
+            break;
+        }
+        w.q = nullptr;                  // nothing is left of p - q: the target's row
         w.without = -1;
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i <= k; i += kThreads)
-        a.out_tokens[first + i] = i < n ? a.tokens[first + i + 1] : i == n ? found : -1;
-    if (threadIdx.x == 0) {
-        if (found < 0) flag(a.device_status, SSD_DEV_BAD_PROBS);
-        a.out_accepted[s] = n;
-        if (a.ring_count) a.ring_count[s] += n + 1;
+    if (split > 1) {                    // no CTA leaves while another reads its sums
+        cluster_arrive();
+        cluster_wait();
     }
+}
+
+template <typename T> cudaError_t launch(const ssd_verify_params &p, cudaStream_t stream) {
+    // CTAs of a window: parts of at least 4,096 tokens, about four CTAs an SM in all
+    int split = 1;
+    while (split < 8 && p.vocab >= split * 2 * 4096 && (int64_t)p.num_seqs * split * 2 <= 152 * 4) split *= 2;
+    const int warps = split * kWarps;
+    const int per = (int)((((int64_t)p.vocab - 1) / warps / 128 + 1) * 128);
+    if ((int64_t)p.num_seqs * split > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t config = {};
+    config.gridDim = dim3((unsigned)(p.num_seqs * split));
+    config.blockDim = dim3(kThreads);
+    config.stream = stream;
+    config.attrs = attr;
+    config.numAttrs = 2;
+    return cudaLaunchKernelEx(&config, verify_kernel<T>, p, split, per);
 }
 
 }  // namespace
 
 cudaError_t launch_verify(const ssd_verify_params &p, cudaStream_t stream) {
-    if (p.prob_dtype == SSD_F32) return enqueue(verify_kernel<float>, dim3((unsigned)p.num_seqs), kThreads, stream, p);
-    return enqueue(verify_kernel<__nv_bfloat16>, dim3((unsigned)p.num_seqs), kThreads, stream, p);
+    return p.prob_dtype == SSD_F32 ? launch<float>(p, stream) : launch<__nv_bfloat16>(p, stream);
 }
 
 }  // namespace ssd
