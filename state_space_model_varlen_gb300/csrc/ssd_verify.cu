@@ -6,9 +6,8 @@
 //
 // The sums decide which whole number comes out, so they are kept to about 45 bits:
 // pairs of floats whose additions keep what rounding drops (Knuth's two-sum; for
-// p - q with p > q Dekker's shorter form), and doubles where there are few terms.
-// In doubles alone the additions of a 128-window batch would take longer than its
-// reads (two fp64 operations a clock and SM).
+// p - q with p > q Dekker's shorter form).  Doubles would take longer than the reads:
+// two operations a clock and SM, 16 clocks for one of a warp.
 //
 // A cluster of CTAs takes a window: each looks for the row where the window stops,
 // sums its part of it, and learns the others' sums through distributed shared
@@ -31,14 +30,54 @@ struct Sum {
         c += ((s - (t - b)) + (v - b)) + rest;
         s = t;
     }
-    __device__ double value() const { return (double)s + (double)c; }
+    __device__ void add(const Sum &o) { add(o.s, o.c); }
+    __device__ void subtract(const Sum &o) { add(-o.s, -o.c); }
+    __device__ bool above(const Sum &o) const { return (s - o.s) + (c - o.c) > 0.f; }
 };
-
-// The sum over the warp's lanes, in all of them.
-__device__ __forceinline__ double warp_total(Sum a) {
+__device__ __forceinline__ Sum times(const Sum &a, float f) {
+    Sum r;
+    r.s = a.s * f;
+    r.c = fmaf(a.s, f, -r.s) + a.c * f;
+    return r;
+}
+__device__ __forceinline__ Sum shuffled(const Sum &a, int lane) {
+    Sum r;
+    r.s = __shfl_sync(0xffffffffu, a.s, lane);
+    r.c = __shfl_sync(0xffffffffu, a.c, lane);
+    return r;
+}
+// of lanes 0 .. lane
+__device__ __forceinline__ Sum scan(Sum a) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a.add(__shfl_xor_sync(0xffffffffu, a.s, o), __shfl_xor_sync(0xffffffffu, a.c, o));
-    return __shfl_sync(0xffffffffu, a.value(), 0);
+    for (int o = 1; o < 32; o <<= 1) {
+        const float s = __shfl_up_sync(0xffffffffu, a.s, o), c = __shfl_up_sync(0xffffffffu, a.c, o);
+        if ((threadIdx.x & 31) >= o) a.add(s, c);
+    }
+    return a;
+}
+// what scan() gave the lane before
+__device__ __forceinline__ Sum before_lane(const Sum &a) {
+    Sum r;
+    r.s = __shfl_up_sync(0xffffffffu, a.s, 1);
+    r.c = __shfl_up_sync(0xffffffffu, a.c, 1);
+    return threadIdx.x & 31 ? r : Sum();
+}
+// The first of n lanes at which `sums`, scanned, pass goal, and what they are before
+// it; or (with goal out of the way, so that the last of any weight is found below)
+// the last one with a sum, or -1.
+__device__ __forceinline__ int owner_of(const Sum &mine, int n, Sum &goal, Sum &before) {
+    const int lane = threadIdx.x & 31;
+    Sum upto = scan(lane < n ? mine : Sum());
+    const Sum base = before;
+    upto.add(base);
+    Sum ahead = before_lane(upto);
+    if (lane == 0) ahead = base;
+    const uint32_t some = __ballot_sync(0xffffffffu, lane < n && mine.s > 0.f);
+    const uint32_t over = some & __ballot_sync(0xffffffffu, upto.above(goal));
+    if (!over) goal.s = __int_as_float(0x7f7fffff);
+    const int at = over ? __ffs(over) - 1 : some ? 31 - __clz(some) : -1;
+    before = shuffled(ahead, at < 0 ? 0 : at);
+    return at;
 }
 
 // Where w comes from: the target's row, less the draft's row or what was drafted.
@@ -77,11 +116,11 @@ __device__ __forceinline__ void flag(int32_t *status, int bit) {
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
-__device__ __forceinline__ double load_of(const double *mine, int rank) {
+__device__ __forceinline__ Sum load_of(const float2 *mine, int rank) {
     uint32_t at;
-    double v;
+    Sum v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(mine)), "r"(rank));
-    asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(at) : "memory");
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.s), "=f"(v.c) : "r"(at) : "memory");
     return v;
 }
 
@@ -138,58 +177,53 @@ template <typename T> __device__ void find_stop(const ssd_verify_params &a, int 
 
 // The token of [lo, hi) where the sum, `before` ahead of lo, passes goal, or else the
 // last of any weight (-1 without one).  A lane takes kLaneRun tokens in a row.
-template <typename T, int N> __device__ int search(const Weights<T> &w, int lo, int hi, double before, double goal) {
+template <typename T, int N> __device__ int search(const Weights<T> &w, int lo, int hi, Sum before, const Sum &goal) {
     const int lane = threadIdx.x & 31;
     int positive = -1;
     for (int base = lo; base < hi; base += 32 * kLaneRun) {
         const int from = min(hi, base + lane * kLaneRun), to = min(hi, from + kLaneRun);
-        Sum sum;
+        Sum mine;
         int t = from;
 #pragma unroll 4
-        for (; t + N <= to; t += N) w.template add<N>(sum, t);
-        for (; t < to; ++t) w.template add<1>(sum, t);
-        const double mine = sum.value();
-        double c = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double d = __shfl_up_sync(0xffffffffu, c, o);
-            if (lane >= o) c += d;
-        }
-        const uint32_t some = __ballot_sync(0xffffffffu, mine > 0.0), over = some & __ballot_sync(0xffffffffu, before + c > goal);
+        for (; t + N <= to; t += N) w.template add<N>(mine, t);
+        for (; t < to; ++t) w.template add<1>(mine, t);
+        const Sum run = scan(mine);
+        Sum upto = run;
+        upto.add(before);
+        const uint32_t some = __ballot_sync(0xffffffffu, mine.s > 0.f), over = some & __ballot_sync(0xffffffffu, upto.above(goal));
         const int at = over ? __ffs(over) - 1 : some ? 31 - __clz(some) : -1;
+        const Sum ahead = before_lane(run);
         if (at >= 0) {          // the lane's tokens one after another; its last of any weight where nothing passes
             int found = -1;
             if (lane == at) {
-                const double left = over ? goal - (before + (c - mine)) : 2.0 * mine;
-                const float gs = (float)left, gc = (float)(left - (double)gs);
-                Sum so_far;
+                Sum left = goal, so_far;
+                left.subtract(before);
+                left.subtract(ahead);
                 for (int i = from; i < to; ++i) {
                     const float2 v = w(i);
                     so_far.add(v.x, v.y);
                     if (v.x > 0.f) {
                         found = i;
-                        if ((so_far.s - gs) + (so_far.c - gc) > 0.f) break;
+                        if (over && so_far.above(left)) break;
                     }
                 }
             }
             positive = __shfl_sync(0xffffffffu, found, at);
             if (over) return positive;
         }
-        before += __shfl_sync(0xffffffffu, c, 31);
+        before.add(shuffled(run, 31));
     }
     return positive;
 }
 
-template <typename T> __global__ void __launch_bounds__(kThreads) verify_kernel(const ssd_verify_params a, int split, int per) {
+template <typename T> __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const ssd_verify_params a, int split, int per) {
     __shared__ Window<T> win;
-    __shared__ double part[kWarps], whole[8], totals[2];
-    __shared__ int found;
+    __shared__ float2 part[2][kWarps], totals[2];       // of the first attempt and of the second
     constexpr int N = 16 / sizeof(T);
     await_previous();
     const int s = blockIdx.x / split, rank = blockIdx.x % split, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, V = a.vocab;
     if (warp == 0) find_stop(a, s, rank == 0, win);
-    const float u_in = a.sample_u[s];
-    const double u = u_in > 0.f ? fmin((double)u_in, 1.0) : 0.0;
+    const float u_in = a.sample_u[s], u = u_in > 0.f ? fminf(u_in, 1.f) : 0.f;
     __syncthreads();
     if (!win.live) return;              // of all CTAs of the cluster
     Weights<T> w = win.w;
@@ -208,62 +242,38 @@ template <typename T> __global__ void __launch_bounds__(kThreads) verify_kernel(
         }
 #pragma unroll 8
         for (int i = t + lane; i < hi; i += 32) w.template add<1>(sum, i);
-        const double mine = warp_total(sum);
-        if (lane == 0) part[warp] = mine;
+        const Sum mine = scan(sum);
+        if (lane == 31) part[attempt][warp] = make_float2(mine.s, mine.c);
         __syncthreads();
-        if (threadIdx.x == 0) {
-            double v = 0.0;
-            for (int i = 0; i < kWarps; ++i) v += part[i];
-            totals[attempt] = v;        // of a first attempt it is still there when others read it late
-            found = -2;
+        // every warp for itself, all the same: the CTA's sum, the others', and where the goal lies
+        Sum warps;
+        if (lane < kWarps) {
+            warps.s = part[attempt][lane].x;
+            warps.c = part[attempt][lane].y;
         }
-        __syncthreads();
+        Sum cta = shuffled(scan(warps), kWarps - 1);
         if (split > 1) {
+            if (threadIdx.x == 0) totals[attempt] = make_float2(cta.s, cta.c);
             cluster_arrive();
             cluster_wait();
+            cta = lane < split ? load_of(&totals[attempt], lane) : Sum();
         }
-        if (threadIdx.x < split) whole[threadIdx.x] = split > 1 ? load_of(&totals[attempt], threadIdx.x) : totals[attempt];
-        __syncthreads();
-        double total = 0.0;
-        for (int i = 0; i < split; ++i) total += whole[i];
+        const Sum total = shuffled(scan(lane < split ? cta : Sum()), split - 1);
         const bool last_try = attempt == 1 || (w.q == nullptr && w.without < 0);
-        if (total > 0.0 || last_try) {
-            // the CTA, then the warp, in whose part the goal lies; the last of any weight for u = 1
-            double goal = u * total, before = 0.0;
-            int owner = -1, last = 0;
-            for (int i = 0; i < split && owner < 0; ++i) {
-                if (whole[i] > 0.0) last = i;
-                if (before + whole[i] > goal) owner = i;
-                else before += whole[i];
-            }
-            if (owner < 0) {
-                owner = last;
-                goal = 4.0 * total;
-            }
+        if (total.s > 0.f || last_try) {
+            Sum goal = times(total, u), before;
+            if (u == 1.f) goal.s = __int_as_float(0x7f7fffff);          // the last of any weight
+            const int owner = max(0, owner_of(cta, split, goal, before));
             if (rank == owner) {
-                int by = -1, last_warp = -1;
-                for (int i = 0; i < kWarps && by < 0; ++i) {
-                    if (part[i] > 0.0) last_warp = i;
-                    if (before + part[i] > goal) by = i;
-                    else before += part[i];
-                }
-                if (by < 0) {
-                    by = last_warp;
-                    goal = 4.0 * total;
-                }
-                if (by < 0) {
-                    if (threadIdx.x == 0) found = -1;
-                } else if (warp == by) {
+                const int by = max(0, owner_of(warps, kWarps, goal, before));
+                if (warp == by) {
                     const int at = wide ? search<T, N>(w, lo, hi, before, goal) : search<T, 1>(w, lo, hi, before, goal);
-                    if (lane == 0) found = at;
-                }
-                __syncthreads();
-                for (int i = threadIdx.x; i <= k; i += kThreads)
-                    a.out_tokens[first + i] = i < n ? a.tokens[first + i + 1] : i == n ? found : -1;
-                if (threadIdx.x == 0) {
-                    if (found < 0) flag(a.device_status, SSD_DEV_BAD_PROBS);
-                    a.out_accepted[s] = n;
-                    if (a.ring_count) a.ring_count[s] += n + 1;
+                    for (int i = lane; i <= k; i += 32) a.out_tokens[first + i] = i < n ? a.tokens[first + i + 1] : i == n ? at : -1;
+                    if (lane == 0) {
+                        if (at < 0) flag(a.device_status, SSD_DEV_BAD_PROBS);
+                        a.out_accepted[s] = n;
+                        if (a.ring_count) a.ring_count[s] += n + 1;
+                    }
                 }
             }
             break;
