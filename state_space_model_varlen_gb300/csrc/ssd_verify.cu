@@ -20,7 +20,7 @@
 namespace ssd {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32, kLaneRun = 32;
+constexpr int kLaneRun = 32;
 
 // s + c, s the rounded sum
 struct Sum {
@@ -31,7 +31,6 @@ struct Sum {
         s = t;
     }
     __device__ void add(const Sum &o) { add(o.s, o.c); }
-    __device__ void subtract(const Sum &o) { add(-o.s, -o.c); }
     __device__ bool above(const Sum &o) const { return (s - o.s) + (c - o.c) > 0.f; }
 };
 __device__ __forceinline__ Sum times(const Sum &a, float f) {
@@ -82,20 +81,35 @@ __device__ __forceinline__ int owner_of(const Sum &mine, int n, Sum &goal, Sum &
 
 // Where w comes from: the target's row, less the draft's row or what was drafted.
 template <typename T> struct Weights {
+    static constexpr int N = 16 / sizeof(T);
     const T *p, *q;
     int without;                // token whose weight is 0, or -1
-    // w of token t with probabilities a and b as a rounded value and what its rounding dropped
+    // w of a token with probabilities a and b as a rounded value and what its rounding dropped
     __device__ static float2 of(float a, float b, bool out) {
         const float d = a - b;
         // 0 < d finite: a > b; b < 0 or not finite does not come with probabilities
         return d > 0.f && d < __int_as_float(0x7f800000) && !out ? make_float2(d, (a - d) - b) : make_float2(0.f, 0.f);
     }
     __device__ float2 operator()(int t) const { return of(to_float(p[t]), q ? to_float(q[t]) : 0.f, t == without); }
-    // adds the weights of tokens t .. t + N - 1
-    template <int N> __device__ void add(Sum &sum, int t) const {
+    // elements that p's row begins behind a 16-byte boundary, and whether q's begins like it
+    __device__ int ahead() const { return (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T)); }
+    __device__ bool alike() const { return ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15) == 0; }
+    __device__ void add_one(Sum &sum, int t) const {
+        const float2 v = (*this)(t);
+        sum.add(v.x, v.y);
+    }
+    // adds tokens t .. t + N - 1, where p + t is a 16-byte boundary
+    __device__ void add(Sum &sum, int t, bool alike) const {
         const Pack<T, N> a = load_pack<T, N>(p + t);
         Pack<T, N> b{};
-        if (q) b = load_pack<T, N>(q + t);
+        if (q) {
+            if (alike) {
+                b = load_pack<T, N>(q + t);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) b.v[i] = q[t + i];
+            }
+        }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const float2 v = of(to_float(a.v[i]), to_float(b.v[i]), t + i == without);
@@ -176,50 +190,52 @@ template <typename T> __device__ void find_stop(const ssd_verify_params &a, int 
 }
 
 // The token of [lo, hi) where the sum, `before` ahead of lo, passes goal, or else the
-// last of any weight (-1 without one).  A lane takes kLaneRun tokens in a row.
-template <typename T, int N> __device__ int search(const Weights<T> &w, int lo, int hi, Sum before, const Sum &goal) {
-    const int lane = threadIdx.x & 31;
+// last of any weight (-1 without one).  A lane takes kLaneRun tokens in a row, which
+// begin at a 16-byte boundary of p but for the row's first.
+template <typename T> __device__ int search(const Weights<T> &w, int lo, int hi, Sum before, const Sum &goal) {
+    constexpr int N = Weights<T>::N;
+    const int lane = threadIdx.x & 31, shift = w.ahead();
+    const bool alike = w.alike();
     int positive = -1;
-    for (int base = lo; base < hi; base += 32 * kLaneRun) {
-        const int from = min(hi, base + lane * kLaneRun), to = min(hi, from + kLaneRun);
+    for (int base = (lo + shift) / N * N - shift; base < hi; base += 32 * kLaneRun) {
+        const int run = base + lane * kLaneRun;
         Sum mine;
-        int t = from;
 #pragma unroll 4
-        for (; t + N <= to; t += N) w.template add<N>(mine, t);
-        for (; t < to; ++t) w.template add<1>(mine, t);
-        const Sum run = scan(mine);
-        Sum upto = run;
-        upto.add(before);
-        const uint32_t some = __ballot_sync(0xffffffffu, mine.s > 0.f), over = some & __ballot_sync(0xffffffffu, upto.above(goal));
-        const int at = over ? __ffs(over) - 1 : some ? 31 - __clz(some) : -1;
-        const Sum ahead = before_lane(run);
-        if (at >= 0) {          // the lane's tokens one after another; its last of any weight where nothing passes
-            int found = -1;
-            if (lane == at) {
-                Sum left = goal, so_far;
-                left.subtract(before);
-                left.subtract(ahead);
-                for (int i = from; i < to; ++i) {
-                    const float2 v = w(i);
-                    so_far.add(v.x, v.y);
-                    if (v.x > 0.f) {
-                        found = i;
-                        if (over && so_far.above(left)) break;
-                    }
-                }
+        for (int t = run; t < run + kLaneRun; t += N) {
+            if (t >= lo && t + N <= hi) {
+                w.add(mine, t, alike);
+            } else {
+                for (int i = max(t, lo); i < min(t + N, hi); ++i) w.add_one(mine, i);
             }
-            positive = __shfl_sync(0xffffffffu, found, at);
+        }
+        const Sum upto = scan(mine);
+        Sum all = upto;
+        all.add(before);
+        const uint32_t some = __ballot_sync(0xffffffffu, mine.s > 0.f), over = some & __ballot_sync(0xffffffffu, all.above(goal));
+        const int at = over ? __ffs(over) - 1 : some ? 31 - __clz(some) : -1;
+        if (at >= 0) {          // that lane's tokens, one a lane
+            const Sum ahead = shuffled(before_lane(upto), at);
+            const int t = base + at * kLaneRun + lane;
+            Sum one;
+            if (t >= lo && t < hi) w.add_one(one, t);
+            Sum sum = scan(one);
+            sum.add(ahead);
+            sum.add(before);
+            const uint32_t any = __ballot_sync(0xffffffffu, one.s > 0.f);
+            const uint32_t passed = any & __ballot_sync(0xffffffffu, sum.above(goal));
+            positive = base + at * kLaneRun + (over && passed ? __ffs(passed) - 1 : 31 - __clz(any));
             if (over) return positive;
         }
-        before.add(shuffled(run, 31));
+        before.add(shuffled(upto, 31));
     }
     return positive;
 }
 
-template <typename T> __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const ssd_verify_params a, int split, int per) {
+template <typename T, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const ssd_verify_params a, int split, int per) {
+    constexpr int kWarps = kThreads / 32, N = Weights<T>::N;
     __shared__ Window<T> win;
     __shared__ float2 part[2][kWarps], totals[2];       // of the first attempt and of the second
-    constexpr int N = 16 / sizeof(T);
     await_previous();
     const int s = blockIdx.x / split, rank = blockIdx.x % split, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, V = a.vocab;
     if (warp == 0) find_stop(a, s, rank == 0, win);
@@ -228,20 +244,17 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 2) verify_kern
     if (!win.live) return;              // of all CTAs of the cluster
     Weights<T> w = win.w;
     const int first = win.first, k = win.k, n = win.n;
-    // a warp sums an unbroken part of the row
-    const int64_t begin = ((int64_t)rank * kWarps + warp) * per;
-    const int lo = (int)min((int64_t)V, begin), hi = (int)min((int64_t)V, begin + per);
+    // a warp sums an unbroken part of the row, from a 16-byte boundary of p on
+    const int64_t begin = ((int64_t)rank * kWarps + warp) * per - w.ahead();
+    const int lo = (int)min((int64_t)V, max((int64_t)0, begin)), hi = (int)max((int64_t)0, min((int64_t)V, begin + per));
+    const int lo_whole = min(hi, lo > 0 ? lo : (N - w.ahead()) % N), hi_whole = lo_whole + (hi - lo_whole) / N * N;
     for (int attempt = 0;; ++attempt) {
-        const bool wide = ((reinterpret_cast<uintptr_t>(w.p) | reinterpret_cast<uintptr_t>(w.q)) & 15) == 0;
+        const bool alike = w.alike();
         Sum sum;
-        int t = lo;
-        if (wide) {
+        if (lo + lane < lo_whole) w.add_one(sum, lo + lane);
 #pragma unroll 4
-            for (int i = lo + lane * N; i + N <= hi; i += 32 * N) w.template add<N>(sum, i);
-            t = hi - (hi - lo) % N;
-        }
-#pragma unroll 8
-        for (int i = t + lane; i < hi; i += 32) w.template add<1>(sum, i);
+        for (int t = lo_whole + lane * N; t < hi_whole; t += 32 * N) w.add(sum, t, alike);
+        if (hi_whole + lane < hi) w.add_one(sum, hi_whole + lane);
         const Sum mine = scan(sum);
         if (lane == 31) part[attempt][warp] = make_float2(mine.s, mine.c);
         __syncthreads();
@@ -267,7 +280,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 2) verify_kern
             if (rank == owner) {
                 const int by = max(0, owner_of(warps, kWarps, goal, before));
                 if (warp == by) {
-                    const int at = wide ? search<T, N>(w, lo, hi, before, goal) : search<T, 1>(w, lo, hi, before, goal);
+                    const int at = search(w, lo, hi, before, goal);
                     for (int i = lane; i <= k; i += 32) a.out_tokens[first + i] = i < n ? a.tokens[first + i + 1] : i == n ? at : -1;
                     if (lane == 0) {
                         if (at < 0) flag(a.device_status, SSD_DEV_BAD_PROBS);
@@ -287,13 +300,10 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 2) verify_kern
     }
 }
 
-template <typename T> cudaError_t launch(const ssd_verify_params &p, cudaStream_t stream) {
-    // CTAs of a window: parts of at least 4,096 tokens, about four CTAs an SM in all
-    int split = 1;
-    while (split < 8 && p.vocab >= split * 2 * 4096 && (int64_t)p.num_seqs * split * 2 <= 152 * 4) split *= 2;
-    const int warps = split * kWarps;
-    const int per = (int)((((int64_t)p.vocab - 1) / warps / 128 + 1) * 128);
-    if ((int64_t)p.num_seqs * split > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+template <typename T, int kThreads> cudaError_t launch(const ssd_verify_params &p, int split, cudaStream_t stream) {
+    constexpr int N = Weights<T>::N;
+    const int warps = split * (kThreads / 32);
+    const int per = (int)((((int64_t)p.vocab + N - 2) / warps / 128 + 1) * 128);       // of a row that begins N - 1 behind a boundary
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -306,7 +316,22 @@ template <typename T> cudaError_t launch(const ssd_verify_params &p, cudaStream_
     config.stream = stream;
     config.attrs = attr;
     config.numAttrs = 2;
-    return cudaLaunchKernelEx(&config, verify_kernel<T>, p, split, per);
+    return cudaLaunchKernelEx(&config, verify_kernel<T, kThreads>, p, split, per);
+}
+
+template <typename T> cudaError_t launch(const ssd_verify_params &p, cudaStream_t stream) {
+    // Threads of a window: as many as let all windows run at once (1,024 an SM), a
+    // token to 16 of a row at most, so that the chain of reads in front of the row is
+    // waited for once; in eight CTAs rather than in large ones.
+    if (p.num_seqs > (1 << 28)) return cudaErrorInvalidConfiguration;
+    int64_t threads = 152 * 1024 / p.num_seqs;
+    if (threads > p.vocab / 16) threads = p.vocab / 16;
+    const int size = threads >= 8 * 512 ? 512 : threads >= 8 * 256 ? 256 : 128;
+    int split = 1;
+    while (split < 8 && split * 2 * size <= threads) split *= 2;
+    return size == 512   ? launch<T, 512>(p, split, stream)
+           : size == 256 ? launch<T, 256>(p, split, stream)
+                         : launch<T, 128>(p, split, stream);
 }
 
 }  // namespace
