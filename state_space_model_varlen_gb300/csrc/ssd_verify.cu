@@ -11,8 +11,8 @@
 //
 // A cluster of CTAs takes a window: each looks for the row where the window stops,
 // sums its part of it, and learns the others' sums through distributed shared
-// memory; the warp in whose part the random number falls reads that part again
-// (from L2).  Bound by HBM for many windows, one row of p and one of q where a draft
+// memory.  Lanes leave the sums of their blocks of tokens in shared memory, so that
+// the warp in whose part the random number falls reads one block again (from L2).  Bound by HBM for many windows, one row of p and one of q where a draft
 // fell; for few by the chain of dependent reads in front of the row.
 #include "ssd_layer_internal.h"
 #include "ssd_mixer_common.cuh"
@@ -20,7 +20,10 @@
 namespace ssd {
 namespace {
 
-constexpr int kLaneRun = 32;
+constexpr int kSnaps = 8;        // blocks of a warp's part whose sums are left
+// 16-byte vectors of a lane in a block, of n values each: 16 tokens, and 32 in a large
+// CTA, whose part of a row of 2^17 is then one block, all of it asked for at once
+constexpr int vectors(int threads, int n) { return (threads == 512 ? 32 : 16) / n; }
 
 // s + c, s the rounded sum
 struct Sum {
@@ -45,10 +48,10 @@ __device__ __forceinline__ Sum shuffled(const Sum &a, int lane) {
     r.c = __shfl_sync(0xffffffffu, a.c, lane);
     return r;
 }
-// of lanes 0 .. lane
-__device__ __forceinline__ Sum scan(Sum a) {
+// of lanes 0 .. lane, over the first kLanes
+template <int kLanes = 32> __device__ __forceinline__ Sum scan(Sum a) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
+    for (int o = 1; o < kLanes; o <<= 1) {
         const float s = __shfl_up_sync(0xffffffffu, a.s, o), c = __shfl_up_sync(0xffffffffu, a.c, o);
         if ((threadIdx.x & 31) >= o) a.add(s, c);
     }
@@ -61,16 +64,14 @@ __device__ __forceinline__ Sum before_lane(const Sum &a) {
     r.c = __shfl_up_sync(0xffffffffu, a.c, 1);
     return threadIdx.x & 31 ? r : Sum();
 }
-// The first of n lanes at which `sums`, scanned, pass goal, and what they are before
-// it; or (with goal out of the way, so that the last of any weight is found below)
-// the last one with a sum, or -1.
-__device__ __forceinline__ int owner_of(const Sum &mine, int n, Sum &goal, Sum &before) {
+// The first of n lanes at which the sums `mine`, which are `upto` added up, pass goal
+// from `before` on, and what they are before it; or (with goal out of the way, so that
+// the last of any weight is found below) the last one with a sum, or -1.
+__device__ __forceinline__ int owner_of(const Sum &mine, Sum upto, int n, Sum &goal, Sum &before) {
     const int lane = threadIdx.x & 31;
-    Sum upto = scan(lane < n ? mine : Sum());
-    const Sum base = before;
-    upto.add(base);
     Sum ahead = before_lane(upto);
-    if (lane == 0) ahead = base;
+    upto.add(before);
+    ahead.add(before);
     const uint32_t some = __ballot_sync(0xffffffffu, lane < n && mine.s > 0.f);
     const uint32_t over = some & __ballot_sync(0xffffffffu, upto.above(goal));
     if (!over) goal.s = __int_as_float(0x7f7fffff);
@@ -90,30 +91,46 @@ template <typename T> struct Weights {
         // 0 < d finite: a > b; b < 0 or not finite does not come with probabilities
         return d > 0.f && d < __int_as_float(0x7f800000) && !out ? make_float2(d, (a - d) - b) : make_float2(0.f, 0.f);
     }
-    __device__ float2 operator()(int t) const { return of(to_float(p[t]), q ? to_float(q[t]) : 0.f, t == without); }
     // elements that p's row begins behind a 16-byte boundary, and whether q's begins like it
     __device__ int ahead() const { return (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T)); }
     __device__ bool alike() const { return ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15) == 0; }
-    __device__ void add_one(Sum &sum, int t) const {
-        const float2 v = (*this)(t);
-        sum.add(v.x, v.y);
-    }
-    // adds tokens t .. t + N - 1, where p + t is a 16-byte boundary
-    __device__ void add(Sum &sum, int t, bool alike) const {
-        const Pack<T, N> a = load_pack<T, N>(p + t);
-        Pack<T, N> b{};
-        if (q) {
-            if (alike) {
-                b = load_pack<T, N>(q + t);
-            } else {
+    // w of tokens t .. t + N - 1, of which those in [lo, hi) count; p + t is a 16-byte boundary
+    struct Vector {
+        Pack<T, N> a, b;
+        bool live;
+    };
+    __device__ Vector load(int t, int lo, int hi, bool alike) const {
+        Vector v{};
+        v.live = t < hi && t + N > lo;
+        if (t >= lo && t + N <= hi) {
+            v.a = load_pack<T, N>(p + t);
+            if (q) {
+                if (alike) {
+                    v.b = load_pack<T, N>(q + t);
+                } else {
 #pragma unroll
-                for (int i = 0; i < N; ++i) b.v[i] = q[t + i];
+                    for (int i = 0; i < N; ++i) v.b.v[i] = q[t + i];
+                }
             }
+        } else if (v.live) {        // the row's ends
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (t + i >= lo && t + i < hi) {
+                    v.a.v[i] = p[t + i];
+                    if (q) v.b.v[i] = q[t + i];
+                }
         }
+        return v;
+    }
+    __device__ float2 of(const Vector &v, int t, int i) const {
+        return of(to_float(v.a.v[i]), to_float(v.b.v[i]), t + i == without);
+    }
+    __device__ void add(Sum &sum, const Vector &v, int t) const {
+        if (!v.live) return;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const float2 v = of(to_float(a.v[i]), to_float(b.v[i]), t + i == without);
-            sum.add(v.x, v.y);
+            const float2 f = of(v, t, i);
+            sum.add(f.x, f.y);
         }
     }
 };
@@ -189,53 +206,46 @@ template <typename T> __device__ void find_stop(const ssd_verify_params &a, int 
     }
 }
 
-// The token of [lo, hi) where the sum, `before` ahead of lo, passes goal, or else the
-// last of any weight (-1 without one).  A lane takes kLaneRun tokens in a row, which
-// begin at a 16-byte boundary of p but for the row's first.
-template <typename T> __device__ int search(const Weights<T> &w, int lo, int hi, Sum before, const Sum &goal) {
-    constexpr int N = Weights<T>::N;
-    const int lane = threadIdx.x & 31, shift = w.ahead();
-    const bool alike = w.alike();
-    int positive = -1;
-    for (int base = (lo + shift) / N * N - shift; base < hi; base += 32 * kLaneRun) {
-        const int run = base + lane * kLaneRun;
+// The token of a run of blocks of [lo, hi), the first at `base`, where the sum, `before`
+// ahead of them, passes goal, or else the last of any weight.  One warp, whose lanes
+// take unbroken runs of tokens.
+template <typename T, int kVectors>
+__device__ int search(const Weights<T> &w, int base, int blocks, int lo, int hi, Sum before, const Sum &goal, bool alike) {
+    constexpr int N = Weights<T>::N, kRun = N * kVectors;
+    const int lane = threadIdx.x & 31;
+    int last = -1;
+    for (int j = 0; j < blocks && base < hi; ++j, base += 32 * kRun) {
+        typename Weights<T>::Vector v[kVectors];
         Sum mine;
-#pragma unroll 4
-        for (int t = run; t < run + kLaneRun; t += N) {
-            if (t >= lo && t + N <= hi) {
-                w.add(mine, t, alike);
-            } else {
-                for (int i = max(t, lo); i < min(t + N, hi); ++i) w.add_one(mine, i);
-            }
-        }
+#pragma unroll
+        for (int i = 0; i < kVectors; ++i) v[i] = w.load(base + lane * kRun + i * N, lo, hi, alike);
+#pragma unroll
+        for (int i = 0; i < kVectors; ++i) w.add(mine, v[i], base + lane * kRun + i * N);
         const Sum upto = scan(mine);
-        Sum all = upto;
-        all.add(before);
-        const uint32_t some = __ballot_sync(0xffffffffu, mine.s > 0.f), over = some & __ballot_sync(0xffffffffu, all.above(goal));
-        const int at = over ? __ffs(over) - 1 : some ? 31 - __clz(some) : -1;
-        if (at >= 0) {          // that lane's tokens, one a lane
-            const Sum ahead = shuffled(before_lane(upto), at);
-            const int t = base + at * kLaneRun + lane;
+        Sum limit = goal, ahead = before;
+        const int at = owner_of(mine, upto, 32, limit, ahead);
+        if (at >= 0) {                  // that run's tokens, one a lane
+            const int t = base + at * kRun + lane;
             Sum one;
-            if (t >= lo && t < hi) w.add_one(one, t);
-            Sum sum = scan(one);
-            sum.add(ahead);
-            sum.add(before);
-            const uint32_t any = __ballot_sync(0xffffffffu, one.s > 0.f);
-            const uint32_t passed = any & __ballot_sync(0xffffffffu, sum.above(goal));
-            positive = base + at * kLaneRun + (over && passed ? __ffs(passed) - 1 : 31 - __clz(any));
-            if (over) return positive;
+            if (lane < kRun && t >= lo && t < hi) {
+                const float2 f = Weights<T>::of(to_float(w.p[t]), w.q ? to_float(w.q[t]) : 0.f, t == w.without);
+                one.add(f.x, f.y);
+            }
+            const bool here = limit.s == goal.s;        // the goal is in this run, not behind all
+            last = base + at * kRun + owner_of(one, scan<kRun>(one), kRun, limit, ahead);
+            if (here) return last;
         }
         before.add(shuffled(upto, 31));
     }
-    return positive;
+    return last;
 }
 
 template <typename T, int kThreads>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const ssd_verify_params a, int split, int per) {
-    constexpr int kWarps = kThreads / 32, N = Weights<T>::N;
+__global__ void __launch_bounds__(kThreads, kThreads == 512 ? 1 : 1024 / kThreads) verify_kernel(const ssd_verify_params a, int split, int per) {
+    constexpr int kWarps = kThreads / 32, N = Weights<T>::N, kVectors = vectors(kThreads, N), kBlock = 32 * N * kVectors;
     __shared__ Window<T> win;
     __shared__ float2 part[2][kWarps], totals[2];       // of the first attempt and of the second
+    __shared__ float2 snaps[kSnaps][kThreads];
     await_previous();
     const int s = blockIdx.x / split, rank = blockIdx.x % split, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, V = a.vocab;
     if (warp == 0) find_stop(a, s, rank == 0, win);
@@ -247,40 +257,64 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const
     // a warp sums an unbroken part of the row, from a 16-byte boundary of p on
     const int64_t begin = ((int64_t)rank * kWarps + warp) * per - w.ahead();
     const int lo = (int)min((int64_t)V, max((int64_t)0, begin)), hi = (int)max((int64_t)0, min((int64_t)V, begin + per));
-    const int lo_whole = min(hi, lo > 0 ? lo : (N - w.ahead()) % N), hi_whole = lo_whole + (hi - lo_whole) / N * N;
+    const int base = lo > 0 ? lo : -w.ahead();
+    const int runs = (per / kBlock - 1) / kSnaps + 1;           // blocks of a sum that is left
     for (int attempt = 0;; ++attempt) {
         const bool alike = w.alike();
         Sum sum;
-        if (lo + lane < lo_whole) w.add_one(sum, lo + lane);
-#pragma unroll 4
-        for (int t = lo_whole + lane * N; t < hi_whole; t += 32 * N) w.add(sum, t, alike);
-        if (hi_whole + lane < hi) w.add_one(sum, hi_whole + lane);
+        for (int i = 0; i < kSnaps; ++i) {
+            Sum here;
+            for (int j = 0; j < runs; ++j) {
+                const int at = base + (i * runs + j) * kBlock + lane * N;
+                if (at - lane * N >= hi) break;
+                typename Weights<T>::Vector v[kVectors];
+#pragma unroll
+                for (int e = 0; e < kVectors; ++e) v[e] = w.load(at + e * 32 * N, lo, hi, alike);
+#pragma unroll
+                for (int e = 0; e < kVectors; ++e) w.add(here, v[e], at + e * 32 * N);
+            }
+            snaps[i][threadIdx.x] = make_float2(here.s, here.c);
+            sum.add(here);
+        }
         const Sum mine = scan(sum);
         if (lane == 31) part[attempt][warp] = make_float2(mine.s, mine.c);
         __syncthreads();
         // every warp for itself, all the same: the CTA's sum, the others', and where the goal lies
-        Sum warps;
+        Sum warps, ctas;
         if (lane < kWarps) {
             warps.s = part[attempt][lane].x;
             warps.c = part[attempt][lane].y;
         }
-        Sum cta = shuffled(scan(warps), kWarps - 1);
+        const Sum warps_upto = scan<kWarps>(warps);
+        ctas = shuffled(warps_upto, kWarps - 1);
         if (split > 1) {
-            if (threadIdx.x == 0) totals[attempt] = make_float2(cta.s, cta.c);
+            if (threadIdx.x == 0) totals[attempt] = make_float2(ctas.s, ctas.c);
             cluster_arrive();
             cluster_wait();
-            cta = lane < split ? load_of(&totals[attempt], lane) : Sum();
+            ctas = lane < split ? load_of(&totals[attempt], lane) : Sum();
         }
-        const Sum total = shuffled(scan(lane < split ? cta : Sum()), split - 1);
+        const Sum ctas_upto = scan<8>(ctas), total = shuffled(ctas_upto, split - 1);
         const bool last_try = attempt == 1 || (w.q == nullptr && w.without < 0);
         if (total.s > 0.f || last_try) {
             Sum goal = times(total, u), before;
             if (u == 1.f) goal.s = __int_as_float(0x7f7fffff);          // the last of any weight
-            const int owner = max(0, owner_of(cta, split, goal, before));
+            const int owner = max(0, owner_of(ctas, ctas_upto, split, goal, before));
             if (rank == owner) {
-                const int by = max(0, owner_of(warps, kWarps, goal, before));
+                const int by = max(0, owner_of(warps, warps_upto, kWarps, goal, before));
                 if (warp == by) {
-                    const int at = search(w, lo, hi, before, goal);
+                    // the sums of the warp's blocks: four lanes add one's 32, then the block of the goal
+                    __syncwarp();
+                    Sum run;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 v = snaps[lane >> 2][warp * 32 + (lane & 3) * 8 + i];
+                        run.add(v.x, v.y);
+                    }
+#pragma unroll
+                    for (int o = 1; o < 4; o <<= 1) run.add(__shfl_xor_sync(0xffffffffu, run.s, o), __shfl_xor_sync(0xffffffffu, run.c, o));
+                    if (lane & 3) run = Sum();
+                    const int from = max(0, owner_of(run, scan(run), 32, goal, before)) >> 2;
+                    const int at = search<T, kVectors>(w, base + from * runs * kBlock, runs, lo, hi, before, goal, alike);
                     for (int i = lane; i <= k; i += 32) a.out_tokens[first + i] = i < n ? a.tokens[first + i + 1] : i == n ? at : -1;
                     if (lane == 0) {
                         if (at < 0) flag(a.device_status, SSD_DEV_BAD_PROBS);
@@ -301,9 +335,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const
 }
 
 template <typename T, int kThreads> cudaError_t launch(const ssd_verify_params &p, int split, cudaStream_t stream) {
-    constexpr int N = Weights<T>::N;
+    constexpr int N = Weights<T>::N, kBlock = 32 * N * vectors(kThreads, N);
     const int warps = split * (kThreads / 32);
-    const int per = (int)((((int64_t)p.vocab + N - 2) / warps / 128 + 1) * 128);       // of a row that begins N - 1 behind a boundary
+    // tokens that a row may begin behind a 16-byte boundary
+    const int slack = aligned_to(p.target_probs, 16) && p.target_stride % N == 0 ? 0 : N - 1;
+    const int per = (int)((((int64_t)p.vocab + slack - 1) / warps / kBlock + 1) * kBlock);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
