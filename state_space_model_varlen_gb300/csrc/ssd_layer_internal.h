@@ -13,8 +13,6 @@ namespace ssd {
 cudaError_t launch_residual_norm_f32(const ssd_residual_norm_params &p, cudaStream_t stream);
 cudaError_t launch_residual_norm_bf16(const ssd_residual_norm_params &p, cudaStream_t stream);
 cudaError_t launch_matvec4(const ssd_matvec4_params &p, cudaStream_t stream);
-// The tensor-core kernel of launch_matvec4, where it takes the call; false where it does not.
-bool launch_matvec4_mma(const ssd_matvec4_params &p, cudaStream_t stream, cudaError_t *error);
 cudaError_t launch_verify(const ssd_verify_params &p, cudaStream_t stream);
 
 // enqueue() with dynamic shared memory (at most 48 KB)

@@ -3,8 +3,7 @@
 //   out[r, o] = bias[o] + sum_k scale[o, g(k)] (code[o, k] - zero[o, g(k)]) x[r, k]
 //
 // The codes are read once for a tile of rows: bound by HBM for few rows.
-#include "ssd_layer_internal.h"
-#include "ssd_mixer_common.cuh"
+#include "ssd_matvec4_mma.cuh"
 
 namespace ssd {
 namespace {
@@ -115,11 +114,97 @@ cudaError_t launch_any(const ssd_matvec4_params &p, cudaStream_t stream) {
     return enqueue(matvec4_any_kernel, grid, 32 * kAnyWarps, stream, p);
 }
 
+// ---------------------------------------------------------------------------
+// The plan of the tensor-core kernel; false where it does not take the call.
+// ---------------------------------------------------------------------------
+int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
+
+bool make_plan(const ssd_matvec4_params &p, Matvec4Plan &q, int &cols, int &shared, bool &whole) {
+    using namespace matvec4;
+    const int K = p.in_features, parts = p.x_dtype == SSD_F32 ? 3 : 1;
+    if (K > (1 << 20)) return false;
+    q.p = p;
+    if (p.x_dtype <= SSD_BF16) q.p.x_scale = nullptr;
+    q.groups = p.group_size >= K ? 1 : (K - 1) / p.group_size + 1;
+    q.x_groups = !q.p.x_scale || p.x_group >= K ? 1 : (K - 1) / p.x_group + 1;
+    const bool unbroken = q.groups == 1 || p.group_size % 32 == 0;
+    if (!unbroken) {
+        // groups of their own blocks, from a whole byte on, that do not waste most of them
+        if (p.group_size % 2 != 0 || p.group_size < 16) return false;
+        q.padded = p.group_size;
+        q.group_blocks = (p.group_size - 1) / 32 + 1;
+        q.blocks = q.groups * q.group_blocks;
+    } else {
+        q.blocks = (K - 1) / 32 + 1;
+        q.group_blocks = q.groups == 1 ? q.blocks : p.group_size / 32;
+    }
+    if (q.x_groups == 1) q.x_group_blocks = q.blocks;
+    else if (unbroken && p.x_group % 32 == 0) q.x_group_blocks = p.x_group / 32;
+    else if (!unbroken && p.x_group == p.group_size) q.x_group_blocks = q.group_blocks;
+    else return false;
+    q.steps = (q.blocks - 1) / 4 + 1;
+    auto magic = [](int blocks) { return (uint32_t)((1ull << 32) / blocks + 1); };
+    q.group_magic = magic(q.group_blocks);
+    q.x_group_magic = magic(q.x_group_blocks);
+    // blocks that share their scales wherever a step begins
+    shared = gcd(4, gcd(q.groups == 1 ? 4 : q.group_blocks, q.x_groups == 1 ? 4 : q.x_group_blocks));
+    whole = unbroken && K % 32 == 0 && p.weight_stride % 16 == 0 && aligned_to(p.weight, 16);
+    cols = 1;
+    while (cols < 8 && cols * 8 < p.rows * parts) cols *= 2;
+    q.row_tile = cols * 8 / parts < p.rows ? cols * 8 / parts : p.rows;
+    q.x_rows = q.row_tile * parts;
+    q.tiles = (p.out_features - 1) / outs(cols) + 1;
+    if ((p.rows - 1) / q.row_tile + 1 > 65535) return false;
+
+    const int per_step = 4 / shared, scales = chunk(cols) * per_step;
+    int at = kWarps * kStages * 16 * mats(cols) * pitch(shared, whole);
+    auto take = [&](int bytes) {
+        const int off = at;
+        at += (bytes + 127) / 128 * 128;
+        return off;
+    };
+    q.off_x = take(2 * q.x_rows * x_pitch(cols));
+    q.off_scale = take(2 * scales * outs(cols) * 4);
+    q.off_zero = take(p.zero ? 2 * scales * outs(cols) * 4 : 0);
+    q.off_xs = take(q.p.x_scale ? 2 * scales * cols * 8 * 4 : 0);
+    q.smem = at;
+    const int sums = (outs(cols) + 4) * q.x_rows * 4;
+    if (q.smem < sums) q.smem = sums;
+    if (q.smem > kSmemLimit) return false;
+
+    // The split whose waves of CTAs take the least, in clocks: a step takes a warp 600 at
+    // best and an SM's eight warps of a CTA 700 together, more where the products bound
+    // it; a CTA begins and ends in about 4,000, in a cluster 6,000.
+    const int fit = kSmemLimit / (q.smem + 1024), resident = fit < 1 ? 1 : fit < ctas(cols) ? fit : ctas(cols);
+    const int64_t passes = (p.rows - 1) / q.row_tile + 1;
+    const int together = cols <= 2 ? 700 : 1100;
+    double least = 0.0;
+    int best = 1;
+    for (int split = 1; split <= 8; split *= 2) {
+        const int64_t steps = ((q.steps - 1) / chunk(cols) / split + 1) * chunk(cols), all = q.tiles * passes * split;
+        if (split > 1 && steps * split >= 2 * (q.steps + chunk(cols))) break;
+        const int64_t waves = (all - 1) / (152 * resident) + 1, side = all < 152 * resident ? (all - 1) / 152 + 1 : resident;
+        const double cost = (double)waves * ((split > 1 ? 6000 : 4000) + steps * (side * together > 600 ? side * together : 600));
+        if (split == 1 || cost < least) {
+            least = cost;
+            best = split;
+        }
+    }
+    q.split = best;
+    return true;
+}
+
 }  // namespace
 
 cudaError_t launch_matvec4(const ssd_matvec4_params &p, cudaStream_t stream) {
-    cudaError_t error;
-    return launch_matvec4_mma(p, stream, &error) ? error : launch_any(p, stream);
+    Matvec4Plan q = {};
+    int cols, shared;
+    bool whole;
+    if (!make_plan(p, q, cols, shared, whole)) return launch_any(p, stream);
+    return cols == 1   ? launch_matvec4_cols1(q, shared, whole, stream)
+           : cols == 2 ? launch_matvec4_cols2(q, shared, whole, stream)
+           : cols == 4 ? launch_matvec4_cols4(q, shared, whole, stream)
+                       : launch_matvec4_cols8(q, shared, whole, stream);
 }
 
 }  // namespace ssd

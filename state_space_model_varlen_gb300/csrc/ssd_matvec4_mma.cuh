@@ -1,0 +1,512 @@
+// Products of few rows with 4-bit weights on the tensor cores.  One translation unit
+// for each number of columns of a pass.
+//
+// A warp multiplies 32 (16 for many columns) outputs by 128 columns of x at a step
+// (mma.m16n8k16, weights as its 16 rows, rows of x as its columns).  code - zero is
+// an integer below 2^4 and exact in bf16, as are 8-bit activations; fp32 activations
+// become three bf16 parts of eight bits each, which together are exact.  Sums within
+// a group are the instruction's fp32 sums; the groups' scales are applied to them in
+// fp32.
+//
+// Bound by HBM for few rows: codes stream through a ring of asynchronous copies of
+// each warp's own, kStages steps deep.  x and the scales come through two buffers in
+// shared memory, a chunk of steps ahead in registers.  A cluster of CTAs shares a
+// tile's columns where there are few tiles; the parts are added in a fixed order.
+//
+// A group of columns is taken in blocks of 32; a group of another size, or a row's
+// end, leaves the last block's x partly zero.  Rows of codes in whole 16 bytes are
+// copied as they are (kWhole); of others the two 16-byte pieces that hold a block are,
+// and its bytes are picked out of them.
+#pragma once
+#include "ssd_layer_internal.h"
+#include "ssd_mixer_common.cuh"
+
+namespace ssd {
+
+struct Matvec4Plan {
+    ssd_matvec4_params p;
+    int row_tile;               // rows of x of a pass
+    int split;                  // CTAs of a cluster
+    int tiles;                  // of outputs
+    int blocks, steps;          // of a row: 32 columns at most, four blocks
+    int groups, x_groups;       // of a row
+    int group_blocks, x_group_blocks;           // blocks of a group
+    uint32_t group_magic, x_group_magic;        // floor(2^32 / blocks of a group) + 1
+    int padded;                 // columns of a group that are not whole blocks, or 0
+    int x_rows;                 // rows of x (their parts) in shared memory
+    int off_x, off_scale, off_zero, off_xs, smem;
+};
+
+// columns8: eights of columns of a pass (1, 2, 4, 8); shared: blocks that share their scales (1, 2, 4)
+cudaError_t launch_matvec4_cols1(const Matvec4Plan &q, int shared, bool whole, cudaStream_t stream);
+cudaError_t launch_matvec4_cols2(const Matvec4Plan &q, int shared, bool whole, cudaStream_t stream);
+cudaError_t launch_matvec4_cols4(const Matvec4Plan &q, int shared, bool whole, cudaStream_t stream);
+cudaError_t launch_matvec4_cols8(const Matvec4Plan &q, int shared, bool whole, cudaStream_t stream);
+
+namespace matvec4 {
+
+constexpr int kStages = 3, kWarps = 8, kThreads = 32 * kWarps, kStep = 128, kSmemLimit = 227 * 1024;
+constexpr int mats(int cols) { return cols <= 4 ? 2 : 1; }          // sixteens of outputs of a warp
+constexpr int chunk(int cols) { return cols <= 2 ? 2 : 1; }         // steps of a buffer of x and scales
+constexpr int ctas(int cols) { return cols <= 2 ? 2 : 1; }          // of an SM, for the registers
+constexpr int outs(int cols) { return kWarps * 16 * mats(cols); }   // of a tile
+// bytes of a row of a stage: whole steps, with a gap where lanes read one another's; or two pieces a block
+constexpr int pitch(int shared, bool whole) { return whole ? (shared == 4 ? 64 : 80) : 144; }
+constexpr int x_pitch(int cols) { return chunk(cols) * kStep * 2 + 64; }    // two rows beside one another in the banks
+
+__host__ __device__ __forceinline__ int group_of(int block, int blocks, uint32_t magic) {
+    return blocks == 1 ? block : (int)(((uint64_t)(uint32_t)block * magic) >> 32);
+}
+
+#ifdef __CUDACC__
+namespace {
+
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// the same from zero
+__device__ __forceinline__ void mma_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// v in a register, which the compiler does not load or compute again at each use
+__device__ __forceinline__ int kept(int v) {
+    int r;
+    asm volatile("mov.b32 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// Codes i and i + 4 of a word (at bits 4 i and 4 i + 16) less their zero, as bf16:
+// the code as the low bits of 128's mantissa, minus 128 + zero.  Exact.
+__device__ __forceinline__ uint32_t codes2(uint32_t word, int i, uint32_t base, uint32_t zero) {
+    uint32_t v, r;              // and, or as one operation (the compiler makes two)
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(word >> (4 * i)), "n"(0x000f000f), "r"(base));
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(zero));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// Eight consecutive values of a row of x as they are stored; zeros behind the first `live`.
+struct Raw { uint32_t w[8]; };
+__device__ __forceinline__ Raw load8(const ssd_matvec4_params &p, int64_t at, int live, bool wide) {
+    Raw r{};
+    if (p.x_dtype == SSD_F32) {
+        const float *src = static_cast<const float *>(p.x) + at;
+        if (wide && live == 8) {
+            *reinterpret_cast<uint4 *>(r.w) = *reinterpret_cast<const uint4 *>(src);
+            *reinterpret_cast<uint4 *>(r.w + 4) = *reinterpret_cast<const uint4 *>(src + 4);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < live) r.w[i] = __float_as_uint(src[i]);
+        }
+    } else if (p.x_dtype == SSD_BF16) {
+        const uint16_t *src = static_cast<const uint16_t *>(p.x) + at;
+        if (wide && live == 8) {
+            *reinterpret_cast<uint4 *>(r.w) = *reinterpret_cast<const uint4 *>(src);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < live) r.w[i / 2] |= (uint32_t)src[i] << (16 * (i & 1));
+        }
+    } else {
+        const uint8_t *src = static_cast<const uint8_t *>(p.x) + at;
+        if (wide && live == 8) {
+            *reinterpret_cast<uint2 *>(r.w) = *reinterpret_cast<const uint2 *>(src);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < live) r.w[i / 4] |= (uint32_t)src[i] << (8 * (i & 3));
+        }
+    }
+    return r;
+}
+__device__ __forceinline__ void to_floats(const Raw &r, int type, float (&v)[8]) {
+    if (type == SSD_F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.w[i]);
+    } else if (type == SSD_BF16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(r.w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
+        }
+    } else if (type == SSD_E4M3) {
+        decode4<SSD_E4M3>(r.w[0], v);
+        decode4<SSD_E4M3>(r.w[1], v + 4);
+    } else {
+        decode4<SSD_I8>(r.w[0], v);
+        decode4<SSD_I8>(r.w[1], v + 4);
+    }
+}
+
+// kCols: eights of columns (rows of x, or their parts) of a pass.  kShared: blocks that
+// certainly share their scales (1, 2, or 4: a step).
+template <int kCols, int kShared, bool kZero, bool kWhole>
+__global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(const __grid_constant__ Matvec4Plan plan) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    constexpr int kMats = mats(kCols), kRows = 16 * kMats, kOuts = outs(kCols), kChunk = chunk(kCols);
+    constexpr int kPitch = pitch(kShared, kWhole), kStageBytes = kRows * kPitch, kXPitch = x_pitch(kCols);
+    constexpr int kFlushes = 4 / kShared, kScales = kChunk * kFlushes;  // of a step, of a chunk
+    constexpr int kItems = kCols * kChunk / 2;                          // eights of x that a thread brings of a chunk
+    constexpr bool kOwn = kWhole && kShared == 4;                       // a lane reads the codes that it copied itself
+    const ssd_matvec4_params &p = plan.p;
+    const int thread = kept(threadIdx.x), lane = thread & 31, g = lane >> 2, t = lane & 3;
+    const int warp = __shfl_sync(0xffffffffu, thread >> 5, 0);          // known to be the same in all lanes
+    const uint32_t base = (uint32_t)kept(0x43004300);                   // 128 in bf16, twice
+    const uint32_t eight = (uint32_t)kept(0x43084308);                  // 128 + 8
+    const int rank = blockIdx.x % plan.split, tile = blockIdx.x / plan.split;
+    const int r0 = blockIdx.y * plan.row_tile, rows = min(plan.row_tile, p.rows - r0);
+    const int parts = p.x_dtype == SSD_F32 ? 3 : 1, cols = rows * parts;
+    const int chunks = (plan.steps - 1) / kChunk + 1;
+    const int chunk0 = (int)((int64_t)chunks * rank / plan.split), chunk1 = (int)((int64_t)chunks * (rank + 1) / plan.split);
+    const int step0 = chunk0 * kChunk, step1 = min(plan.steps, chunk1 * kChunk);
+    const int64_t o_tile = (int64_t)tile * kOuts, o_warp = o_tile + warp * kRows;
+    const bool busy = o_warp < p.out_features;                          // the warp has outputs
+    const bool x8 = p.x_scale != nullptr;
+    uint8_t *const ring = smem + warp * (kStages * kStageBytes);
+    await_previous();
+
+    // first column of a block, and the end of the columns that are its
+    auto columns = [&](int block, int &end) {
+        if (plan.padded == 0) {
+            end = p.in_features;
+            return block * 32;
+        }
+        const int group = group_of(block, plan.group_blocks, plan.group_magic);
+        end = min(p.in_features, (group + 1) * plan.padded);
+        return group * plan.padded + (block - group * plan.group_blocks) * 32;
+    };
+
+    // ---- codes ----
+    const uint8_t *src[2 * kMats];                      // rows g + 8 h: of the lane's 16 bytes (kWhole), or their beginning
+#pragma unroll
+    for (int h = 0; h < 2 * kMats; ++h)
+        src[h] = p.weight + min(o_warp + g + 8 * h, (int64_t)p.out_features - 1) * p.weight_stride;
+    int to_step = step0, to_stage = 0;
+    const int row_bytes = kept(p.in_features / 2), whole_steps = kept(p.in_features / kStep);
+    auto issue = [&]() {
+        if (busy && to_step < step1) {
+            uint8_t *const dst = ring + to_stage * kStageBytes;
+            if constexpr (kWhole) {
+                const int byte = to_step * (kStep / 2) + t * 16;
+                const bool live = to_step < whole_steps || byte < row_bytes;
+#pragma unroll
+                for (int h = 0; h < 2 * kMats; ++h)
+                    copy_async<16>(dst + (g + 8 * h) * kPitch + t * 16, src[h] + (live ? byte : 0), live);
+            } else {
+                // 16 rows x 4 blocks x 2 pieces at a time; pieces that pass the matrix's ends byte by byte
+                const uint8_t *const end = p.weight + (int64_t)(p.out_features - 1) * p.weight_stride + (p.in_features + 1) / 2;
+#pragma unroll 1
+                for (int i = lane; i < kRows * 8; i += 32) {
+                    const int row = i >> 3, block = to_step * 4 + (i >> 1 & 3);
+                    uint8_t *const to = dst + row * kPitch + (i & 7) * 16;
+                    if (block >= plan.blocks) {
+                        *reinterpret_cast<uint4 *>(to) = make_uint4(0, 0, 0, 0);
+                        continue;
+                    }
+                    int stop;
+                    const uint8_t *from = p.weight + min(o_warp + row, (int64_t)p.out_features - 1) * p.weight_stride + columns(block, stop) / 2;
+                    from += (i & 1) * 16 - (int)(reinterpret_cast<uintptr_t>(from) & 15);
+                    if (from >= p.weight && from + 16 <= end) {
+                        copy_async<16>(to, from, true);
+                    } else {
+                        for (int b = 0; b < 16; ++b) to[b] = from + b >= p.weight && from + b < end ? from[b] : 0;
+                    }
+                }
+            }
+        }
+        ++to_step;
+        to_stage = to_stage + 1 == kStages ? 0 : to_stage + 1;
+        commit_async();
+    };
+#pragma unroll 1
+    for (int q = 0; q < kStages - 1; ++q) issue();
+
+    // ---- x and scales: a chunk's into registers, and from there into a buffer ----
+    const int x_size = p.x_dtype == SSD_F32 || p.x_dtype == SSD_BF16 ? 16 : 8;
+    const int x_elem = p.x_dtype == SSD_F32 ? 4 : p.x_dtype == SSD_BF16 ? 2 : 1;
+    const bool x_wide = reinterpret_cast<uintptr_t>(p.x) % x_size == 0 && p.x_stride * x_elem % x_size == 0 &&
+                        plan.padded * x_elem % x_size == 0;
+    const int64_t o_mine = min(o_tile + thread, (int64_t)p.out_features - 1);  // whose scales the thread brings
+    Raw x_raw[kItems];
+    uint32_t scale_raw[kScales], zero_raw[kScales];
+    float xs_raw = 0.f;
+    auto bring = [&](int c) {
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int item = thread + i * kThreads, r = item / (kChunk * 16), e = item % (kChunk * 16);
+            const int block = c * kChunk * 4 + e / 4;
+            int live = 0, k = 0;
+            if (r < rows && block < plan.blocks) {
+                int end;
+                k = columns(block, end) + (e & 3) * 8;
+                live = max(0, min(8, end - k));
+            }
+            x_raw[i] = Raw{};
+            if (live > 0) x_raw[i] = load8(p, (int64_t)(r0 + r) * p.x_stride + k, live, x_wide);
+        }
+        if (thread < kOuts) {
+#pragma unroll
+            for (int f = 0; f < kScales; ++f) {
+                const int block = min(c * kChunk * 4 + f * kShared, plan.blocks - 1);
+                const int64_t at = o_mine * plan.groups + group_of(block, plan.group_blocks, plan.group_magic);
+                scale_raw[f] = p.scale_dtype == SSD_F32 ? static_cast<const uint32_t *>(p.scale)[at]
+                                                        : static_cast<const uint16_t *>(p.scale)[at];
+                if (kZero) zero_raw[f] = p.zero[at];
+            }
+        }
+        if (x8 && thread < kScales * kCols * 8) {
+            const int col = thread % (kCols * 8), block = min(c * kChunk * 4 + thread / (kCols * 8) * kShared, plan.blocks - 1);
+            const int group = group_of(block, plan.x_group_blocks, plan.x_group_magic);
+            xs_raw = col < rows ? p.x_scale[(int64_t)(r0 + col) * plan.x_groups + group] : 0.f;
+        }
+    };
+    auto put_away = [&](int buffer) {
+        uint8_t *const xs = smem + plan.off_x + buffer * (plan.x_rows * kXPitch);
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int item = thread + i * kThreads, r = item / (kChunk * 16), e = item % (kChunk * 16);
+            if (r >= rows) continue;
+            float v[8];
+            to_floats(x_raw[i], p.x_dtype, v);
+            // eights of a step in the order in which quad lane t reads its j-th word: 4 j + t
+            const int at = kOwn ? (e & ~15) | (e & 3) << 2 | (e >> 2 & 3) : e;
+#pragma unroll
+            for (int part = 0; part < 3; ++part) {
+                if (part >= parts) break;
+                uint32_t u[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    u[j] = __float_as_uint(v[j]);
+                    if (v[j] != v[j]) u[j] = 0x7fc00000u;
+                    const float cut = __uint_as_float(u[j] & 0xffff0000u);
+                    v[j] = fabsf(cut) < __int_as_float(0x7f800000) ? v[j] - cut : 0.f;
+                }
+                // values i and i + 4 side by side, as the codes of a word come
+                const uint4 w = make_uint4(__byte_perm(u[0], u[4], 0x7632), __byte_perm(u[1], u[5], 0x7632),
+                                           __byte_perm(u[2], u[6], 0x7632), __byte_perm(u[3], u[7], 0x7632));
+                *reinterpret_cast<uint4 *>(xs + (part * rows + r) * kXPitch + at * 16) = w;
+            }
+        }
+        if (thread < kOuts) {
+            float *const scales = reinterpret_cast<float *>(smem + plan.off_scale) + buffer * (kScales * kOuts) + thread;
+            uint32_t *const zeros = reinterpret_cast<uint32_t *>(smem + plan.off_zero) + buffer * (kScales * kOuts) + thread;
+#pragma unroll
+            for (int f = 0; f < kScales; ++f) {
+                scales[f * kOuts] = p.scale_dtype == SSD_F32    ? __uint_as_float(scale_raw[f])
+                                    : p.scale_dtype == SSD_BF16 ? __uint_as_float(scale_raw[f] << 16)
+                                                                : __half2float(__ushort_as_half((unsigned short)scale_raw[f]));
+                if (kZero) zeros[f * kOuts] = 0x43004300u + zero_raw[f] * 0x00010001u;
+            }
+        }
+        if (x8 && thread < kScales * kCols * 8)
+            reinterpret_cast<float *>(smem + plan.off_xs)[buffer * (kScales * kCols * 8) + thread] = xs_raw;
+    };
+
+    bring(chunk0);
+    put_away(0);
+    __syncthreads();
+
+    // A column that is not there is computed from the last one and not looked at.
+    int x_at[kCols];
+#pragma unroll
+    for (int n = 0; n < kCols; ++n) x_at[n] = plan.off_x + min(n * 8 + g, cols - 1) * kXPitch + t * 16;
+    float sum[kMats][kCols][4];
+#pragma unroll
+    for (int m = 0; m < kMats; ++m)
+#pragma unroll
+        for (int n = 0; n < kCols; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[m][n][i] = 0.f;
+    int stage = 0, buffer = 0;
+#pragma unroll 1
+    for (int c = chunk0; c < chunk1; ++c) {
+        if (c + 1 < chunk1) bring(c + 1);
+        const uint8_t *const x_now = smem + buffer * (plan.x_rows * kXPitch);
+        const float *const scales = reinterpret_cast<const float *>(smem + plan.off_scale) + buffer * (kScales * kOuts) + warp * kRows + g;
+        const uint32_t *const zeros = reinterpret_cast<const uint32_t *>(smem + plan.off_zero) + buffer * (kScales * kOuts) + warp * kRows + g;
+        const float *const x_scales = reinterpret_cast<const float *>(smem + plan.off_xs) + buffer * (kScales * kCols * 8) + 2 * t;
+#pragma unroll
+        for (int s = 0; s < kChunk; ++s) {
+            const int step = c * kChunk + s;
+            if (!busy || step >= step1) break;
+            wait_async<kStages - 2>();
+            if constexpr (!kOwn) __syncwarp();          // a lane reads what its neighbours copied
+            issue();
+            const uint8_t *const codes = ring + stage * kStageBytes + g * kPitch + (kOwn ? t * 16 : t * 4);
+            stage = stage + 1 == kStages ? 0 : stage + 1;
+            uint32_t words[2 * kMats][4];
+            if constexpr (kOwn) {
+#pragma unroll
+                for (int h = 0; h < 2 * kMats; ++h)
+                    *reinterpret_cast<uint4 *>(words[h]) = *reinterpret_cast<const uint4 *>(codes + 8 * h * kPitch);
+            }
+#pragma unroll
+            for (int f = 0; f < kFlushes; ++f) {
+                if (kFlushes > 1 && step * 4 + f * kShared >= plan.blocks) break;
+                uint32_t zero[2 * kMats];               // 128 + zero, twice
+#pragma unroll
+                for (int h = 0; h < 2 * kMats; ++h) zero[h] = kZero ? zeros[(s * kFlushes + f) * kOuts + 8 * h] : eight;
+                float acc[kMats][kCols][4];
+#pragma unroll
+                for (int b = 0; b < kShared; ++b) {
+                    const int w = f * kShared + b;
+                    uint32_t a0[kMats][4], a1[kMats][4];
+                    int shift = 0;
+                    if constexpr (!kWhole) {
+                        int stop;
+                        shift = columns(min(step * 4 + w, plan.blocks - 1), stop) / 2;
+                    }
+#pragma unroll
+                    for (int m = 0; m < kMats; ++m) {
+                        uint32_t pair[2];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if constexpr (kOwn) {
+                                pair[h] = words[2 * m + h][w];
+                            } else if constexpr (kWhole) {
+                                pair[h] = *reinterpret_cast<const uint32_t *>(codes + (16 * m + 8 * h) * kPitch + w * 16);
+                            } else {
+                                const int off = (int)((reinterpret_cast<uintptr_t>(src[2 * m + h]) + shift) & 15);
+                                const uint8_t *at = codes + (16 * m + 8 * h) * kPitch + w * 32 + (off & ~3);
+                                pair[h] = __funnelshift_r(*reinterpret_cast<const uint32_t *>(at), *reinterpret_cast<const uint32_t *>(at + 4),
+                                                          8 * (off & 3));
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            a0[m][2 * i] = codes2(pair[0], i, base, zero[2 * m]);
+                            a0[m][2 * i + 1] = codes2(pair[1], i, base, zero[2 * m + 1]);
+                            a1[m][2 * i] = codes2(pair[0], i + 2, base, zero[2 * m]);
+                            a1[m][2 * i + 1] = codes2(pair[1], i + 2, base, zero[2 * m + 1]);
+                        }
+                    }
+#pragma unroll
+                    for (int n = 0; n < kCols; ++n) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(x_now + x_at[n] + s * (kStep * 2) + w * 64);
+#pragma unroll
+                        for (int m = 0; m < kMats; ++m) {
+                            if (b == 0) mma_first(acc[m][n], a0[m], v.x, v.y);
+                            else mma(acc[m][n], a0[m], v.x, v.y);
+                            mma(acc[m][n], a1[m], v.z, v.w);
+                        }
+                    }
+                }
+                float scale[2 * kMats];
+#pragma unroll
+                for (int h = 0; h < 2 * kMats; ++h) scale[h] = scales[(s * kFlushes + f) * kOuts + 8 * h];
+#pragma unroll
+                for (int n = 0; n < kCols; ++n) {
+                    if (x8) {
+                        const float2 u = *reinterpret_cast<const float2 *>(x_scales + (s * kFlushes + f) * (kCols * 8) + n * 8);
+#pragma unroll
+                        for (int m = 0; m < kMats; ++m) {
+                            acc[m][n][0] *= u.x;
+                            acc[m][n][1] *= u.y;
+                            acc[m][n][2] *= u.x;
+                            acc[m][n][3] *= u.y;
+                        }
+                    }
+#pragma unroll
+                    for (int m = 0; m < kMats; ++m)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) sum[m][n][i] = fmaf(acc[m][n][i], scale[2 * m + i / 2], sum[m][n][i]);
+                }
+            }
+        }
+        buffer ^= 1;
+        if (c + 1 < chunk1) put_away(buffer);
+        __syncthreads();
+    }
+
+    // The sums, through shared memory (everything there has been read): [column][output].
+    constexpr int kLine = kOuts + 4;
+    float *const own = reinterpret_cast<float *>(smem);
+#pragma unroll
+    for (int m = 0; m < kMats; ++m)
+#pragma unroll
+        for (int n = 0; n < kCols; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int col = n * 8 + 2 * t + (i & 1);
+                if (col < cols) own[col * kLine + warp * kRows + 16 * m + g + 8 * (i >> 1)] = sum[m][n][i];
+            }
+    if (plan.split > 1) cluster_barrier();
+    else __syncthreads();
+    const uint32_t local = (uint32_t)__cvta_generic_to_shared(own);
+    for (int i = rank * kThreads + thread; i < rows * kOuts; i += plan.split * kThreads) {
+        const int r = i / kOuts, o = i % kOuts;
+        if (o_tile + o >= p.out_features) continue;
+        float v = 0.f;
+        for (int c = 0; c < plan.split; ++c) {
+            uint32_t at = local + (r * kLine + o) * 4;
+            if (plan.split > 1) asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(at), "r"(c));
+            for (int part = 0; part < parts; ++part) {
+                float f;
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(at + part * rows * (kLine * 4)) : "memory");
+                v += f;
+            }
+        }
+        const int64_t at = (int64_t)(r0 + r) * p.out_stride + o_tile + o;
+        if (p.out_dtype == SSD_F32) {
+            if (p.bias) v += static_cast<const float *>(p.bias)[o_tile + o];
+            static_cast<float *>(p.out)[at] = v;
+        } else {
+            if (p.bias) v += to_float(static_cast<const __nv_bfloat16 *>(p.bias)[o_tile + o]);
+            static_cast<__nv_bfloat16 *>(p.out)[at] = from_float<__nv_bfloat16>(v);
+        }
+    }
+    if (plan.split > 1) cluster_barrier();              // no CTA leaves while another reads its sums
+}
+
+template <int kCols, int kShared, bool kZero, bool kWhole> cudaError_t run(const Matvec4Plan &q, cudaStream_t stream) {
+    auto f = matvec4_mma_kernel<kCols, kShared, kZero, kWhole>;
+    // the most that any plan takes, so that one call of a process and device is enough
+    static unsigned long long set = 0;          // bit d: device d (the first 64)
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    if (device >= 64 || !(__atomic_load_n(&set, __ATOMIC_ACQUIRE) >> device & 1)) {
+        e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+        if (e != cudaSuccess) return e;
+        if (device < 64) __atomic_fetch_or(&set, 1ull << device, __ATOMIC_RELEASE);
+    }
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)q.split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t config = {};
+    config.gridDim = dim3((unsigned)(q.tiles * q.split), (unsigned)((q.p.rows - 1) / q.row_tile + 1));
+    config.blockDim = dim3(kThreads);
+    config.dynamicSmemBytes = (size_t)q.smem;
+    config.stream = stream;
+    config.attrs = attr;
+    config.numAttrs = 2;
+    return cudaLaunchKernelEx(&config, f, q);
+}
+
+template <int kCols, int kShared> cudaError_t run(const Matvec4Plan &q, bool whole, cudaStream_t stream) {
+    if (q.p.zero) return whole ? run<kCols, kShared, true, true>(q, stream) : run<kCols, kShared, true, false>(q, stream);
+    return whole ? run<kCols, kShared, false, true>(q, stream) : run<kCols, kShared, false, false>(q, stream);
+}
+
+template <int kCols> cudaError_t run(const Matvec4Plan &q, int shared, bool whole, cudaStream_t stream) {
+    return shared == 4   ? run<kCols, 4>(q, whole, stream)
+           : shared == 2 ? run<kCols, 2>(q, whole, stream)
+                         : run<kCols, 1>(q, whole, stream);
+}
+
+}  // namespace
+#endif
+}  // namespace matvec4
+}  // namespace ssd
