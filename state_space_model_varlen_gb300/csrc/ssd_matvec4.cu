@@ -153,7 +153,6 @@ bool make_plan(const ssd_matvec4_params &p, Matvec4Plan &q, int &cols, int &shar
     while (cols < 8 && cols * 8 < p.rows * parts) cols *= 2;
     q.row_tile = cols * 8 / parts < p.rows ? cols * 8 / parts : p.rows;
     q.x_rows = q.row_tile * parts;
-    q.tiles = (p.out_features - 1) / outs(cols) + 1;
     if ((p.rows - 1) / q.row_tile + 1 > 65535) return false;
 
     const int per_step = 4 / shared, scales = chunk(cols) * per_step;
@@ -168,29 +167,32 @@ bool make_plan(const ssd_matvec4_params &p, Matvec4Plan &q, int &cols, int &shar
     q.off_zero = take(p.zero ? 2 * scales * outs(cols) * 4 : 0);
     q.off_xs = take(q.p.x_scale ? 2 * scales * cols * 8 * 4 : 0);
     q.smem = at;
-    const int sums = (outs(cols) + 4) * q.x_rows * 4;
+    const int sums = (outs(cols) + 8) * q.x_rows * 4;
     if (q.smem < sums) q.smem = sums;
     if (q.smem > kSmemLimit) return false;
 
-    // The split whose waves of CTAs take the least, in clocks: a step takes a warp 600 at
-    // best and an SM's eight warps of a CTA 700 together, more where the products bound
-    // it; a CTA begins and ends in about 4,000, in a cluster 6,000.
+    // The split and the ways whose waves of CTAs take the least, in clocks.  A step is
+    // about so many instructions of a warp; eight warps of an SM take a step in four
+    // times as many clocks, 16 in seven; a CTA begins and ends in 5,000, in a cluster
+    // 7,000 (measured).
     const int fit = kSmemLimit / (q.smem + 1024), resident = fit < 1 ? 1 : fit < ctas(cols) ? fit : ctas(cols);
     const int64_t passes = (p.rows - 1) / q.row_tile + 1;
-    const int together = cols <= 2 ? 700 : 1100;
+    const int work = 250 + 16 * cols + per_step * (20 + 12 * cols);
     double least = 0.0;
-    int best = 1;
-    for (int split = 1; split <= 8; split *= 2) {
-        const int64_t steps = ((q.steps - 1) / chunk(cols) / split + 1) * chunk(cols), all = q.tiles * passes * split;
-        if (split > 1 && steps * split >= 2 * (q.steps + chunk(cols))) break;
-        const int64_t waves = (all - 1) / (152 * resident) + 1, side = all < 152 * resident ? (all - 1) / 152 + 1 : resident;
-        const double cost = (double)waves * ((split > 1 ? 6000 : 4000) + steps * (side * together > 600 ? side * together : 600));
-        if (split == 1 || cost < least) {
-            least = cost;
-            best = split;
+    for (int ways = 1; ways <= chunk(cols); ways *= 2)
+        for (int split = 1; split <= 8; split *= 2) {
+            const int chunks = ((q.steps - 1) / chunk(cols)) / split + 1;
+            if (split > 1 && split > (q.steps - 1) / chunk(cols) + 1) break;
+            const int64_t tiles = (p.out_features - 1) / (outs(cols) / ways) + 1, all = tiles * passes * split;
+            const int64_t waves = (all - 1) / (152 * resident) + 1, side = all <= 152 ? 1 : resident;
+            const double cost = (double)waves * ((split > 1 ? 7000 : 5000) + (double)chunks * chunk(cols) / ways * work * (side == 1 ? 4 : 7));
+            if (q.split == 0 || cost < least) {
+                least = cost;
+                q.split = split;
+                q.ways = ways;
+                q.tiles = (int)tiles;
+            }
         }
-    }
-    q.split = best;
     return true;
 }
 

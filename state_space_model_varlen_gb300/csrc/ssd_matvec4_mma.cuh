@@ -2,16 +2,16 @@
 // for each number of columns of a pass.
 //
 // A warp multiplies 32 (16 for many columns) outputs by 128 columns of x at a step
-// (mma.m16n8k16, weights as its 16 rows, rows of x as its columns).  code - zero is
-// an integer below 2^4 and exact in bf16, as are 8-bit activations; fp32 activations
-// become three bf16 parts of eight bits each, which together are exact.  Sums within
-// a group are the instruction's fp32 sums; the groups' scales are applied to them in
-// fp32.
+// (mma.m16n8k16, weights as its 16 rows, rows of x as its columns).  (code - zero) / 64
+// is exact in bf16, as are 8-bit activations; fp32 activations become three bf16 parts
+// of eight bits each, which together are exact.  Sums within a group are the
+// instruction's fp32 sums; the groups' scales, times 64, are applied to them in fp32.
 //
 // Bound by HBM for few rows: codes stream through a ring of asynchronous copies of
 // each warp's own, kStages steps deep.  x and the scales come through two buffers in
-// shared memory, a chunk of steps ahead in registers.  A cluster of CTAs shares a
-// tile's columns where there are few tiles; the parts are added in a fixed order.
+// shared memory, a chunk of steps ahead in registers.  Where there are few tiles the
+// warps of a pair take every other step of half as many outputs, and a cluster of CTAs
+// shares a tile's columns; the parts are added in a fixed order.
 //
 // A group of columns is taken in blocks of 32; a group of another size, or a row's
 // end, leaves the last block's x partly zero.  Rows of codes in whole 16 bytes are
@@ -27,6 +27,7 @@ struct Matvec4Plan {
     ssd_matvec4_params p;
     int row_tile;               // rows of x of a pass
     int split;                  // CTAs of a cluster
+    int ways;                   // warps that share outputs: 1 or 2
     int tiles;                  // of outputs
     int blocks, steps;          // of a row: 32 columns at most, four blocks
     int groups, x_groups;       // of a row
@@ -45,7 +46,7 @@ cudaError_t launch_matvec4_cols8(const Matvec4Plan &q, int shared, bool whole, c
 
 namespace matvec4 {
 
-constexpr int kStages = 3, kWarps = 8, kThreads = 32 * kWarps, kStep = 128, kSmemLimit = 227 * 1024;
+constexpr int kStages = 4, kWarps = 8, kThreads = 32 * kWarps, kStep = 128, kSmemLimit = 227 * 1024;
 constexpr int mats(int cols) { return cols <= 4 ? 2 : 1; }          // sixteens of outputs of a warp
 constexpr int chunk(int cols) { return cols <= 2 ? 2 : 1; }         // steps of a buffer of x and scales
 constexpr int ctas(int cols) { return cols <= 2 ? 2 : 1; }          // of an SM, for the registers
@@ -80,12 +81,14 @@ __device__ __forceinline__ int kept(int v) {
     return r;
 }
 
-// Codes i and i + 4 of a word (at bits 4 i and 4 i + 16) less their zero, as bf16:
-// the code as the low bits of 128's mantissa, minus 128 + zero.  Exact.
-__device__ __forceinline__ uint32_t codes2(uint32_t word, int i, uint32_t base, uint32_t zero) {
-    uint32_t v, r;              // and, or as one operation (the compiler makes two)
-    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(word >> (4 * i)), "n"(0x000f000f), "r"(base));
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(zero));
+// Codes i and i + 4 of a word (at bits 4 i and 4 i + 16) less their zero, over 64, as
+// bf16: the low eight bits of a bf16 number without exponent bits above them are its
+// value in units of 2^-133, subnormal or not, so that codes at bits 0 and 4 need no
+// shift.  powers[i & 1] is 2^127 or 2^123, twice; zero is -zero / 64, twice.  Exact.
+__device__ __forceinline__ uint32_t codes2(uint32_t word, int i, const uint32_t (&powers)[2], uint32_t zero) {
+    const uint32_t v = (i >= 2 ? word >> 8 : word) & (i & 1 ? 0x00f000f0u : 0x000f000fu);
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(powers[i & 1]), "r"(zero));
     return r;
 }
 
@@ -160,15 +163,18 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
     const ssd_matvec4_params &p = plan.p;
     const int thread = kept(threadIdx.x), lane = thread & 31, g = lane >> 2, t = lane & 3;
     const int warp = __shfl_sync(0xffffffffu, thread >> 5, 0);          // known to be the same in all lanes
-    const uint32_t base = (uint32_t)kept(0x43004300);                   // 128 in bf16, twice
-    const uint32_t eight = (uint32_t)kept(0x43084308);                  // 128 + 8
+    const uint32_t powers[2] = {(uint32_t)kept(0x7f007f00), (uint32_t)kept(0x7d007d00)};
+    const uint32_t eight = (uint32_t)kept((int)0xbe00be00u);            // -8 / 64, twice
+    const int ways = kChunk == 2 ? plan.ways : 1, half = warp & (ways - 1);
+    const int outs_now = kOuts / ways;                                  // of the tile
     const int rank = blockIdx.x % plan.split, tile = blockIdx.x / plan.split;
     const int r0 = blockIdx.y * plan.row_tile, rows = min(plan.row_tile, p.rows - r0);
     const int parts = p.x_dtype == SSD_F32 ? 3 : 1, cols = rows * parts;
     const int chunks = (plan.steps - 1) / kChunk + 1;
     const int chunk0 = (int)((int64_t)chunks * rank / plan.split), chunk1 = (int)((int64_t)chunks * (rank + 1) / plan.split);
     const int step0 = chunk0 * kChunk, step1 = min(plan.steps, chunk1 * kChunk);
-    const int64_t o_tile = (int64_t)tile * kOuts, o_warp = o_tile + warp * kRows;
+    const int o_first = (kChunk == 2 ? warp / ways : warp) * kRows;     // of the warp's in the tile
+    const int64_t o_tile = (int64_t)tile * outs_now, o_warp = o_tile + o_first;
     const bool busy = o_warp < p.out_features;                          // the warp has outputs
     const bool x8 = p.x_scale != nullptr;
     uint8_t *const ring = smem + warp * (kStages * kStageBytes);
@@ -190,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
 #pragma unroll
     for (int h = 0; h < 2 * kMats; ++h)
         src[h] = p.weight + min(o_warp + g + 8 * h, (int64_t)p.out_features - 1) * p.weight_stride;
-    int to_step = step0, to_stage = 0;
+    int to_step = step0 + half, to_stage = 0;
     const int row_bytes = kept(p.in_features / 2), whole_steps = kept(p.in_features / kStep);
     auto issue = [&]() {
         if (busy && to_step < step1) {
@@ -223,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
                 }
             }
         }
-        ++to_step;
+        to_step += ways;
         to_stage = to_stage + 1 == kStages ? 0 : to_stage + 1;
         commit_async();
     };
@@ -253,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
             x_raw[i] = Raw{};
             if (live > 0) x_raw[i] = load8(p, (int64_t)(r0 + r) * p.x_stride + k, live, x_wide);
         }
-        if (thread < kOuts) {
+        if (thread < outs_now) {
 #pragma unroll
             for (int f = 0; f < kScales; ++f) {
                 const int block = min(c * kChunk * 4 + f * kShared, plan.blocks - 1);
@@ -296,15 +302,15 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
                 *reinterpret_cast<uint4 *>(xs + (part * rows + r) * kXPitch + at * 16) = w;
             }
         }
-        if (thread < kOuts) {
+        if (thread < outs_now) {
             float *const scales = reinterpret_cast<float *>(smem + plan.off_scale) + buffer * (kScales * kOuts) + thread;
             uint32_t *const zeros = reinterpret_cast<uint32_t *>(smem + plan.off_zero) + buffer * (kScales * kOuts) + thread;
 #pragma unroll
             for (int f = 0; f < kScales; ++f) {
-                scales[f * kOuts] = p.scale_dtype == SSD_F32    ? __uint_as_float(scale_raw[f])
-                                    : p.scale_dtype == SSD_BF16 ? __uint_as_float(scale_raw[f] << 16)
-                                                                : __half2float(__ushort_as_half((unsigned short)scale_raw[f]));
-                if (kZero) zeros[f * kOuts] = 0x43004300u + zero_raw[f] * 0x00010001u;
+                scales[f * kOuts] = 64.f * (p.scale_dtype == SSD_F32    ? __uint_as_float(scale_raw[f])
+                                            : p.scale_dtype == SSD_BF16 ? __uint_as_float(scale_raw[f] << 16)
+                                                                        : __half2float(__ushort_as_half((unsigned short)scale_raw[f])));
+                if (kZero) zeros[f * kOuts] = (__float_as_uint((float)zero_raw[f] * -0.015625f) >> 16) * 0x00010001u;
             }
         }
         if (x8 && thread < kScales * kCols * 8)
@@ -331,11 +337,11 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
     for (int c = chunk0; c < chunk1; ++c) {
         if (c + 1 < chunk1) bring(c + 1);
         const uint8_t *const x_now = smem + buffer * (plan.x_rows * kXPitch);
-        const float *const scales = reinterpret_cast<const float *>(smem + plan.off_scale) + buffer * (kScales * kOuts) + warp * kRows + g;
-        const uint32_t *const zeros = reinterpret_cast<const uint32_t *>(smem + plan.off_zero) + buffer * (kScales * kOuts) + warp * kRows + g;
+        const float *const scales = reinterpret_cast<const float *>(smem + plan.off_scale) + buffer * (kScales * kOuts) + o_first + g;
+        const uint32_t *const zeros = reinterpret_cast<const uint32_t *>(smem + plan.off_zero) + buffer * (kScales * kOuts) + o_first + g;
         const float *const x_scales = reinterpret_cast<const float *>(smem + plan.off_xs) + buffer * (kScales * kCols * 8) + 2 * t;
-#pragma unroll
-        for (int s = 0; s < kChunk; ++s) {
+#pragma unroll 1
+        for (int s = half; s < kChunk; s += ways) {
             const int step = c * kChunk + s;
             if (!busy || step >= step1) break;
             wait_async<kStages - 2>();
@@ -352,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
 #pragma unroll
             for (int f = 0; f < kFlushes; ++f) {
                 if (kFlushes > 1 && step * 4 + f * kShared >= plan.blocks) break;
-                uint32_t zero[2 * kMats];               // 128 + zero, twice
+                uint32_t zero[2 * kMats];               // -zero / 64, twice
 #pragma unroll
                 for (int h = 0; h < 2 * kMats; ++h) zero[h] = kZero ? zeros[(s * kFlushes + f) * kOuts + 8 * h] : eight;
                 float acc[kMats][kCols][4];
@@ -383,10 +389,10 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
                         }
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            a0[m][2 * i] = codes2(pair[0], i, base, zero[2 * m]);
-                            a0[m][2 * i + 1] = codes2(pair[1], i, base, zero[2 * m + 1]);
-                            a1[m][2 * i] = codes2(pair[0], i + 2, base, zero[2 * m]);
-                            a1[m][2 * i + 1] = codes2(pair[1], i + 2, base, zero[2 * m + 1]);
+                            a0[m][2 * i] = codes2(pair[0], i, powers, zero[2 * m]);
+                            a0[m][2 * i + 1] = codes2(pair[1], i, powers, zero[2 * m + 1]);
+                            a1[m][2 * i] = codes2(pair[0], i + 2, powers, zero[2 * m]);
+                            a1[m][2 * i + 1] = codes2(pair[1], i + 2, powers, zero[2 * m + 1]);
                         }
                     }
 #pragma unroll
@@ -428,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
     }
 
     // The sums, through shared memory (everything there has been read): [column][output].
-    constexpr int kLine = kOuts + 4;
+    const int line = outs_now + 4;
     float *const own = reinterpret_cast<float *>(smem);
 #pragma unroll
     for (int m = 0; m < kMats; ++m)
@@ -437,21 +443,21 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int col = n * 8 + 2 * t + (i & 1);
-                if (col < cols) own[col * kLine + warp * kRows + 16 * m + g + 8 * (i >> 1)] = sum[m][n][i];
+                if (col < cols) own[(half * cols + col) * line + o_first + 16 * m + g + 8 * (i >> 1)] = sum[m][n][i];
             }
     if (plan.split > 1) cluster_barrier();
     else __syncthreads();
     const uint32_t local = (uint32_t)__cvta_generic_to_shared(own);
-    for (int i = rank * kThreads + thread; i < rows * kOuts; i += plan.split * kThreads) {
-        const int r = i / kOuts, o = i % kOuts;
+    for (int i = rank * kThreads + thread; i < rows * outs_now; i += plan.split * kThreads) {
+        const int r = i / outs_now, o = i % outs_now;
         if (o_tile + o >= p.out_features) continue;
         float v = 0.f;
         for (int c = 0; c < plan.split; ++c) {
-            uint32_t at = local + (r * kLine + o) * 4;
+            uint32_t at = local + (r * line + o) * 4;
             if (plan.split > 1) asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(at), "r"(c));
-            for (int part = 0; part < parts; ++part) {
+            for (int part = 0; part < parts * ways; ++part) {
                 float f;
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(at + part * rows * (kLine * 4)) : "memory");
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(at + part * rows * (line * 4)) : "memory");
                 v += f;
             }
         }
