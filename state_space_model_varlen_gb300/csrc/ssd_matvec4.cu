@@ -155,19 +155,20 @@ bool make_plan(const ssd_matvec4_params &p, Matvec4Plan &q, int &cols, int &shar
     q.x_rows = q.row_tile * parts;
     if ((p.rows - 1) / q.row_tile + 1 > 65535) return false;
 
-    const int per_step = 4 / shared, scales = chunk(cols) * per_step;
-    int at = kWarps * kStages * 16 * mats(cols) * pitch(shared, whole);
+    const int per_step = 4 / shared, scales = chunk(cols, shared) * per_step;
+    const int steps_of_chunk = chunk(cols, shared);
+    int at = kWarps * stages(shared, whole) * 16 * mats(cols) * pitch(shared, whole);
     auto take = [&](int bytes) {
         const int off = at;
         at += (bytes + 127) / 128 * 128;
         return off;
     };
-    q.off_x = take(2 * q.x_rows * x_pitch(cols));
-    q.off_scale = take(2 * scales * outs(cols) * 4);
-    q.off_zero = take(p.zero ? 2 * scales * outs(cols) * 4 : 0);
+    q.off_x = take(2 * q.x_rows * x_pitch(cols, shared));
+    q.off_scale = take(2 * scales * scale_line(cols) * 4);
+    q.off_zero = take(p.zero ? 2 * scales * scale_line(cols) * 4 : 0);
     q.off_xs = take(q.p.x_scale ? 2 * scales * cols * 8 * 4 : 0);
     q.smem = at;
-    const int sums = (outs(cols) + 8) * q.x_rows * 4;
+    const int sums = (outs(cols) + 16) * q.x_rows * 4;
     if (q.smem < sums) q.smem = sums;
     if (q.smem > kSmemLimit) return false;
 
@@ -179,13 +180,13 @@ bool make_plan(const ssd_matvec4_params &p, Matvec4Plan &q, int &cols, int &shar
     const int64_t passes = (p.rows - 1) / q.row_tile + 1;
     const int work = 250 + 16 * cols + per_step * (20 + 12 * cols);
     double least = 0.0;
-    for (int ways = 1; ways <= chunk(cols); ways *= 2)
+    for (int ways = 1; ways <= steps_of_chunk; ways *= 2)
         for (int split = 1; split <= 8; split *= 2) {
-            const int chunks = ((q.steps - 1) / chunk(cols)) / split + 1;
-            if (split > 1 && split > (q.steps - 1) / chunk(cols) + 1) break;
+            const int chunks = (q.steps - 1) / steps_of_chunk / split + 1;
+            if (split > 1 && split > (q.steps - 1) / steps_of_chunk + 1) break;
             const int64_t tiles = (p.out_features - 1) / (outs(cols) / ways) + 1, all = tiles * passes * split;
             const int64_t waves = (all - 1) / (152 * resident) + 1, side = all <= 152 ? 1 : resident;
-            const double cost = (double)waves * ((split > 1 ? 7000 : 5000) + (double)chunks * chunk(cols) / ways * work * (side == 1 ? 4 : 7));
+            const double cost = (double)waves * ((split > 1 ? 7000 : 5000) + (double)chunks * steps_of_chunk / ways * work * (side == 1 ? 4 : 7));
             if (q.split == 0 || cost < least) {
                 least = cost;
                 q.split = split;

@@ -8,9 +8,9 @@
 // instruction's fp32 sums; the groups' scales, times 64, are applied to them in fp32.
 //
 // Bound by HBM for few rows: codes stream through a ring of asynchronous copies of
-// each warp's own, kStages steps deep.  x and the scales come through two buffers in
+// each warp's own, a few steps deep.  x and the scales come through two buffers in
 // shared memory, a chunk of steps ahead in registers.  Where there are few tiles the
-// warps of a pair take every other step of half as many outputs, and a cluster of CTAs
+// two or four warps take the steps of the same outputs in turn, and a cluster of CTAs
 // shares a tile's columns; the parts are added in a fixed order.
 //
 // A group of columns is taken in blocks of 32; a group of another size, or a row's
@@ -27,7 +27,7 @@ struct Matvec4Plan {
     ssd_matvec4_params p;
     int row_tile;               // rows of x of a pass
     int split;                  // CTAs of a cluster
-    int ways;                   // warps that share outputs: 1 or 2
+    int ways;                   // warps that share outputs: 1, 2 or 4, at most the steps of a chunk
     int tiles;                  // of outputs
     int blocks, steps;          // of a row: 32 columns at most, four blocks
     int groups, x_groups;       // of a row
@@ -46,14 +46,17 @@ cudaError_t launch_matvec4_cols8(const Matvec4Plan &q, int shared, bool whole, c
 
 namespace matvec4 {
 
-constexpr int kStages = 4, kWarps = 8, kThreads = 32 * kWarps, kStep = 128, kSmemLimit = 227 * 1024;
+constexpr int kWarps = 8, kThreads = 32 * kWarps, kStep = 128, kSmemLimit = 227 * 1024;
 constexpr int mats(int cols) { return cols <= 4 ? 2 : 1; }          // sixteens of outputs of a warp
-constexpr int chunk(int cols) { return cols <= 2 ? 2 : 1; }         // steps of a buffer of x and scales
+constexpr int chunk(int cols, int shared) { return cols == 1 && shared == 4 ? 4 : cols <= 2 ? 2 : 1; }    // steps of a buffer of x and scales
+// steps of codes in the ring of a warp: what two CTAs an SM leave room for
+constexpr int stages(int shared, bool whole) { return !whole ? 2 : shared == 4 ? 4 : 3; }
 constexpr int ctas(int cols) { return cols <= 2 ? 2 : 1; }          // of an SM, for the registers
 constexpr int outs(int cols) { return kWarps * 16 * mats(cols); }   // of a tile
+constexpr int scale_line(int cols) { return outs(cols) + 4; }       // a gap: the scales of an output come from lanes side by side
 // bytes of a row of a stage: whole steps, with a gap where lanes read one another's; or two pieces a block
 constexpr int pitch(int shared, bool whole) { return whole ? (shared == 4 ? 64 : 80) : 144; }
-constexpr int x_pitch(int cols) { return chunk(cols) * kStep * 2 + 64; }    // two rows beside one another in the banks
+constexpr int x_pitch(int cols, int shared) { return chunk(cols, shared) * kStep * 2 + 64; }    // two rows beside one another in the banks
 
 __host__ __device__ __forceinline__ int group_of(int block, int blocks, uint32_t magic) {
     return blocks == 1 ? block : (int)(((uint64_t)(uint32_t)block * magic) >> 32);
@@ -94,6 +97,13 @@ __device__ __forceinline__ uint32_t codes2(uint32_t word, int i, const uint32_t 
 
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// 16 bytes of codes into shared memory, zeros where `live` is false; L2 fetches the 256
+// bytes around them, which the row's next steps take.
+__device__ __forceinline__ void copy_codes(void *dst, const uint8_t *src, bool live) {
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(live ? 16 : 0) : "memory");
 }
 
 // Eight consecutive values of a row of x as they are stored; zeros behind the first `live`.
@@ -155,9 +165,11 @@ __device__ __forceinline__ void to_floats(const Raw &r, int type, float (&v)[8])
 template <int kCols, int kShared, bool kZero, bool kWhole>
 __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(const __grid_constant__ Matvec4Plan plan) {
     extern __shared__ __align__(128) uint8_t smem[];
-    constexpr int kMats = mats(kCols), kRows = 16 * kMats, kOuts = outs(kCols), kChunk = chunk(kCols);
-    constexpr int kPitch = pitch(kShared, kWhole), kStageBytes = kRows * kPitch, kXPitch = x_pitch(kCols);
+    constexpr int kMats = mats(kCols), kRows = 16 * kMats, kOuts = outs(kCols), kChunk = chunk(kCols, kShared);
+    constexpr int kStages = stages(kShared, kWhole);
+    constexpr int kPitch = pitch(kShared, kWhole), kStageBytes = kRows * kPitch, kXPitch = x_pitch(kCols, kShared);
     constexpr int kFlushes = 4 / kShared, kScales = kChunk * kFlushes;  // of a step, of a chunk
+    constexpr int kScaleLine = scale_line(kCols);
     constexpr int kItems = kCols * kChunk / 2;                          // eights of x that a thread brings of a chunk
     constexpr bool kOwn = kWhole && kShared == 4;                       // a lane reads the codes that it copied itself
     const ssd_matvec4_params &p = plan.p;
@@ -165,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
     const int warp = __shfl_sync(0xffffffffu, thread >> 5, 0);          // known to be the same in all lanes
     const uint32_t powers[2] = {(uint32_t)kept(0x7f007f00), (uint32_t)kept(0x7d007d00)};
     const uint32_t eight = (uint32_t)kept((int)0xbe00be00u);            // -8 / 64, twice
-    const int ways = kChunk == 2 ? plan.ways : 1, half = warp & (ways - 1);
+    const int ways = kChunk > 1 ? plan.ways : 1, turn = warp & (ways - 1);
     const int outs_now = kOuts / ways;                                  // of the tile
     const int rank = blockIdx.x % plan.split, tile = blockIdx.x / plan.split;
     const int r0 = blockIdx.y * plan.row_tile, rows = min(plan.row_tile, p.rows - r0);
@@ -173,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
     const int chunks = (plan.steps - 1) / kChunk + 1;
     const int chunk0 = (int)((int64_t)chunks * rank / plan.split), chunk1 = (int)((int64_t)chunks * (rank + 1) / plan.split);
     const int step0 = chunk0 * kChunk, step1 = min(plan.steps, chunk1 * kChunk);
-    const int o_first = (kChunk == 2 ? warp / ways : warp) * kRows;     // of the warp's in the tile
+    const int o_first = (kChunk > 1 ? warp / ways : warp) * kRows;     // of the warp's in the tile
     const int64_t o_tile = (int64_t)tile * outs_now, o_warp = o_tile + o_first;
     const bool busy = o_warp < p.out_features;                          // the warp has outputs
     const bool x8 = p.x_scale != nullptr;
@@ -196,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
 #pragma unroll
     for (int h = 0; h < 2 * kMats; ++h)
         src[h] = p.weight + min(o_warp + g + 8 * h, (int64_t)p.out_features - 1) * p.weight_stride;
-    int to_step = step0 + half, to_stage = 0;
+    int to_step = step0 + turn, to_stage = 0;
     const int row_bytes = kept(p.in_features / 2), whole_steps = kept(p.in_features / kStep);
     auto issue = [&]() {
         if (busy && to_step < step1) {
@@ -206,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
                 const bool live = to_step < whole_steps || byte < row_bytes;
 #pragma unroll
                 for (int h = 0; h < 2 * kMats; ++h)
-                    copy_async<16>(dst + (g + 8 * h) * kPitch + t * 16, src[h] + (live ? byte : 0), live);
+                    copy_codes(dst + (g + 8 * h) * kPitch + t * 16, src[h] + (live ? byte : 0), live);
             } else {
                 // 16 rows x 4 blocks x 2 pieces at a time; pieces that pass the matrix's ends byte by byte
                 const uint8_t *const end = p.weight + (int64_t)(p.out_features - 1) * p.weight_stride + (p.in_features + 1) / 2;
@@ -222,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
                     const uint8_t *from = p.weight + min(o_warp + row, (int64_t)p.out_features - 1) * p.weight_stride + columns(block, stop) / 2;
                     from += (i & 1) * 16 - (int)(reinterpret_cast<uintptr_t>(from) & 15);
                     if (from >= p.weight && from + 16 <= end) {
-                        copy_async<16>(to, from, true);
+                        copy_codes(to, from, true);
                     } else {
                         for (int b = 0; b < 16; ++b) to[b] = from + b >= p.weight && from + b < end ? from[b] : 0;
                     }
@@ -241,7 +253,8 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
     const int x_elem = p.x_dtype == SSD_F32 ? 4 : p.x_dtype == SSD_BF16 ? 2 : 1;
     const bool x_wide = reinterpret_cast<uintptr_t>(p.x) % x_size == 0 && p.x_stride * x_elem % x_size == 0 &&
                         plan.padded * x_elem % x_size == 0;
-    const int64_t o_mine = min(o_tile + thread, (int64_t)p.out_features - 1);  // whose scales the thread brings
+    const int scale_f = thread % kScales, scale_row = thread / kScales;         // the first scale that the thread brings
+    const int scale_rows = (int)min((int64_t)outs_now, p.out_features - o_tile);
     Raw x_raw[kItems];
     uint32_t scale_raw[kScales], zero_raw[kScales];
     float xs_raw = 0.f;
@@ -259,19 +272,22 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
             x_raw[i] = Raw{};
             if (live > 0) x_raw[i] = load8(p, (int64_t)(r0 + r) * p.x_stride + k, live, x_wide);
         }
-        if (thread < outs_now) {
+        // neighbours take the scales of one output
+        const int block = min(c * kChunk * 4 + scale_f * kShared, plan.blocks - 1);
+        const int64_t at = (o_tile + scale_row) * plan.groups + group_of(block, plan.group_blocks, plan.group_magic);
 #pragma unroll
-            for (int f = 0; f < kScales; ++f) {
-                const int block = min(c * kChunk * 4 + f * kShared, plan.blocks - 1);
-                const int64_t at = o_mine * plan.groups + group_of(block, plan.group_blocks, plan.group_magic);
-                scale_raw[f] = p.scale_dtype == SSD_F32 ? static_cast<const uint32_t *>(p.scale)[at]
-                                                        : static_cast<const uint16_t *>(p.scale)[at];
-                if (kZero) zero_raw[f] = p.zero[at];
+        for (int i = 0; i < kScales; ++i) {
+            const int row = scale_row + i * (kThreads / kScales);
+            if (row < scale_rows) {
+                const int64_t e = at + (int64_t)(i * (kThreads / kScales)) * plan.groups;
+                scale_raw[i] = p.scale_dtype == SSD_F32 ? static_cast<const uint32_t *>(p.scale)[e]
+                                                        : static_cast<const uint16_t *>(p.scale)[e];
+                if (kZero) zero_raw[i] = p.zero[e];
             }
         }
         if (x8 && thread < kScales * kCols * 8) {
-            const int col = thread % (kCols * 8), block = min(c * kChunk * 4 + thread / (kCols * 8) * kShared, plan.blocks - 1);
-            const int group = group_of(block, plan.x_group_blocks, plan.x_group_magic);
+            const int col = thread % (kCols * 8), x_block = min(c * kChunk * 4 + thread / (kCols * 8) * kShared, plan.blocks - 1);
+            const int group = group_of(x_block, plan.x_group_blocks, plan.x_group_magic);
             xs_raw = col < rows ? p.x_scale[(int64_t)(r0 + col) * plan.x_groups + group] : 0.f;
         }
     };
@@ -302,15 +318,16 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
                 *reinterpret_cast<uint4 *>(xs + (part * rows + r) * kXPitch + at * 16) = w;
             }
         }
-        if (thread < outs_now) {
-            float *const scales = reinterpret_cast<float *>(smem + plan.off_scale) + buffer * (kScales * kOuts) + thread;
-            uint32_t *const zeros = reinterpret_cast<uint32_t *>(smem + plan.off_zero) + buffer * (kScales * kOuts) + thread;
+        float *const scales = reinterpret_cast<float *>(smem + plan.off_scale) + buffer * (kScales * kScaleLine) + scale_f * kScaleLine;
+        uint32_t *const zeros = reinterpret_cast<uint32_t *>(smem + plan.off_zero) + buffer * (kScales * kScaleLine) + scale_f * kScaleLine;
 #pragma unroll
-            for (int f = 0; f < kScales; ++f) {
-                scales[f * kOuts] = 64.f * (p.scale_dtype == SSD_F32    ? __uint_as_float(scale_raw[f])
-                                            : p.scale_dtype == SSD_BF16 ? __uint_as_float(scale_raw[f] << 16)
-                                                                        : __half2float(__ushort_as_half((unsigned short)scale_raw[f])));
-                if (kZero) zeros[f * kOuts] = (__float_as_uint((float)zero_raw[f] * -0.015625f) >> 16) * 0x00010001u;
+        for (int i = 0; i < kScales; ++i) {
+            const int row = scale_row + i * (kThreads / kScales);
+            if (row < scale_rows) {
+                scales[row] = 64.f * (p.scale_dtype == SSD_F32    ? __uint_as_float(scale_raw[i])
+                                      : p.scale_dtype == SSD_BF16 ? __uint_as_float(scale_raw[i] << 16)
+                                                                  : __half2float(__ushort_as_half((unsigned short)scale_raw[i])));
+                if (kZero) zeros[row] = (__float_as_uint((float)zero_raw[i] * -0.015625f) >> 16) * 0x00010001u;
             }
         }
         if (x8 && thread < kScales * kCols * 8)
@@ -337,11 +354,11 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
     for (int c = chunk0; c < chunk1; ++c) {
         if (c + 1 < chunk1) bring(c + 1);
         const uint8_t *const x_now = smem + buffer * (plan.x_rows * kXPitch);
-        const float *const scales = reinterpret_cast<const float *>(smem + plan.off_scale) + buffer * (kScales * kOuts) + o_first + g;
-        const uint32_t *const zeros = reinterpret_cast<const uint32_t *>(smem + plan.off_zero) + buffer * (kScales * kOuts) + o_first + g;
+        const float *const scales = reinterpret_cast<const float *>(smem + plan.off_scale) + buffer * (kScales * kScaleLine) + o_first + g;
+        const uint32_t *const zeros = reinterpret_cast<const uint32_t *>(smem + plan.off_zero) + buffer * (kScales * kScaleLine) + o_first + g;
         const float *const x_scales = reinterpret_cast<const float *>(smem + plan.off_xs) + buffer * (kScales * kCols * 8) + 2 * t;
 #pragma unroll 1
-        for (int s = half; s < kChunk; s += ways) {
+        for (int s = turn; s < kChunk; s += ways) {
             const int step = c * kChunk + s;
             if (!busy || step >= step1) break;
             wait_async<kStages - 2>();
@@ -360,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
                 if (kFlushes > 1 && step * 4 + f * kShared >= plan.blocks) break;
                 uint32_t zero[2 * kMats];               // -zero / 64, twice
 #pragma unroll
-                for (int h = 0; h < 2 * kMats; ++h) zero[h] = kZero ? zeros[(s * kFlushes + f) * kOuts + 8 * h] : eight;
+                for (int h = 0; h < 2 * kMats; ++h) zero[h] = kZero ? zeros[(s * kFlushes + f) * kScaleLine + 8 * h] : eight;
                 float acc[kMats][kCols][4];
 #pragma unroll
                 for (int b = 0; b < kShared; ++b) {
@@ -408,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
                 }
                 float scale[2 * kMats];
 #pragma unroll
-                for (int h = 0; h < 2 * kMats; ++h) scale[h] = scales[(s * kFlushes + f) * kOuts + 8 * h];
+                for (int h = 0; h < 2 * kMats; ++h) scale[h] = scales[(s * kFlushes + f) * kScaleLine + 8 * h];
 #pragma unroll
                 for (int n = 0; n < kCols; ++n) {
                     if (x8) {
@@ -443,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int col = n * 8 + 2 * t + (i & 1);
-                if (col < cols) own[(half * cols + col) * line + o_first + 16 * m + g + 8 * (i >> 1)] = sum[m][n][i];
+                if (col < cols) own[(turn * cols + col) * line + o_first + 16 * m + g + 8 * (i >> 1)] = sum[m][n][i];
             }
     if (plan.split > 1) cluster_barrier();
     else __syncthreads();
