@@ -174,8 +174,8 @@ bool make_plan(const ssd_matvec4_params &p, Matvec4Plan &q, int &cols, int &shar
 
     // The split and the ways whose waves of CTAs take the least, in clocks.  A step is
     // about so many instructions of a warp; eight warps of an SM take a step in four
-    // times as many clocks, 16 in seven; a CTA begins and ends in 5,000, in a cluster
-    // 7,000 (measured).
+    // times as many clocks, 16 in seven; a chunk's x and scales take 800, a CTA begins
+    // and ends in 5,000, in a cluster 7,000 (measured).
     const int fit = kSmemLimit / (q.smem + 1024), resident = fit < 1 ? 1 : fit < ctas(cols) ? fit : ctas(cols);
     const int64_t passes = (p.rows - 1) / q.row_tile + 1;
     const int work = 250 + 16 * cols + per_step * (20 + 12 * cols);
@@ -186,7 +186,8 @@ bool make_plan(const ssd_matvec4_params &p, Matvec4Plan &q, int &cols, int &shar
             if (split > 1 && split > (q.steps - 1) / steps_of_chunk + 1) break;
             const int64_t tiles = (p.out_features - 1) / (outs(cols) / ways) + 1, all = tiles * passes * split;
             const int64_t waves = (all - 1) / (152 * resident) + 1, side = all <= 152 ? 1 : resident;
-            const double cost = (double)waves * ((split > 1 ? 7000 : 5000) + (double)chunks * steps_of_chunk / ways * work * (side == 1 ? 4 : 7));
+            const double cost = (double)waves * ((split > 1 ? 7000 : 5000) + 800.0 * chunks +
+                                                        (double)chunks * steps_of_chunk / ways * work * (side == 1 ? 4 : 7));
             if (q.split == 0 || cost < least) {
                 least = cost;
                 q.split = split;

@@ -48,7 +48,7 @@ namespace matvec4 {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps, kStep = 128, kSmemLimit = 227 * 1024;
 constexpr int mats(int cols) { return cols <= 4 ? 2 : 1; }          // sixteens of outputs of a warp
-constexpr int chunk(int cols, int shared) { return cols == 1 && shared == 4 ? 4 : cols <= 2 ? 2 : 1; }    // steps of a buffer of x and scales
+constexpr int chunk(int cols, int shared) { return cols == 1 && shared == 4 ? 4 : cols <= 4 ? 2 : 1; }    // steps of a buffer of x and scales
 // steps of codes in the ring of a warp: what two CTAs an SM leave room for
 constexpr int stages(int shared, bool whole) { return !whole ? 2 : shared == 4 ? 4 : 3; }
 constexpr int ctas(int cols) { return cols <= 2 ? 2 : 1; }          // of an SM, for the registers
@@ -106,58 +106,51 @@ __device__ __forceinline__ void copy_codes(void *dst, const uint8_t *src, bool l
                  "r"(live ? 16 : 0) : "memory");
 }
 
-// Eight consecutive values of a row of x as they are stored; zeros behind the first `live`.
+// Eight consecutive values of a row of x as they are stored, by loads of `grain` bytes
+// (16, 4, 2 or 1, at most the element's own but for 8-bit ones); zeros behind the first `live`.
 struct Raw { uint32_t w[8]; };
-__device__ __forceinline__ Raw load8(const ssd_matvec4_params &p, int64_t at, int live, bool wide) {
+__device__ __forceinline__ Raw load8(const ssd_matvec4_params &p, int64_t at, int live, int grain) {
     Raw r{};
-    if (p.x_dtype == SSD_F32) {
-        const float *src = static_cast<const float *>(p.x) + at;
-        if (wide && live == 8) {
-            *reinterpret_cast<uint4 *>(r.w) = *reinterpret_cast<const uint4 *>(src);
-            *reinterpret_cast<uint4 *>(r.w + 4) = *reinterpret_cast<const uint4 *>(src + 4);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < live) r.w[i] = __float_as_uint(src[i]);
-        }
-    } else if (p.x_dtype == SSD_BF16) {
-        const uint16_t *src = static_cast<const uint16_t *>(p.x) + at;
-        if (wide && live == 8) {
-            *reinterpret_cast<uint4 *>(r.w) = *reinterpret_cast<const uint4 *>(src);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < live) r.w[i / 2] |= (uint32_t)src[i] << (16 * (i & 1));
-        }
-    } else {
-        const uint8_t *src = static_cast<const uint8_t *>(p.x) + at;
-        if (wide && live == 8) {
+    const int size = p.x_dtype == SSD_F32 ? 4 : p.x_dtype == SSD_BF16 ? 2 : 1;
+    const uint8_t *src = static_cast<const uint8_t *>(p.x) + at * size;
+    if (live == 8 && grain == 16) {
+        if (size == 1) {
             *reinterpret_cast<uint2 *>(r.w) = *reinterpret_cast<const uint2 *>(src);
         } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < live) r.w[i / 4] |= (uint32_t)src[i] << (8 * (i & 3));
+            *reinterpret_cast<uint4 *>(r.w) = *reinterpret_cast<const uint4 *>(src);
+            if (size == 4) *reinterpret_cast<uint4 *>(r.w + 4) = *reinterpret_cast<const uint4 *>(src + 16);
         }
+    } else if (live == 8 && grain == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < 2 * size) r.w[i] = reinterpret_cast<const uint32_t *>(src)[i];
+    } else if (size == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < live) r.w[i] = reinterpret_cast<const uint32_t *>(src)[i];
+    } else if (size == 2) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < live) r.w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(src)[i] << (16 * (i & 1));
+    } else if (live == 8 && grain == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(src)[i] << (16 * (i & 1));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < live) r.w[i / 4] |= (uint32_t)src[i] << (8 * (i & 3));
     }
     return r;
 }
-__device__ __forceinline__ void to_floats(const Raw &r, int type, float (&v)[8]) {
-    if (type == SSD_F32) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.w[i]);
-    } else if (type == SSD_BF16) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(r.w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
-        }
-    } else if (type == SSD_E4M3) {
-        decode4<SSD_E4M3>(r.w[0], v);
-        decode4<SSD_E4M3>(r.w[1], v + 4);
-    } else {
-        decode4<SSD_I8>(r.w[0], v);
-        decode4<SSD_I8>(r.w[1], v + 4);
-    }
+// the upper halves of a and b
+__device__ __forceinline__ uint32_t upper(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
+// bf16 values of 8-bit codes, i and i + 4 side by side
+template <int kType> __device__ __forceinline__ uint4 side_by_side(const Raw &r) {
+    float v[8];
+    decode4<kType>(r.w[0], v);
+    decode4<kType>(r.w[1], v + 4);
+    return make_uint4(upper(__float_as_uint(v[0]), __float_as_uint(v[4])), upper(__float_as_uint(v[1]), __float_as_uint(v[5])),
+                      upper(__float_as_uint(v[2]), __float_as_uint(v[6])), upper(__float_as_uint(v[3]), __float_as_uint(v[7])));
 }
 
 // kCols: eights of columns (rows of x, or their parts) of a pass.  kShared: blocks that
@@ -249,10 +242,9 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
     for (int q = 0; q < kStages - 1; ++q) issue();
 
     // ---- x and scales: a chunk's into registers, and from there into a buffer ----
-    const int x_size = p.x_dtype == SSD_F32 || p.x_dtype == SSD_BF16 ? 16 : 8;
     const int x_elem = p.x_dtype == SSD_F32 ? 4 : p.x_dtype == SSD_BF16 ? 2 : 1;
-    const bool x_wide = reinterpret_cast<uintptr_t>(p.x) % x_size == 0 && p.x_stride * x_elem % x_size == 0 &&
-                        plan.padded * x_elem % x_size == 0;
+    const int x_low = (int)(reinterpret_cast<uintptr_t>(p.x) | (uintptr_t)(p.x_stride * x_elem) | (uintptr_t)(plan.padded * x_elem));
+    const int x_grain = x_low % (x_elem == 1 ? 8 : 16) == 0 ? 16 : x_low % 4 == 0 ? 4 : x_low % 2 == 0 ? 2 : 1;
     const int scale_f = thread % kScales, scale_row = thread / kScales;         // the first scale that the thread brings
     const int scale_rows = (int)min((int64_t)outs_now, p.out_features - o_tile);
     Raw x_raw[kItems];
@@ -270,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
                 live = max(0, min(8, end - k));
             }
             x_raw[i] = Raw{};
-            if (live > 0) x_raw[i] = load8(p, (int64_t)(r0 + r) * p.x_stride + k, live, x_wide);
+            if (live > 0) x_raw[i] = load8(p, (int64_t)(r0 + r) * p.x_stride + k, live, x_grain);
         }
         // neighbours take the scales of one output
         const int block = min(c * kChunk * 4 + scale_f * kShared, plan.blocks - 1);
@@ -297,25 +289,33 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
         for (int i = 0; i < kItems; ++i) {
             const int item = thread + i * kThreads, r = item / (kChunk * 16), e = item % (kChunk * 16);
             if (r >= rows) continue;
-            float v[8];
-            to_floats(x_raw[i], p.x_dtype, v);
-            // eights of a step in the order in which quad lane t reads its j-th word: 4 j + t
+            // values i and i + 4 side by side, as the codes of a word come; eights of a step
+            // in the order in which quad lane t reads its j-th word: 4 j + t
             const int at = kOwn ? (e & ~15) | (e & 3) << 2 | (e >> 2 & 3) : e;
+            uint4 *const to = reinterpret_cast<uint4 *>(xs + r * kXPitch + at * 16);
+            const Raw &raw = x_raw[i];
+            if (p.x_dtype == SSD_BF16) {
+                *to = make_uint4(__byte_perm(raw.w[0], raw.w[2], 0x5410), upper(raw.w[0], raw.w[2]),
+                                 __byte_perm(raw.w[1], raw.w[3], 0x5410), upper(raw.w[1], raw.w[3]));
+            } else if (p.x_dtype == SSD_E4M3) {
+                *to = side_by_side<SSD_E4M3>(raw);
+            } else if (p.x_dtype == SSD_I8) {
+                *to = side_by_side<SSD_I8>(raw);
+            } else {
+                float v[8];
 #pragma unroll
-            for (int part = 0; part < 3; ++part) {
-                if (part >= parts) break;
-                uint32_t u[8];
+                for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(raw.w[j]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    u[j] = __float_as_uint(v[j]);
-                    if (v[j] != v[j]) u[j] = 0x7fc00000u;
-                    const float cut = __uint_as_float(u[j] & 0xffff0000u);
-                    v[j] = fabsf(cut) < __int_as_float(0x7f800000) ? v[j] - cut : 0.f;
+                for (int part = 0; part < 3; ++part) {
+                    uint32_t u[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {       // the upper bits, and what is left of a finite number
+                        u[j] = v[j] != v[j] ? 0x7fc00000u : __float_as_uint(v[j]);
+                        const float cut = __uint_as_float(u[j] & 0xffff0000u);
+                        v[j] = fabsf(cut) < __int_as_float(0x7f800000) ? v[j] - cut : 0.f;
+                    }
+                    to[part * rows * (kXPitch / 16)] = make_uint4(upper(u[0], u[4]), upper(u[1], u[5]), upper(u[2], u[6]), upper(u[3], u[7]));
                 }
-                // values i and i + 4 side by side, as the codes of a word come
-                const uint4 w = make_uint4(__byte_perm(u[0], u[4], 0x7632), __byte_perm(u[1], u[5], 0x7632),
-                                           __byte_perm(u[2], u[6], 0x7632), __byte_perm(u[3], u[7], 0x7632));
-                *reinterpret_cast<uint4 *>(xs + (part * rows + r) * kXPitch + at * 16) = w;
             }
         }
         float *const scales = reinterpret_cast<float *>(smem + plan.off_scale) + buffer * (kScales * kScaleLine) + scale_f * kScaleLine;
