@@ -99,28 +99,12 @@ __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
-// 16 bytes of codes into shared memory, zeros where `live` is false; L2 fetches the 256
-// bytes around them, which the row's next steps take.
-__device__ __forceinline__ void copy_codes(void *dst, const uint8_t *src, bool live) {
-    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
-                 "r"(live ? 16 : 0) : "memory");
-}
-
-// Eight consecutive values of a row of x as they are stored, by loads of `grain` bytes
-// (16, 4, 2 or 1, at most the element's own but for 8-bit ones); zeros behind the first `live`.
+// Eight consecutive values of `size` bytes of a row of x as they are stored, by loads of
+// at most 4 bytes, of which `grain` is the alignment; zeros behind the first `live`.
 struct Raw { uint32_t w[8]; };
-__device__ __forceinline__ Raw load8(const ssd_matvec4_params &p, int64_t at, int live, int grain) {
+__device__ __forceinline__ Raw load8(const uint8_t *src, int size, int live, int grain) {
     Raw r{};
-    const int size = p.x_dtype == SSD_F32 ? 4 : p.x_dtype == SSD_BF16 ? 2 : 1;
-    const uint8_t *src = static_cast<const uint8_t *>(p.x) + at * size;
-    if (live == 8 && grain == 16) {
-        if (size == 1) {
-            *reinterpret_cast<uint2 *>(r.w) = *reinterpret_cast<const uint2 *>(src);
-        } else {
-            *reinterpret_cast<uint4 *>(r.w) = *reinterpret_cast<const uint4 *>(src);
-            if (size == 4) *reinterpret_cast<uint4 *>(r.w + 4) = *reinterpret_cast<const uint4 *>(src + 16);
-        }
-    } else if (live == 8 && grain == 4) {
+    if (live == 8 && grain >= 4) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (i < 2 * size) r.w[i] = reinterpret_cast<const uint32_t *>(src)[i];
@@ -211,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
                 const bool live = to_step < whole_steps || byte < row_bytes;
 #pragma unroll
                 for (int h = 0; h < 2 * kMats; ++h)
-                    copy_codes(dst + (g + 8 * h) * kPitch + t * 16, src[h] + (live ? byte : 0), live);
+                    copy_async<16>(dst + (g + 8 * h) * kPitch + t * 16, src[h] + (live ? byte : 0), live);
             } else {
                 // 16 rows x 4 blocks x 2 pieces at a time; pieces that pass the matrix's ends byte by byte
                 const uint8_t *const end = p.weight + (int64_t)(p.out_features - 1) * p.weight_stride + (p.in_features + 1) / 2;
@@ -227,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
                     const uint8_t *from = p.weight + min(o_warp + row, (int64_t)p.out_features - 1) * p.weight_stride + columns(block, stop) / 2;
                     from += (i & 1) * 16 - (int)(reinterpret_cast<uintptr_t>(from) & 15);
                     if (from >= p.weight && from + 16 <= end) {
-                        copy_codes(to, from, true);
+                        copy_async<16>(to, from, true);
                     } else {
                         for (int b = 0; b < 16; ++b) to[b] = from + b >= p.weight && from + b < end ? from[b] : 0;
                     }
@@ -247,61 +231,95 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
     const int x_grain = x_low % (x_elem == 1 ? 8 : 16) == 0 ? 16 : x_low % 4 == 0 ? 4 : x_low % 2 == 0 ? 2 : 1;
     const int scale_f = thread % kScales, scale_row = thread / kScales;         // the first scale that the thread brings
     const int scale_rows = (int)min((int64_t)outs_now, p.out_features - o_tile);
+    // eights of x that the thread brings: one place in the chunk, of every kNext-th row
+    constexpr int kEights = kChunk * 16, kNext = kThreads / kEights;
+    const int x_e = thread % kEights, x_row = thread / kEights;
+    const uint8_t *const x_src = static_cast<const uint8_t *>(p.x) + (int64_t)(r0 + x_row) * p.x_stride * x_elem;
+    const int64_t x_next = (int64_t)kNext * p.x_stride * x_elem;
+    const uint8_t *const scale_src =
+        static_cast<const uint8_t *>(p.scale) + (o_tile + scale_row) * plan.groups * (p.scale_dtype == SSD_F32 ? 4 : 2);
+    const uint8_t *const zero_src = kZero ? p.zero + (o_tile + scale_row) * plan.groups : nullptr;
+    const int scale_next = kThreads / kScales;
     Raw x_raw[kItems];
     uint32_t scale_raw[kScales], zero_raw[kScales];
     float xs_raw = 0.f;
     auto bring = [&](int c) {
-#pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-            const int item = thread + i * kThreads, r = item / (kChunk * 16), e = item % (kChunk * 16);
-            const int block = c * kChunk * 4 + e / 4;
+        {
+            const int block = c * kChunk * 4 + x_e / 4;
             int live = 0, k = 0;
-            if (r < rows && block < plan.blocks) {
+            if (block < plan.blocks) {
                 int end;
-                k = columns(block, end) + (e & 3) * 8;
+                k = columns(block, end) + (x_e & 3) * 8;
                 live = max(0, min(8, end - k));
             }
-            x_raw[i] = Raw{};
-            if (live > 0) x_raw[i] = load8(p, (int64_t)(r0 + r) * p.x_stride + k, live, x_grain);
-        }
-        // neighbours take the scales of one output
-        const int block = min(c * kChunk * 4 + scale_f * kShared, plan.blocks - 1);
-        const int64_t at = (o_tile + scale_row) * plan.groups + group_of(block, plan.group_blocks, plan.group_magic);
+            const uint8_t *from = x_src + (int64_t)k * x_elem;
+            const bool wide = live == 8 && x_grain == 16;
 #pragma unroll
-        for (int i = 0; i < kScales; ++i) {
-            const int row = scale_row + i * (kThreads / kScales);
-            if (row < scale_rows) {
-                const int64_t e = at + (int64_t)(i * (kThreads / kScales)) * plan.groups;
-                scale_raw[i] = p.scale_dtype == SSD_F32 ? static_cast<const uint32_t *>(p.scale)[e]
-                                                        : static_cast<const uint16_t *>(p.scale)[e];
-                if (kZero) zero_raw[i] = p.zero[e];
+            for (int i = 0; i < kItems; ++i, from += x_next) {
+                uint4 *const to = reinterpret_cast<uint4 *>(x_raw[i].w);
+                x_raw[i] = Raw{};
+                if (x_row + i * kNext >= rows || live == 0) continue;
+                if (!wide) {
+                    x_raw[i] = load8(from, x_elem, live, x_grain);
+                } else if (x_elem == 1) {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(from);
+                    to[0] = make_uint4(v.x, v.y, 0, 0);
+                } else {
+                    to[0] = *reinterpret_cast<const uint4 *>(from);
+                    if (x_elem == 4) to[1] = *reinterpret_cast<const uint4 *>(from + 16);
+                }
+            }
+        }
+        {
+            // neighbours take the scales of one output
+            const int block = min(c * kChunk * 4 + scale_f * kShared, plan.blocks - 1);
+            const int group = group_of(block, plan.group_blocks, plan.group_magic);
+            if (p.scale_dtype == SSD_F32) {
+                const uint8_t *from = scale_src + group * 4;
+#pragma unroll
+                for (int i = 0; i < kScales; ++i, from += (int64_t)scale_next * plan.groups * 4)
+                    if (scale_row + i * scale_next < scale_rows) scale_raw[i] = *reinterpret_cast<const uint32_t *>(from);
+            } else {
+                const uint8_t *from = scale_src + group * 2;
+#pragma unroll
+                for (int i = 0; i < kScales; ++i, from += (int64_t)scale_next * plan.groups * 2)
+                    if (scale_row + i * scale_next < scale_rows) scale_raw[i] = *reinterpret_cast<const uint16_t *>(from);
+            }
+            if constexpr (kZero) {
+                const uint8_t *from = zero_src + group;
+#pragma unroll
+                for (int i = 0; i < kScales; ++i, from += (int64_t)scale_next * plan.groups)
+                    if (scale_row + i * scale_next < scale_rows) zero_raw[i] = *from;
             }
         }
         if (x8 && thread < kScales * kCols * 8) {
-            const int col = thread % (kCols * 8), x_block = min(c * kChunk * 4 + thread / (kCols * 8) * kShared, plan.blocks - 1);
-            const int group = group_of(x_block, plan.x_group_blocks, plan.x_group_magic);
+            const int col = thread % (kCols * 8), block = min(c * kChunk * 4 + thread / (kCols * 8) * kShared, plan.blocks - 1);
+            const int group = group_of(block, plan.x_group_blocks, plan.x_group_magic);
             xs_raw = col < rows ? p.x_scale[(int64_t)(r0 + col) * plan.x_groups + group] : 0.f;
         }
     };
     auto put_away = [&](int buffer) {
-        uint8_t *const xs = smem + plan.off_x + buffer * (plan.x_rows * kXPitch);
+        // values i and i + 4 side by side, as the codes of a word come; eights of a step
+        // in the order in which quad lane t reads its j-th word: 4 j + t
+        const int place = kOwn ? (x_e & ~15) | (x_e & 3) << 2 | (x_e >> 2 & 3) : x_e;
+        uint8_t *const xs = smem + plan.off_x + buffer * (plan.x_rows * kXPitch) + x_row * kXPitch + place * 16;
+        auto each = [&](auto store) {
 #pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-            const int item = thread + i * kThreads, r = item / (kChunk * 16), e = item % (kChunk * 16);
-            if (r >= rows) continue;
-            // values i and i + 4 side by side, as the codes of a word come; eights of a step
-            // in the order in which quad lane t reads its j-th word: 4 j + t
-            const int at = kOwn ? (e & ~15) | (e & 3) << 2 | (e >> 2 & 3) : e;
-            uint4 *const to = reinterpret_cast<uint4 *>(xs + r * kXPitch + at * 16);
-            const Raw &raw = x_raw[i];
-            if (p.x_dtype == SSD_BF16) {
+            for (int i = 0; i < kItems; ++i)
+                if (x_row + i * kNext < rows) store(reinterpret_cast<uint4 *>(xs + i * kNext * kXPitch), x_raw[i]);
+        };
+        if (p.x_dtype == SSD_BF16) {
+            each([](uint4 *to, const Raw &raw) {
                 *to = make_uint4(__byte_perm(raw.w[0], raw.w[2], 0x5410), upper(raw.w[0], raw.w[2]),
                                  __byte_perm(raw.w[1], raw.w[3], 0x5410), upper(raw.w[1], raw.w[3]));
-            } else if (p.x_dtype == SSD_E4M3) {
-                *to = side_by_side<SSD_E4M3>(raw);
-            } else if (p.x_dtype == SSD_I8) {
-                *to = side_by_side<SSD_I8>(raw);
-            } else {
+            });
+        } else if (p.x_dtype == SSD_E4M3) {
+            each([](uint4 *to, const Raw &raw) { *to = side_by_side<SSD_E4M3>(raw); });
+        } else if (p.x_dtype == SSD_I8) {
+            each([](uint4 *to, const Raw &raw) { *to = side_by_side<SSD_I8>(raw); });
+        } else {
+            const int next_part = rows * (kXPitch / 16);
+            each([next_part](uint4 *to, const Raw &raw) {
                 float v[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(raw.w[j]);
@@ -314,21 +332,25 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
                         const float cut = __uint_as_float(u[j] & 0xffff0000u);
                         v[j] = fabsf(cut) < __int_as_float(0x7f800000) ? v[j] - cut : 0.f;
                     }
-                    to[part * rows * (kXPitch / 16)] = make_uint4(upper(u[0], u[4]), upper(u[1], u[5]), upper(u[2], u[6]), upper(u[3], u[7]));
+                    to[part * next_part] = make_uint4(upper(u[0], u[4]), upper(u[1], u[5]), upper(u[2], u[6]), upper(u[3], u[7]));
                 }
-            }
+            });
         }
-        float *const scales = reinterpret_cast<float *>(smem + plan.off_scale) + buffer * (kScales * kScaleLine) + scale_f * kScaleLine;
-        uint32_t *const zeros = reinterpret_cast<uint32_t *>(smem + plan.off_zero) + buffer * (kScales * kScaleLine) + scale_f * kScaleLine;
+        float *const scales = reinterpret_cast<float *>(smem + plan.off_scale) + (buffer * kScales + scale_f) * kScaleLine + scale_row;
+        uint32_t *const zeros = reinterpret_cast<uint32_t *>(smem + plan.off_zero) + (buffer * kScales + scale_f) * kScaleLine + scale_row;
+        auto put_scales = [&](auto value) {
 #pragma unroll
-        for (int i = 0; i < kScales; ++i) {
-            const int row = scale_row + i * (kThreads / kScales);
-            if (row < scale_rows) {
-                scales[row] = 64.f * (p.scale_dtype == SSD_F32    ? __uint_as_float(scale_raw[i])
-                                      : p.scale_dtype == SSD_BF16 ? __uint_as_float(scale_raw[i] << 16)
-                                                                  : __half2float(__ushort_as_half((unsigned short)scale_raw[i])));
-                if (kZero) zeros[row] = (__float_as_uint((float)zero_raw[i] * -0.015625f) >> 16) * 0x00010001u;
-            }
+            for (int i = 0; i < kScales; ++i)
+                if (scale_row + i * scale_next < scale_rows) scales[i * scale_next] = 64.f * value(scale_raw[i]);
+        };
+        if (p.scale_dtype == SSD_F32) put_scales([](uint32_t v) { return __uint_as_float(v); });
+        else if (p.scale_dtype == SSD_BF16) put_scales([](uint32_t v) { return __uint_as_float(v << 16); });
+        else put_scales([](uint32_t v) { return __half2float(__ushort_as_half((unsigned short)v)); });
+        if constexpr (kZero) {
+#pragma unroll
+            for (int i = 0; i < kScales; ++i)
+                if (scale_row + i * scale_next < scale_rows)
+                    zeros[i * scale_next] = (__float_as_uint((float)zero_raw[i] * -0.015625f) >> 16) * 0x00010001u;
         }
         if (x8 && thread < kScales * kCols * 8)
             reinterpret_cast<float *>(smem + plan.off_xs)[buffer * (kScales * kCols * 8) + thread] = xs_raw;
@@ -366,6 +388,12 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
             issue();
             const uint8_t *const codes = ring + stage * kStageBytes + g * kPitch + (kOwn ? t * 16 : t * 4);
             stage = stage + 1 == kStages ? 0 : stage + 1;
+            const float *const s_scales = scales + s * (kFlushes * kScaleLine), *const s_x = x_scales + s * (kFlushes * kCols * 8);
+            const uint32_t *const s_zeros = zeros + s * (kFlushes * kScaleLine);
+            const uint8_t *x[kCols];
+#pragma unroll
+            for (int n = 0; n < kCols; ++n) x[n] = x_now + s * (kStep * 2) + x_at[n];
+            const int flushes = kFlushes == 1 ? 1 : min(kFlushes, (plan.blocks - step * 4 + kShared - 1) / kShared);
             uint32_t words[2 * kMats][4];
             if constexpr (kOwn) {
 #pragma unroll
@@ -374,10 +402,10 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
             }
 #pragma unroll
             for (int f = 0; f < kFlushes; ++f) {
-                if (kFlushes > 1 && step * 4 + f * kShared >= plan.blocks) break;
+                if (f >= flushes) break;
                 uint32_t zero[2 * kMats];               // -zero / 64, twice
 #pragma unroll
-                for (int h = 0; h < 2 * kMats; ++h) zero[h] = kZero ? zeros[(s * kFlushes + f) * kScaleLine + 8 * h] : eight;
+                for (int h = 0; h < 2 * kMats; ++h) zero[h] = kZero ? s_zeros[f * kScaleLine + 8 * h] : eight;
                 float acc[kMats][kCols][4];
 #pragma unroll
                 for (int b = 0; b < kShared; ++b) {
@@ -414,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
                     }
 #pragma unroll
                     for (int n = 0; n < kCols; ++n) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(x_now + x_at[n] + s * (kStep * 2) + w * 64);
+                        const uint4 v = *reinterpret_cast<const uint4 *>(x[n] + w * 64);
 #pragma unroll
                         for (int m = 0; m < kMats; ++m) {
                             if (b == 0) mma_first(acc[m][n], a0[m], v.x, v.y);
@@ -425,11 +453,11 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
                 }
                 float scale[2 * kMats];
 #pragma unroll
-                for (int h = 0; h < 2 * kMats; ++h) scale[h] = scales[(s * kFlushes + f) * kScaleLine + 8 * h];
+                for (int h = 0; h < 2 * kMats; ++h) scale[h] = s_scales[f * kScaleLine + 8 * h];
 #pragma unroll
                 for (int n = 0; n < kCols; ++n) {
                     if (x8) {
-                        const float2 u = *reinterpret_cast<const float2 *>(x_scales + (s * kFlushes + f) * (kCols * 8) + n * 8);
+                        const float2 u = *reinterpret_cast<const float2 *>(s_x + f * (kCols * 8) + n * 8);
 #pragma unroll
                         for (int m = 0; m < kMats; ++m) {
                             acc[m][n][0] *= u.x;
