@@ -177,24 +177,25 @@ bool make_plan(const ssd_matvec4_params &p, Matvec4Plan &q, int &cols, int &shar
     // times as many clocks, 16 in seven; a chunk's x and scales take 800, a CTA begins
     // and ends in 5,000, in a cluster 7,000 (measured).
     const int fit = kSmemLimit / (q.smem + 1024), resident = fit < 1 ? 1 : fit < ctas(cols) ? fit : ctas(cols);
-    const int64_t passes = (p.rows - 1) / q.row_tile + 1;
+    const int passes = (p.rows - 1) / q.row_tile + 1;
     const int work = 250 + 16 * cols + per_step * (20 + 12 * cols);
+    const int chunks = (q.steps - 1) / steps_of_chunk + 1;
     double least = 0.0;
-    for (int ways = 1; ways <= steps_of_chunk; ways *= 2)
-        for (int split = 1; split <= 8; split *= 2) {
-            const int chunks = (q.steps - 1) / steps_of_chunk / split + 1;
-            if (split > 1 && split > (q.steps - 1) / steps_of_chunk + 1) break;
-            const int64_t tiles = (p.out_features - 1) / (outs(cols) / ways) + 1, all = tiles * passes * split;
-            const int64_t waves = (all - 1) / (152 * resident) + 1, side = all <= 152 ? 1 : resident;
-            const double cost = (double)waves * ((split > 1 ? 7000 : 5000) + 800.0 * chunks +
-                                                        (double)chunks * steps_of_chunk / ways * work * (side == 1 ? 4 : 7));
+    for (int ways = 1; ways <= steps_of_chunk; ways *= 2) {
+        const int outs_now = outs(cols) / ways, tiles = (p.out_features - 1) / outs_now + 1;
+        for (int split = 1; split <= 8 && split <= chunks; split *= 2) {
+            const int mine = (chunks - 1) / split + 1;
+            const double all = (double)passes * tiles * split, rounds = all / (152 * resident), whole_rounds = (double)(int64_t)rounds;
+            const double waves = whole_rounds < rounds ? whole_rounds + 1 : whole_rounds;
+            const double cost = waves * ((split > 1 ? 7000 : 5000) + 800 * mine + mine * (steps_of_chunk / ways) * (double)work * (all <= 152 || resident == 1 ? 4 : 7));
             if (q.split == 0 || cost < least) {
                 least = cost;
                 q.split = split;
                 q.ways = ways;
-                q.tiles = (int)tiles;
+                q.tiles = tiles;
             }
         }
+    }
     return true;
 }
 

@@ -48,7 +48,7 @@ namespace matvec4 {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps, kStep = 128, kSmemLimit = 227 * 1024;
 constexpr int mats(int cols) { return cols <= 4 ? 2 : 1; }          // sixteens of outputs of a warp
-constexpr int chunk(int cols, int shared) { return cols == 1 && shared == 4 ? 4 : cols <= 4 ? 2 : 1; }    // steps of a buffer of x and scales
+constexpr int chunk(int cols, int shared) { return cols == 1 && shared == 4 ? 4 : 2; }    // steps of a buffer of x and scales
 // steps of codes in the ring of a warp: what two CTAs an SM leave room for
 constexpr int stages(int shared, bool whole) { return !whole ? 2 : shared == 4 ? 4 : 3; }
 constexpr int ctas(int cols) { return cols <= 2 ? 2 : 1; }          // of an SM, for the registers
@@ -99,40 +99,35 @@ __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
-// Eight consecutive values of `size` bytes of a row of x as they are stored, by loads of
+// Eight consecutive values of kSize bytes of a row of x as they are stored, by loads of
 // at most 4 bytes, of which `grain` is the alignment; zeros behind the first `live`.
 struct Raw { uint32_t w[8]; };
-__device__ __forceinline__ Raw load8(const uint8_t *src, int size, int live, int grain) {
+template <int kSize> __device__ __forceinline__ Raw load8(const uint8_t *src, int live, int grain) {
     Raw r{};
     if (live == 8 && grain >= 4) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < 2 * size) r.w[i] = reinterpret_cast<const uint32_t *>(src)[i];
-    } else if (size == 4) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < live) r.w[i] = reinterpret_cast<const uint32_t *>(src)[i];
-    } else if (size == 2) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < live) r.w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(src)[i] << (16 * (i & 1));
-    } else if (live == 8 && grain == 2) {
+        for (int i = 0; i < 2 * kSize; ++i) r.w[i] = reinterpret_cast<const uint32_t *>(src)[i];
+    } else if (kSize == 1 && live == 8 && grain == 2) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) r.w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(src)[i] << (16 * (i & 1));
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < live) r.w[i / 4] |= (uint32_t)src[i] << (8 * (i & 3));
+        for (int i = 0; i < 8; ++i) {
+            if (i >= live) continue;
+            if constexpr (kSize == 4) r.w[i] = reinterpret_cast<const uint32_t *>(src)[i];
+            else if constexpr (kSize == 2) r.w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(src)[i] << (16 * (i & 1));
+            else r.w[i / 4] |= (uint32_t)src[i] << (8 * (i & 3));
+        }
     }
     return r;
 }
 // the upper halves of a and b
 __device__ __forceinline__ uint32_t upper(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
 // bf16 values of 8-bit codes, i and i + 4 side by side
-template <int kType> __device__ __forceinline__ uint4 side_by_side(const Raw &r) {
+template <int kType> __device__ __forceinline__ uint4 side_by_side(const uint4 &r) {
     float v[8];
-    decode4<kType>(r.w[0], v);
-    decode4<kType>(r.w[1], v + 4);
+    decode4<kType>(r.x, v);
+    decode4<kType>(r.y, v + 4);
     return make_uint4(upper(__float_as_uint(v[0]), __float_as_uint(v[4])), upper(__float_as_uint(v[1]), __float_as_uint(v[5])),
                       upper(__float_as_uint(v[2]), __float_as_uint(v[6])), upper(__float_as_uint(v[3]), __float_as_uint(v[7])));
 }
@@ -147,7 +142,10 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
     constexpr int kPitch = pitch(kShared, kWhole), kStageBytes = kRows * kPitch, kXPitch = x_pitch(kCols, kShared);
     constexpr int kFlushes = 4 / kShared, kScales = kChunk * kFlushes;  // of a step, of a chunk
     constexpr int kScaleLine = scale_line(kCols);
-    constexpr int kItems = kCols * kChunk / 2;                          // eights of x that a thread brings of a chunk
+    // eights of x that a thread brings of a chunk, and of them in fp32, which take two registers' places
+    constexpr int kEights = kChunk * 16, kNext = kThreads / kEights;
+    constexpr int kItems = kCols * 8 / kNext, kItems32 = (kCols * 8 / 3 - 1) / kNext + 1;
+    constexpr int kRaw = kItems > 2 * kItems32 ? kItems : 2 * kItems32;
     constexpr bool kOwn = kWhole && kShared == 4;                       // a lane reads the codes that it copied itself
     const ssd_matvec4_params &p = plan.p;
     const int thread = kept(threadIdx.x), lane = thread & 31, g = lane >> 2, t = lane & 3;
@@ -232,7 +230,6 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
     const int scale_f = thread % kScales, scale_row = thread / kScales;         // the first scale that the thread brings
     const int scale_rows = (int)min((int64_t)outs_now, p.out_features - o_tile);
     // eights of x that the thread brings: one place in the chunk, of every kNext-th row
-    constexpr int kEights = kChunk * 16, kNext = kThreads / kEights;
     const int x_e = thread % kEights, x_row = thread / kEights;
     const uint8_t *const x_src = static_cast<const uint8_t *>(p.x) + (int64_t)(r0 + x_row) * p.x_stride * x_elem;
     const int64_t x_next = (int64_t)kNext * p.x_stride * x_elem;
@@ -240,9 +237,10 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
         static_cast<const uint8_t *>(p.scale) + (o_tile + scale_row) * plan.groups * (p.scale_dtype == SSD_F32 ? 4 : 2);
     const uint8_t *const zero_src = kZero ? p.zero + (o_tile + scale_row) * plan.groups : nullptr;
     const int scale_next = kThreads / kScales;
-    Raw x_raw[kItems];
+    uint4 x_raw[kRaw];          // item i at i, or in fp32 at 2 i and 2 i + 1
     uint32_t scale_raw[kScales], zero_raw[kScales];
-    float xs_raw = 0.f;
+    constexpr int kXScales = (kScales * kCols * 8 - 1) / kThreads + 1;
+    float xs_raw[kXScales];
     auto bring = [&](int c) {
         {
             const int block = c * kChunk * 4 + x_e / 4;
@@ -254,19 +252,35 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
             }
             const uint8_t *from = x_src + (int64_t)k * x_elem;
             const bool wide = live == 8 && x_grain == 16;
+            if (x_elem == 4) {
 #pragma unroll
-            for (int i = 0; i < kItems; ++i, from += x_next) {
-                uint4 *const to = reinterpret_cast<uint4 *>(x_raw[i].w);
-                x_raw[i] = Raw{};
-                if (x_row + i * kNext >= rows || live == 0) continue;
-                if (!wide) {
-                    x_raw[i] = load8(from, x_elem, live, x_grain);
-                } else if (x_elem == 1) {
-                    const uint2 v = *reinterpret_cast<const uint2 *>(from);
-                    to[0] = make_uint4(v.x, v.y, 0, 0);
-                } else {
-                    to[0] = *reinterpret_cast<const uint4 *>(from);
-                    if (x_elem == 4) to[1] = *reinterpret_cast<const uint4 *>(from + 16);
+                for (int i = 0; i < kItems32; ++i, from += x_next) {
+                    x_raw[2 * i] = x_raw[2 * i + 1] = make_uint4(0, 0, 0, 0);
+                    if (x_row + i * kNext >= rows || live == 0) continue;
+                    if (wide) {
+                        x_raw[2 * i] = *reinterpret_cast<const uint4 *>(from);
+                        x_raw[2 * i + 1] = *reinterpret_cast<const uint4 *>(from + 16);
+                    } else {
+                        const Raw r = load8<4>(from, live, x_grain);
+                        x_raw[2 * i] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+                        x_raw[2 * i + 1] = make_uint4(r.w[4], r.w[5], r.w[6], r.w[7]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kItems; ++i, from += x_next) {
+                    x_raw[i] = make_uint4(0, 0, 0, 0);
+                    if (x_row + i * kNext >= rows || live == 0) continue;
+                    if (!wide) {
+                        const Raw r = x_elem == 2 ? load8<2>(from, live, x_grain) : load8<1>(from, live, x_grain);
+                        x_raw[i] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+                    } else if (x_elem == 2) {
+                        x_raw[i] = *reinterpret_cast<const uint4 *>(from);
+                    } else {
+                        const uint2 v = *reinterpret_cast<const uint2 *>(from);
+                        x_raw[i].x = v.x;
+                        x_raw[i].y = v.y;
+                    }
                 }
             }
         }
@@ -292,37 +306,41 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
                     if (scale_row + i * scale_next < scale_rows) zero_raw[i] = *from;
             }
         }
-        if (x8 && thread < kScales * kCols * 8) {
-            const int col = thread % (kCols * 8), block = min(c * kChunk * 4 + thread / (kCols * 8) * kShared, plan.blocks - 1);
-            const int group = group_of(block, plan.x_group_blocks, plan.x_group_magic);
-            xs_raw = col < rows ? p.x_scale[(int64_t)(r0 + col) * plan.x_groups + group] : 0.f;
-        }
+        if (x8)
+#pragma unroll
+            for (int i = 0; i < kXScales; ++i) {
+                const int item = thread + i * kThreads, col = item % (kCols * 8), f = item / (kCols * 8);
+                xs_raw[i] = 0.f;
+                if (f >= kScales || col >= rows) continue;
+                const int group = group_of(min(c * kChunk * 4 + f * kShared, plan.blocks - 1), plan.x_group_blocks, plan.x_group_magic);
+                xs_raw[i] = p.x_scale[(int64_t)(r0 + col) * plan.x_groups + group];
+            }
     };
     auto put_away = [&](int buffer) {
         // values i and i + 4 side by side, as the codes of a word come; eights of a step
         // in the order in which quad lane t reads its j-th word: 4 j + t
         const int place = kOwn ? (x_e & ~15) | (x_e & 3) << 2 | (x_e >> 2 & 3) : x_e;
         uint8_t *const xs = smem + plan.off_x + buffer * (plan.x_rows * kXPitch) + x_row * kXPitch + place * 16;
-        auto each = [&](auto store) {
+        auto each = [&](auto eight) {
 #pragma unroll
             for (int i = 0; i < kItems; ++i)
-                if (x_row + i * kNext < rows) store(reinterpret_cast<uint4 *>(xs + i * kNext * kXPitch), x_raw[i]);
+                if (x_row + i * kNext < rows) *reinterpret_cast<uint4 *>(xs + i * kNext * kXPitch) = eight(x_raw[i]);
         };
         if (p.x_dtype == SSD_BF16) {
-            each([](uint4 *to, const Raw &raw) {
-                *to = make_uint4(__byte_perm(raw.w[0], raw.w[2], 0x5410), upper(raw.w[0], raw.w[2]),
-                                 __byte_perm(raw.w[1], raw.w[3], 0x5410), upper(raw.w[1], raw.w[3]));
+            each([](const uint4 &r) {
+                return make_uint4(__byte_perm(r.x, r.z, 0x5410), upper(r.x, r.z), __byte_perm(r.y, r.w, 0x5410), upper(r.y, r.w));
             });
         } else if (p.x_dtype == SSD_E4M3) {
-            each([](uint4 *to, const Raw &raw) { *to = side_by_side<SSD_E4M3>(raw); });
+            each([](const uint4 &r) { return side_by_side<SSD_E4M3>(r); });
         } else if (p.x_dtype == SSD_I8) {
-            each([](uint4 *to, const Raw &raw) { *to = side_by_side<SSD_I8>(raw); });
+            each([](const uint4 &r) { return side_by_side<SSD_I8>(r); });
         } else {
-            const int next_part = rows * (kXPitch / 16);
-            each([next_part](uint4 *to, const Raw &raw) {
-                float v[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(raw.w[j]);
+            for (int i = 0; i < kItems32; ++i) {
+                if (x_row + i * kNext >= rows) continue;
+                const uint4 lo = x_raw[2 * i], hi = x_raw[2 * i + 1];
+                float v[8] = {__uint_as_float(lo.x), __uint_as_float(lo.y), __uint_as_float(lo.z), __uint_as_float(lo.w),
+                              __uint_as_float(hi.x), __uint_as_float(hi.y), __uint_as_float(hi.z), __uint_as_float(hi.w)};
 #pragma unroll
                 for (int part = 0; part < 3; ++part) {
                     uint32_t u[8];
@@ -332,9 +350,10 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
                         const float cut = __uint_as_float(u[j] & 0xffff0000u);
                         v[j] = fabsf(cut) < __int_as_float(0x7f800000) ? v[j] - cut : 0.f;
                     }
-                    to[part * next_part] = make_uint4(upper(u[0], u[4]), upper(u[1], u[5]), upper(u[2], u[6]), upper(u[3], u[7]));
+                    *reinterpret_cast<uint4 *>(xs + (i * kNext + part * rows) * kXPitch) =
+                        make_uint4(upper(u[0], u[4]), upper(u[1], u[5]), upper(u[2], u[6]), upper(u[3], u[7]));
                 }
-            });
+            }
         }
         float *const scales = reinterpret_cast<float *>(smem + plan.off_scale) + (buffer * kScales + scale_f) * kScaleLine + scale_row;
         uint32_t *const zeros = reinterpret_cast<uint32_t *>(smem + plan.off_zero) + (buffer * kScales + scale_f) * kScaleLine + scale_row;
@@ -352,8 +371,11 @@ __global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(cons
                 if (scale_row + i * scale_next < scale_rows)
                     zeros[i * scale_next] = (__float_as_uint((float)zero_raw[i] * -0.015625f) >> 16) * 0x00010001u;
         }
-        if (x8 && thread < kScales * kCols * 8)
-            reinterpret_cast<float *>(smem + plan.off_xs)[buffer * (kScales * kCols * 8) + thread] = xs_raw;
+        if (x8)
+#pragma unroll
+            for (int i = 0; i < kXScales; ++i)
+                if (thread + i * kThreads < kScales * kCols * 8)
+                    reinterpret_cast<float *>(smem + plan.off_xs)[buffer * (kScales * kCols * 8) + thread + i * kThreads] = xs_raw[i];
     };
 
     bring(chunk0);
