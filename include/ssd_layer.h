@@ -91,21 +91,22 @@ ssd_status ssd_residual_norm(const ssd_residual_norm_params *params, struct CUst
  * (k even) or high (k odd) half of byte k / 2 of the row.  x is fp32 or bf16, or
  * 8-bit codes times x_scale[r, k / x_group] (what ssd_residual_norm leaves).
  * All arithmetic is in fp32, each output is rounded once; a group's columns may be
- * added before their scale is applied (15 |x| group_size has to be a fp32 number).
- * It is made for few rows: more of them are computed as exactly, and read the
- * weights again.
+ * added before their scale is applied (15 |x| group_size has to be a fp32 number,
+ * scales are below 2^121).  It is made for few rows: more of them are computed as
+ * exactly, and read the weights again (once for every 32 rows, 10 of fp32).
  * Layouts:
  *   x       [rows, in_features] x_dtype, row stride x_stride elements
  *   x_scale [rows, ceil(in_features / x_group)] fp32, dense (8-bit x alone)
  *   weight  [out_features, ceil(in_features / 2)] bytes, row stride weight_stride
  *   scale   [out_features, ceil(in_features / group_size)] scale_dtype, dense
- *   zero    the same, one byte each, dense, values 0 .. 15 (or NULL)
+ *   zero    the same, one byte each, dense (or NULL)
  *   bias    [out_features] out_dtype (or NULL)
  *   out     [rows, out_features] out_dtype, row stride out_stride elements
- * Any in_features and group_size are computed; rows of whole 16 bytes (in_features
- * a multiple of 32, weight and weight_stride of 16) and groups of a multiple of 32
- * columns take the tensor cores.  in_features and out_features up to 2^30
- * (SSD_ERR_UNSUPPORTED above), and rows whose tiles a grid holds (500,000).    */
+ * Any in_features, group_size and x_group are computed.  The tensor cores take even
+ * group sizes from 16 on (and x_group a multiple of 32 with group_size, or equal to
+ * it, or a row); multiples of 32 without waste, and fastest rows of whole 16 bytes.
+ * in_features and out_features up to 2^30 (SSD_ERR_UNSUPPORTED above), and rows
+ * whose tiles a grid holds (500,000).                                       */
 typedef struct {
     int32_t rows;
     int32_t in_features;

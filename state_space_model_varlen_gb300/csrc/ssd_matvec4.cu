@@ -107,7 +107,8 @@ __global__ void __launch_bounds__(32 * kAnyWarps) matvec4_any_kernel(const ssd_m
         }
 }
 
-cudaError_t launch_any(const ssd_matvec4_params &p, cudaStream_t stream) {
+cudaError_t launch_any(ssd_matvec4_params p, cudaStream_t stream) {
+    if (p.x_dtype <= SSD_BF16) p.x_scale = nullptr;
     const int per = kAnyWarps * kOuts;
     const dim3 grid((p.out_features - 1) / per + 1, (p.rows - 1) / kAnyRows + 1);
     if (grid.y > 65535) return cudaErrorInvalidConfiguration;
@@ -150,7 +151,7 @@ bool make_plan(const ssd_matvec4_params &p, Matvec4Plan &q, int &cols, int &shar
     shared = gcd(4, gcd(q.groups == 1 ? 4 : q.group_blocks, q.x_groups == 1 ? 4 : q.x_group_blocks));
     whole = unbroken && K % 32 == 0 && p.weight_stride % 16 == 0 && aligned_to(p.weight, 16);
     cols = 1;
-    while (cols < 8 && cols * 8 < p.rows * parts) cols *= 2;
+    while (cols < 4 && cols * 8 < p.rows * parts) cols *= 2;
     q.row_tile = cols * 8 / parts < p.rows ? cols * 8 / parts : p.rows;
     q.x_rows = q.row_tile * parts;
     if ((p.rows - 1) / q.row_tile + 1 > 65535) return false;
@@ -176,7 +177,7 @@ bool make_plan(const ssd_matvec4_params &p, Matvec4Plan &q, int &cols, int &shar
     // about so many instructions of a warp; eight warps of an SM take a step in four
     // times as many clocks, 16 in seven; a chunk's x and scales take 800, a CTA begins
     // and ends in 5,000, in a cluster 7,000 (measured).
-    const int fit = kSmemLimit / (q.smem + 1024), resident = fit < 1 ? 1 : fit < ctas(cols) ? fit : ctas(cols);
+    const int fit = kSmemLimit / (q.smem + 1024), resident = fit < 1 ? 1 : fit < kCtas ? fit : kCtas;
     const int passes = (p.rows - 1) / q.row_tile + 1;
     const int work = 250 + 16 * cols + per_step * (20 + 12 * cols);
     const int chunks = (q.steps - 1) / steps_of_chunk + 1;
@@ -208,8 +209,7 @@ cudaError_t launch_matvec4(const ssd_matvec4_params &p, cudaStream_t stream) {
     if (!make_plan(p, q, cols, shared, whole)) return launch_any(p, stream);
     return cols == 1   ? launch_matvec4_cols1(q, shared, whole, stream)
            : cols == 2 ? launch_matvec4_cols2(q, shared, whole, stream)
-           : cols == 4 ? launch_matvec4_cols4(q, shared, whole, stream)
-                       : launch_matvec4_cols8(q, shared, whole, stream);
+                       : launch_matvec4_cols4(q, shared, whole, stream);
 }
 
 }  // namespace ssd

@@ -38,20 +38,19 @@ struct Matvec4Plan {
     int off_x, off_scale, off_zero, off_xs, smem;
 };
 
-// columns8: eights of columns of a pass (1, 2, 4, 8); shared: blocks that share their scales (1, 2, 4)
+// for passes of 8, 16 and 32 columns; shared: blocks that share their scales (1, 2, 4)
 cudaError_t launch_matvec4_cols1(const Matvec4Plan &q, int shared, bool whole, cudaStream_t stream);
 cudaError_t launch_matvec4_cols2(const Matvec4Plan &q, int shared, bool whole, cudaStream_t stream);
 cudaError_t launch_matvec4_cols4(const Matvec4Plan &q, int shared, bool whole, cudaStream_t stream);
-cudaError_t launch_matvec4_cols8(const Matvec4Plan &q, int shared, bool whole, cudaStream_t stream);
 
 namespace matvec4 {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps, kStep = 128, kSmemLimit = 227 * 1024;
-constexpr int mats(int cols) { return cols <= 4 ? 2 : 1; }          // sixteens of outputs of a warp
+constexpr int mats(int cols) { return cols <= 2 ? 2 : 1; }          // sixteens of outputs of a warp
 constexpr int chunk(int cols, int shared) { return cols == 1 && shared == 4 ? 4 : 2; }    // steps of a buffer of x and scales
 // steps of codes in the ring of a warp: what two CTAs an SM leave room for
 constexpr int stages(int shared, bool whole) { return !whole ? 2 : shared == 4 ? 4 : 3; }
-constexpr int ctas(int cols) { return cols <= 2 ? 2 : 1; }          // of an SM, for the registers
+constexpr int kCtas = 2;                                            // of an SM, for the registers
 constexpr int outs(int cols) { return kWarps * 16 * mats(cols); }   // of a tile
 constexpr int scale_line(int cols) { return outs(cols) + 4; }       // a gap: the scales of an output come from lanes side by side
 // bytes of a row of a stage: whole steps, with a gap where lanes read one another's; or two pieces a block
@@ -135,7 +134,7 @@ template <int kType> __device__ __forceinline__ uint4 side_by_side(const uint4 &
 // kCols: eights of columns (rows of x, or their parts) of a pass.  kShared: blocks that
 // certainly share their scales (1, 2, or 4: a step).
 template <int kCols, int kShared, bool kZero, bool kWhole>
-__global__ void __launch_bounds__(kThreads, ctas(kCols)) matvec4_mma_kernel(const __grid_constant__ Matvec4Plan plan) {
+__global__ void __launch_bounds__(kThreads, kCtas) matvec4_mma_kernel(const __grid_constant__ Matvec4Plan plan) {
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int kMats = mats(kCols), kRows = 16 * kMats, kOuts = outs(kCols), kChunk = chunk(kCols, kShared);
     constexpr int kStages = stages(kShared, kWhole);

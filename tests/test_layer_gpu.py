@@ -267,6 +267,52 @@ def test_matvec_large(rows, K, O):
     _mv_case(rows, K, O, 32, "f32" if rows < 20 else "e4m3", zero=True)
 
 
+@pytest.mark.parametrize("rows", [3, 12, 20, 70])
+@pytest.mark.parametrize("group", [32, 64, 128, 1 << 20, 16, 48, 50])
+@pytest.mark.parametrize("zero", [False, True])
+@pytest.mark.parametrize("K", [800, 802])
+def test_matvec_variants(rows, group, zero, K):
+    """Each number of columns of a pass, of blocks that share scales, with zeros or not, for rows of whole 16 bytes or not."""
+    _mv_case(rows, K, 300, group, "bf16", "f32", zero=zero)
+    if K % group == 0 or group > K:
+        _mv_case(rows, K, 300, group, "e4m3", "f16", zero=zero, x_group=min(group, K))
+
+
+@pytest.mark.parametrize("rows,O,K", [(1, 64, 4096), (1, 300, 8192), (4, 130, 2176), (1, 5000, 512), (16, 64, 8192), (30, 40, 4224),
+                                      (1, 40000, 640), (2, 9, 65536)])
+def test_matvec_shares_of_columns(rows, O, K):
+    """Columns shared by the warps of a CTA and by the CTAs of a cluster."""
+    for group in (128, 32):
+        _mv_case(rows, K, O, group, zero=True, bias=True)
+
+
+def test_matvec_long_rows():
+    """More columns than the tensor-core kernel counts."""
+    _mv_case(2, (1 << 20) + 64, 3, 128, "bf16", zero=True)
+
+
+def test_matvec_zeros_of_a_whole_byte():
+    torch = _torch()
+    d = Draw(6)
+    w, s, z = d.ints(0, 256, 20, 128, dtype="u8"), d.rand(20, 2), d.ints(0, 256, 20, 2, dtype="u8")
+    x = d.randn(3, 256, dtype="bf16")
+    got = layer.matvec4(x, w, s, group_size=128, zero=z, out_dtype=torch.float32)
+    want, err = R.matvec4(_np(x), w.cpu().numpy(), _np(s), z.cpu().numpy(), None, 128)
+    M.check(_np(got), want, err, "f32", "product")
+
+
+@pytest.mark.parametrize("group", [64, 25])
+def test_matvec_ignores_a_scale_of_x_that_has_none(group):
+    torch = _torch()
+    d = Draw(7)
+    x, w, s = d.randn(2, 256, dtype="bf16"), d.ints(0, 256, 20, 128, dtype="u8"), d.rand(20, -(-256 // group))
+    want, out = layer.matvec4(x, w, s, group_size=group), torch.empty(2, 20, dtype=_t("bf16"), device="cuda")
+    p = layer.make_matvec4_params(x, w, s, out, group_size=group)
+    p.x_scale, p.x_group = s.data_ptr(), 0
+    layer.call_matvec4(p, torch.cuda.current_stream().cuda_stream)
+    assert torch.equal(out, want)
+
+
 def test_matvec_weights_at_large_offsets():
     """A matrix whose rows lie more than 2^32 bytes apart from the first."""
     torch = _torch()
