@@ -182,6 +182,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) matvec4_mma_kernel(const __gr
 #pragma unroll
     for (int h = 0; h < 2 * kMats; ++h)
         src[h] = p.weight + min(o_warp + g + 8 * h, (int64_t)p.out_features - 1) * p.weight_stride;
+    const uint8_t *const last_row = p.weight + (int64_t)(p.out_features - 1) * p.weight_stride;
+    const uint8_t *const codes_end = last_row + (p.in_features + 1) / 2;
+    const uint8_t *const piece_src = p.weight + (o_warp + (lane >> 3)) * p.weight_stride;
     int to_step = step0 + turn, to_stage = 0;
     const int row_bytes = kept(p.in_features / 2), whole_steps = kept(p.in_features / kStep);
     auto issue = [&]() {
@@ -194,23 +197,26 @@ __global__ void __launch_bounds__(kThreads, kCtas) matvec4_mma_kernel(const __gr
                 for (int h = 0; h < 2 * kMats; ++h)
                     copy_async<16>(dst + (g + 8 * h) * kPitch + t * 16, src[h] + (live ? byte : 0), live);
             } else {
-                // 16 rows x 4 blocks x 2 pieces at a time; pieces that pass the matrix's ends byte by byte
-                const uint8_t *const end = p.weight + (int64_t)(p.out_features - 1) * p.weight_stride + (p.in_features + 1) / 2;
-#pragma unroll 1
-                for (int i = lane; i < kRows * 8; i += 32) {
-                    const int row = i >> 3, block = to_step * 4 + (i >> 1 & 3);
-                    uint8_t *const to = dst + row * kPitch + (i & 7) * 16;
-                    if (block >= plan.blocks) {
-                        *reinterpret_cast<uint4 *>(to) = make_uint4(0, 0, 0, 0);
-                        continue;
-                    }
+                // 4 rows x 4 blocks x 2 pieces at a time; pieces that pass the matrix's ends byte by byte
+                const int block = to_step * 4 + (lane >> 1 & 3);
+                uint8_t *to = dst + (lane >> 3) * kPitch + (lane & 7) * 16;
+                if (block >= plan.blocks) {
+#pragma unroll
+                    for (int i = 0; i < kRows / 4; ++i, to += 4 * kPitch) *reinterpret_cast<uint4 *>(to) = make_uint4(0, 0, 0, 0);
+                } else {
                     int stop;
-                    const uint8_t *from = p.weight + min(o_warp + row, (int64_t)p.out_features - 1) * p.weight_stride + columns(block, stop) / 2;
-                    from += (i & 1) * 16 - (int)(reinterpret_cast<uintptr_t>(from) & 15);
-                    if (from >= p.weight && from + 16 <= end) {
-                        copy_async<16>(to, from, true);
-                    } else {
-                        for (int b = 0; b < 16; ++b) to[b] = from + b >= p.weight && from + b < end ? from[b] : 0;
+                    const int off = columns(block, stop) / 2;
+                    const uint8_t *row = piece_src + off;
+                    int64_t o = o_warp + (lane >> 3);
+#pragma unroll 4
+                    for (int i = 0; i < kRows / 4; ++i, to += 4 * kPitch, o += 4, row += 4 * p.weight_stride) {
+                        const uint8_t *from = o < p.out_features ? row : last_row + off;
+                        from += (lane & 1) * 16 - (int)(reinterpret_cast<uintptr_t>(from) & 15);
+                        if (from >= p.weight && from + 16 <= codes_end) {
+                            copy_async<16>(to, from, true);
+                        } else {
+                            for (int b = 0; b < 16; ++b) to[b] = from + b >= p.weight && from + b < codes_end ? from[b] : 0;
+                        }
                     }
                 }
             }
@@ -219,9 +225,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) matvec4_mma_kernel(const __gr
         to_stage = to_stage + 1 == kStages ? 0 : to_stage + 1;
         commit_async();
     };
-#pragma unroll 1
-    for (int q = 0; q < kStages - 1; ++q) issue();
-
     // ---- x and scales: a chunk's into registers, and from there into a buffer ----
     const int x_elem = p.x_dtype == SSD_F32 ? 4 : p.x_dtype == SSD_BF16 ? 2 : 1;
     const int x_low = (int)(reinterpret_cast<uintptr_t>(p.x) | (uintptr_t)(p.x_stride * x_elem) | (uintptr_t)(plan.padded * x_elem));
@@ -378,6 +381,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) matvec4_mma_kernel(const __gr
     };
 
     bring(chunk0);
+#pragma unroll 1
+    for (int q = 0; q < kStages - 1; ++q) issue();
     put_away(0);
     __syncthreads();
 
