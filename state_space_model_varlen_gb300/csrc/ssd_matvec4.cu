@@ -167,7 +167,7 @@ bool make_plan(const ssd_matvec4_params &p, Matvec4Plan &q, int &cols, int &shar
     q.off_x = take(2 * q.x_rows * x_pitch(cols, shared));
     q.off_scale = take(2 * scales * scale_line(cols) * 4);
     q.off_zero = take(p.zero ? 2 * scales * scale_line(cols) * 4 : 0);
-    q.off_xs = take(q.p.x_scale ? 2 * scales * cols * 8 * 4 : 0);
+    q.off_xs = take(q.x_groups > 1 ? 2 * scales * cols * 8 * 4 : 0);
     q.smem = at;
     const int sums = (outs(cols) + 16) * q.x_rows * 4;
     if (q.smem < sums) q.smem = sums;

@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) matvec4_mma_kernel(const __gr
     const int o_first = (kChunk > 1 ? warp / ways : warp) * kRows;     // of the warp's in the tile
     const int64_t o_tile = (int64_t)tile * outs_now, o_warp = o_tile + o_first;
     const bool busy = o_warp < p.out_features;                          // the warp has outputs
-    const bool x8 = p.x_scale != nullptr;
+    const bool x8 = p.x_scale != nullptr && plan.x_groups > 1;          // one scale of a whole row is applied at the end
     uint8_t *const ring = smem + warp * (kStages * kStageBytes);
     await_previous();
 
@@ -532,6 +532,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) matvec4_mma_kernel(const __gr
                 v += f;
             }
         }
+        if (p.x_scale != nullptr && plan.x_groups == 1) v *= p.x_scale[r0 + r];
         const int64_t at = (int64_t)(r0 + r) * p.out_stride + o_tile + o;
         if (p.out_dtype == SSD_F32) {
             if (p.bias) v += static_cast<const float *>(p.bias)[o_tile + o];
