@@ -7,11 +7,24 @@
 // of eight bits each, which together are exact.  Sums within a group are the
 // instruction's fp32 sums; the groups' scales, times 64, are applied to them in fp32.
 //
-// Bound by HBM for few rows: codes stream through a ring of asynchronous copies of
-// each warp's own, a few steps deep.  x and the scales come through two buffers in
-// shared memory, a chunk of steps ahead in registers.  Where there are few tiles the
-// two or four warps take the steps of the same outputs in turn, and a cluster of CTAs
-// shares a tile's columns; the parts are added in a fixed order.
+// Bound by HBM in principle, by instructions in fact: of about 300 a step of 32
+// outputs x 128 columns 160 unpack the codes, 16 are products, and with the loop's the
+// integer pipe takes most of the time (the unpacking and the products alone ran at 8.1
+// TB/s of codes with 8 warps an SM).  Codes stream through a ring of asynchronous copies
+// of each warp's own, a few steps deep.  x and the scales come through two buffers in
+// shared memory, a chunk of steps ahead in registers.  Where there are few tiles two or
+// four warps take the steps of the same outputs in turn, and a cluster of CTAs shares a
+// tile's columns; the parts are added in a fixed order.
+//
+// Measured (floor at the copy rate): 1 row of 4,096 to 18,560 outputs, groups of 128,
+// 12.1 us (5.8); 3 rows of 4,096 to 131,072 62.6 us (41); 16 rows of 2,560 to 10,576,
+// groups of 32 with zeros, 18.4 us (2.4: scales and zeros take as many instructions as the
+// products).  Rows of 4,102 columns, which no 16-byte copy takes whole, 29 us where rows
+// of 4,096 take 12; 32 rows 29 us, 64 rows 49.  Before: tiles of 32 outputs whose columns
+// eight warps shared, all of x in shared memory (head 63 us; 22 to 29 us where x of many
+// rows left one CTA an SM, and whole rows alone); codes shifted to the mantissa's end and
+// 128 + zero subtracted (three shifts a word for one: 73 for 69 us); 64 columns a pass
+// with one CTA an SM (64 rows 56 for 51 us).
 //
 // A group of columns is taken in blocks of 32; a group of another size, or a row's
 // end, leaves the last block's x partly zero.  Rows of codes in whole 16 bytes are

