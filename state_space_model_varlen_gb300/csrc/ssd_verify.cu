@@ -40,6 +40,11 @@ struct Sum {
         c += ((s - (t - b)) + (v - b)) + rest;
         s = t;
     }
+    __device__ void add(float v) {
+        const float t = s + v, b = t - s;
+        c += (s - (t - b)) + (v - b);
+        s = t;
+    }
     __device__ void add(const Sum &o) { add(o.s, o.c); }
     __device__ bool above(const Sum &o) const { return (s - o.s) + (c - o.c) > 0.f; }
 };
@@ -129,16 +134,34 @@ template <typename T> struct Weights {
         }
         return v;
     }
-    __device__ float2 of(const Vector &v, int t, int i) const {
-        return of(to_float(v.a.v[i]), to_float(v.b.v[i]), t + i == without);
-    }
-    __device__ void add(Sum &sum, const Vector &v, int t) const {
+    // The same sums for numbers that are finite, which is seen from the sum; others one by one.
+    __device__ void add(Sum &sum, Vector v, int t) const {
         if (!v.live) return;
+        if ((unsigned)(without - t) < (unsigned)N) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float2 f = of(v, t, i);
-            sum.add(f.x, f.y);
+            for (int i = 0; i < N; ++i)
+                if (t + i == without) v.a.v[i] = from_float<T>(0.f);
         }
+        Sum now = sum;
+        if (q) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float a = to_float(v.a.v[i]), b = to_float(v.b.v[i]), d = a - b;
+                now.add(fmaxf(d, 0.f), d > 0.f ? (a - d) - b : 0.f);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) now.add(fmaxf(to_float(v.a.v[i]), 0.f));
+        }
+        if (!(now.s < __int_as_float(0x7f800000))) {
+            now = sum;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float2 f = of(to_float(v.a.v[i]), to_float(v.b.v[i]), false);
+                now.add(f.x, f.y);
+            }
+        }
+        sum = now;
     }
 };
 
