@@ -134,14 +134,9 @@ template <typename T> struct Weights {
         }
         return v;
     }
-    // The same sums for numbers that are finite, which is seen from the sum; others one by one.
-    __device__ void add(Sum &sum, Vector v, int t) const {
+    // Adds them, fast where they are finite, which is seen from the sum; else one by one.
+    __device__ void add(Sum &sum, const Vector &v, int t, int lo, int hi) const {
         if (!v.live) return;
-        if ((unsigned)(without - t) < (unsigned)N) {
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (t + i == without) v.a.v[i] = from_float<T>(0.f);
-        }
         Sum now = sum;
         if (q) {
 #pragma unroll
@@ -153,15 +148,16 @@ template <typename T> struct Weights {
 #pragma unroll
             for (int i = 0; i < N; ++i) now.add(fmaxf(to_float(v.a.v[i]), 0.f));
         }
-        if (!(now.s < __int_as_float(0x7f800000))) {
-            now = sum;
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const float2 f = of(to_float(v.a.v[i]), to_float(v.b.v[i]), false);
-                now.add(f.x, f.y);
-            }
-        }
+        if (!(now.s < __int_as_float(0x7f800000)) || (unsigned)(without - t) < (unsigned)N) now = careful(*this, sum, t, lo, hi);
         sum = now;
+    }
+    static __device__ __noinline__ Sum careful(const Weights w, Sum sum, int t, int lo, int hi) {
+#pragma unroll 1
+        for (int i = max(t, lo); i < min(t + N, hi); ++i) {
+            const float2 f = of(to_float(w.p[i]), w.q ? to_float(w.q[i]) : 0.f, i == w.without);
+            sum.add(f.x, f.y);
+        }
+        return sum;
     }
 };
 
@@ -250,7 +246,7 @@ __device__ int search(const Weights<T> &w, int base, int blocks, int lo, int hi,
 #pragma unroll
         for (int i = 0; i < kVectors; ++i) v[i] = w.load(base + lane * kRun + i * N, lo, hi, alike);
 #pragma unroll
-        for (int i = 0; i < kVectors; ++i) w.add(mine, v[i], base + lane * kRun + i * N);
+        for (int i = 0; i < kVectors; ++i) w.add(mine, v[i], base + lane * kRun + i * N, lo, hi);
         const Sum upto = scan(mine);
         Sum limit = goal, ahead = before;
         const int at = owner_of(mine, upto, 32, limit, ahead);
@@ -301,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 1 : 1024 / kThread
 #pragma unroll
                 for (int e = 0; e < kVectors; ++e) v[e] = w.load(at + e * 32 * N, lo, hi, alike);
 #pragma unroll
-                for (int e = 0; e < kVectors; ++e) w.add(here, v[e], at + e * 32 * N);
+                for (int e = 0; e < kVectors; ++e) w.add(here, v[e], at + e * 32 * N, lo, hi);
             }
             snaps[i][threadIdx.x] = make_float2(here.s, here.c);
             sum.add(here);
