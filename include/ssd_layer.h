@@ -23,7 +23,7 @@
  * graph.  Invalid arguments return an error status and launch nothing; every
  * pointer must be aligned to its element type, else SSD_ERR_INVALID_ARG.
  * Outputs must not overlap inputs or one another unless it is said that they
- * may.  Results do not depend on how often or beside what a call runs.
+ * may.  The same call gives the same bits each time, whatever runs beside it.
  */
 #ifndef SSD_LAYER_H_
 #define SSD_LAYER_H_

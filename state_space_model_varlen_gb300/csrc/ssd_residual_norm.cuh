@@ -130,10 +130,31 @@ template <typename T, int V> __device__ __forceinline__ Pack<T, V> packed(const 
 constexpr int kRowThreads = 128;        // of a CTA that takes a row a warp
 template <int V> constexpr int kMost = V == 1 ? 1024 : 512;     // of one that takes one row: what the registers allow
 
+// V values from column c on, or those of them that the row has; and back
+template <bool kShift, typename T, int V> __device__ __forceinline__ Pack<T, V> get(const T *row, int c, int columns) {
+    if (!kShift || (c >= 0 && c + V <= columns)) return load_pack<T, V>(row + c);
+    Pack<T, V> p{};
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+        if (c + j >= 0 && c + j < columns) p.v[j] = row[c + j];
+    return p;
+}
+template <bool kShift, typename T, int V> __device__ __forceinline__ void put(T *row, int c, int columns, const Pack<T, V> &p) {
+    if (!kShift || (c >= 0 && c + V <= columns)) {
+        store_pack<T, V>(row + c, p);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+        if (c + j >= 0 && c + j < columns) row[c + j] = p.v[j];
+}
+
 // kWarp: a warp takes a row, else the CTA does; C: vectors of a thread at most.
-template <typename IoT, typename ResT, int V, bool kWarp, int C, bool kCodes>
+// kShift: rows that begin anywhere, all alike: `first` + row stride elements behind a
+// boundary of V; the vectors begin at the boundary, and the weights come one by one.
+template <typename IoT, typename ResT, int V, bool kWarp, int C, bool kCodes, bool kShift = false>
 __global__ void __launch_bounds__(kWarp ? kRowThreads : kMost<V>)
-    residual_norm_kernel(const ssd_residual_norm_params a, int lanes) {
+    residual_norm_kernel(const ssd_residual_norm_params a, int lanes, int first) {
     extern __shared__ float most[];     // largest magnitude of a vector, then inv of a group
     __shared__ float part[32];
     constexpr int kPairs = (V + 1) / 2;
@@ -142,23 +163,35 @@ __global__ void __launch_bounds__(kWarp ? kRowThreads : kMost<V>)
     const int64_t number = kWarp ? (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
     if (kWarp && number >= a.rows) return;
     const Row<IoT, ResT> row(a, number);
+    const int shift = kShift ? (int)((first + number * a.x_stride) % V) : 0;
+    auto column = [&](int k) { return (k * team + id) * V - shift; };
     Pack<IoT, V> x[C], w[C];
     Pack<ResT, V> res[C];
 #pragma unroll
     for (int k = 0; k < C; ++k) {
-        const int c = (k * team + id) * V;
+        const int c = column(k);
         x[k] = w[k] = Pack<IoT, V>{};
         res[k] = Pack<ResT, V>{};
         if (c < a.columns) {
-            x[k] = load_pack<IoT, V>(row.x + c);
-            if (row.res) res[k] = load_pack<ResT, V>(row.res + c);
+            x[k] = get<kShift, IoT, V>(row.x, c, a.columns);
+            if (row.res) res[k] = get<kShift, ResT, V>(row.res, c, a.columns);
         }
     }
     // weights ahead of the sum too, unless they would take single elements a register each
+    auto weights = [&](int k) {
+        const int c = column(k);
+        if (!row.w || c >= a.columns) return;
+        if constexpr (kShift) {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (c + j >= 0 && c + j < a.columns) w[k].v[j] = row.w[c + j];
+        } else {
+            w[k] = load_pack<IoT, V>(row.w + c);
+        }
+    };
     if constexpr (V > 1)
 #pragma unroll
-        for (int k = 0; k < C; ++k)
-            if (row.w && (k * team + id) * V < a.columns) w[k] = load_pack<IoT, V>(row.w + (k * team + id) * V);
+        for (int k = 0; k < C; ++k) weights(k);
     float2 v[C][kPairs], two = make_float2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < C; ++k) {
@@ -174,13 +207,13 @@ __global__ void __launch_bounds__(kWarp ? kRowThreads : kMost<V>)
     if (row.res_out)
 #pragma unroll
         for (int k = 0; k < C; ++k)
-            if ((k * team + id) * V < a.columns) store_pack<ResT, V>(row.res_out + (k * team + id) * V, packed<ResT, V>(v[k]));
+            if (column(k) < a.columns) put<kShift, ResT, V>(row.res_out, column(k), a.columns, packed<ResT, V>(v[k]));
     const float sum = kWarp ? warp_sum(two.x + two.y) : cta_sum(two.x + two.y, part);
     const float r = 1.f / sqrtf(sum / (float)a.columns + a.eps);
 #pragma unroll
     for (int k = 0; k < C; ++k) {
-        const int c = (k * team + id) * V;
-        if (V == 1 && row.w && c < a.columns) w[k] = load_pack<IoT, V>(row.w + c);
+        const int c = column(k);
+        if constexpr (V == 1) weights(k);
         float2 f[kPairs];
         unpack<IoT, V>(w[k], f);
 #pragma unroll
@@ -188,7 +221,7 @@ __global__ void __launch_bounds__(kWarp ? kRowThreads : kMost<V>)
             v[k][j] = mul2(v[k][j], make_float2(r, r));
             if (row.w) v[k][j] = mul2(v[k][j], f[j]);
         }
-        if (row.out && c < a.columns) store_pack<IoT, V>(row.out + c, packed<IoT, V>(v[k]));
+        if (row.out && c < a.columns) put<kShift, IoT, V>(row.out, c, a.columns, packed<IoT, V>(v[k]));
     }
     if constexpr (kCodes) {
         const int G = a.scale_group, per = G / V;       // vectors of a group
@@ -257,28 +290,28 @@ __global__ void __launch_bounds__(kWarp ? kRowThreads : kMost<V>)
     }
 }
 
-template <typename IoT, typename ResT, int V, bool kCodes>
-cudaError_t launch_row(const ssd_residual_norm_params &p, cudaStream_t stream, bool *taken) {
-    const int vectors = p.columns / V, per = kCodes ? p.scale_group / V : 1;
+template <typename IoT, typename ResT, int V, bool kCodes, bool kShift = false>
+cudaError_t launch_row(const ssd_residual_norm_params &p, cudaStream_t stream, bool *taken, int first = 0) {
+    const int vectors = kShift ? (p.columns + V - 2) / V + 1 : p.columns / V, per = kCodes ? p.scale_group / V : 1;
     const bool shuffled = per <= 32 && (per & (per - 1)) == 0;
     const int lanes = kCodes && shuffled ? per : 0;
     const size_t entries = kCodes && !shuffled ? (size_t)vectors + p.columns / p.scale_group : 0;
     auto go = [&](auto kernel, int64_t ctas, int threads, size_t rows) {
         if (ctas > 0x7fffffffLL || rows * entries * 4 > 48 * 1024) return cudaErrorInvalidConfiguration;
         *taken = true;
-        return enqueue_shared(kernel, dim3((unsigned)ctas), threads, rows * entries * 4, stream, p, lanes);
+        return enqueue_shared(kernel, dim3((unsigned)ctas), threads, rows * entries * 4, stream, p, lanes, first);
     };
     constexpr int kShort = V == 1 ? 4 : 2;
     if (vectors <= 32 * kShort)
-        return go(residual_norm_kernel<IoT, ResT, V, true, kShort, kCodes>, (p.rows + 3) / 4, kRowThreads, kRowThreads / 32);
+        return go(residual_norm_kernel<IoT, ResT, V, true, kShort, kCodes, kShift>, (p.rows + 3) / 4, kRowThreads, kRowThreads / 32);
     auto whole = [&](auto kernel, int chunks) {
         return go(kernel, p.rows, 32 * ((vectors + 32 * chunks - 1) / (32 * chunks)), 1);
     };
     if constexpr (V == 1) {
         if (vectors <= kMost<V> * 10) return whole(residual_norm_kernel<IoT, ResT, V, false, 10, kCodes>, 10);
     } else {
-        if (vectors <= kMost<V> * 4) return whole(residual_norm_kernel<IoT, ResT, V, false, 4, kCodes>, 4);
-        if (vectors <= kMost<V> * 8) return whole(residual_norm_kernel<IoT, ResT, V, false, 8, kCodes>, 8);
+        if (vectors <= kMost<V> * 4) return whole(residual_norm_kernel<IoT, ResT, V, false, 4, kCodes, kShift>, 4);
+        if (vectors <= kMost<V> * 8) return whole(residual_norm_kernel<IoT, ResT, V, false, 8, kCodes, kShift>, 8);
     }
     return cudaErrorInvalidConfiguration;
 }
@@ -292,8 +325,18 @@ template <typename IoT, typename ResT> cudaError_t launch_norm(const ssd_residua
                (!p.out || (p.out_stride % v == 0 && aligned_to(p.out, io))) &&
                (!p.out_codes || (p.scale_group % v == 0 && p.codes_stride % v == 0 && aligned_to(p.out_codes, v)));
     };
+    // rows that all begin alike, if not at a boundary: in vectors of four from the boundary on
+    constexpr int kBeside = 4;
+    const int first = (int)(reinterpret_cast<uintptr_t>(p.x) / sizeof(IoT) % kBeside);
+    auto alike = [&](const void *q, int64_t stride, size_t size) {
+        return !q || ((int)(reinterpret_cast<uintptr_t>(q) / size % kBeside) == first &&
+                      (stride - p.x_stride) % kBeside == 0);
+    };
+    const bool beside = !p.out_codes && p.x_stride < (1LL << 40) && alike(p.residual, p.residual_stride, sizeof(ResT)) &&
+                        alike(p.residual_out, p.residual_out_stride, sizeof(ResT)) && alike(p.out, p.out_stride, sizeof(IoT));
     bool taken = false;
     cudaError_t e;
+    auto shifted = [&] { return launch_row<IoT, ResT, kBeside, false, true>(p, stream, &taken, first); };
     auto row = [&](auto width) {
         constexpr int V = decltype(width)::value;
         return p.out_codes ? launch_row<IoT, ResT, V, true>(p, stream, &taken) : launch_row<IoT, ResT, V, false>(p, stream, &taken);
@@ -301,9 +344,10 @@ template <typename IoT, typename ResT> cudaError_t launch_norm(const ssd_residua
     if constexpr (sizeof(IoT) == 2) {
         e = can(8)   ? row(std::integral_constant<int, 8>())
             : can(4) ? row(std::integral_constant<int, 4>())
+            : beside ? shifted()
                      : row(std::integral_constant<int, 1>());
     } else {
-        e = can(4) ? row(std::integral_constant<int, 4>()) : row(std::integral_constant<int, 1>());
+        e = can(4) ? row(std::integral_constant<int, 4>()) : beside ? shifted() : row(std::integral_constant<int, 1>());
     }
     if (taken) return e;
     if (p.rows > 0x7fffffffLL) return cudaErrorInvalidConfiguration;

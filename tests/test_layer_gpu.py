@@ -146,6 +146,30 @@ def test_norm_in_place(cols, code):
     assert torch.equal(x3, (x.float() * 2).bfloat16())
 
 
+@pytest.mark.parametrize("cols", [1, 2, 3, 37, 255, 1001, 2009, 9999, 16387])
+@pytest.mark.parametrize("io,res", [("bf16", "f32"), ("f32", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("at", [0, 3])
+def test_norm_rows_that_begin_anywhere(cols, io, res, at):
+    """Odd dense rows, whose beginnings go through all alignments, also from an odd element on, out of place and in place."""
+    torch = _torch()
+    d = Draw(cols)
+    rows = 9
+    flat = lambda dtype: d.randn(rows * cols + at, dtype=dtype)[at:].view(rows, cols)      # noqa: E731
+    x, r, w = flat(io), flat(res), d.randn(cols, dtype=io)
+    out, total = torch.full_like(flat(io), 7.0), torch.full_like(flat(res), 7.0)
+    layer.residual_rms_norm(x, w, residual=r, residual_out=total, out=out)
+    (v, ev), (n, en) = R.residual_norm(_np(x), _np(r), _np(w), 1e-5)
+    M.check(_np(out), n, en, io, "norm")
+    M.check(_np(total), v, ev, res, "sum")
+    kept, kept_r = flat(io), flat(res)
+    x2, r2 = kept, kept_r
+    x2.copy_(x)
+    r2.copy_(r)
+    layer.residual_rms_norm(x2, w, residual=r2, residual_out=r2, out=x2)
+    M.check(_np(x2), n, en, io, "norm")
+    M.check(_np(r2), v, ev, res, "sum")
+
+
 @pytest.mark.parametrize("cols,group", [(64, 32), (4096, 128), (4096, 4096), (3100, 100), (70000, 100)])
 @pytest.mark.parametrize("code", ["e4m3", "i8"])
 def test_norm_special_values(cols, group, code):
