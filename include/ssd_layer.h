@@ -146,7 +146,7 @@ ssd_status ssd_matvec4(const ssd_matvec4_params *params, struct CUstream_st *str
  *   new = the lowest token t whose w[0] + .. + w[t] > sample_u[s] (w[0] + .. + w[V-1])
  *
  * which leaves tokens distributed as the target's where the random numbers are
- * uniform in [0, 1) (values outside count as the nearest end).  Products,
+ * uniform in [0, 1) (values outside count as the nearest end, NaN as 0).  Products,
  * differences and comparisons are exact, the sums are kept to about 2^-44 of the
  * total.  Entries of w that are not positive and finite count as zero; where none
  * is left, new is -1 and SSD_DEV_BAD_PROBS is set.  Rows need not sum to one.
