@@ -31,6 +31,9 @@
 // copied as they are (kWhole); of others the two 16-byte pieces that hold a block are,
 // and its bytes are picked out of them.
 #pragma once
+
+#include <type_traits>
+
 #include "ssd_layer_internal.h"
 #include "ssd_mixer_common.cuh"
 
@@ -531,29 +534,52 @@ __global__ void __launch_bounds__(kThreads, kCtas) matvec4_mma_kernel(const __gr
             }
     if (plan.split > 1) cluster_barrier();
     else __syncthreads();
+    // four outputs of a row at a time
     const uint32_t local = (uint32_t)__cvta_generic_to_shared(own);
-    for (int i = rank * kThreads + thread; i < rows * outs_now; i += plan.split * kThreads) {
-        const int r = i / outs_now, o = i % outs_now;
-        if (o_tile + o >= p.out_features) continue;
-        float v = 0.f;
+    const int fours = outs_now / 4, log_fours = __ffs(fours) - 1;
+    const bool out_wide = p.out_stride % 4 == 0 && reinterpret_cast<uintptr_t>(p.out) % (p.out_dtype == SSD_F32 ? 16 : 8) == 0;
+    for (int i = rank * kThreads + thread; i < rows * fours; i += plan.split * kThreads) {
+        const int r = i >> log_fours, o = (i & (fours - 1)) * 4;
+        const int live = (int)min((int64_t)4, p.out_features - o_tile - o);
+        if (live <= 0) continue;
+        float v[4] = {};
         for (int c = 0; c < plan.split; ++c) {
             uint32_t at = local + (r * line + o) * 4;
             if (plan.split > 1) asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(at), "r"(c));
             for (int part = 0; part < parts * ways; ++part) {
-                float f;
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(at + part * rows * (line * 4)) : "memory");
-                v += f;
+                float4 f;
+                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w) : "r"(at + part * rows * (line * 4)) : "memory");
+                v[0] += f.x;
+                v[1] += f.y;
+                v[2] += f.z;
+                v[3] += f.w;
             }
         }
-        if (p.x_scale != nullptr && plan.x_groups == 1) v *= p.x_scale[r0 + r];
-        const int64_t at = (int64_t)(r0 + r) * p.out_stride + o_tile + o;
-        if (p.out_dtype == SSD_F32) {
-            if (p.bias) v += static_cast<const float *>(p.bias)[o_tile + o];
-            static_cast<float *>(p.out)[at] = v;
-        } else {
-            if (p.bias) v += to_float(static_cast<const __nv_bfloat16 *>(p.bias)[o_tile + o]);
-            static_cast<__nv_bfloat16 *>(p.out)[at] = from_float<__nv_bfloat16>(v);
+        if (p.x_scale != nullptr && plan.x_groups == 1) {
+            const float scale = p.x_scale[r0 + r];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] *= scale;
         }
+        const int64_t at = (int64_t)(r0 + r) * p.out_stride + o_tile + o;
+        auto finish = [&](auto *out, const auto *bias) {
+            using T = std::remove_reference_t<decltype(*out)>;
+            Pack<T, 4> q;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (bias && j < live) v[j] += to_float(bias[o_tile + o + j]);
+                q.v[j] = from_float<T>(v[j]);
+            }
+            if (live == 4 && out_wide) {
+                store_pack<T, 4>(out + at, q);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j < live) out[at + j] = q.v[j];
+            }
+        };
+        if (p.out_dtype == SSD_F32) finish(static_cast<float *>(p.out), static_cast<const float *>(p.bias));
+        else finish(static_cast<__nv_bfloat16 *>(p.out), static_cast<const __nv_bfloat16 *>(p.bias));
     }
     if (plan.split > 1) cluster_barrier();              // no CTA leaves while another reads its sums
 }
@@ -582,7 +608,7 @@ template <int kCols, int kShared, bool kZero, bool kWhole> cudaError_t run(const
     config.dynamicSmemBytes = (size_t)q.smem;
     config.stream = stream;
     config.attrs = attr;
-    config.numAttrs = 2;
+    config.numAttrs = q.split > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&config, f, q);
 }
 

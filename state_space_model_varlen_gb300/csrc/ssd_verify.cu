@@ -378,7 +378,7 @@ template <typename T, int kThreads> cudaError_t launch(const ssd_verify_params &
     config.blockDim = dim3(kThreads);
     config.stream = stream;
     config.attrs = attr;
-    config.numAttrs = 2;
+    config.numAttrs = split > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&config, verify_kernel<T, kThreads>, p, split, per);
 }
 
