@@ -17,14 +17,15 @@
 // tile's columns; the parts are added in a fixed order.
 //
 // Measured (floor at the copy rate): 1 row of 4,096 to 18,560 outputs, groups of 128,
-// 12.1 us (5.8); 3 rows of 4,096 to 131,072 62.6 us (41); 16 rows of 2,560 to 10,576,
-// groups of 32 with zeros, 18.4 us (2.4: scales and zeros take as many instructions as the
+// 12.0 us (5.8); 3 rows of 4,096 to 131,072 61.7 us (41); 16 rows of 2,560 to 10,576,
+// groups of 32 with zeros, 16.4 us (2.4: scales and zeros take as many instructions as the
 // products).  Rows of 4,102 columns, which no 16-byte copy takes whole, 29 us where rows
-// of 4,096 take 12; 32 rows 29 us, 64 rows 49.  Before: tiles of 32 outputs whose columns
+// of 4,096 take 12; 16 rows 17 us, 32 26, 64 44.  Before: tiles of 32 outputs whose columns
 // eight warps shared, all of x in shared memory (head 63 us; 22 to 29 us where x of many
 // rows left one CTA an SM, and whole rows alone); codes shifted to the mantissa's end and
 // 128 + zero subtracted (three shifts a word for one: 73 for 69 us); 64 columns a pass
-// with one CTA an SM (64 rows 56 for 51 us).
+// with one CTA an SM (64 rows 56 for 51 us); the parts added one output at a time (16 rows
+// 19.7 for 16.9).
 //
 // A group of columns is taken in blocks of 32; a group of another size, or a row's
 // end, leaves the last block's x partly zero.  Rows of codes in whole 16 bytes are
