@@ -130,8 +130,8 @@ template <typename T, int V> __device__ __forceinline__ Pack<T, V> packed(const 
     return p;
 }
 
-constexpr int kRowThreads = 128;        // of a CTA that takes a row a warp
-template <int V> constexpr int kMost = V == 1 ? 1024 : 512;     // of one that takes one row: what the registers allow
+constexpr int kRowThreads = 128;        // of a CTA that takes several rows
+template <int V> constexpr int kMost = V <= 2 ? 1024 : 512;     // of one that takes one row: what the registers allow
 
 // V values from column c on, or those of them that the row has; and back
 template <bool kShift, typename T, int V> __device__ __forceinline__ Pack<T, V> get(const T *row, int c, int columns) {
@@ -152,19 +152,23 @@ template <bool kShift, typename T, int V> __device__ __forceinline__ void put(T 
         if (c + j >= 0 && c + j < columns) row[c + j] = p.v[j];
 }
 
-// kWarp: a warp takes a row, else the CTA does; C: vectors of a thread at most.
+// kLanes: lanes that take a row (4 to 32), or 0: the CTA does; C: vectors of a thread at most.
 // kShift: rows that begin anywhere, all alike: `first` + row stride elements behind a
 // boundary of V; the vectors begin at the boundary, and the weights come one by one.
-template <typename IoT, typename ResT, int V, bool kWarp, int C, bool kCodes, bool kShift = false>
-__global__ void __launch_bounds__(kWarp ? kRowThreads : kMost<V>)
+template <typename IoT, typename ResT, int V, int kLanes, int C, bool kCodes, bool kShift = false>
+__global__ void __launch_bounds__(kLanes ? kRowThreads : kMost<V>)
     residual_norm_kernel(const ssd_residual_norm_params a, int lanes, int first) {
     extern __shared__ float most[];     // largest magnitude of a vector, then inv of a group
     __shared__ float part[32];
     constexpr int kPairs = (V + 1) / 2;
     await_previous();
-    const int id = kWarp ? threadIdx.x & 31 : threadIdx.x, team = kWarp ? 32 : blockDim.x;
-    const int64_t number = kWarp ? (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
-    if (kWarp && number >= a.rows) return;
+    constexpr bool kWarp = kLanes != 0;
+    const int id = kWarp ? threadIdx.x % (kWarp ? kLanes : 1) : threadIdx.x, team = kWarp ? kLanes : blockDim.x;
+    int64_t number = blockIdx.x;
+    if (kWarp) number = number * (kRowThreads / (kWarp ? kLanes : 1)) + threadIdx.x / (kWarp ? kLanes : 1);
+    const bool live = !kWarp || number < a.rows;        // behind the last row: lanes that only take part in the sums
+    if (!live) number = a.rows - 1;
+    const int columns = live ? a.columns : 0;
     const Row<IoT, ResT> row(a, number);
     const int shift = kShift ? (int)((first + number * a.x_stride) % V) : 0;
     auto column = [&](int k) { return (k * team + id) * V - shift; };
@@ -175,19 +179,19 @@ __global__ void __launch_bounds__(kWarp ? kRowThreads : kMost<V>)
         const int c = column(k);
         x[k] = w[k] = Pack<IoT, V>{};
         res[k] = Pack<ResT, V>{};
-        if (c < a.columns) {
-            x[k] = get<kShift, IoT, V>(row.x, c, a.columns);
-            if (row.res) res[k] = get<kShift, ResT, V>(row.res, c, a.columns);
+        if (c < columns) {
+            x[k] = get<kShift, IoT, V>(row.x, c, columns);
+            if (row.res) res[k] = get<kShift, ResT, V>(row.res, c, columns);
         }
     }
     // weights ahead of the sum too, unless they would take single elements a register each
     auto weights = [&](int k) {
         const int c = column(k);
-        if (!row.w || c >= a.columns) return;
+        if (!row.w || c >= columns) return;
         if constexpr (kShift) {
 #pragma unroll
             for (int j = 0; j < V; ++j)
-                if (c + j >= 0 && c + j < a.columns) w[k].v[j] = row.w[c + j];
+                if (c + j >= 0 && c + j < columns) w[k].v[j] = row.w[c + j];
         } else {
             w[k] = load_pack<IoT, V>(row.w + c);
         }
@@ -210,8 +214,8 @@ __global__ void __launch_bounds__(kWarp ? kRowThreads : kMost<V>)
     if (row.res_out)
 #pragma unroll
         for (int k = 0; k < C; ++k)
-            if (column(k) < a.columns) put<kShift, ResT, V>(row.res_out, column(k), a.columns, packed<ResT, V>(v[k]));
-    const float sum = kWarp ? warp_sum(two.x + two.y) : cta_sum(two.x + two.y, part);
+            if (column(k) < columns) put<kShift, ResT, V>(row.res_out, column(k), columns, packed<ResT, V>(v[k]));
+    const float sum = kWarp ? lanes_sum<kWarp ? kLanes : 32>(two.x + two.y) : cta_sum(two.x + two.y, part);
     const float r = 1.f / sqrtf(sum / (float)a.columns + a.eps);
 #pragma unroll
     for (int k = 0; k < C; ++k) {
@@ -224,7 +228,7 @@ __global__ void __launch_bounds__(kWarp ? kRowThreads : kMost<V>)
             v[k][j] = mul2(v[k][j], make_float2(r, r));
             if (row.w) v[k][j] = mul2(v[k][j], f[j]);
         }
-        if (row.out && c < a.columns) put<kShift, IoT, V>(row.out, c, a.columns, packed<IoT, V>(v[k]));
+        if (row.out && c < columns) put<kShift, IoT, V>(row.out, c, columns, packed<IoT, V>(v[k]));
     }
     if constexpr (kCodes) {
         const int G = a.scale_group, per = G / V;       // vectors of a group
@@ -248,7 +252,7 @@ __global__ void __launch_bounds__(kWarp ? kRowThreads : kMost<V>)
                 const int at = k * team + id;
                 float scale;
                 code_scale(a, m[k], &inv[k], &scale);
-                if ((id & (lanes - 1)) == 0 && at * V < a.columns) row.scale[at / lanes] = scale;
+                if ((id & (lanes - 1)) == 0 && at * V < columns) row.scale[at / lanes] = scale;
             }
         } else {
             float *const mine = most + (kWarp ? (threadIdx.x >> 5) * (a.columns / V + a.columns / G) : 0);
@@ -259,10 +263,10 @@ __global__ void __launch_bounds__(kWarp ? kRowThreads : kMost<V>)
             };
 #pragma unroll
             for (int k = 0; k < C; ++k)
-                if ((k * team + id) * V < a.columns) mine[k * team + id] = m[k];
+                if ((k * team + id) * V < columns) mine[k * team + id] = m[k];
             sync();
             const int lane = threadIdx.x & 31;
-            for (int g = kWarp ? 0 : threadIdx.x >> 5; g < a.columns / G; g += kWarp ? 1 : team >> 5) {
+            for (int g = kWarp ? 0 : threadIdx.x >> 5; g < columns / G; g += kWarp ? 1 : team >> 5) {
                 float u = 0.f;
                 for (int i = lane; i < per; i += 32) u = max_abs(u, mine[g * per + i], mine[g * per + i]);
                 u = lanes_max<32>(u);
@@ -275,12 +279,12 @@ __global__ void __launch_bounds__(kWarp ? kRowThreads : kMost<V>)
             }
             sync();
 #pragma unroll
-            for (int k = 0; k < C; ++k) inv[k] = (k * team + id) * V < a.columns ? invs[(k * team + id) / per] : 0.f;
+            for (int k = 0; k < C; ++k) inv[k] = (k * team + id) * V < columns ? invs[(k * team + id) / per] : 0.f;
         }
 #pragma unroll
         for (int k = 0; k < C; ++k) {
             const int c = (k * team + id) * V;
-            if (c >= a.columns) continue;
+            if (c >= columns) continue;
             float f[2 * kPairs];
 #pragma unroll
             for (int j = 0; j < kPairs; ++j) {
@@ -305,16 +309,25 @@ cudaError_t launch_row(const ssd_residual_norm_params &p, cudaStream_t stream, b
         return enqueue_shared(kernel, dim3((unsigned)ctas), threads, rows * entries * 4, stream, p, lanes, first);
     };
     constexpr int kShort = V == 1 ? 4 : 2;
-    if (vectors <= 32 * kShort)
-        return go(residual_norm_kernel<IoT, ResT, V, true, kShort, kCodes, kShift>, (p.rows + 3) / 4, kRowThreads, kRowThreads / 32);
+    auto several = [&](auto kernel, int of_a_row) {     // rows of a CTA
+        const int rows = kRowThreads / of_a_row;
+        return go(kernel, (p.rows + rows - 1) / rows, kRowThreads, rows);
+    };
+    if constexpr (V >= 4 && !kShift)
+        if (shuffled) {
+            if (vectors <= 4) return several(residual_norm_kernel<IoT, ResT, V, 4, 1, kCodes>, 4);
+            if (vectors <= 8) return several(residual_norm_kernel<IoT, ResT, V, 8, 1, kCodes>, 8);
+            if (vectors <= 16) return several(residual_norm_kernel<IoT, ResT, V, 16, 1, kCodes>, 16);
+        }
+    if (vectors <= 32 * kShort) return several(residual_norm_kernel<IoT, ResT, V, 32, kShort, kCodes, kShift>, 32);
     auto whole = [&](auto kernel, int chunks) {
         return go(kernel, p.rows, 32 * ((vectors + 32 * chunks - 1) / (32 * chunks)), 1);
     };
     if constexpr (V == 1) {
-        if (vectors <= kMost<V> * 10) return whole(residual_norm_kernel<IoT, ResT, V, false, 10, kCodes>, 10);
+        if (vectors <= kMost<V> * 10) return whole(residual_norm_kernel<IoT, ResT, V, 0, 10, kCodes>, 10);
     } else {
-        if (vectors <= kMost<V> * 4) return whole(residual_norm_kernel<IoT, ResT, V, false, 4, kCodes, kShift>, 4);
-        if (vectors <= kMost<V> * 8) return whole(residual_norm_kernel<IoT, ResT, V, false, 8, kCodes, kShift>, 8);
+        if (vectors <= kMost<V> * 4) return whole(residual_norm_kernel<IoT, ResT, V, 0, 4, kCodes, kShift>, 4);
+        if (vectors <= kMost<V> * 8) return whole(residual_norm_kernel<IoT, ResT, V, 0, 8, kCodes, kShift>, 8);
     }
     return cudaErrorInvalidConfiguration;
 }
@@ -328,29 +341,32 @@ template <typename IoT, typename ResT> cudaError_t launch_norm(const ssd_residua
                (!p.out || (p.out_stride % v == 0 && aligned_to(p.out, io))) &&
                (!p.out_codes || (p.scale_group % v == 0 && p.codes_stride % v == 0 && aligned_to(p.out_codes, v)));
     };
-    // rows that all begin alike, if not at a boundary: in vectors of four from the boundary on
-    constexpr int kBeside = 4;
-    const int first = (int)(reinterpret_cast<uintptr_t>(p.x) / sizeof(IoT) % kBeside);
-    auto alike = [&](const void *q, int64_t stride, size_t size) {
-        return !q || ((int)(reinterpret_cast<uintptr_t>(q) / size % kBeside) == first &&
-                      (stride - p.x_stride) % kBeside == 0);
-    };
-    const bool beside = !p.out_codes && p.x_stride < (1LL << 40) && alike(p.residual, p.residual_stride, sizeof(ResT)) &&
-                        alike(p.residual_out, p.residual_out_stride, sizeof(ResT)) && alike(p.out, p.out_stride, sizeof(IoT));
     bool taken = false;
-    cudaError_t e;
-    auto shifted = [&] { return launch_row<IoT, ResT, kBeside, false, true>(p, stream, &taken, first); };
+    cudaError_t e = cudaErrorInvalidConfiguration;
+    // rows that all begin alike, if not at a boundary: in vectors from the boundary on
+    auto beside = [&](auto width) {
+        constexpr int V = decltype(width)::value;
+        const int first = (int)(reinterpret_cast<uintptr_t>(p.x) / sizeof(IoT) % V);
+        auto alike = [&](const void *q, int64_t stride, size_t size) {
+            return !q || ((int)(reinterpret_cast<uintptr_t>(q) / size % V) == first && (stride - p.x_stride) % V == 0);
+        };
+        if (p.out_codes || p.x_stride >= (1LL << 40) || !alike(p.residual, p.residual_stride, sizeof(ResT)) ||
+            !alike(p.residual_out, p.residual_out_stride, sizeof(ResT)) || !alike(p.out, p.out_stride, sizeof(IoT)))
+            return cudaErrorInvalidConfiguration;
+        return launch_row<IoT, ResT, V, false, true>(p, stream, &taken, first);
+    };
     auto row = [&](auto width) {
         constexpr int V = decltype(width)::value;
         return p.out_codes ? launch_row<IoT, ResT, V, true>(p, stream, &taken) : launch_row<IoT, ResT, V, false>(p, stream, &taken);
     };
-    if constexpr (sizeof(IoT) == 2) {
-        e = can(8)   ? row(std::integral_constant<int, 8>())
-            : can(4) ? row(std::integral_constant<int, 4>())
-            : beside ? shifted()
-                     : row(std::integral_constant<int, 1>());
-    } else {
-        e = can(4) ? row(std::integral_constant<int, 4>()) : beside ? shifted() : row(std::integral_constant<int, 1>());
+    using std::integral_constant;
+    if (sizeof(IoT) == 2 && can(8)) e = row(integral_constant<int, sizeof(IoT) == 2 ? 8 : 4>());
+    else if (can(4)) e = row(integral_constant<int, 4>());
+    else if (sizeof(IoT) == 2 && can(2)) e = row(integral_constant<int, sizeof(IoT) == 2 ? 2 : 1>());
+    if (!taken && !can(4)) {
+        if (sizeof(IoT) == 2 && p.columns > 8192) e = beside(integral_constant<int, sizeof(IoT) == 2 ? 8 : 4>());
+        if (!taken) e = beside(integral_constant<int, 4>());
+        if (!taken) e = row(integral_constant<int, 1>());
     }
     if (taken) return e;
     if (p.rows > 0x7fffffffLL) return cudaErrorInvalidConfiguration;

@@ -193,6 +193,22 @@ def test_norm_special_values(cols, group, code):
     assert torch.isfinite(o[1, :-1]).all() and torch.isfinite(o[4, :-1]).all()
 
 
+@pytest.mark.parametrize("cols,group", [(8, 4), (16, 16), (32, 32), (32, 8), (40, 8), (64, 32), (96, 32), (128, 128), (128, 16),
+                                        (256, 64), (24, 24), (36, 12), (894, 298), (30, 10)])
+@pytest.mark.parametrize("rows", [1, 7, 33, 130])
+@pytest.mark.parametrize("io,res", [("bf16", "f32"), ("f32", "bf16")])
+def test_norm_short_rows(cols, group, rows, io, res):
+    """Several rows of a warp, the last of them not there."""
+    _norm_case(rows, cols, io, res, "e4m3", group, seed=rows)
+    _norm_case(rows, cols, io, res, seed=rows)
+
+
+@pytest.mark.parametrize("cols", [894, 2002, 12002, 13665, 16382, 20001])
+@pytest.mark.parametrize("res", ["f32", "bf16"])
+def test_norm_rows_of_two_and_long_odd_ones(cols, res):
+    _norm_case(3, cols, "bf16", res)
+
+
 def test_norm_many_rows():
     """More rows than one wave of CTAs, each the same as alone."""
     torch = _torch()
