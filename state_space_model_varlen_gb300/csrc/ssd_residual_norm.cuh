@@ -3,10 +3,10 @@
 //
 //   v = x + residual;  n = v / sqrt(mean(v^2) + eps) weight;  codes of n by groups
 //
-// Each value is read once and written once: bound by HBM.  A warp takes a short row,
-// a CTA a longer one; either holds the row in registers from the sum of squares to
-// the stores, all its loads issued together.  The largest magnitude of a group of
-// 1, 2, 4 .. 32 vectors comes from the lanes that hold it, of others from one entry
+// Each value is read once and written once: bound by HBM.  Four to 32 lanes take a
+// short row, a CTA a longer one; either holds the row in registers from the sum of
+// squares to the stores, all its loads issued together.  The largest magnitude of a group
+// of 1, 2, 4 .. 32 vectors comes from the lanes that hold it, of others from one entry
 // a vector in shared memory.
 //
 // Measured: 16,384 rows of 2,560 bf16 columns with an fp32 residual 73 us, 6.87 TB/s (at
@@ -15,7 +15,8 @@
 // and the codes instead of kept: 331 and 1,959 us.  Odd dense rows, whose vectors begin at
 // the boundary before the row: 21,897 x 2,009 fp32 54 us (96 %; element by element 86),
 // 30,000 x 2,001 bf16 with a bf16 residual 126 us (56 %: a weight at a time, and the ends;
-// vectors of eight 141, weights put together from two vectors 147).
+// vectors of eight 141, weights put together from two vectors 147); even bf16 rows in
+// pairs, 34,830 x 894 33 us (56 %).  46,479 rows of 32 with codes 7 us, 21 with a warp a row.
 #pragma once
 
 #include <type_traits>
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(kLanes ? kRowThreads : kMost<V>)
             if (row.res) res[k] = get<kShift, ResT, V>(row.res, c, columns);
         }
     }
-    // weights ahead of the sum too, unless they would take single elements a register each
+    // weights ahead of the sum too, unless they come one by one into too many registers
     auto weights = [&](int k) {
         const int c = column(k);
         if (!row.w || c >= columns) return;
@@ -196,7 +197,8 @@ __global__ void __launch_bounds__(kLanes ? kRowThreads : kMost<V>)
             w[k] = load_pack<IoT, V>(row.w + c);
         }
     };
-    if constexpr (V > 1)
+    constexpr bool kEarly = V > 1 && !(kShift && V == 8);
+    if constexpr (kEarly)
 #pragma unroll
         for (int k = 0; k < C; ++k) weights(k);
     float2 v[C][kPairs], two = make_float2(0.f, 0.f);
@@ -220,7 +222,7 @@ __global__ void __launch_bounds__(kLanes ? kRowThreads : kMost<V>)
 #pragma unroll
     for (int k = 0; k < C; ++k) {
         const int c = column(k);
-        if constexpr (V == 1) weights(k);
+        if constexpr (!kEarly) weights(k);
         float2 f[kPairs];
         unpack<IoT, V>(w[k], f);
 #pragma unroll
