@@ -79,14 +79,16 @@ __device__ __forceinline__ Sum before_lane(const Sum &a) {
 }
 // The first of n lanes at which the sums `mine`, which are `upto` added up, pass goal
 // from `before` on, and what they are before it; or (with goal out of the way, so that
-// the last of any weight is found below) the last one with a sum, or -1.
-__device__ __forceinline__ int owner_of(const Sum &mine, Sum upto, int n, Sum &goal, Sum &before) {
+// the last of any weight is found below) the last one with a sum, or -1.  `passed`: which
+// of the two; goal does not tell, as it may be out of the way already.
+__device__ __forceinline__ int owner_of(const Sum &mine, Sum upto, int n, Sum &goal, Sum &before, bool &passed) {
     const int lane = threadIdx.x & 31;
     Sum ahead = before_lane(upto);
     upto.add(before);
     ahead.add(before);
     const uint32_t some = __ballot_sync(0xffffffffu, lane < n && mine.s > 0.f);
     const uint32_t over = some & __ballot_sync(0xffffffffu, upto.above(goal));
+    passed = over != 0;
     if (!over) goal.s = __int_as_float(0x7f7fffff);
     const int at = over ? __ffs(over) - 1 : some ? 31 - __clz(some) : -1;
     before = shuffled(ahead, at < 0 ? 0 : at);
@@ -250,7 +252,8 @@ __device__ int search(const Weights<T> &w, int base, int blocks, int lo, int hi,
         for (int i = 0; i < kVectors; ++i) w.add(mine, v[i], base + lane * kRun + i * N, lo, hi);
         const Sum upto = scan(mine);
         Sum limit = goal, ahead = before;
-        const int at = owner_of(mine, upto, 32, limit, ahead);
+        bool here, there;               // the goal is in this run, or behind all that there is of this block
+        const int at = owner_of(mine, upto, 32, limit, ahead, here);
         if (at >= 0) {                  // that run's tokens, one a lane
             const int t = base + at * kRun + lane;
             Sum one;
@@ -258,8 +261,7 @@ __device__ int search(const Weights<T> &w, int base, int blocks, int lo, int hi,
                 const float2 f = Weights<T>::of(to_float(w.p[t]), w.q ? to_float(w.q[t]) : 0.f, t == w.without);
                 one.add(f.x, f.y);
             }
-            const bool here = limit.s == goal.s;        // the goal is in this run, not behind all
-            last = base + at * kRun + owner_of(one, scan<kRun>(one), kRun, limit, ahead);
+            last = base + at * kRun + owner_of(one, scan<kRun>(one), kRun, limit, ahead, there);
             if (here) return last;
         }
         before.add(shuffled(upto, 31));
@@ -325,9 +327,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 1 : 1024 / kThread
         if (total.s > 0.f || last_try) {
             Sum goal = times(total, u), before;
             if (u == 1.f) goal.s = __int_as_float(0x7f7fffff);          // the last of any weight
-            const int owner = max(0, owner_of(ctas, ctas_upto, split, goal, before));
+            bool passed;
+            const int owner = max(0, owner_of(ctas, ctas_upto, split, goal, before, passed));
             if (rank == owner) {
-                const int by = max(0, owner_of(warps, warps_upto, kWarps, goal, before));
+                const int by = max(0, owner_of(warps, warps_upto, kWarps, goal, before, passed));
                 if (warp == by) {
                     // the sums of the warp's blocks: four lanes add one's 32, then the block of the goal
                     __syncwarp();
@@ -340,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 1 : 1024 / kThread
 #pragma unroll
                     for (int o = 1; o < 4; o <<= 1) run.add(__shfl_xor_sync(0xffffffffu, run.s, o), __shfl_xor_sync(0xffffffffu, run.c, o));
                     if (lane & 3) run = Sum();
-                    const int from = max(0, owner_of(run, scan(run), 32, goal, before)) >> 2;
+                    const int from = max(0, owner_of(run, scan(run), 32, goal, before, passed)) >> 2;
                     const int at = search<T, kVectors>(w, base + from * runs * kBlock, runs, lo, hi, before, goal, alike);
                     for (int i = lane; i <= k; i += 32) a.out_tokens[first + i] = i < n ? a.tokens[first + i + 1] : i == n ? at : -1;
                     if (lane == 0) {

@@ -1,0 +1,59 @@
+"""The layer operators at the ends of what their calls allow, on the GPU."""
+import numpy as np
+import pytest
+
+from tests.test_layer_gpu import Draw, _probs, _torch, _verify_check, _windows
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------
+# verification: many windows of a large vocabulary, where a sum that is left covers several blocks of a row
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("S,V", [(192, 131072), (256, 100003), (700, 17000), (1024, 50280), (1024, 32000)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_verify_many_windows_of_large_vocabularies(S, V, dtype):
+    """Windows of one token and of two, the draft of every other one rejected, so that rows of p and of p - q are sampled, at
+    0, inside, just below 1, at 1 and above; rows whose last blocks, or all but one, are without weight."""
+    torch = _torch()
+    d = Draw(S + V)
+    lens = [1 + s % 2 for s in range(S)]
+    T, D = sum(lens), S // 2
+    cu = _windows(lens)
+    target, q = _probs(d, T, V, dtype), _probs(d, D, V, dtype)
+    tokens = d.ints(1, V, T)
+    au = torch.zeros(D, device="cuda")
+    au[::2] = 1.0                               # above what p / q can be at the token: rejected
+    first = cu[1:-1:2].long()                   # of the windows of two
+    ones = cu[:-1:2].long()
+    drafted = tokens[first + 1].long()
+    target[first[::2], drafted[::2]] = 0.0
+    for i, live in enumerate((V - 600, V // 3, 700, 1)):        # columns behind which there is nothing
+        for rows in (ones[1 + i::7], first[2 * (1 + i)::14]):
+            target[rows, live:] = 0.0
+    q[2::4, :] = 0.0                            # all of the target's row is left
+    su = d.rand(S)
+    at = torch.arange(S, device="cuda") // 2 % 6
+    for i, u in enumerate((0.0, 1.0 - 2.0 ** -24, 1.0, 2.0)):
+        su[at == i] = u
+    out, acc, _, status = _verify_check(target, q, tokens, cu, au, su)
+    assert status == 0 and (acc[1::4] == 0).all() and (acc[0::2] == 0).all()
+    # without the oracle: at 1 and above the last token of any weight
+    picked = torch.from_numpy(out).cuda()[ones]
+    last = (torch.arange(V, device="cuda") * (target[ones] > 0)).amax(1)
+    end = su[::2] >= 1
+    assert end.sum() > S // 8 and torch.equal(picked[end].long(), last[end])
+
+
+def test_verify_gives_a_window_the_same_token_whatever_stands_beside_it():
+    torch = _torch()
+    d = Draw(17)
+    V = 131072
+    rows = _probs(d, 6, V, "f32")
+    u = torch.tensor([0.0, 0.3, 1.0 - 2.0 ** -24, 1.0, 2.0, 0.999], device="cuda")
+    zeros = torch.zeros(6, dtype=torch.int32, device="cuda")
+    alone = _verify_check(rows, None, zeros, _windows([1] * 6), None, u)[0]
+    S = 300
+    many = _verify_check(rows.repeat(S // 6, 1), None, zeros.repeat(S // 6), _windows([1] * S), None, u.repeat(S // 6))[0]
+    assert np.array_equal(many.reshape(-1, 6), np.tile(alone, (S // 6, 1)))
+    assert alone[3] == alone[4] == V - 1
