@@ -15,7 +15,7 @@ cudaError_t launch_residual_norm_bf16(const ssd_residual_norm_params &p, cudaStr
 cudaError_t launch_matvec4(const ssd_matvec4_params &p, cudaStream_t stream);
 cudaError_t launch_verify(const ssd_verify_params &p, cudaStream_t stream);
 
-// enqueue() with dynamic shared memory (at most 48 KB)
+// enqueue() with dynamic shared memory (at most 48 KB with the arrays that the kernel declares itself)
 template <typename... Params, typename... Args>
 cudaError_t enqueue_shared(void (*kernel)(Params...), dim3 grid, int threads, size_t shared, cudaStream_t stream,
                            const Args &...args) {

@@ -132,6 +132,8 @@ template <typename T, int V> __device__ __forceinline__ Pack<T, V> packed(const 
 }
 
 constexpr int kRowThreads = 128;        // of a CTA that takes several rows
+constexpr int kParts = 32;              // sums of a CTA's warps
+constexpr size_t kMostShared = 48 * 1024 - kParts * sizeof(float);      // beside them, of a launch without an opt-in
 template <int V> constexpr int kMost = V <= 2 ? 1024 : 512;     // of one that takes one row: what the registers allow
 
 // V values from column c on, or those of them that the row has; and back
@@ -160,7 +162,7 @@ template <typename IoT, typename ResT, int V, int kLanes, int C, bool kCodes, bo
 __global__ void __launch_bounds__(kLanes ? kRowThreads : kMost<V>)
     residual_norm_kernel(const ssd_residual_norm_params a, int lanes, int first) {
     extern __shared__ float most[];     // largest magnitude of a vector, then inv of a group
-    __shared__ float part[32];
+    __shared__ float part[kParts];
     constexpr int kPairs = (V + 1) / 2;
     await_previous();
     constexpr bool kWarp = kLanes != 0;
@@ -306,7 +308,7 @@ cudaError_t launch_row(const ssd_residual_norm_params &p, cudaStream_t stream, b
     const int lanes = kCodes && shuffled ? per : 0;
     const size_t entries = kCodes && !shuffled ? (size_t)vectors + p.columns / p.scale_group : 0;
     auto go = [&](auto kernel, int64_t ctas, int threads, size_t rows) {
-        if (ctas > 0x7fffffffLL || rows * entries * 4 > 48 * 1024) return cudaErrorInvalidConfiguration;
+        if (ctas > 0x7fffffffLL || rows * entries * 4 > kMostShared) return cudaErrorInvalidConfiguration;
         *taken = true;
         return enqueue_shared(kernel, dim3((unsigned)ctas), threads, rows * entries * 4, stream, p, lanes, first);
     };

@@ -2,7 +2,7 @@
 import numpy as np
 import pytest
 
-from tests.test_layer_gpu import Draw, _probs, _torch, _verify_check, _windows
+from tests.test_layer_gpu import Draw, _norm_case, _probs, _torch, _verify_check, _windows
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +57,14 @@ def test_verify_gives_a_window_the_same_token_whatever_stands_beside_it():
     many = _verify_check(rows.repeat(S // 6, 1), None, zeros.repeat(S // 6), _windows([1] * S), None, u.repeat(S // 6))[0]
     assert np.array_equal(many.reshape(-1, 6), np.tile(alone, (S // 6, 1)))
     assert alone[3] == alone[4] == V - 1
+
+
+# ---------------------------------------------------------------------------
+# residual norm: groups of codes whose shared memory is at the limit of a launch
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("cols,group", [(9189, 3), (9192, 3), (9195, 3), (9213, 3), (9219, 3), (10210, 5), (10215, 5), (10240, 5),
+                                        (10245, 5)])
+@pytest.mark.parametrize("io,res", [("f32", "f32"), ("bf16", "f32")])
+def test_norm_codes_of_long_rows_in_small_odd_groups(cols, group, io, res):
+    _norm_case(2, cols, io, res, "e4m3", group, seed=cols)
+    _norm_case(2, cols, io, None, "i8", group, out=False, seed=cols)
