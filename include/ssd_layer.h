@@ -36,7 +36,8 @@ extern "C" {
 
 /* bits OR-ed into *device_status by ssd_verify_drafts */
 #define SSD_DEV_BAD_TOKEN 64   /* a drafted token outside [0, vocab)           */
-#define SSD_DEV_BAD_PROBS 128  /* a row without a positive finite probability  */
+#define SSD_DEV_BAD_PROBS 128  /* a row without a positive finite probability, */
+                               /* or whose sum is no finite fp32 number        */
 
 /* ------------------------------------------------------------------------
  * Residual addition and RMS norm.  For row t:
@@ -149,7 +150,8 @@ ssd_status ssd_matvec4(const ssd_matvec4_params *params, struct CUstream_st *str
  * uniform in [0, 1) (values outside count as the nearest end, NaN as 0).  Products,
  * differences and comparisons are exact, the sums are kept to about 2^-44 of the
  * total.  Entries of w that are not positive and finite count as zero; where none
- * is left, new is -1 and SSD_DEV_BAD_PROBS is set.  Rows need not sum to one.
+ * is left, or their sum is beyond fp32's largest number, new is -1 and
+ * SSD_DEV_BAD_PROBS is set.  Rows need not sum to one.
  *
  *   out_tokens[cu_seqlens[s] + i] = d_(i+1) for i < n, new for i = n, -1 behind
  *   out_accepted[s] = n

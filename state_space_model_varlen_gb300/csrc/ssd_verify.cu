@@ -344,7 +344,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 1 : 1024 / kThread
                     for (int o = 1; o < 4; o <<= 1) run.add(__shfl_xor_sync(0xffffffffu, run.s, o), __shfl_xor_sync(0xffffffffu, run.c, o));
                     if (lane & 3) run = Sum();
                     const int from = max(0, owner_of(run, scan(run), 32, goal, before, passed)) >> 2;
-                    const int at = search<T, kVectors>(w, base + from * runs * kBlock, runs, lo, hi, before, goal, alike);
+                    // a sum that fp32 does not hold is infinite, and says nothing of where the goal lies
+                    const int at = total.s < __int_as_float(0x7f800000)
+                                       ? search<T, kVectors>(w, base + from * runs * kBlock, runs, lo, hi, before, goal, alike)
+                                       : -1;
                     for (int i = lane; i <= k; i += 32) a.out_tokens[first + i] = i < n ? a.tokens[first + i + 1] : i == n ? at : -1;
                     if (lane == 0) {
                         if (at < 0) flag(a.device_status, SSD_DEV_BAD_PROBS);

@@ -2,6 +2,7 @@
 import numpy as np
 import pytest
 
+from state_space_model_varlen_gb300 import layer
 from tests.test_layer_gpu import Draw, _norm_case, _probs, _torch, _verify_check, _windows
 
 pytestmark = pytest.mark.gpu
@@ -57,6 +58,31 @@ def test_verify_gives_a_window_the_same_token_whatever_stands_beside_it():
     many = _verify_check(rows.repeat(S // 6, 1), None, zeros.repeat(S // 6), _windows([1] * S), None, u.repeat(S // 6))[0]
     assert np.array_equal(many.reshape(-1, 6), np.tile(alone, (S // 6, 1)))
     assert alone[3] == alone[4] == V - 1
+
+
+@pytest.mark.parametrize("S", [5, 400])
+def test_verify_rows_whose_sum_is_no_fp32_number(S):
+    """Finite weights that add up to more than fp32 holds pick no token; others beside them, up to its end, do."""
+    torch = _torch()
+    V, big = 20000, 2.0 ** 127
+    p = torch.zeros(2 * S, V, device="cuda")
+    q = torch.zeros(S, V, device="cuda")
+    tokens = torch.full((2 * S,), 7, dtype=torch.int32, device="cuda")
+    p[0::2, 8] = big
+    p[0::2, 9000] = big * 0.5                   # 0.75 2^128: u = 0.5 is token 8, 0.75 token 9000
+    over = torch.arange(S) % 3 == 1
+    p[0::2][over, V - 1] = big * 0.75
+    su = torch.where(torch.arange(S, device="cuda") % 2 == 0, 0.5, 0.75)
+    out, acc = (torch.full((n,), -77, dtype=torch.int32, device="cuda") for n in (2 * S, S))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for draft in (q, None):
+        out.fill_(-77)
+        status.zero_()
+        layer.verify_drafts(p, tokens, _windows([2] * S), torch.full((S,), 0.5, device="cuda"), su, draft_probs=draft,
+                            out_tokens=out, out_accepted=acc, device_status=status)
+        want = torch.where(su == 0.5, 8, 9000).int()
+        want[over.cuda()] = -1
+        assert torch.equal(out[0::2], want) and (out[1::2] == -1).all() and (acc == 0).all() and int(status) == 128
 
 
 # ---------------------------------------------------------------------------
