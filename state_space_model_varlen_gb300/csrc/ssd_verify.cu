@@ -47,7 +47,8 @@ struct Sum {
         s = t;
     }
     __device__ void add(const Sum &o) { add(o.s, o.c); }
-    __device__ bool above(const Sum &o) const { return (s - o.s) + (c - o.c) > 0.f; }
+    // unit times this is above o; unit is a power of two
+    __device__ bool above(const Sum &o, float unit) const { return fmaf(s, unit, -o.s) + fmaf(c, unit, -o.c) > 0.f; }
 };
 __device__ __forceinline__ Sum times(const Sum &a, float f) {
     Sum r;
@@ -80,14 +81,15 @@ __device__ __forceinline__ Sum before_lane(const Sum &a) {
 // The first of n lanes at which the sums `mine`, which are `upto` added up, pass goal
 // from `before` on, and what they are before it; or (with goal out of the way, so that
 // the last of any weight is found below) the last one with a sum, or -1.  `passed`: which
-// of the two; goal does not tell, as it may be out of the way already.
-__device__ __forceinline__ int owner_of(const Sum &mine, Sum upto, int n, Sum &goal, Sum &before, bool &passed) {
+// of the two; goal does not tell, as it may be out of the way already.  goal is in
+// 1 / unit, the sums are not.
+__device__ __forceinline__ int owner_of(const Sum &mine, Sum upto, int n, Sum &goal, float unit, Sum &before, bool &passed) {
     const int lane = threadIdx.x & 31;
     Sum ahead = before_lane(upto);
     upto.add(before);
     ahead.add(before);
     const uint32_t some = __ballot_sync(0xffffffffu, lane < n && mine.s > 0.f);
-    const uint32_t over = some & __ballot_sync(0xffffffffu, upto.above(goal));
+    const uint32_t over = some & __ballot_sync(0xffffffffu, upto.above(goal, unit));
     passed = over != 0;
     if (!over) goal.s = __int_as_float(0x7f7fffff);
     const int at = over ? __ffs(over) - 1 : some ? 31 - __clz(some) : -1;
@@ -239,7 +241,7 @@ template <typename T> __device__ void find_stop(const ssd_verify_params &a, int 
 // ahead of them, passes goal, or else the last of any weight.  One warp, whose lanes
 // take unbroken runs of tokens.
 template <typename T, int kVectors>
-__device__ int search(const Weights<T> &w, int base, int blocks, int lo, int hi, Sum before, const Sum &goal, bool alike) {
+__device__ int search(const Weights<T> &w, int base, int blocks, int lo, int hi, Sum before, const Sum &goal, float unit, bool alike) {
     constexpr int N = Weights<T>::N, kRun = N * kVectors;
     const int lane = threadIdx.x & 31;
     int last = -1;
@@ -253,7 +255,7 @@ __device__ int search(const Weights<T> &w, int base, int blocks, int lo, int hi,
         const Sum upto = scan(mine);
         Sum limit = goal, ahead = before;
         bool here, there;               // the goal is in this run, or behind all that there is of this block
-        const int at = owner_of(mine, upto, 32, limit, ahead, here);
+        const int at = owner_of(mine, upto, 32, limit, unit, ahead, here);
         if (at >= 0) {                  // that run's tokens, one a lane
             const int t = base + at * kRun + lane;
             Sum one;
@@ -261,7 +263,7 @@ __device__ int search(const Weights<T> &w, int base, int blocks, int lo, int hi,
                 const float2 f = Weights<T>::of(to_float(w.p[t]), w.q ? to_float(w.q[t]) : 0.f, t == w.without);
                 one.add(f.x, f.y);
             }
-            last = base + at * kRun + owner_of(one, scan<kRun>(one), kRun, limit, ahead, there);
+            last = base + at * kRun + owner_of(one, scan<kRun>(one), kRun, limit, unit, ahead, there);
             if (here) return last;
         }
         before.add(shuffled(upto, 31));
@@ -322,15 +324,20 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 1 : 1024 / kThread
             cluster_wait();
             ctas = lane < split ? load_of(&totals[attempt], lane) : Sum();
         }
-        const Sum ctas_upto = scan<8>(ctas), total = shuffled(ctas_upto, split - 1);
+        const Sum ctas_upto = scan<8>(ctas);
+        Sum total = shuffled(ctas_upto, split - 1);
         const bool last_try = attempt == 1 || (w.q == nullptr && w.without < 0);
         if (total.s > 0.f || last_try) {
+            // u total is a fraction of fp32's smallest numbers where the total is small: there in 2^-80
+            const float unit = total.s < 8.673617379884035e-19f ? 1.2089258196146292e24f : 1.f;         // 2^-60, 2^80
+            total.s *= unit;
+            total.c *= unit;
             Sum goal = times(total, u), before;
             if (u == 1.f) goal.s = __int_as_float(0x7f7fffff);          // the last of any weight
             bool passed;
-            const int owner = max(0, owner_of(ctas, ctas_upto, split, goal, before, passed));
+            const int owner = max(0, owner_of(ctas, ctas_upto, split, goal, unit, before, passed));
             if (rank == owner) {
-                const int by = max(0, owner_of(warps, warps_upto, kWarps, goal, before, passed));
+                const int by = max(0, owner_of(warps, warps_upto, kWarps, goal, unit, before, passed));
                 if (warp == by) {
                     // the sums of the warp's blocks: four lanes add one's 32, then the block of the goal
                     __syncwarp();
@@ -343,10 +350,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 1 : 1024 / kThread
 #pragma unroll
                     for (int o = 1; o < 4; o <<= 1) run.add(__shfl_xor_sync(0xffffffffu, run.s, o), __shfl_xor_sync(0xffffffffu, run.c, o));
                     if (lane & 3) run = Sum();
-                    const int from = max(0, owner_of(run, scan(run), 32, goal, before, passed)) >> 2;
+                    const int from = max(0, owner_of(run, scan(run), 32, goal, unit, before, passed)) >> 2;
                     // a sum that fp32 does not hold is infinite, and says nothing of where the goal lies
                     const int at = total.s < __int_as_float(0x7f800000)
-                                       ? search<T, kVectors>(w, base + from * runs * kBlock, runs, lo, hi, before, goal, alike)
+                                       ? search<T, kVectors>(w, base + from * runs * kBlock, runs, lo, hi, before, goal, unit, alike)
                                        : -1;
                     for (int i = lane; i <= k; i += 32) a.out_tokens[first + i] = i < n ? a.tokens[first + i + 1] : i == n ? at : -1;
                     if (lane == 0) {

@@ -85,6 +85,22 @@ def test_verify_rows_whose_sum_is_no_fp32_number(S):
         assert torch.equal(out[0::2], want) and (out[1::2] == -1).all() and (acc == 0).all() and int(status) == 128
 
 
+@pytest.mark.parametrize("unit", [2.0 ** -149, 2.0 ** -130, 2.0 ** -100, 2.0 ** -59, 2.0 ** 90])
+@pytest.mark.parametrize("S,V", [(64, 300), (400, 20000)])
+def test_verify_rows_of_any_magnitude(unit, S, V):
+    """Whole multiples of a unit: sums and, with random numbers of few bits, products are exact in 64 bits.  Tokens do not
+    depend on the unit, that of fp32's smallest number among them."""
+    torch = _torch()
+    d = Draw(V)
+    w = d.ints(0, 4, 1, V).float() * (torch.arange(V, device="cuda") % 7 == 3)
+    p = (w.double() * unit).float().repeat(S, 1)
+    assert torch.equal(p[0].double() / unit, w[0].double())
+    u = torch.arange(S, device="cuda").float() / 512
+    zeros = torch.zeros(S, dtype=torch.int32, device="cuda")
+    got = _verify_check(p, None, zeros, _windows([1] * S), None, u)
+    assert np.array_equal(got[0], _verify_check(w.repeat(S, 1), None, zeros, _windows([1] * S), None, u)[0])
+
+
 # ---------------------------------------------------------------------------
 # residual norm: groups of codes whose shared memory is at the limit of a launch
 # ---------------------------------------------------------------------------
