@@ -154,7 +154,7 @@ bool make_plan(const ssd_matvec4_params &p, Matvec4Plan &q, int &cols, int &shar
     shared = gcd(4, gcd(q.groups == 1 ? 4 : q.group_blocks, q.x_groups == 1 ? 4 : q.x_group_blocks));
     whole = unbroken && K % 32 == 0 && p.weight_stride % 16 == 0 && aligned_to(p.weight, 16);
     cols = 1;
-    while (cols < 4 && cols * 8 < p.rows * parts) cols *= 2;
+    while (cols < 4 && cols * 8 < (int64_t)p.rows * parts) cols *= 2;
     q.row_tile = cols * 8 / parts < p.rows ? cols * 8 / parts : p.rows;
     q.x_rows = q.row_tile * parts;
     if ((p.rows - 1) / q.row_tile + 1 > 65535) return false;

@@ -50,6 +50,12 @@ def _row_count(n, **tensors):
             raise ValueError("%s must have %d rows, not %d" % (what, n, t.shape[0]))
 
 
+def _i32(*sizes):
+    """Sizes for fields of 32 bits.  What these do not hold becomes the largest number that they do, which the library
+    refuses: a wrapped one could pass its checks, and the call would then read and write by it."""
+    return [min(n, 0x7fffffff) for n in sizes]
+
+
 # ---------------------------------------------------------------------------
 # residual norm
 # ---------------------------------------------------------------------------
@@ -61,26 +67,27 @@ def make_residual_norm_params(x, weight=None, out=None, *, residual=None, residu
     torch = _torch()
     p = ResidualNormParams()
     _hold(p, x, weight, out, residual, residual_out, codes, scale)
-    p.rows, p.columns = x.shape[0], mixer._row_numel(x)
+    columns = mixer._row_numel(x)
+    p.rows, (p.columns,) = x.shape[0], _i32(columns)
     _row_count(p.rows, out=out, residual=residual, residual_out=residual_out, codes=codes, scale=scale)
     p.io_dtype, p.eps = _io(x), float(eps)
     p.x, p.x_stride = _rows(x)
     stream = residual if residual is not None else residual_out
     p.residual_dtype = p.io_dtype if stream is None else _io(stream)
-    p.residual, p.residual_stride = _rows(residual, None, p.columns)
-    p.residual_out, p.residual_out_stride = _rows(residual_out, None if stream is None else stream.dtype, p.columns)
-    _shape(weight, (p.columns,), "weight")
+    p.residual, p.residual_stride = _rows(residual, None, columns)
+    p.residual_out, p.residual_out_stride = _rows(residual_out, None if stream is None else stream.dtype, columns)
+    _shape(weight, (columns,), "weight")
     p.weight = _ptr(weight, x.dtype)
-    p.out, p.out_stride = _rows(out, x.dtype, p.columns)
+    p.out, p.out_stride = _rows(out, x.dtype, columns)
     if (codes is None) != (scale is None):
         raise ValueError("codes and scale go together")
     if codes is not None:
         p.code_dtype = _code(codes, "codes")
-        p.out_codes, p.codes_stride = _rows(codes, None, p.columns)
+        p.out_codes, p.codes_stride = _rows(codes, None, columns)
         p.out_scale = _ptr(scale, torch.float32)
-        if scale.dim() != 2 or scale.shape[1] < 1 or p.columns % scale.shape[1]:
-            raise ValueError("scale must be [rows, groups], groups a divisor of the %d columns" % p.columns)
-        p.scale_group = p.columns // scale.shape[1]
+        if scale.dim() != 2 or scale.shape[1] < 1 or columns % scale.shape[1]:
+            raise ValueError("scale must be [rows, groups], groups a divisor of the %d columns" % columns)
+        p.scale_group, = _i32(columns // scale.shape[1])
     return p
 
 
@@ -126,16 +133,18 @@ def make_matvec4_params(x, weight, scale, out, *, group_size, zero=None, bias=No
     _hold(p, x, weight, scale, out, zero, bias, x_scale)
     M, K = x.shape
     O = weight.shape[0]
-    p.rows, p.in_features, p.out_features, p.group_size = M, K, O, int(group_size)
-    if p.group_size < 1:
+    group_size = int(group_size)
+    if group_size < 1:
         raise ValueError("group_size must be positive")
+    p.rows, p.in_features, p.out_features = _i32(M, K, O)
+    p.group_size = min(group_size, 1 << 30)     # the longest row's: one group
     if x.dtype in (torch.float8_e4m3fn, torch.int8):
         p.x_dtype = _code(x, "x")
         if x_scale is None:
             raise ValueError("x in 8 bits needs x_scale")
         if x_scale.dim() != 2 or x_scale.shape[0] != M or x_scale.shape[1] < 1 or K % x_scale.shape[1]:
             raise ValueError("x_scale must be [rows, groups], groups a divisor of the %d columns" % K)
-        p.x_group, p.x_scale = K // x_scale.shape[1], _ptr(x_scale, torch.float32)
+        (p.x_group,), p.x_scale = _i32(K // x_scale.shape[1]), _ptr(x_scale, torch.float32)
     else:
         p.x_dtype = _io(x)
         if x_scale is not None:
@@ -143,7 +152,7 @@ def make_matvec4_params(x, weight, scale, out, *, group_size, zero=None, bias=No
     p.x, p.x_stride = _rows(x)
     _shape(weight, (O, (K + 1) // 2), "weight")
     p.weight, p.weight_stride = _rows(weight, torch.uint8)
-    groups = -(-K // p.group_size)
+    groups = -(-K // group_size)
     _shape(scale, (O, groups), "scale")
     _shape(zero, (O, groups), "zero")
     p.scale_dtype = binding._dtype_code(scale, (SSD_F32, SSD_BF16, SSD_F16))
@@ -186,7 +195,7 @@ def make_verify_params(target_probs, tokens, cu_seqlens, accept_u, sample_u, out
           device_status)
     T, V = target_probs.shape
     S, n = cu_seqlens.shape[0] - 1, 0 if accept_u is None else accept_u.shape[0]
-    p.total_tokens, p.num_drafts, p.num_seqs, p.vocab = T, n, S, V
+    p.total_tokens, p.num_drafts, (p.num_seqs, p.vocab) = T, n, _i32(S, V)
     p.prob_dtype = _io(target_probs)
     p.target_probs, p.target_stride = _rows(target_probs)
     if draft_probs is not None:

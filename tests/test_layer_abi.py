@@ -258,3 +258,47 @@ def test_reference_verification_keeps_the_targets_distribution():
                 assert status == 0
                 mass[out[0]] += q[d] / len(grid) ** 2
     np.testing.assert_allclose(mass, p, atol=0.011)
+
+
+# ---- sizes that a 32-bit field does not hold ---------------------------------
+WIDE = 1 << 32
+
+
+def test_a_group_longer_than_32_bits_is_one_group_of_the_row():
+    """A wrapped size of 32 would read a scale for every 32 columns where there is one."""
+    x, w, s, out = _t(3, 64), _t(4, 32, dtype=U8), _t(4, 1), _t(3, 4)
+    for group in (WIDE + 32, WIDE, (1 << 31) + 32, 1 << 31, (1 << 31) - 1, 1 << 30, 64):
+        p = layer.make_matvec4_params(x, w, s, out, group_size=group)
+        assert p.in_features == 64 and p.group_size >= 64
+    for group in (0, -1, -WIDE + 32):
+        with pytest.raises(ValueError):
+            layer.make_matvec4_params(x, w, s, out, group_size=group)
+
+
+@pytest.mark.parametrize("more", [0, 64, 1 << 31, WIDE + 64])
+def test_sizes_past_32_bits_do_not_wrap_into_small_ones(more):
+    """They stay sizes that the library refuses."""
+    def t(*shape, dtype=torch.float32):
+        return torch.empty(*shape, dtype=dtype, device="meta")
+    n = WIDE + more
+    p = layer.make_residual_norm_params(t(1, n), t(n), t(1, n))
+    assert p.columns > 1 << 20
+    p = layer.make_residual_norm_params(t(1, n), t(n), None, codes=t(1, n, dtype=FP8), scale=t(1, 1))
+    assert p.columns > 1 << 20
+    p = layer.make_matvec4_params(t(1, n), t(4, n // 2, dtype=U8), t(4, 1), t(1, 4), group_size=n)
+    assert p.in_features > 1 << 30
+    p = layer.make_matvec4_params(t(1, 64), t(n, 32, dtype=U8), t(n, 1), t(1, n), group_size=64)
+    assert p.out_features > 1 << 30
+    p = layer.make_matvec4_params(t(n, 64), t(4, 32, dtype=U8), t(4, 1), t(n, 4), group_size=64)
+    assert p.rows >= 1 << 30
+    for x_dtype, parts in ((F32, 3), (BF16, 1), (E4M3, 1)):     # refused before anything is enqueued
+        with pytest.raises(layer.LayerError) as e:
+            mixer._call("ssd_matvec4", _mv(rows=p.rows, x_dtype=x_dtype), 0)
+        assert e.value.code == UNSUPPORTED
+    args = [t(5, n), t(5, dtype=I32), t(3, dtype=I32), t(3), t(2), t(5, dtype=I32), t(2, dtype=I32)]
+    assert layer.make_verify_params(*args).vocab > 1 << 30
+    args = [t(5, 7), t(5, dtype=I32), t(n + 1, dtype=I32), t(3), t(n), t(5, dtype=I32), t(n, dtype=I32)]
+    p = layer.make_verify_params(*args)
+    with pytest.raises(layer.LayerError) as e:
+        mixer._call("ssd_verify_drafts", _verify(num_seqs=p.num_seqs), 0)
+    assert e.value.code == UNSUPPORTED
