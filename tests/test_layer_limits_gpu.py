@@ -3,7 +3,8 @@ import numpy as np
 import pytest
 
 from state_space_model_varlen_gb300 import layer
-from tests.test_layer_gpu import Draw, _norm_case, _probs, _torch, _verify_check, _windows
+from tests import layer_reference as R
+from tests.test_layer_gpu import Draw, _norm_case, _np, _probs, _t, _torch, _verify_check, _windows
 
 pytestmark = pytest.mark.gpu
 
@@ -110,3 +111,34 @@ def test_verify_rows_of_any_magnitude(unit, S, V):
 def test_norm_codes_of_long_rows_in_small_odd_groups(cols, group, io, res):
     _norm_case(2, cols, io, res, "e4m3", group, seed=cols)
     _norm_case(2, cols, io, None, "i8", group, out=False, seed=cols)
+
+
+# ---------------------------------------------------------------------------
+# 4-bit products: rows so long that a bound of roundings says little
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("rows,K,O", [(2, (1 << 20) + 64, 5), (9, (1 << 20) + 7, 3), (3, 1 << 20, 5), (2, 65536, 70), (20, 32768, 40),
+                                      (3, 65502, 33)])
+@pytest.mark.parametrize("x", ["bf16", "f32", "e4m3", "i8"])
+@pytest.mark.parametrize("group", [128, 32, 50, 7, 1 << 30])
+def test_matvec_long_rows_exactly(rows, K, O, x, group):
+    """Few columns of x are not zero, and scales are powers of two: every sum is a multiple of 2^-4 below 2^20, which fp32
+    holds whatever the order, so that the product has to be the exact one."""
+    torch = _torch()
+    d = Draw(rows + K + O)
+    groups = -(-K // group)
+    w, z = d.ints(0, 256, O, (K + 1) // 2, dtype="u8"), d.ints(6, 11, O, groups, dtype="u8")
+    s = torch.exp2(d.ints(-2, 3, O, groups).float())
+    values = d.ints(0, 2, rows, K).float() * 2 - 1
+    xv = torch.where(d.rand(rows, K) < min(1.0, 4000.0 / K), values, 0.0)
+    for k in (0, 1, 1023, 1024, K // 2, (1 << 20) - 1, 1 << 20, K - 2, K - 1):      # ends of rows and of chunks
+        if k < K:
+            xv[:, k] = 100.0 if x != "e4m3" else 104.0
+    xs, x_group = None, 1
+    if x in R.LIM:
+        x_group = K // 2 if K % 2 == 0 else K
+        xs = torch.exp2(d.ints(-2, 1, rows, K // x_group).float())
+    got = layer.matvec4(xv.to(_t(x)), w, s, group_size=group, zero=z, x_scale=xs, out_dtype=torch.float32)
+    size = np.abs(_np(xv)).sum(1).max() * 10 * 4
+    assert size < 2 ** 20
+    want, _ = R.matvec4(_np(xv), w.cpu().numpy(), _np(s), z.cpu().numpy(), None, group, _np(xs), x_group)
+    assert np.array_equal(_np(got), want)
