@@ -50,7 +50,9 @@ extern "C" {
  *
  * The norm is of v before it is rounded, the codes are of n before it is
  * rounded.  The codes of scale_group columns share one fp32 scale by the rule of
- * SSD_E4M3 and SSD_I8 (ssd_mixer.h), to nearest even.
+ * SSD_E4M3 and SSD_I8 (ssd_mixer.h), to nearest even.  Squares and their sum are in
+ * fp32: where the sum is beyond it n is 0 (NaN where v is not finite), and with
+ * eps = 0 a row of zeros has no norm (NaN).
  * Layouts, with row strides in elements:
  *   x, out        [rows, columns] io_dtype          weight [columns] or NULL
  *   residual, residual_out [rows, columns] residual_dtype
@@ -94,7 +96,8 @@ ssd_status ssd_residual_norm(const ssd_residual_norm_params *params, struct CUst
  * All arithmetic is in fp32, each output is rounded once; a group's columns may be
  * added before their scale is applied (15 |x| group_size has to be a fp32 number,
  * scales are below 2^121).  It is made for few rows: more of them are computed as
- * exactly, and read the weights again (once for every 32 rows, 10 of fp32).
+ * exactly, and read and unpack the weights again, which takes its time each time
+ * (once for every 32 rows, 10 of fp32).
  * Layouts:
  *   x       [rows, in_features] x_dtype, row stride x_stride elements
  *   x_scale [rows, ceil(in_features / x_group)] fp32, dense (8-bit x alone)
@@ -103,8 +106,8 @@ ssd_status ssd_residual_norm(const ssd_residual_norm_params *params, struct CUst
  *   zero    the same, one byte each, dense (or NULL)
  *   bias    [out_features] out_dtype (or NULL)
  *   out     [rows, out_features] out_dtype, row stride out_stride elements
- * Any in_features, group_size and x_group are computed.  The tensor cores take even
- * group sizes from 16 on (and x_group a multiple of 32 with group_size, or equal to
+ * Any in_features, group_size and x_group are computed.  The tensor cores take rows
+ * of up to 2^20 columns, even group sizes from 16 on (and x_group a multiple of 32 with group_size, or equal to
  * it, or a row); multiples of 32 without waste, and fastest rows of whole 16 bytes.
  * in_features and out_features up to 2^30 (SSD_ERR_UNSUPPORTED above), and rows
  * whose tiles a grid holds (500,000).                                       */

@@ -4,7 +4,7 @@
 //
 // Here the kernel for any sizes, and the plan of the one on the tensor cores
 // (ssd_matvec4_mma.cuh), which takes all but groups of odd sizes or below 16 columns,
-// activation scales across groups, and rows of more than 2^20 columns.
+// activation scales that no block of 32 columns keeps to, and rows of more than 2^20 columns.
 #include "ssd_matvec4_mma.cuh"
 
 namespace ssd {

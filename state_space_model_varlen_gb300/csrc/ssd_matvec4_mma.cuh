@@ -7,10 +7,13 @@
 // of eight bits each, which together are exact.  Sums within a group are the
 // instruction's fp32 sums; the groups' scales, times 64, are applied to them in fp32.
 //
-// Bound by HBM in principle, by instructions in fact: of about 300 a step of 32
-// outputs x 128 columns 160 unpack the codes, 16 are products, and with the loop's the
-// integer pipe takes most of the time (the unpacking and the products alone ran at 8.1
-// TB/s of codes with 8 warps an SM).  Codes stream through a ring of asynchronous copies
+// Bound by HBM in principle, by latency in fact, at the 9 to 16 warps an SM that two
+// CTAs make; no pipe is full.  One row of 4,096 to 18,560 issues in 47 % of the cycles (the
+// integer pipe is 38 % busy) and waits at the chunk's barrier, for fixed latencies and for
+// the first codes; 16 rows with groups of 32 in 36 % (25), 166 CTAs where 304 have room; the
+// head of 2^17 outputs in 61 % (50) while its 512 CTAs, 1.7 rounds of those places, run.
+// A step of 32 outputs x 128 columns is about 300 instructions, of which 160 unpack the
+// codes and 16 are products (these alone ran at 8.1 TB/s of codes with 8 warps an SM).  Codes stream through a ring of asynchronous copies
 // of each warp's own, a few steps deep.  x and the scales come through two buffers in
 // shared memory, a chunk of steps ahead in registers.  Where there are few tiles two or
 // four warps take the steps of the same outputs in turn, and a cluster of CTAs shares a
@@ -18,8 +21,7 @@
 //
 // Measured (floor at the copy rate): 1 row of 4,096 to 18,560 outputs, groups of 128,
 // 12.0 us (5.8); 3 rows of 4,096 to 131,072 61.7 us (41); 16 rows of 2,560 to 10,576,
-// groups of 32 with zeros, 16.4 us (2.4: scales and zeros take as many instructions as the
-// products).  Rows of 4,102 columns, which no 16-byte copy takes whole, 29 us where rows
+// groups of 32 with zeros, 16.4 us (2.4; scales and zeros of every block besides).  Rows of 4,102 columns, which no 16-byte copy takes whole, 29 us where rows
 // of 4,096 take 12; 16 rows 17 us, 32 26, 64 44.  Before: tiles of 32 outputs whose columns
 // eight warps shared, all of x in shared memory (head 63 us; 22 to 29 us where x of many
 // rows left one CTA an SM, and whole rows alone); codes shifted to the mantissa's end and

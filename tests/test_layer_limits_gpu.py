@@ -142,3 +142,22 @@ def test_matvec_long_rows_exactly(rows, K, O, x, group):
     assert size < 2 ** 20
     want, _ = R.matvec4(_np(xv), w.cpu().numpy(), _np(s), z.cpu().numpy(), None, group, _np(xs), x_group)
     assert np.array_equal(_np(got), want)
+
+
+@pytest.mark.parametrize("cols", [32, 640, 2009, 40000])
+@pytest.mark.parametrize("code", [None, "e4m3"])
+def test_norm_rows_whose_squares_fp32_does_not_hold(cols, code):
+    """A sum of squares beyond fp32 gives zeros, NaN where the row is not finite; zeros with eps = 0 give NaN; the row
+    beside them is as it is alone."""
+    torch = _torch()
+    d = Draw(cols)
+    x = d.randn(4, cols)
+    x[0], x[2], x[3, 1] = 2.0 ** 66, 0.0, float("inf")
+    kw = dict(eps=0.0, **(dict(code_dtype=_t(code), scale_group=cols) if code else {}))
+    got, alone = layer.residual_rms_norm(x, **kw), layer.residual_rms_norm(x[1:2], **kw)
+    if code:
+        (got, scale), (alone, s1) = got, alone
+        assert float(scale[0]) == 0.0 and torch.isnan(scale[2:]).all() and float(scale[1]) == float(s1)
+    else:
+        assert torch.isnan(got[2]).all() and torch.isnan(got[3, 1]) and (got[3, 2:] == 0).all()
+    assert (got[0].float() == 0).all() and torch.equal(got[1:2].float(), alone.float())
